@@ -71,7 +71,11 @@
 extern "C" {
 #endif
 
-enum dspark_dtype { DSPARK_F32 = 0, DSPARK_BF16 = 1 };
+enum dspark_dtype {
+    DSPARK_F32 = 0,
+    DSPARK_BF16 = 1,
+    DSPARK_E4M3 = 2                  /* 8-bit float, 4 exponent and 3 fraction bits: key-value caches only */
+};
 
 enum dspark_status {
     DSPARK_OK = 0,
@@ -82,7 +86,8 @@ enum dspark_status {
     DSPARK_ERR_TIMEOUT = -5,         /* a bounded device wait ran out */
     DSPARK_ERR_BAD_TOKEN = -6,       /* a token id outside [0, V) reached a kernel */
     DSPARK_ERR_UNIMPLEMENTED = -7,
-    DSPARK_ERR_WORKSPACE = -8        /* workspace null, misaligned or too small */
+    DSPARK_ERR_WORKSPACE = -8,       /* workspace null, misaligned or too small */
+    DSPARK_ERR_BAD_PAGE = -9         /* a page id, length or offset outside its range reached a kernel */
 };
 
 /* Text for a status code (static storage). */
@@ -93,7 +98,8 @@ const char* dspark_version(void);
 /*
  * Synchronises `stream`, then reads and clears the device status word at the
  * start of workspace `ws` (any workspace this library was given).  Returns
- * DSPARK_OK, DSPARK_ERR_BAD_TOKEN, DSPARK_ERR_TIMEOUT or DSPARK_ERR_CUDA.
+ * DSPARK_OK, DSPARK_ERR_BAD_TOKEN, DSPARK_ERR_BAD_PAGE, DSPARK_ERR_TIMEOUT or
+ * DSPARK_ERR_CUDA.
  */
 int dspark_workspace_status(void* ws, void* stream);
 
@@ -447,6 +453,142 @@ int dspark_sts_fit(const float* c, const int32_t* accept_len, int N, int gamma,
  * double, all device.  No workspace.
  */
 int dspark_sts_apply(const float* c, int N, int gamma, const double* t, float* out, void* stream);
+
+/* ------------------------------------------------- attention and its cache */
+
+/*
+ * The target model's attention around a cycle (no counterpart on the pages,
+ * which start from the logits): the keys and values of new tokens are written
+ * into a paged cache, attention of the new tokens reads it (the verification
+ * block: the last accepted token and up to gamma drafts, so 1 .. gamma + 1
+ * tokens per request, of another count for every request when the scheduler
+ * picked the lengths), whole prompts attend to themselves, and a request's
+ * cached tokens are read back.
+ *
+ * Paged cache.  Token j of a request lies in page page_table[j / page] at
+ * slot j % page; heads are separate planes of a page.
+ *   k, v       [n_pages, n_kv_heads, page, head_dim]  dtype
+ *   k_scale, v_scale  [n_pages, n_kv_heads, page]     float, DSPARK_E4M3 only (else NULL):
+ *                     the stored row is code * scale
+ *   dtype      DSPARK_BF16 or DSPARK_E4M3
+ * Requirements: n_pages >= 1, page in {16, 32, 64, 128, 256}, n_kv_heads in
+ * [1, 4096], head_dim 64 or 128 (SHAPE); k, v and the scales 16-byte aligned
+ * device memory of the current device (INVALID_ARG).  The struct is read on
+ * the host during the call.
+ */
+typedef struct {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    int dtype;
+    int n_pages, page, n_kv_heads, head_dim;
+} dspark_kv_cache_t;
+
+/*
+ * The requests of one call.  Request r brings the new tokens
+ * [q_off[r], q_off[r+1]) of the packed token axis; with them it has kv_len[r]
+ * tokens, so its new token i (from 0) stands at position
+ * kv_len[r] - (q_off[r+1] - q_off[r]) + i.
+ *   q_off      [R + 1] int32, not decreasing
+ *   kv_len     [R]     int32 (NULL for dspark_kv_read)
+ *   page_table [R, max_pages] int32; entries past a request's pages are never read
+ *   T          length of the packed token axis (q_off[R] <= T)
+ * R >= 1, max_pages >= 1, T >= 0 (SHAPE); T = 0 returns OK at once.
+ * A request whose offsets decrease is empty.  An offset outside [0, T], a kv_len outside
+ * [0, max_pages * page] is taken as the nearest value in range; a token of a page
+ * whose id is outside [0, n_pages) is not written and reads as zeros.  In each of
+ * these cases the status word records DSPARK_ERR_BAD_PAGE.
+ */
+typedef struct {
+    const int32_t* q_off;
+    const int32_t* kv_len;
+    const int32_t* page_table;
+    int R, max_pages, T;
+} dspark_kv_batch_t;
+
+/* Workspace bytes of dspark_kv_write and dspark_kv_read (the status word). */
+size_t dspark_kv_workspace_size(void);
+
+/*
+ * Write the new tokens' keys and values to their places in the cache.
+ *   K, V     [T, n_kv_heads, head_dim] bfloat16; k_stride and v_stride are the
+ *            elements from one token to the next (a slice of a fused
+ *            projection needs no copy): multiples of 8, at least
+ *            n_kv_heads * head_dim; K and V 16-byte aligned
+ * DSPARK_BF16: the rows are copied.  DSPARK_E4M3: with a = max |x| over a row
+ * (one token, one head), scale = a / 448 and each code is the e4m3 value
+ * nearest to x * 448 / a (ties to even, decided as in exact arithmetic);
+ * a = 0 gives scale 0 and codes 0; a row that holds a NaN or an infinity gets
+ * codes 0 and a scale of that kind, and reads back as NaN.
+ * A token whose position is negative is not written; two tokens of a call
+ * must not share a place.
+ */
+int dspark_kv_write(const dspark_kv_cache_t* cache, const dspark_kv_batch_t* batch,
+                    const void* K, const void* V, int64_t k_stride, int64_t v_stride,
+                    void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Read cached tokens back: token j of request r (j < q_off[r+1] - q_off[r],
+ * from its first token on) goes to row q_off[r] + j of
+ *   K, V     [T, n_kv_heads, head_dim] bfloat16 (device, caller-owned, 16-byte aligned)
+ * as code * scale rounded once (DSPARK_E4M3), or bit for bit (DSPARK_BF16).
+ * batch->kv_len is not read.
+ */
+int dspark_kv_read(const dspark_kv_cache_t* cache, const dspark_kv_batch_t* batch,
+                   void* K, void* V, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of dspark_attn_paged; 0 for unsupported sizes. */
+size_t dspark_attn_paged_workspace_size(int R, int T, int n_heads, int n_kv_heads, int head_dim);
+
+/*
+ * Attention of the new tokens over the cache (which already holds them:
+ * dspark_kv_write).  Query head h reads key-value head h / (n_heads /
+ * n_kv_heads).  New token i of request r sees the keys j <= its own position:
+ *   s_j = scale * (q . k_j),  out = sum_j softmax(s)_j v_j,  lse = ln sum_j exp(s_j)
+ *   q    [T, n_heads, head_dim] bfloat16, q_stride elements from token to token
+ *        (a multiple of 8, at least n_heads * head_dim); 16-byte aligned
+ *   out  [T, n_heads, head_dim] bfloat16, 16-byte aligned
+ *   lse  [T, n_heads] float, may be NULL
+ * A token that sees no key (its position is negative) gets out = 0 and
+ * lse = -inf.  Rows of out and lse that belong to no request stay untouched.
+ * Products take bf16 factors (e4m3 codes are widened exactly, their scales
+ * multiply scores and weights in float32) and are summed in float32; softmax
+ * weights are rounded to bf16 for the product with V; the sum, maximum and
+ * lse are float32.  The order of all sums depends on the sizes and the
+ * device only, so reruns agree bit for bit.
+ * Cached values past kv_len[r] never matter, whatever bits they hold; K and V
+ * of the kv_len[r] tokens themselves must be finite.
+ * n_heads is a multiple of n_kv_heads, n_heads / n_kv_heads <= 128, scale
+ * finite.
+ */
+int dspark_attn_paged(const void* q, int64_t q_stride, const dspark_kv_cache_t* cache,
+                      const dspark_kv_batch_t* batch, int n_heads, float scale,
+                      void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of dspark_attn_prompt; 0 for unsupported sizes. */
+size_t dspark_attn_prompt_workspace_size(int B, int T, int n_heads, int n_kv_heads, int head_dim);
+
+/*
+ * Causal attention over whole prompts, packed one after another: sequence b
+ * is tokens [seq_off[b], seq_off[b+1]), and its token i sees its tokens
+ * j <= i.  Scores, softmax, precision and grouped heads as dspark_attn_paged.
+ *   q    [T, n_heads, head_dim] bfloat16     k, v [T, n_kv_heads, head_dim] bfloat16
+ *        with q_stride, k_stride, v_stride elements from token to token
+ *        (multiples of 8, at least the heads times head_dim); 16-byte aligned
+ *        device memory of the current device
+ *   seq_off [B + 1] int32, not decreasing, in [0, T] (a value outside is taken as
+ *        the nearest in range; the status word records DSPARK_ERR_BAD_PAGE)
+ *   out  [T, n_heads, head_dim] bfloat16, lse [T, n_heads] float or NULL; rows
+ *        that belong to no sequence stay untouched
+ * Sequences never mix: values of one, finite or not, cannot reach another's
+ * rows.  B >= 1, T >= 0 (T = 0 returns OK at once), head_dim 64 or 128,
+ * n_heads / n_kv_heads <= 128.
+ */
+int dspark_attn_prompt(const void* q, const void* k, const void* v,
+                       int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                       const int32_t* seq_off, int B, int T, int n_heads, int n_kv_heads, int head_dim,
+                       float scale, void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------- random */
 

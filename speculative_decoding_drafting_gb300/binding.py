@@ -20,13 +20,15 @@ from . import _build
 
 F32 = 0
 BF16 = 1
+E4M3 = 2
 
 _lock = threading.Lock()
 _lib = None
 
 STATUS = {0: "ok", -1: "invalid argument", -2: "unsupported dtype", -3: "unsupported sizes",
           -4: "CUDA runtime error", -5: "bounded device wait ran out", -6: "token id outside [0, V)",
-          -7: "not implemented", -8: "workspace null, misaligned or too small"}
+          -7: "not implemented", -8: "workspace null, misaligned or too small",
+          -9: "page id, length or offset outside its range"}
 
 
 class DsparkError(RuntimeError):
@@ -84,6 +86,15 @@ def load(build_if_missing: bool = True):
         L.dspark_sts_fit.argtypes = [P, P, i32, i32, P, i32, i32, P, P, P, P, P, sz, P]
         L.dspark_sts_apply.argtypes = [P, i32, i32, P, P, P]
         L.dspark_philox4x32_10.argtypes = [P, P, P, i32, P]
+        i64 = ctypes.c_int64
+        for name in ("dspark_kv_workspace_size", "dspark_attn_paged_workspace_size",
+                     "dspark_attn_prompt_workspace_size"):
+            getattr(L, name).argtypes = [] if name == "dspark_kv_workspace_size" else [i32] * 5
+            getattr(L, name).restype = sz
+        L.dspark_kv_write.argtypes = [P, P, P, P, i64, i64, P, sz, P]
+        L.dspark_kv_read.argtypes = [P, P, P, P, P, sz, P]
+        L.dspark_attn_paged.argtypes = [P, i64, P, P, i32, f32, P, P, P, sz, P]
+        L.dspark_attn_prompt.argtypes = [P, P, P, i64, i64, i64, P, i32, i32, i32, i32, i32, f32, P, P, P, sz, P]
         L.dspark_workspace_set_wait.argtypes = [P, u64, i32, P]
         L.dspark_profile_enable.argtypes = [i32]
         L.dspark_profile_collect.argtypes = [P, P, i32]
@@ -94,7 +105,8 @@ def load(build_if_missing: bool = True):
                      "dspark_schedule_threshold",
                      "dspark_sts_fit",
                      "dspark_sts_apply", "dspark_philox4x32_10", "dspark_workspace_set_wait",
-                     "dspark_workspace_status", "dspark_profile_enable", "dspark_profile_collect"):
+                     "dspark_workspace_status", "dspark_profile_enable", "dspark_profile_collect",
+                     "dspark_kv_write", "dspark_kv_read", "dspark_attn_paged", "dspark_attn_prompt"):
             getattr(L, name).restype = i32
         _lib = L
         return _lib
@@ -426,6 +438,167 @@ def sts_apply(c, t, out=None, stream=None):
         out = torch.empty_like(c)
     code = L.dspark_sts_apply(_p(c), N, gamma, _p(t), _p(out), _stream(stream))
     _check("dspark_sts_apply", code)
+    return out
+
+
+class _Cache(ctypes.Structure):
+    """dspark_kv_cache_t."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("dtype", ctypes.c_int), ("n_pages", ctypes.c_int),
+                ("page", ctypes.c_int), ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int)]
+
+
+class _Batch(ctypes.Structure):
+    """dspark_kv_batch_t."""
+    _fields_ = [("q_off", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("R", ctypes.c_int), ("max_pages", ctypes.c_int), ("T", ctypes.c_int)]
+
+
+class KvCache:
+    """One layer's paged key-value cache: k and v [n_pages, n_kv_heads, page,
+    head_dim] in bfloat16 or float8_e4m3fn; the latter with float32 scales
+    k_scale and v_scale [n_pages, n_kv_heads, page]."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise TypeError(f"the cache must be bfloat16 or float8_e4m3fn, got {k.dtype}")
+        if k.dim() != 4:
+            raise ValueError("the cache must have shape (n_pages, n_kv_heads, page, head_dim)")
+        _shape("v", v, k.shape, k.dtype)
+        f8 = k.dtype == torch.float8_e4m3fn
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if f8 != (t is not None):
+                raise ValueError(f"{name} goes with a float8_e4m3fn cache, and only with one")
+            _shape(name, t, k.shape[:3], torch.float32)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_pages, self.n_kv_heads, self.page, self.head_dim = k.shape
+
+    @classmethod
+    def empty(cls, n_pages: int, n_kv_heads: int, page: int, head_dim: int, dtype=torch.bfloat16, device="cuda"):
+        """A new cache; its memory is not cleared (unwritten places are never read)."""
+        shape = (n_pages, n_kv_heads, page, head_dim)
+        k, v = (torch.empty(shape, dtype=dtype, device=device) for _ in range(2))
+        if dtype != torch.float8_e4m3fn:
+            return cls(k, v)
+        return cls(k, v, *(torch.empty(shape[:3], dtype=torch.float32, device=device) for _ in range(2)))
+
+    def _struct(self) -> _Cache:
+        dt = BF16 if self.k.dtype == torch.bfloat16 else E4M3
+        return _Cache(_p(self.k), _p(self.v), _p(self.k_scale), _p(self.v_scale), dt, self.n_pages, self.page,
+                      self.n_kv_heads, self.head_dim)
+
+
+def _batch(q_off, kv_len, page_table, T) -> _Batch:
+    if page_table.dim() != 2:
+        raise ValueError("page_table must have shape (R, max_pages)")
+    R, max_pages = page_table.shape
+    _shape("page_table", page_table, (R, max_pages), torch.int32)
+    _shape("q_off", q_off, (R + 1,), torch.int32)
+    _shape("kv_len", kv_len, (R,), torch.int32)
+    return _Batch(_p(q_off), _p(kv_len), _p(page_table), R, max_pages, T)
+
+
+def _token_rows(name: str, t, T, heads, dim):
+    """Data pointer and token stride of a bf16 [T, heads, dim] tensor whose
+    tokens may be strided (a slice of a fused projection)."""
+    _shape(name, t, (T, heads, dim), torch.bfloat16)
+    if not t.is_cuda:
+        raise ValueError("libdspark takes CUDA tensors")
+    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), (t.stride(0) if T > 1 else heads * dim)
+
+
+def kv_write(cache: KvCache, K, V, q_off, kv_len, page_table, ws=None, stream=None):
+    """Write new tokens' keys and values into the cache (``dspark_kv_write``);
+    returns the workspace (its status word records bad pages)."""
+    L = load()
+    T = K.shape[0]
+    b = _batch(q_off, kv_len, page_table, T)
+    kp, ks = _token_rows("K", K, T, cache.n_kv_heads, cache.head_dim)
+    vp, vs = _token_rows("V", V, T, cache.n_kv_heads, cache.head_dim)
+    c = cache._struct()
+    if ws is None:
+        ws = _workspace(L.dspark_kv_workspace_size(), cache.k.device)
+    code = L.dspark_kv_write(ctypes.byref(c), ctypes.byref(b), kp, vp, ks, vs, _p(ws), ws.numel(), _stream(stream))
+    _check("dspark_kv_write", code)
+    return ws
+
+
+def kv_read(cache: KvCache, kv_off, page_table, n_tokens: int, ws=None, out=None, stream=None):
+    """Cached tokens back as bf16 (``dspark_kv_read``): request r's first
+    kv_off[r+1] - kv_off[r] tokens go to rows kv_off[r].. of K and V
+    [n_tokens, n_kv_heads, head_dim]."""
+    L = load()
+    shape = (n_tokens, cache.n_kv_heads, cache.head_dim)
+    b = _batch(kv_off, None, page_table, n_tokens)
+    if out is None:
+        out = {name: torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device) for name in ("K", "V")}
+    for name in ("K", "V"):
+        _shape(name, out[name], shape, torch.bfloat16)
+    c = cache._struct()
+    if ws is None:
+        ws = _workspace(L.dspark_kv_workspace_size(), cache.k.device)
+    code = L.dspark_kv_read(ctypes.byref(c), ctypes.byref(b), _p(out["K"]), _p(out["V"]), _p(ws), ws.numel(),
+                            _stream(stream))
+    _check("dspark_kv_read", code)
+    out["ws"] = ws
+    return out
+
+
+def _attn_out(out, lse, T, heads, dim, dev):
+    if out is None:
+        out = dict(out=torch.empty((T, heads, dim), dtype=torch.bfloat16, device=dev))
+        if lse:
+            out["lse"] = torch.empty((T, heads), dtype=torch.float32, device=dev)
+    _shape("out", out["out"], (T, heads, dim), torch.bfloat16)
+    _shape("lse", out.get("lse"), (T, heads), torch.float32)
+    return out
+
+
+def attn_paged(q, cache: KvCache, q_off, kv_len, page_table, scale: Optional[float] = None, lse: bool = False,
+               ws=None, out=None, stream=None):
+    """Attention of the new tokens q [T, n_heads, head_dim] over the paged
+    cache (``dspark_attn_paged``); ``scale`` None: 1 / sqrt(head_dim).  Returns
+    a dict with ``out`` and, on request, ``lse`` [T, n_heads]."""
+    L = load()
+    T, heads, dim = q.shape
+    b = _batch(q_off, kv_len, page_table, T)
+    qp, qs = _token_rows("q", q, T, heads, cache.head_dim)
+    out = _attn_out(out, lse, T, heads, dim, q.device)
+    c = cache._struct()
+    if ws is None:
+        ws = _workspace(L.dspark_attn_paged_workspace_size(b.R, T, heads, cache.n_kv_heads, dim), q.device)
+    code = L.dspark_attn_paged(qp, qs, ctypes.byref(c), ctypes.byref(b), heads,
+                               float(dim ** -0.5 if scale is None else scale), _p(out["out"]), _p(out.get("lse")),
+                               _p(ws), ws.numel(), _stream(stream))
+    _check("dspark_attn_paged", code)
+    out["ws"] = ws
+    return out
+
+
+def attn_prompt(q, k, v, seq_off, scale: Optional[float] = None, lse: bool = False, ws=None, out=None, stream=None):
+    """Causal attention over whole packed prompts (``dspark_attn_prompt``):
+    q [T, n_heads, head_dim], k and v [T, n_kv_heads, head_dim], sequence b the
+    tokens seq_off[b] .. seq_off[b+1].  Returns a dict as ``attn_paged``."""
+    L = load()
+    T, heads, dim = q.shape
+    if k.dim() != 3:
+        raise ValueError("k must have shape (T, n_kv_heads, head_dim)")
+    kv_heads = k.shape[1]
+    B = seq_off.numel() - 1
+    _shape("seq_off", seq_off, (B + 1,), torch.int32)
+    qp, qs = _token_rows("q", q, T, heads, dim)
+    kp, ks = _token_rows("k", k, T, kv_heads, dim)
+    vp, vs = _token_rows("v", v, T, kv_heads, dim)
+    out = _attn_out(out, lse, T, heads, dim, q.device)
+    if ws is None:
+        ws = _workspace(L.dspark_attn_prompt_workspace_size(B, T, heads, kv_heads, dim), q.device)
+    code = L.dspark_attn_prompt(qp, kp, vp, qs, ks, vs, _p(seq_off), B, T, heads, kv_heads, dim,
+                                float(dim ** -0.5 if scale is None else scale), _p(out["out"]), _p(out.get("lse")),
+                                _p(ws), ws.numel(), _stream(stream))
+    _check("dspark_attn_prompt", code)
+    out["ws"] = ws
     return out
 
 

@@ -85,6 +85,7 @@ const char* dspark_strerror(int status) {
         case DSPARK_ERR_BAD_TOKEN: return "token id outside [0, V)";
         case DSPARK_ERR_UNIMPLEMENTED: return "not implemented";
         case DSPARK_ERR_WORKSPACE: return "workspace null, misaligned or too small";
+        case DSPARK_ERR_BAD_PAGE: return "page id, length or offset outside its range";
         default: return "unknown status";
     }
 }
@@ -114,6 +115,7 @@ int dspark_workspace_status(void* ws, void* stream) {
         if (cudaStreamSynchronize(s) != cudaSuccess) return DSPARK_ERR_CUDA;
     }
     if (word & kStatBadToken) return DSPARK_ERR_BAD_TOKEN;
+    if (word & kStatBadPage) return DSPARK_ERR_BAD_PAGE;
     if (word & kStatTimeout) return DSPARK_ERR_TIMEOUT;
     return DSPARK_OK;
 }
@@ -323,6 +325,130 @@ int dspark_schedule_threshold(const float* c, int R, int gamma, float theta, int
     if (!c || !verify_len || (mode != 0 && mode != 1)) return DSPARK_ERR_INVALID_ARG;
     return cuda_status(launch_schedule_threshold(c, R, gamma, theta, mode, verify_len,
                                                  static_cast<cudaStream_t>(stream)));
+}
+
+// The cache's own checks, shared by the three calls that take one.
+static int check_cache(const dspark_kv_cache_t* c) {
+    if (!c) return DSPARK_ERR_INVALID_ARG;
+    if (c->dtype != DSPARK_BF16 && c->dtype != DSPARK_E4M3) return DSPARK_ERR_UNSUPPORTED_DTYPE;
+    if (c->head_dim != 64 && c->head_dim != 128) return DSPARK_ERR_SHAPE;
+    if (c->n_pages < 1 || c->n_kv_heads < 1 || c->n_kv_heads > 4096) return DSPARK_ERR_SHAPE;
+    if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128 && c->page != 256) return DSPARK_ERR_SHAPE;
+    if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return DSPARK_ERR_INVALID_ARG;
+    if (c->dtype == DSPARK_E4M3 &&
+        (!c->k_scale || !c->v_scale || !aligned16(c->k_scale) || !aligned16(c->v_scale)))
+        return DSPARK_ERR_INVALID_ARG;
+    return DSPARK_OK;
+}
+
+static bool cache_on_device(const dspark_kv_cache_t* c) {
+    return on_current_device(c->k) && on_current_device(c->v) &&
+           (c->dtype != DSPARK_E4M3 || (on_current_device(c->k_scale) && on_current_device(c->v_scale)));
+}
+
+// Sizes first; the pointers only count when there is a token (T = 0 is done).
+static int check_batch_sizes(const dspark_kv_batch_t* b) {
+    if (!b) return DSPARK_ERR_INVALID_ARG;
+    return b->R < 1 || b->max_pages < 1 || b->T < 0 ? DSPARK_ERR_SHAPE : DSPARK_OK;
+}
+
+static bool stride_ok(int64_t stride, int heads, int dim) {
+    return stride % 8 == 0 && stride >= (int64_t)heads * dim && stride < (int64_t(1) << 36);
+}
+
+static int check_heads(int n_heads, int n_kv_heads, int head_dim) {
+    if (head_dim != 64 && head_dim != 128) return DSPARK_ERR_SHAPE;
+    if (n_kv_heads < 1 || n_kv_heads > 4096 || n_heads < 1 || n_heads % n_kv_heads || n_heads / n_kv_heads > 128)
+        return DSPARK_ERR_SHAPE;
+    return DSPARK_OK;
+}
+
+size_t dspark_kv_workspace_size(void) { return sizeof(WsHeader); }
+
+int dspark_kv_write(const dspark_kv_cache_t* cache, const dspark_kv_batch_t* batch, const void* K, const void* V,
+                    int64_t k_stride, int64_t v_stride, void* ws, size_t ws_bytes, void* stream) {
+    int st = check_cache(cache);
+    if (st) return st;
+    st = check_batch_sizes(batch);
+    if (st) return st;
+    if (batch->T == 0) return DSPARK_OK;
+    if (!K || !V || !aligned16(K) || !aligned16(V) || !batch->q_off || !batch->kv_len || !batch->page_table)
+        return DSPARK_ERR_INVALID_ARG;
+    if (!stride_ok(k_stride, cache->n_kv_heads, cache->head_dim) ||
+        !stride_ok(v_stride, cache->n_kv_heads, cache->head_dim))
+        return DSPARK_ERR_INVALID_ARG;
+    if (!ws || !aligned256(ws) || ws_bytes < sizeof(WsHeader)) return DSPARK_ERR_WORKSPACE;
+    if (!cache_on_device(cache)) return DSPARK_ERR_INVALID_ARG;
+    return cuda_status(launch_kv_write(*cache, *batch, K, V, k_stride, v_stride, ws, static_cast<cudaStream_t>(stream)));
+}
+
+int dspark_kv_read(const dspark_kv_cache_t* cache, const dspark_kv_batch_t* batch, void* K, void* V, void* ws,
+                   size_t ws_bytes, void* stream) {
+    int st = check_cache(cache);
+    if (st) return st;
+    st = check_batch_sizes(batch);
+    if (st) return st;
+    if (batch->T == 0) return DSPARK_OK;
+    if (!K || !V || !aligned16(K) || !aligned16(V) || !batch->q_off || !batch->page_table)
+        return DSPARK_ERR_INVALID_ARG;
+    if (!ws || !aligned256(ws) || ws_bytes < sizeof(WsHeader)) return DSPARK_ERR_WORKSPACE;
+    if (!cache_on_device(cache)) return DSPARK_ERR_INVALID_ARG;
+    return cuda_status(launch_kv_read(*cache, *batch, K, V, ws, static_cast<cudaStream_t>(stream)));
+}
+
+size_t dspark_attn_paged_workspace_size(int R, int T, int n_heads, int n_kv_heads, int head_dim) {
+    if (R < 1 || T < 0 || check_heads(n_heads, n_kv_heads, head_dim)) return 0;
+    return attn_paged_workspace_bytes(R, T, n_heads, n_kv_heads, head_dim);
+}
+
+int dspark_attn_paged(const void* q, int64_t q_stride, const dspark_kv_cache_t* cache,
+                      const dspark_kv_batch_t* batch, int n_heads, float scale, void* out, float* lse, void* ws,
+                      size_t ws_bytes, void* stream) {
+    int st = check_cache(cache);
+    if (st) return st;
+    st = check_batch_sizes(batch);
+    if (st) return st;
+    st = check_heads(n_heads, cache->n_kv_heads, cache->head_dim);
+    if (st) return st;
+    if (!std::isfinite(scale)) return DSPARK_ERR_INVALID_ARG;
+    if (batch->T == 0) return DSPARK_OK;
+    if (!q || !out || !aligned16(q) || !aligned16(out) || !batch->q_off || !batch->kv_len || !batch->page_table)
+        return DSPARK_ERR_INVALID_ARG;
+    if (!stride_ok(q_stride, n_heads, cache->head_dim)) return DSPARK_ERR_INVALID_ARG;
+    if (!ws || !aligned256(ws) ||
+        ws_bytes < attn_paged_workspace_bytes(batch->R, batch->T, n_heads, cache->n_kv_heads, cache->head_dim))
+        return DSPARK_ERR_WORKSPACE;
+    if (!cache_on_device(cache)) return DSPARK_ERR_INVALID_ARG;
+    return cuda_status(launch_attn_paged(q, q_stride, *cache, *batch, n_heads, scale, out, lse, ws,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+size_t dspark_attn_prompt_workspace_size(int B, int T, int n_heads, int n_kv_heads, int head_dim) {
+    if (B < 1 || T < 0 || check_heads(n_heads, n_kv_heads, head_dim)) return 0;
+    return attn_prompt_workspace_bytes(B, T, n_heads, n_kv_heads, head_dim);
+}
+
+int dspark_attn_prompt(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                       int64_t v_stride, const int32_t* seq_off, int B, int T, int n_heads, int n_kv_heads,
+                       int head_dim, float scale, void* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+    if (B < 1 || T < 0) return DSPARK_ERR_SHAPE;
+    int st = check_heads(n_heads, n_kv_heads, head_dim);
+    if (st) return st;
+    if (!std::isfinite(scale)) return DSPARK_ERR_INVALID_ARG;
+    if (T == 0) return DSPARK_OK;
+    if (!q || !k || !v || !out || !seq_off || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out))
+        return DSPARK_ERR_INVALID_ARG;
+    if (!stride_ok(q_stride, n_heads, head_dim) || !stride_ok(k_stride, n_kv_heads, head_dim) ||
+        !stride_ok(v_stride, n_kv_heads, head_dim))
+        return DSPARK_ERR_INVALID_ARG;
+    if (!ws || !aligned256(ws) || ws_bytes < attn_prompt_workspace_bytes(B, T, n_heads, n_kv_heads, head_dim))
+        return DSPARK_ERR_WORKSPACE;
+    if (!on_current_device(q) || !on_current_device(k) || !on_current_device(v)) return DSPARK_ERR_INVALID_ARG;
+    PromptArgs a;
+    a.q = q; a.k = k; a.v = v; a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
+    a.seq_off = seq_off; a.B = B; a.T = T; a.n_heads = n_heads; a.n_kv_heads = n_kv_heads; a.head_dim = head_dim;
+    a.scale = scale; a.out = out; a.lse = lse; a.ws = ws;
+    return cuda_status(launch_attn_prompt(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -18,7 +18,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Device status bits kept in the first word of every workspace.
-enum : uint32_t { kStatBadToken = 1u, kStatTimeout = 2u };
+enum : uint32_t { kStatBadToken = 1u, kStatTimeout = 2u, kStatBadPage = 4u };
 
 struct WsHeader {
     uint32_t status;

@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/dspark.h"
+
 namespace dspark {
 
 // Per-(request, step, V-slice) partial state of the draft's reduction over V:
@@ -127,6 +129,29 @@ cudaError_t launch_schedule_threshold(const float* c, int R, int gamma, float th
                                       cudaStream_t s);
 cudaError_t launch_schedule(const float* c, const double* sps, int n_sps, int R, int gamma, const int32_t* budget,
                             int32_t* len, double* theta, int32_t* nstar, void* ws, cudaStream_t s);
+
+struct PromptArgs {
+    const void* q;
+    const void* k;
+    const void* v;
+    int64_t q_stride, k_stride, v_stride;   // elements from one token to the next
+    const int32_t* seq_off;
+    int B, T, n_heads, n_kv_heads, head_dim;
+    float scale;
+    void* out;
+    float* lse;
+    void* ws;
+};
+
+cudaError_t launch_kv_write(const dspark_kv_cache_t& c, const dspark_kv_batch_t& b, const void* K, const void* V,
+                            int64_t k_stride, int64_t v_stride, void* ws, cudaStream_t s);
+cudaError_t launch_kv_read(const dspark_kv_cache_t& c, const dspark_kv_batch_t& b, void* K, void* V, void* ws,
+                           cudaStream_t s);
+size_t attn_paged_workspace_bytes(int R, int T, int n_heads, int n_kv_heads, int head_dim);
+cudaError_t launch_attn_paged(const void* q, int64_t q_stride, const dspark_kv_cache_t& c, const dspark_kv_batch_t& b,
+                              int n_heads, float scale, void* out, float* lse, void* ws, cudaStream_t s);
+size_t attn_prompt_workspace_bytes(int B, int T, int n_heads, int n_kv_heads, int head_dim);
+cudaError_t launch_attn_prompt(const PromptArgs& a, cudaStream_t s);
 
 int num_sms();
 

@@ -23,7 +23,8 @@ const char* const kNames[] = {"draft_prep",      "draft_sweep_generic", "draft_s
                               "verify_sample",   "schedule",            "draft_prep_rnn",   "draft_rnn_gru",
                               "schedule_threshold", "sts_hist",           "sts_ece",          "sts_advance",
                               "sts_apply",          "sts_fix",
-                              "draft_rnn_gru_finish"};
+                              "draft_rnn_gru_finish", "kv_write",        "kv_read",          "attn_paged",
+                              "attn_paged_join",    "attn_prompt"};
 
 cudaEvent_t take() {
     if (!g_pool.empty()) {

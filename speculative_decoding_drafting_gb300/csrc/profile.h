@@ -23,6 +23,11 @@ enum ProfName : int {
     kPStsApply = 15,
     kPStsFix = 16,
     kPDraftRnnGruFinish = 17,
+    kPKvWrite = 18,
+    kPKvRead = 19,
+    kPAttnPaged = 20,
+    kPAttnPagedJoin = 21,
+    kPAttnPrompt = 22,
 };
 
 void prof_begin(int name, cudaStream_t s);
