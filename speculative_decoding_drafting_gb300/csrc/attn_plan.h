@@ -1,0 +1,138 @@
+// attn_plan.h -- how paged attention splits its work (plain C++, also
+// compiled for the host, where its index ranges are checked).
+//
+// An item is one row tile of one request and one key-value head: up to
+// kRowTile of the request's rows (row = new token x query heads of the group,
+// heads fastest) over the keys that its last row sees, in tiles of kKeyTile
+// keys, at least one.  Items are numbered request, row tile, head; the tiles
+// of all items form one line, which is cut into equal spans, one per CTA, so
+// that requests of any mix of lengths load the device evenly.  An item that a
+// cut goes through leaves one partial result per piece.
+#pragma once
+
+#include <stdint.h>
+
+#if defined(__CUDACC__)
+#define DSPARK_HD __host__ __device__ __forceinline__
+#else
+#define DSPARK_HD inline
+#endif
+
+namespace dspark {
+
+constexpr int kKeyTile = 128;
+constexpr int kRowTile = 64;
+
+struct PlanInput {
+    const int32_t* q_off;
+    const int32_t* kv_len;
+    int R, T, group, kv_heads;
+    int64_t most;                  // max_pages * page
+};
+
+// A request's first row of the token axis, its new tokens and its keys, with
+// values out of range clamped.
+struct Request {
+    int a, q_len, kv_len;
+};
+DSPARK_HD int plan_clamp(int64_t x, int64_t hi) { return (int)(x < 0 ? 0 : (x > hi ? hi : x)); }
+DSPARK_HD Request plan_request(const PlanInput& p, int r) {
+    const int a = plan_clamp(p.q_off[r], p.T), b = plan_clamp(p.q_off[r + 1], p.T);
+    return Request{a, b > a ? b - a : 0, plan_clamp(p.kv_len[r], p.most < 0x7FFFFFFF ? p.most : 0x7FFFFFFF)};
+}
+DSPARK_HD int plan_row_tiles(const PlanInput& p, const Request& q) {
+    return (int)(((int64_t)q.q_len * p.group + kRowTile - 1) / kRowTile);
+}
+// Keys that row rho (of q_len * group) sees.
+DSPARK_HD int plan_seen(const PlanInput& p, const Request& q, int64_t rho) {
+    return plan_clamp((int64_t)q.kv_len - q.q_len + rho / p.group + 1, q.kv_len);
+}
+// Keys that row tile j reads, and how many key tiles they take.
+DSPARK_HD int plan_tile_keys(const PlanInput& p, const Request& q, int j) {
+    const int64_t rows = (int64_t)q.q_len * p.group, end = (int64_t)(j + 1) * kRowTile;
+    return plan_seen(p, q, (end < rows ? end : rows) - 1);
+}
+DSPARK_HD int plan_key_tiles(int keys) { return keys > 0 ? (keys - 1) / kKeyTile + 1 : 1; }
+DSPARK_HD int64_t plan_request_tiles(const PlanInput& p, int r) {
+    const Request q = plan_request(p, r);
+    const int n = plan_row_tiles(p, q);
+    int64_t sum = 0;
+    for (int j = 0; j < n; ++j) sum += plan_key_tiles(plan_tile_keys(p, q, j));
+    return sum * p.kv_heads;
+}
+// How many of `grid` CTAs get a span: none is left empty between two others,
+// since every CTA from an item's first to its last leaves a piece.
+DSPARK_HD int plan_spans(int64_t total, int grid) { return total < grid ? (int)total : grid; }
+// First tile of CTA c of n = plan_spans() (c = n: the end).
+DSPARK_HD int64_t plan_cut(int64_t total, int c, int n) { return total / n * c + total % n * c / n; }
+// The CTA whose span holds tile g.
+DSPARK_HD int plan_owner(int64_t total, int64_t g, int n) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (plan_cut(total, mid, n) <= g) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// One CTA's piece of an item: key tiles [t0, t1) of tiles.
+struct Segment {
+    int r, j, h;
+    int t0, t1, tiles;
+    int keys;                      // keys the row tile reads
+    int rows;                      // rows of the row tile
+    Request q;
+};
+
+// Walks a span of the line of tiles.
+struct Cursor {
+    int r, j, h, t;
+    int64_t left;
+    Request q;
+
+    // start inside request r, `skip` tiles after its first
+    DSPARK_HD void start(const PlanInput& p, int r_, int64_t skip, int64_t n) {
+        r = r_;
+        j = h = t = 0;
+        left = n;
+        if (n <= 0) return;
+        q = plan_request(p, r);
+        for (;; ++j) {
+            const int tiles = plan_key_tiles(plan_tile_keys(p, q, j));
+            if (skip < (int64_t)tiles * p.kv_heads) {
+                h = (int)(skip / tiles);
+                t = (int)(skip % tiles);
+                return;
+            }
+            skip -= (int64_t)tiles * p.kv_heads;
+        }
+    }
+    DSPARK_HD bool next(const PlanInput& p, Segment& s) {
+        if (left <= 0) return false;
+        while (q.q_len == 0) q = plan_request(p, ++r);     // left > 0: a request with rows follows
+        const int64_t rows = (int64_t)q.q_len * p.group - (int64_t)j * kRowTile;
+        s.r = r;
+        s.j = j;
+        s.h = h;
+        s.q = q;
+        s.keys = plan_tile_keys(p, q, j);
+        s.tiles = plan_key_tiles(s.keys);
+        s.rows = (int)(rows < kRowTile ? rows : kRowTile);
+        s.t0 = t;
+        s.t1 = (int)(s.tiles - t < left ? s.tiles : t + left);
+        left -= s.t1 - s.t0;
+        t = 0;
+        if (left > 0 && ++h == p.kv_heads) {
+            h = 0;
+            if (++j == plan_row_tiles(p, q)) {
+                j = 0;
+                ++r;
+                q = plan_request(p, r);
+            }
+        }
+        return true;
+    }
+};
+
+}  // namespace dspark

@@ -505,7 +505,7 @@ bool make_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, void* base, cons
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     // host-side guard: a swizzled box row must fit the 128-byte swizzle span
-    const cuuint32_t es = (dt == CU_TENSOR_MAP_DATA_TYPE_FLOAT32) ? 4u : 2u;
+    const cuuint32_t es = dt == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 4u : (dt == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? 1u : 2u);
     if (swz != CU_TENSOR_MAP_SWIZZLE_NONE && box[0] * es > 128u) return false;
     if ((box[0] * es) % 16u) return false;
     cuuint32_t estr[3] = {1, 1, 1};
@@ -648,6 +648,11 @@ cudaError_t launch_typed(DraftArgs& a, int k, cudaStream_t s) {
 }  // namespace
 
 bool draft_tc_encode_available() { return encode_fn() != nullptr; }
+
+bool make_tensor_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base, const cuuint64_t* dims,
+                     const cuuint64_t* strides_bytes, const cuuint32_t* box, CUtensorMapSwizzle swz) {
+    return make_map(m, dt, rank, const_cast<void*>(base), dims, strides_bytes, box, swz);
+}
 
 bool draft_tc_make_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, void* base, const cuuint64_t* dims,
                        const cuuint64_t* strides_bytes, const cuuint32_t* box) {
