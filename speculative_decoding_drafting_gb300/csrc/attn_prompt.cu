@@ -1,69 +1,590 @@
-// attn_prompt.cu -- causal attention over whole prompts, packed one after another.
+// attn_prompt.cu -- causal attention over whole prompts, packed one after
+// another (sm_103a: TMA, tcgen05, TMEM).
 //
-// One warp per (token, query head): its lanes hold head_dim / 32 values each
-// and walk the keys with the running maximum and sum of a softmax.
+// A row is one token of one query head; a row tile is 128 rows: the whole
+// group of query heads that share a key-value head, for 128 / group tokens
+// (groups that do not divide 128 leave a few rows unused).  So a tile of keys
+// is loaded once for the group, short sequences fill the tensor core's rows
+// with heads, and causality wastes less than a tile of 128 tokens would.
+//
+//   S = Q K^T [128 rows x 128 keys]   P = 2^(S c - m)   O += P V
+//
+// One persistent CTA per SM works on two row tiles at a time, so that one
+// tile's softmax runs beside the other's products:
+//   warp 0      TMA producer: the two Q tiles, then K and V tiles into a ring
+//   warp 1      MMA issuer: S_s and O_s in TMEM, P_s over S_s's columns (bf16)
+//   warps 2, 3  zero the rows of the last V tile that no row of the item may
+//               see (0 times another sequence's NaN would be NaN)
+//   warps 4-11  softmax, one warpgroup per row tile, one row per thread: no
+//               exchange between threads; the reference m is raised only when
+//               a score exceeds it by more than 2^8, so the accumulator is
+//               rescaled once or twice per item rather than at every tile
+// Items (a pair of row tiles and a key-value head) are handed out from the
+// longest to the shortest, forwards and backwards over the CTAs in turn.
+#include <cfloat>
+
+#include <cuda.h>
+
 #include "kernels.h"
 #include "kv.cuh"
 #include "profile.h"
+#include "sm100.cuh"
 
 namespace dspark {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kRows = 128;              // rows of a row tile
+constexpr int kKeys = 128;              // keys of a key tile
+constexpr int kThreads = 384;
+constexpr int kPlanThreads = 1024;
+constexpr float kFloorRef = -1e30f;
+constexpr float kLazy = 8.f;
 
 template <int HD>
-__global__ void __launch_bounds__(kWarps * 32) attn_prompt_kernel(PromptArgs p) {
-    constexpr int N = HD / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (blockIdx.x == 0) check_requests(p.seq_off, nullptr, p.B, p.T, 0, p.ws);
-    const int t = (int)(w / p.n_heads), h = (int)(w % p.n_heads);
-    if (t >= p.T) return;
-    const int b = find_request(p.seq_off, p.B, t);
-    const RowRange rows = row_range(p.seq_off, b, p.T);
-    if (t < rows.a || t >= rows.b) return;
-    const int kvh = h / (p.n_heads / p.n_kv_heads);
-    const float scale2 = p.scale * kLog2e;
-    float q[N], o[N];
-    const uint16_t* src = static_cast<const uint16_t*>(p.q) + (size_t)t * p.q_stride + (size_t)h * HD + lane * N;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        q[i] = bf16_bits_to_float(src[i]) * scale2;
-        o[i] = 0.f;
-    }
-    float m = -INFINITY, l = 0.f;
-    const uint16_t* k = static_cast<const uint16_t*>(p.k) + (size_t)kvh * HD + lane * N;
-    const uint16_t* v = static_cast<const uint16_t*>(p.v) + (size_t)kvh * HD + lane * N;
-    for (int j = rows.a; j <= t; ++j) {
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) s = fmaf(q[i], bf16_bits_to_float(__ldg(k + (size_t)j * p.k_stride + i)), s);
-        s = warp_sum(s);
-        const float mn = fmaxf(m, s), f = ex2_approx(m - mn), e = ex2_approx(s - mn);
-        m = mn;
-        l = fmaf(l, f, e);
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            o[i] = fmaf(o[i], f, e * bf16_bits_to_float(__ldg(v + (size_t)j * p.v_stride + i)));
-    }
-    uint16_t* dst = static_cast<uint16_t*>(p.out) + ((size_t)t * p.n_heads + h) * HD + lane * N;
-#pragma unroll
-    for (int i = 0; i < N; ++i) dst[i] = __bfloat16_as_ushort(__float2bfloat16_rn(o[i] / l));
-    if (p.lse && lane == 0) p.lse[(size_t)t * p.n_heads + h] = (float)((double)m * 0.6931471805599453 + log((double)l));
+struct Cfg {
+    static constexpr int kHalves = HD / 64;
+    static constexpr int kHalfBytes = 128 * 128;             // 128 rows of one 128-byte swizzle atom
+    static constexpr int kTileBytes = kHalves * kHalfBytes;
+    static constexpr int kStages = HD == 128 ? 5 : 8;        // ring of K and V tiles
+    static constexpr int kOffQ = kStages * kTileBytes;
+    static constexpr int kOffMisc = kOffQ + 2 * kTileBytes;
+};
+
+struct Misc {
+    uint64_t full[8], empty[8];
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], o_free[2];
+    uint64_t fix, fixed, done;
+    WaitState wst;
+    uint32_t tmem;
+};
+
+template <int HD>
+constexpr size_t smem_bytes() {
+    return 1024 + Cfg<HD>::kOffMisc + sizeof(Misc);
 }
+
+struct Params {
+    const int32_t* seq_off;
+    const int2* list;                   // (sequence, pair of row tiles), longest first
+    const int* count;                   // entries of the list
+    int most;                           // entries that the workspace holds
+    uint16_t* out;
+    float* lse;
+    void* ws;
+    int B, T, heads, kv_heads, group, toks;   // toks: tokens of a row tile
+    float scale2;                       // scale log2(e)
+};
+
+// The list of (sequence, pair of row tiles) entries in descending order of
+// their length (the tile's place in its sequence), by a counting sort over
+// 1024 classes of places.  Entries of a class stand in any order: each item's
+// result depends on the item alone.
+__global__ void __launch_bounds__(kPlanThreads) attn_prompt_plan(Params p, int2* list, int* count) {
+    pdl_launch_dependents();
+    using u64 = unsigned long long;                          // overlapping sequences (bad offsets) can sum to anything
+    __shared__ u64 at[kPlanThreads];
+    __shared__ u64 warp_sum_sh[32];
+    __shared__ int most;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) most = 1;
+    at[tid] = 0;
+    __syncthreads();
+    check_requests(p.seq_off, nullptr, p.B, p.T, 0, p.ws);
+    const int pair = 2 * p.toks;
+    int mine = 1;
+    for (int b = tid; b < p.B; b += kPlanThreads) {
+        const RowRange r = row_range(p.seq_off, b, p.T);
+        mine = max(mine, (r.b - r.a + pair - 1) / pair);
+    }
+    if (mine > 1) atomicMax(&most, mine);
+    __syncthreads();
+    const int64_t n_class = most;
+    auto each = [&](auto f) {
+        for (int b = warp; b < p.B; b += kPlanThreads / 32) {
+            const RowRange r = row_range(p.seq_off, b, p.T);
+            const int n = (r.b - r.a + pair - 1) / pair;
+            for (int t = lane; t < n; t += 32) f(b, t, kPlanThreads - 1 - (int)((int64_t)t * kPlanThreads / n_class));
+        }
+    };
+    each([&](int, int, int c) { atomicAdd(&at[c], u64(1)); });
+    __syncthreads();
+    // exclusive sums over the classes
+    const u64 v = at[tid];
+    u64 upto = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+    }
+    if (lane == 31) warp_sum_sh[warp] = upto;
+    __syncthreads();
+    u64 base = 0;
+    for (int i = 0; i < warp; ++i) base += warp_sum_sh[i];
+    at[tid] = base + upto - v;
+    if (tid == kPlanThreads - 1) *count = (int)min(base + upto, (u64)p.most);
+    __syncthreads();
+    // only offsets that decrease can give more entries than the workspace has
+    // room for (sequences that overlap); what does not fit is left out
+    each([&](int b, int t, int c) {
+        const u64 k = atomicAdd(&at[c], u64(1));
+        if (k < (u64)p.most) list[k] = make_int2(b, t);
+    });
+}
+
+struct Item {
+    int a, len;                         // the sequence's first row and its tokens
+    int tok0;                           // first token of row tile 0
+    int h;                              // key-value head
+    int n[2];                           // key tiles of each row tile (0: no rows)
+    int keys;                           // keys that the item's last token sees
+};
+
+__device__ __forceinline__ bool get_item(const Params& p, int64_t total, int round, Item& it) {
+    const int64_t n = gridDim.x, c = blockIdx.x;
+    const int64_t k = (int64_t)round * n + ((round & 1) ? n - 1 - c : c);
+    if (k >= total) return false;
+    const int2 e = __ldcg(p.list + k / p.kv_heads);          // written by the kernel before this one
+    it.h = (int)(k % p.kv_heads);
+    const RowRange r = row_range(p.seq_off, e.x, p.T);
+    it.a = r.a;
+    it.len = r.b - r.a;
+    it.tok0 = e.y * 2 * p.toks;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const int first = it.tok0 + s * p.toks, last = min(it.len, first + p.toks);
+        it.n[s] = first < it.len ? (last + kKeys - 1) / kKeys : 0;
+    }
+    it.keys = min(it.len, it.tok0 + 2 * p.toks);
+    return true;
+}
+
+// Packed pairs of float32 (one instruction for two values).
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// 32 columns of this thread's lane, without waiting; tmem_ready() on the same
+// registers makes them usable.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+          "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+          "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr));
+}
+#define DSPARK_PIN32(v)                                                                                              \
+    "+f"((v)[0]), "+f"((v)[1]), "+f"((v)[2]), "+f"((v)[3]), "+f"((v)[4]), "+f"((v)[5]), "+f"((v)[6]), "+f"((v)[7]), \
+        "+f"((v)[8]), "+f"((v)[9]), "+f"((v)[10]), "+f"((v)[11]), "+f"((v)[12]), "+f"((v)[13]), "+f"((v)[14]),      \
+        "+f"((v)[15]), "+f"((v)[16]), "+f"((v)[17]), "+f"((v)[18]), "+f"((v)[19]), "+f"((v)[20]), "+f"((v)[21]),    \
+        "+f"((v)[22]), "+f"((v)[23]), "+f"((v)[24]), "+f"((v)[25]), "+f"((v)[26]), "+f"((v)[27]), "+f"((v)[28]),    \
+        "+f"((v)[29]), "+f"((v)[30]), "+f"((v)[31])
+// Waits for this thread's tensor-memory loads; v is usable afterwards (the
+// registers are operands, so no use of them can be scheduled before it).
+__device__ __forceinline__ void tmem_ready(float* v) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : DSPARK_PIN32(v)::"memory");
+}
+__device__ __forceinline__ void tmem_pin(float* v) { asm volatile("" : DSPARK_PIN32(v)); }
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+
+struct Maps {
+    CUtensorMap q, k, v;
+};
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_prompt_kernel(const __grid_constant__ Maps maps, const Params p) {
+    using C = Cfg<HD>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Misc* M = reinterpret_cast<Misc*>(smem + C::kOffMisc);
+    volatile WaitState* ab = &M->wst;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&M->full[i], 1);
+            mbar_init(&M->empty[i], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&M->q_full[s], 1);
+            mbar_init(&M->q_empty[s], 1);
+            mbar_init(&M->s_full[s], 1);
+            mbar_init(&M->p_full[s], 4);
+            mbar_init(&M->pv_done[s], 1);
+            mbar_init(&M->o_free[s], 4);
+        }
+        mbar_init(&M->fix, 1);
+        mbar_init(&M->fixed, 2);
+        mbar_init(&M->done, 1);
+        M->wst.abort = 0;
+        M->wst.limit = ws_wait_limit(p.ws);
+        fence_mbar_init();
+        prefetch_tmap(&maps.q);
+        prefetch_tmap(&maps.k);
+        prefetch_tmap(&maps.v);
+    }
+    if (warp == 1) tmem_alloc(&M->tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = M->tmem;
+    pdl_wait();                                               // the list
+    const int64_t total = (int64_t)__ldcg(p.count) * p.kv_heads;
+    Item it;
+
+    if (warp == 0) {
+        // ---------------- producer (one thread)
+        if (lane == 0) {
+            const uint64_t pol_q = policy_evict_first(), pol_kv = policy_evict_last();
+            uint32_t g = 0, nq[2] = {0, 0};
+            bool ok = true;
+            auto tile = [&](const CUtensorMap* m, int j) {
+                const int st = (int)(g % C::kStages);
+                ok = ok && mbar_wait(&M->empty[st], ((g / C::kStages) & 1u) ^ 1u, ab);
+                if (!ok) return;
+                mbar_expect_tx(&M->full[st], (uint32_t)C::kTileBytes);
+                for (int hf = 0; hf < C::kHalves; ++hf)
+                    tma_load_3d(smem + st * C::kTileBytes + hf * C::kHalfBytes, m, &M->full[st], hf * 64, it.h,
+                                it.a + j * kKeys, pol_kv);
+                ++g;
+            };
+            auto query = [&](int s) {
+                if (!it.n[s]) return;
+                ok = ok && mbar_wait(&M->q_empty[s], (nq[s] & 1u) ^ 1u, ab);
+                if (!ok) return;
+                ++nq[s];
+                mbar_expect_tx(&M->q_full[s], (uint32_t)(p.toks * p.group * HD * 2));
+                for (int hf = 0; hf < C::kHalves; ++hf)
+                    tma_load_3d(smem + C::kOffQ + s * C::kTileBytes + hf * C::kHalfBytes, &maps.q, &M->q_full[s], hf * 64,
+                                it.h * p.group, it.a + it.tok0 + s * p.toks, pol_q);
+            };
+            for (int round = 0; ok && get_item(p, total, round, it); ++round) {
+                const int n = max(it.n[0], it.n[1]);
+                query(0);
+                tile(&maps.k, 0);
+                query(1);
+                tile(&maps.v, 0);
+                for (int j = 1; ok && j < n; ++j) {
+                    tile(&maps.k, j);
+                    tile(&maps.v, j);
+                }
+            }
+            // copies in flight land before the CTA may leave
+            if (ab->abort) {
+                for (uint32_t k = g > C::kStages ? g - C::kStages : 0; k < g; ++k)
+                    mbar_wait_for(&M->full[k % C::kStages], (k / C::kStages) & 1u, ab->limit);
+                for (int s = 0; s < 2; ++s)
+                    if (nq[s]) mbar_wait_for(&M->q_full[s], (nq[s] - 1u) & 1u, ab->limit);
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer (one thread)
+        if (lane == 0) {
+            constexpr uint32_t id_qk = idesc_bf16_f32(128, 128, false, false);
+            constexpr uint32_t id_pv = idesc_bf16_f32(128, HD, false, true);
+            uint32_t g = 0, nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0}, nfix = 0;
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                ok = ok && mbar_wait(bar, parity, ab);
+                tc_fence_after();
+                return ok;
+            };
+            auto scores = [&](int s, uint32_t at) {
+                const uint8_t* qt = smem + C::kOffQ + s * C::kTileBytes;
+                const uint8_t* kt = smem + (at % C::kStages) * C::kTileBytes;
+#pragma unroll
+                for (int kk = 0; kk < HD / 16; ++kk) {
+                    const int off = (kk / 4) * C::kHalfBytes + (kk % 4) * 32;
+                    umma_bf16(tmem + (uint32_t)(s * 128), smem_desc_sw128(qt + off, 16, 1024),
+                              smem_desc_sw128(kt + off, 16, 1024), id_qk, kk ? 1u : 0u);
+                }
+                umma_commit(&M->s_full[s]);
+            };
+            auto product = [&](int s, uint32_t at, bool first) {
+                const uint8_t* vt = smem + (at % C::kStages) * C::kTileBytes;
+#pragma unroll
+                for (int kk = 0; kk < kKeys / 16; ++kk)
+                    umma_bf16_ts(tmem + (uint32_t)(256 + s * HD), tmem + (uint32_t)(s * 128 + kk * 8),
+                                 smem_desc_sw128(vt + kk * 2048, C::kHalfBytes, 1024), id_pv, (!first || kk) ? 1u : 0u);
+                umma_commit(&M->pv_done[s]);
+            };
+            for (int round = 0; ok && get_item(p, total, round, it); ++round) {
+                const int n = max(it.n[0], it.n[1]);
+                // ring entries of this item: K_j at g + 2 j, V_j at g + 2 j + 1
+                if (!wait(&M->full[g % C::kStages], (g / C::kStages) & 1u)) break;
+                for (int s = 0; s < 2; ++s) {
+                    if (!it.n[s]) continue;
+                    if (!wait(&M->q_full[s], nq[s]++ & 1u)) break;
+                    scores(s, g);
+                    if (it.n[s] == 1) umma_commit(&M->q_empty[s]);
+                }
+                if (!ok) break;
+                umma_commit(&M->empty[g % C::kStages]);
+                for (int j = 0; ok && j < n; ++j) {
+                    const uint32_t vi = g + 2 * j + 1, ki = vi + 1;
+                    if (!wait(&M->full[vi % C::kStages], (vi / C::kStages) & 1u)) break;
+                    bool fix = j == n - 1 && it.keys - j * kKeys < kKeys;
+                    if (fix) mbar_arrive(&M->fix);            // warps 2 and 3 start while P is still being made
+                    for (int s = 0; s < 2; ++s) {
+                        if (j >= it.n[s]) continue;
+                        if (j == 0 && no[s] > 0 && !wait(&M->o_free[s], (no[s] - 1u) & 1u)) break;
+                        if (!wait(&M->p_full[s], np[s]++ & 1u)) break;
+                        if (fix && !wait(&M->fixed, nfix++ & 1u)) break;
+                        fix = false;
+                        product(s, vi, j == 0);
+                        if (j + 1 < it.n[s]) {
+                            if (!wait(&M->full[ki % C::kStages], (ki / C::kStages) & 1u)) break;
+                            scores(s, ki);
+                            if (j + 2 == it.n[s]) umma_commit(&M->q_empty[s]);
+                        }
+                    }
+                    if (!ok) break;
+                    umma_commit(&M->empty[vi % C::kStages]);
+                    if (j + 1 < n) umma_commit(&M->empty[ki % C::kStages]);
+                }
+                for (int s = 0; s < 2; ++s) no[s] += it.n[s] ? 1u : 0u;
+                g += 2 * n;
+            }
+            // the tensor core is idle before its memory is given back
+            umma_commit(&M->done);
+            mbar_wait_for(&M->done, 0, ab->limit);
+        }
+    } else if (warp < 4) {
+        // ---------------- zero the last V tile's rows past the item's keys
+        uint32_t g = 0, nfix = 0;
+        for (int round = 0; get_item(p, total, round, it); ++round) {
+            const int n = max(it.n[0], it.n[1]);
+            const int valid = it.keys - (n - 1) * kKeys;
+            const uint32_t vi = g + 2 * n - 1;
+            g += 2 * n;
+            if (valid >= kKeys) continue;
+            // the MMA issuer saw the tile arrive and asks for the zeros
+            if (!__all_sync(0xffffffffu, mbar_wait(&M->fix, nfix++ & 1u, ab))) break;
+            uint8_t* vt = smem + (vi % C::kStages) * C::kTileBytes;
+            for (int x = valid * 8 + (warp - 2) * 32 + lane; x < kKeys * 8; x += 64)
+#pragma unroll
+                for (int hf = 0; hf < C::kHalves; ++hf)
+                    *reinterpret_cast<uint4*>(vt + hf * C::kHalfBytes + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&M->fixed);
+        }
+    } else {
+        // ---------------- softmax: thread = row
+        const int s = (warp - 4) >> 2, wq = warp & 3;
+        const int row = wq * 32 + lane;
+        const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+        const uint32_t tS = tmem + lanes + (uint32_t)(s * 128);
+        const uint32_t tO = tmem + lanes + (uint32_t)(256 + s * HD);
+        const int rt = row / p.group, rg = row - rt * p.group;   // token and head of the row inside its tile
+        const float c = p.scale2;
+        const uint64_t c2 = pack2(c, c);
+        uint32_t ns = 0, npv = 0;
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, ab));
+            tc_fence_after();
+            return ok;
+        };
+        for (int round = 0; ok && get_item(p, total, round, it); ++round) {
+            const int n = it.n[s];
+            if (!n) continue;
+            const int tok = it.tok0 + s * p.toks + rt;           // sees keys 0 .. tok
+            const int first = it.tok0 + s * p.toks;
+            float ref = kFloorRef;
+            uint64_t l2 = 0;                                     // two partial sums
+            for (int j = 0; ok && j < n; ++j) {
+                if (!wait(&M->s_full[s], ns++ & 1u)) break;
+                float x[128];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) tmem_ld32_async(tS + q * 32, x + q * 32);
+                tmem_ready(x);
+#pragma unroll
+                for (int q = 1; q < 4; ++q) tmem_pin(x + q * 32);
+                if ((j + 1) * kKeys - 1 > first) {               // a row of the tile does not see all keys
+                    const int lim = tok - j * kKeys;
+                    const float hidden = c < 0.f ? INFINITY : -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 128; ++i)
+                        if (i > lim) x[i] = hidden;
+                }
+                // the row's largest score (a negative scale makes it the smallest product)
+                float mx[4] = {x[0], x[1], x[2], x[3]};
+                if (c >= 0.f) {
+#pragma unroll
+                    for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
+                } else {
+#pragma unroll
+                    for (int i = 4; i < 128; ++i) mx[i & 3] = fminf(mx[i & 3], x[i]);
+                }
+                const float top = c >= 0.f ? fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c
+                                           : fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3])) * c;
+                if (__any_sync(0xffffffffu, top > ref + kLazy)) {
+                    const float m = fmaxf(ref, top), f = ex2_approx(ref - m);
+                    ref = m;
+                    float a, b;
+                    unpack2(l2, a, b);
+                    l2 = pack2(a * f, b * f);
+                    if (j > 0) {
+                        if (!wait(&M->pv_done[s], (npv - 1u) & 1u)) break;
+#pragma unroll
+                        for (int q = 0; q < HD / 16; ++q) {
+                            float o[16];
+                            tmem_ld16(tO + q * 16, o);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] *= f;
+                            tmem_st16(tO + q * 16, o);
+                        }
+                    }
+                }
+                const uint64_t r2 = pack2(-ref, -ref);
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        float a, b;
+                        unpack2(fma2(pack2(x[hf * 64 + 2 * i], x[hf * 64 + 2 * i + 1]), c2, r2), a, b);
+                        a = ex2_approx(a);
+                        b = ex2_approx(b);
+                        l2 = add2(l2, pack2(a, b));
+                        // bf16 for the product with V; the sum keeps float32
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+                        pk[i] = reinterpret_cast<const uint32_t&>(h);
+                    }
+                    tmem_st32(tS + hf * 32, pk);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&M->p_full[s]);
+                ++npv;
+            }
+            if (!ok || !wait(&M->pv_done[s], (npv - 1u) & 1u)) break;
+            float a, b;
+            unpack2(l2, a, b);
+            const float l = a + b, inv = 1.f / l;
+            const bool valid = row < p.toks * p.group && tok < it.len;
+            const size_t at = (size_t)(it.a + tok) * p.heads + (size_t)it.h * p.group + rg;
+#pragma unroll
+            for (int q = 0; q < HD / 16; ++q) {
+                float o[16];
+                tmem_ld16(tO + q * 16, o);
+                uint32_t pk[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * i] * inv, o[2 * i + 1] * inv);
+                    pk[i] = reinterpret_cast<const uint32_t&>(h);
+                }
+                if (valid) {
+                    uint4* dst = reinterpret_cast<uint4*>(p.out + at * HD + q * 16);
+                    dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&M->o_free[s]);
+            if (valid && p.lse) p.lse[at] = (ref + log2f(l)) * kLn2;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && M->wst.abort) raise_status(p.ws, kStatTimeout);
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int HD>
+cudaError_t launch(const Maps& maps, const Params& p, cudaStream_t s) {
+    const size_t smem = smem_bytes<HD>();
+    cudaError_t e = cudaFuncSetAttribute(attn_prompt_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    prof_begin(kPAttnPromptPlan, s);
+    e = launch_kernel(attn_prompt_plan, dim3(1), dim3(kPlanThreads), 0, s, false, p, const_cast<int2*>(p.list),
+                      const_cast<int*>(p.count));
+    prof_end(s);
+    if (e != cudaSuccess) return e;
+    prof_begin(kPAttnPrompt, s);
+    e = launch_kernel(attn_prompt_kernel<HD>, dim3(num_sms()), dim3(kThreads), smem, s, true, maps, p);
+    prof_end(s);
+    return e;
+}
+
+int tile_tokens(int group) { return kRows / group; }
 
 }  // namespace
 
-size_t attn_prompt_workspace_bytes(int, int, int, int, int) { return sizeof(WsHeader); }
+// sum over sequences of ceil(tokens / pair) is at most T / pair + B
+static size_t list_entries(int B, int T, int group) { return (size_t)T / (2 * tile_tokens(group)) + (size_t)B; }
+
+size_t attn_prompt_workspace_bytes(int B, int T, int n_heads, int n_kv_heads, int) {
+    return sizeof(WsHeader) + 256 + align_up(list_entries(B, T, n_heads / n_kv_heads) * sizeof(int2), 256);
+}
 
 cudaError_t launch_attn_prompt(const PromptArgs& a, cudaStream_t s) {
-    const dim3 grid((unsigned)(((int64_t)a.T * a.n_heads + kWarps - 1) / kWarps)), block(kWarps * 32);
-    auto kern = a.head_dim == 64 ? attn_prompt_kernel<64> : attn_prompt_kernel<128>;
-    prof_begin(kPAttnPrompt, s);
-    const cudaError_t e = launch_kernel(kern, grid, block, 0, s, false, a);
-    prof_end(s);
-    return e;
+    uint8_t* w = static_cast<uint8_t*>(a.ws) + sizeof(WsHeader);
+    Params p;
+    p.seq_off = a.seq_off;
+    p.count = reinterpret_cast<const int*>(w);
+    p.list = reinterpret_cast<const int2*>(w + 256);
+    p.out = static_cast<uint16_t*>(a.out);
+    p.lse = a.lse;
+    p.ws = a.ws;
+    p.B = a.B;
+    p.T = a.T;
+    p.heads = a.n_heads;
+    p.kv_heads = a.n_kv_heads;
+    p.group = a.n_heads / a.n_kv_heads;
+    p.toks = tile_tokens(p.group);
+    p.most = (int)list_entries(a.B, a.T, p.group);
+    // hidden keys are infinite before the scale: at scale 0 the smallest normal
+    // number keeps them so, and every finite score still counts as 0
+    p.scale2 = a.scale == 0.f ? FLT_MIN : a.scale * kLog2e;
+    Maps maps;
+    auto map = [&](CUtensorMap* m, const void* base, int heads, int64_t stride, cuuint32_t b1, cuuint32_t b2) {
+        const cuuint64_t dims[3] = {(cuuint64_t)a.head_dim, (cuuint64_t)heads, (cuuint64_t)a.T};
+        const cuuint64_t str[2] = {(cuuint64_t)a.head_dim * 2, (cuuint64_t)stride * 2};
+        const cuuint32_t box[3] = {64, b1, b2};
+        return make_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    if (!map(&maps.q, a.q, a.n_heads, a.q_stride, (cuuint32_t)p.group, (cuuint32_t)p.toks) ||
+        !map(&maps.k, a.k, a.n_kv_heads, a.k_stride, 1, kKeys) || !map(&maps.v, a.v, a.n_kv_heads, a.v_stride, 1, kKeys))
+        return cudaErrorInvalidValue;
+    return a.head_dim == 64 ? launch<64>(maps, p, s) : launch<128>(maps, p, s);
 }
 
 }  // namespace dspark

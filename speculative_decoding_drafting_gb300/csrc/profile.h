@@ -28,6 +28,7 @@ enum ProfName : int {
     kPAttnPaged = 20,
     kPAttnPagedJoin = 21,
     kPAttnPrompt = 22,
+    kPAttnPromptPlan = 23,
 };
 
 void prof_begin(int name, cudaStream_t s);
