@@ -159,26 +159,6 @@ __device__ __forceinline__ bool get_item(const Params& p, int64_t total, int rou
     return true;
 }
 
-// Packed pairs of float32 (one instruction for two values).
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 // 32 columns of this thread's lane, without waiting; tmem_ready() on the same
 // registers makes them usable.
 __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float* v) {
@@ -461,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int q = 0; q < HD / 16; ++q) {
                             float o[16];
-                            tmem_ld16(tO + q * 16, o);
+                            tmem_ldn<16>(tO + q * 16, o);
 #pragma unroll
                             for (int i = 0; i < 16; ++i) o[i] *= f;
                             tmem_st16(tO + q * 16, o);
@@ -500,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int q = 0; q < HD / 16; ++q) {
                 float o[16];
-                tmem_ld16(tO + q * 16, o);
+                tmem_ldn<16>(tO + q * 16, o);
                 uint32_t pk[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {

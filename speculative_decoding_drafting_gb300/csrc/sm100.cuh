@@ -29,6 +29,31 @@ __device__ __forceinline__ uint32_t ld_relaxed_gpu(const uint32_t* p) {
     return v;
 }
 
+// Packed pairs of float32 (one instruction for two values).
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2x(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // ---------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
@@ -233,6 +258,11 @@ __device__ __forceinline__ uint64_t smem_desc_plain(const void* p, uint32_t lbo,
            (((uint64_t)(sbo >> 4) & 0x3FFFull) << 32) | (1ull << 46);
 }
 
+// The same for rows of 64 bytes (64-byte swizzle, layout value 4).
+__device__ __forceinline__ uint64_t smem_desc_sw64(const void* p, uint32_t lbo, uint32_t sbo) {
+    return smem_desc_plain(p, lbo, sbo) | (4ull << 61);
+}
+
 // Instruction descriptor of kind::f16: f32 accumulate, bf16 A and B,
 // A K-major, B given by b_mn_major, N >> 3 in bits 17-22, M >> 4 in bits 24-28.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool b_mn_major) {
@@ -251,6 +281,20 @@ __device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t adesc, uint6
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// kind::f8f6f4: e4m3 A and B (format value 0), both K-major, f32 accumulate;
+// one MMA takes K = 32.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
@@ -347,6 +391,74 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// N = 4, 8, 16 or 32 consecutive 32-bit columns of this thread's lane, usable on
+// return: the registers are operands of the wait, so that no use of them can
+// be scheduled before it.
+template <int N>
+__device__ __forceinline__ void tmem_ldn(uint32_t taddr, float (&v)[N]) {
+    static_assert(N == 4 || N == 8 || N == 16 || N == 32, "column counts in use");
+    if constexpr (N == 4) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                     : "r"(taddr));
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]) ::"memory");
+    }
+    if constexpr (N == 8) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=f"(v[0 % N]), "=f"(v[1 % N]), "=f"(v[2 % N]), "=f"(v[3 % N]), "=f"(v[4 %
+                       N]), "=f"(v[5 % N]), "=f"(v[6 % N]), "=f"(v[7 % N])
+                     : "r"(taddr));
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : "+f"(v[0 % N]), "+f"(v[1 % N]), "+f"(v[2 % N]), "+f"(v[3 % N]), "+f"(v[4 %
+                       N]), "+f"(v[5 % N]), "+f"(v[6 % N]), "+f"(v[7 % N]) ::"memory");
+    }
+    if constexpr (N == 16) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                     : "=f"(v[0 % N]), "=f"(v[1 % N]), "=f"(v[2 % N]), "=f"(v[3 % N]), "=f"(v[4 %
+                       N]), "=f"(v[5 % N]), "=f"(v[6 % N]), "=f"(v[7 % N]), "=f"(v[8 % N]), "=f"(v[9
+                       % N]), "=f"(v[10 % N]), "=f"(v[11 % N]), "=f"(v[12 % N]), "=f"(v[13 % N]),
+                       "=f"(v[14 % N]), "=f"(v[15 % N])
+                     : "r"(taddr));
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : "+f"(v[0 % N]), "+f"(v[1 % N]), "+f"(v[2 % N]), "+f"(v[3 % N]), "+f"(v[4 %
+                       N]), "+f"(v[5 % N]), "+f"(v[6 % N]), "+f"(v[7 % N]), "+f"(v[8 % N]), "+f"(v[9
+                       % N]), "+f"(v[10 % N]), "+f"(v[11 % N]), "+f"(v[12 % N]), "+f"(v[13 % N]),
+                       "+f"(v[14 % N]), "+f"(v[15 % N]) ::"memory");
+    }
+    if constexpr (N == 32) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                     : "=f"(v[0 % N]), "=f"(v[1 % N]), "=f"(v[2 % N]), "=f"(v[3 % N]), "=f"(v[4 %
+                       N]), "=f"(v[5 % N]), "=f"(v[6 % N]), "=f"(v[7 % N]), "=f"(v[8 % N]), "=f"(v[9
+                       % N]), "=f"(v[10 % N]), "=f"(v[11 % N]), "=f"(v[12 % N]), "=f"(v[13 % N]),
+                       "=f"(v[14 % N]), "=f"(v[15 % N]), "=f"(v[16 % N]), "=f"(v[17 % N]), "=f"(v[18
+                       % N]), "=f"(v[19 % N]), "=f"(v[20 % N]), "=f"(v[21 % N]), "=f"(v[22 % N]),
+                       "=f"(v[23 % N]), "=f"(v[24 % N]), "=f"(v[25 % N]), "=f"(v[26 % N]), "=f"(v[27
+                       % N]), "=f"(v[28 % N]), "=f"(v[29 % N]), "=f"(v[30 % N]), "=f"(v[31 % N])
+                     : "r"(taddr));
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : "+f"(v[0 % N]), "+f"(v[1 % N]), "+f"(v[2 % N]), "+f"(v[3 % N]), "+f"(v[4 %
+                       N]), "+f"(v[5 % N]), "+f"(v[6 % N]), "+f"(v[7 % N]), "+f"(v[8 % N]), "+f"(v[9
+                       % N]), "+f"(v[10 % N]), "+f"(v[11 % N]), "+f"(v[12 % N]), "+f"(v[13 % N]),
+                       "+f"(v[14 % N]), "+f"(v[15 % N]), "+f"(v[16 % N]), "+f"(v[17 % N]), "+f"(v[18
+                       % N]), "+f"(v[19 % N]), "+f"(v[20 % N]), "+f"(v[21 % N]), "+f"(v[22 % N]),
+                       "+f"(v[23 % N]), "+f"(v[24 % N]), "+f"(v[25 % N]), "+f"(v[26 % N]), "+f"(v[27
+                       % N]), "+f"(v[28 % N]), "+f"(v[29 % N]), "+f"(v[30 % N]), "+f"(v[31 % N]) ::"memory");
+    }
+}
+
+// Registers per thread of the calling warpgroup (all its warps make the call).
+// A launch has its threads times its registers in all; shares that add up to
+// no more than that never wait.
+template <int N>
+__device__ __forceinline__ void regs_raise() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_lower() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 }  // namespace dspark
