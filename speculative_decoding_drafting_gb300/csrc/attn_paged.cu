@@ -16,11 +16,12 @@
 // tiles (attn_plan.h); pieces of split items go to the workspace and a second
 // launch joins them in a fixed order.
 //
-//   warp 0      TMA producer: K and V tiles page by page (a page id out of
-//               range lies past the tensor's end, so it reads as zeros)
-//   warp 1      MMA issuer
-//   warp 2      Q rows of the next item (e4m3 caches: split, see below)
-//   warp 3      the list of this CTA's segments, a few ahead of the others
+//   warp 0      K tiles by TMA, page by page (a page id out of range lies past
+//               the tensor's end, so it reads as zeros), and e4m3 scales
+//   warp 1      the scores' MMAs
+//   warp 2      the list of this CTA's segments, a few ahead of the others, and
+//               V tiles by TMA
+//   warp 3      the products' MMAs
 //   warps 4-19  four softmax units of four warps, 32 rows of Q each.  Items of
 //               up to 32 rows go through four streams of key tiles (unit u
 //               takes every fourth), wider ones through two streams of two
@@ -30,19 +31,27 @@
 //               a row is raised only when a score exceeds it by more than 2^8
 //               (a vote per tile; p <= 2^8 is far inside bf16 and float32), so
 //               a tile costs no maximum over its keys.
+//   warps 20-23 bring the next segment's Q rows, then join the streams of the
+//               finished one and store it, while the units are at the next
+//               (accumulators alternate)
+// A role's instruction takes the SM about ten cycles (24 warps of different
+// code), so the loops below are kept short.
 //
 // e4m3 caches: K tiles go to the tensor core as they are.  Each row of Q is
-// split into 2^e (hi + lo / 16) with hi, lo in e4m3, 2^e such that the row's
-// largest value is in [128, 256): bf16's 8 significant bits are two times
-// e4m3's 4, so the split is exact down to 2^-22 of the row's largest value.
-// hi and lo are 2 x N columns of one product of twice bf16's rate.  V is
-// widened to bf16 instead, since weights want more than a few terms of 4 bits;
-// the units that made a tile's weights do it, the one shared-memory pass that
-// e4m3 costs.
+// split into 2^e (hi + lo), both e4m3, 2^e such that the row's largest value is
+// in [128, 256): bf16's 8 significant bits are two times e4m3's 4, and e4m3
+// holds a value of 128's rounding error (1 .. 8) down to 2^-9, so the split is
+// exact except for values below 2^-10 of the row's largest, which are off by
+// 2^-18 of it at most.  hi and lo follow one another along K.
+// V tiles are widened to fp16 (one instruction for two values) by the units
+// that made the tile's weights, the one shared-memory pass that e4m3 costs.
+// V's scale joins the exponent, w = 2^(score + log2 scale - m + 10), so that
+// the weights, whatever the scales, lie below 2^14 with fp16's 11 bits down to
+// 2^-24 of the row's largest; the sum takes w / scale.
 //
 // Keys a row must not see get weight 0 by selection, not by multiplication;
 // V rows past the item's last key are zeroed in shared memory, since 0 times
-// a stale NaN would be NaN (widened e4m3 codes are always finite).
+// a stale NaN would be NaN.
 #include <type_traits>
 
 #include <cuda.h>
@@ -58,8 +67,6 @@ namespace dspark {
 namespace {
 
 constexpr float kFloorRef = -1e30f;     // reference before any score: finite, below every score
-constexpr float kLazy = 8.f;            // bits a score may exceed its reference by
-
 constexpr int kUnits = 4;               // softmax units of 128 threads
 constexpr int kUnitRows = 32;           // columns of S^T a unit handles
 
@@ -69,62 +76,79 @@ struct Cfg {
     static constexpr int kHalves = HD / 64;                                // 128-byte swizzle atoms of a row
     static constexpr int kHalfBytes = kKeyTile * 128;
     static constexpr int kLoadBytes = F8 ? kKeyTile * HD : kTileBytes;     // a tile as it lies in the cache
-    static constexpr int kK = F8 ? (HD == 128 ? 3 : 6) : (HD == 128 ? 2 : 5);       // K tiles on the way
-    static constexpr int kV = F8 ? (HD == 128 ? 2 : 4) : (HD == 128 ? 3 : 5);       // V tiles
-    static constexpr int kW = F8 ? 2 : 0;                                  // widened V tiles
+    static constexpr int kK = F8 ? (HD == 128 ? 2 : 4) : (HD == 128 ? 2 : 5);       // K tiles on the way
+    static constexpr int kV = F8 ? (HD == 128 ? 4 : 6) : (HD == 128 ? 3 : 5);       // V tiles
+    static constexpr int kW = F8 ? (HD == 128 ? 2 : 3) : 0;                // widened V tiles
     static constexpr int kSc = F8 ? 4 : 0;                                 // scales of a tile (K, V)
     static constexpr int kScBytes = 2048;                                  // 2 x 128 scales, 16-token pages at 128-byte pitch
     static constexpr int kPBytes = kKeyTile * kUnitRows * 2;               // a unit's P^T
-    static constexpr int kQBytes = kRowTile * HD * 2;                      // bf16 rows, or hi and lo
-    static constexpr int kQ = F8 ? 2 : 1;
-    static constexpr int kWMod = kW ? kW : 1, kScMod = kSc ? kSc : 1;      // divisors (unused without e4m3)
-    static constexpr uint32_t kColO = F8 ? 256 : 128;                      // TMEM column of the accumulators
-    static constexpr uint32_t kTmem = F8 ? 512 : 256;
+    // two Q places; at head_dim 128 an item of more than 32 rows takes both
+    static constexpr int kQRows = HD == 128 ? 32 : 64;
+    static constexpr int kQBytes = kQRows * HD * 2;                        // bf16 rows, or hi and lo
+    static constexpr int kScMod = kSc ? kSc : 1;                           // divisor (unused without e4m3)
+    // bits by which a weight's exponent is lifted, and may exceed that
+    static constexpr float kLift = F8 ? 10.f : 0.f, kLazy = F8 ? 4.f : 8.f;
     static constexpr int kOffV = kK * kLoadBytes;
     static constexpr int kOffW = kOffV + kV * kLoadBytes;
     static constexpr int kOffP = kOffW + kW * kTileBytes;
     static constexpr int kOffQ = kOffP + kUnits * kPBytes;
-    static constexpr int kOffSc = kOffQ + kQ * kQBytes;
+    static constexpr int kOffSc = kOffQ + 2 * kQBytes;
     static constexpr int kOffMisc = kOffSc + kSc * kScBytes;
 };
-constexpr int kThreads = 32 * (4 + 4 * kUnits);
-constexpr uint32_t kReaders = 3 + 4 * kUnits;                              // warps that read a segment
-constexpr int kSegs = 4;                // segments in flight between the roles
+constexpr uint32_t kColO = kUnits * kUnitRows;                             // TMEM: scores, then two sets of accumulators
+constexpr uint32_t kTmem = 512;
+constexpr int kThreads = 32 * (8 + 4 * kUnits);
+constexpr uint32_t kReaders = 8 + 4 * kUnits;                              // arrivals that free a segment's place
+constexpr int kSegs = 8;                // segments in flight between the roles
 
 // A segment as the roles read it from shared memory (rows = 0: the end).
 struct SegInfo {
     int r, j, h;
     int t0, n, tiles;                  // key tiles [t0, t0 + n) of tiles
     int keys, rows;
+    int tok, head;                     // the first row's new token and its place in the group
+    uint32_t line;                     // key tiles of the segments before it
+    uint32_t run;                      // the same for the first of the segments of equal shape that it belongs to
+    int qp;                            // its Q place: 0, 1, or 2 for both
+    uint32_t q_use;                    // how often place 0 (low half) and 1 have been used before
     Request q;
 };
 
 struct alignas(16) Misc {
     SegInfo seg[kSegs];
     uint64_t seg_full[kSegs], seg_empty[kSegs];
-    float nref[kUnits][kUnitRows];     // minus the reference of a row
+    float zero[kUnitRows];
+    float ref[kUnits][kUnitRows];      // reference of a row
+    float nref[kUnits][kUnitRows];     // kLift minus it
     float qm[kUnits][kUnitRows];       // 2^e of a row's split
-    float fac[kUnits][kUnitRows];      // factor of a raised reference, then of the join
-    float red[kUnits][4][kUnitRows];   // per-warp maxima, then sums
+    float fac[kUnits][kUnitRows];      // factor of a raised reference
+    float red[kUnits][4][kUnitRows];   // per-warp maxima, and sums
     int lim[kUnits][kUnitRows];        // keys a row sees
-    float q_scale[2][kRowTile];        // 2^e of the Q buffers' rows
-    int64_t row_at[2][kRowTile];       // a row's place in out's rows (-1: no row), by parity of the segment
+    float q_scale[2 * kRowTile];       // 2^e of the Q places' rows
+    // what a finished segment hands on, by its parity
+    float fin_m[2][kUnits][kUnitRows];
+    float fin_l[2][kUnits][kUnitRows];
+    float join[kUnits][kUnitRows];     // factor of a stream's row
+    uint8_t* row_at[kRowTile];         // a row's place in out or in the piece (null: no row)
     int64_t scan[32];
     int64_t total, start_skip;
     int start_r;
     uint32_t tmem;
     WaitState wst;
-    uint64_t k_full[6], k_empty[6], v_full[5], v_empty[5];
-    uint64_t w_empty[2];               // widened V tiles (p_full says that one is made)
+    uint64_t k_full[5], k_empty[5], v_full[6], v_empty[6];
+    uint64_t w_empty[3];               // widened V tiles (p_full says that one is made)
     uint64_t c_full[4], c_empty[4];    // scales
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[kUnits], p_full[kUnits], pv_done[kUnits];
-    uint64_t o_free, done;
+    uint64_t o_done[2], l_done[2], e_free[2];   // a segment's accumulators, its sums; both read
+    uint64_t done;
 };
 
 template <int HD, bool F8>
 constexpr size_t smem_bytes() {
-    return 1024 + Cfg<HD, F8>::kOffMisc + sizeof(Misc);
+    constexpr size_t bytes = 1024 + Cfg<HD, F8>::kOffMisc + sizeof(Misc);
+    static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
+    return bytes;
 }
 
 // What a CTA tells the join about the item that its span ends inside of.
@@ -152,17 +176,33 @@ struct Maps {
     CUtensorMap k, v, ks, vs;
 };
 
-// Sums over the 32 lanes of N = 16 or 32 values per lane; lane i gets the sum
-// of value i % N.
-template <int N>
-__device__ __forceinline__ float lane_sums(float (&x)[N]) {
+// mbar_wait in few instructions, of which there are many: the first try in
+// place, the rest in one function.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile WaitState* w) {
+    const uint64_t t0 = sm_cycles();
+    do {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok) return true;
+    } while (!w->abort && sm_cycles() - t0 <= w->limit);
+    w->abort = 1;
+    return false;
+}
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile WaitState* w) {
+    return mbar_test(bar, parity) || wait_on(smem_u32(bar), parity, w);
+}
+
+// Sums over the 32 lanes of 32 values per lane; lane i gets the sum of value i.
+__device__ __forceinline__ float lane_sums(float (&x)[32]) {
     const int lane = threadIdx.x & 31;
-    if constexpr (N == 16) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], 16);
-    }
-#pragma unroll
-    for (int o = N / 2; o > 0; o >>= 1) {
+    for (int o = 16; o > 0; o >>= 1) {
         const bool up = lane & o;
 #pragma unroll
         for (int i = 0; i < o; ++i) {
@@ -186,7 +226,7 @@ __device__ __forceinline__ int swz_f8(int r, int c) {
 }
 
 // One lane's 8 values of a Q row that `LANES` lanes share: e4m3 codes of hi
-// and lo with q = 2^e (hi + lo / 16), and 2^e (NaN for a row that is not
+// and lo with q = 2^e (hi + lo), and 2^e (NaN for a row that is not
 // finite, which makes its scores NaN).
 template <int LANES>
 __device__ __forceinline__ float split_e4m3(uint4 v, uint2& hi, uint2& lo) {
@@ -208,11 +248,18 @@ __device__ __forceinline__ float split_e4m3(uint4 v, uint2& hi, uint2& lo) {
         const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3);
         const float2 f = __half22float2(reinterpret_cast<const __half2&>(back));
         h[i] = c;
-        l[i] = __nv_cvt_float2_to_fp8x2(make_float2((a - f.x) * 16.f, (b - f.y) * 16.f), __NV_SATFINITE, __NV_E4M3);
+        l[i] = __nv_cvt_float2_to_fp8x2(make_float2(a - f.x, b - f.y), __NV_SATFINITE, __NV_E4M3);
     }
     hi = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
     lo = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
     return big >= 0x7F80u ? NAN : scale;
+}
+
+// The Q places of a segment: f(place, earlier uses of it) for each.
+template <typename F>
+__device__ __forceinline__ void q_places(const SegInfo& s, F f) {
+    if (s.qp != 1) f(0, s.q_use & 0xFFFFu);
+    if (s.qp != 0) f(1, s.q_use >> 16);
 }
 
 // A row tile's layout over units: width (columns of Q in use), streams.
@@ -221,55 +268,25 @@ struct Shape {
     bool wide;
     __device__ __forceinline__ explicit Shape(int rows)
         : cols(rows <= 16 ? 16 : (rows <= 32 ? 32 : 64)), streams(rows > 32 ? 2 : 4), wide(rows > 32) {}
-    __device__ __forceinline__ int stream_of(int unit) const { return wide ? unit >> 1 : unit; }
-    // TMEM columns of a stream's scores (e4m3: lo follows hi after cols columns)
-    template <bool F8>
-    __device__ __forceinline__ uint32_t scores(int stream) const {
-        return (uint32_t)stream * (F8 ? (wide ? 128u : 64u) : (wide ? 64u : 32u));
+    // stream of key tile i of a segment
+    __device__ __forceinline__ int stream_at(const SegInfo& s, int i) const {
+        return (int)((s.line - s.run + (uint32_t)i) & (uint32_t)(streams - 1));
     }
-    __device__ __forceinline__ uint32_t accum(int stream) const { return (uint32_t)stream * (wide ? 64u : 32u); }
+    __device__ __forceinline__ int stream_of(int unit) const { return wide ? unit >> 1 : unit; }
+    // first TMEM column of a stream's scores, and of its accumulator in a set
+    __device__ __forceinline__ uint32_t column(int stream) const { return (uint32_t)stream * (wide ? 64u : 32u); }
 };
 
 // ------------------------------------------------------------------ softmax
 struct SoftState {
     uint32_t tiles;                    // key tiles this unit has taken
-    uint32_t line;                     // key tiles of all streams so far
     uint32_t seg;                      // segments so far
 };
 
-// Output columns [c0, c0 + K) of the item: the streams' accumulators times
-// their factors.
-template <int HD, int K>
-__device__ __forceinline__ void store_columns(const PagedParams& p, const Misc* M, const Shape& sh,
-                                              uint32_t tO, int c0, int used, int parity, bool whole, float* part,
-                                              int d, bool store) {
-    float o[K];
-#pragma unroll
-    for (int c = 0; c < K; ++c) o[c] = 0.f;
-    for (int st = 0; st < used; ++st) {
-        float x[K];
-        const int unit = sh.wide ? 2 * st + (c0 >> 5) : st;
-        tmem_ldn<K>(tO + sh.accum(st) + (uint32_t)c0, x);
-#pragma unroll
-        for (int c = 0; c < K; ++c) o[c] = fmaf(x[c], M->fac[unit][(c0 + c) & 31], o[c]);
-    }
-    if (!store) return;
-#pragma unroll
-    for (int c = 0; c < K; ++c) {
-        const int64_t at = M->row_at[parity][c0 + c];
-        if (at < 0) continue;
-        if (whole)
-            p.out[(size_t)at * HD + d] = __bfloat16_as_ushort(__float2bfloat16_rn(o[c]));
-        else
-            part[2 * kRowTile + (c0 + c) * HD + d] = o[c];
-    }
-}
-
-// One segment's key tiles of unit u, COLS of its rows; then the streams'
-// results are joined and written.  Every thread of all units walks the same
-// barriers even after a wait ran out (the results are then not stored), so
-// that no named barrier is left waiting.
-template <int HD, bool F8, int COLS>
+// One segment's key tiles of unit u.  The unit's threads all
+// walk the same barriers even after a wait ran out (the results are then not
+// stored), so that no named barrier is left waiting.
+template <int HD, bool F8>
 __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo& sg, Misc* M, uint8_t* smem,
                                              uint32_t tmem, int u, SoftState& st) {
     using C = Cfg<HD, F8>;
@@ -277,251 +294,316 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
     const Shape sh(sg.rows);
     const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
     const int tr = wq * 32 + lane;                            // key of the tile; head_dim index of O^T
+    const int cols = min(sh.cols, kUnitRows);                 // 16 or 32 rows of this unit
     const int bar = 1 + u, parity = st.seg & 1;
     const int stream = sh.stream_of(u), coff = sh.wide ? (u & 1) * kUnitRows : 0;
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
-    const uint32_t tS = tmem + lanes + sh.scores<F8>(stream) + (uint32_t)coff;
-    const uint32_t tO = tmem + lanes + C::kColO;
+    const uint32_t tS = tmem + lanes + (uint32_t)(u * kUnitRows);
+    const uint32_t tO = tmem + lanes + kColO * (1 + parity) + (uint32_t)(u * kUnitRows);
     uint8_t* P = smem + C::kOffP + u * C::kPBytes;
-    const PlanInput& pl = p.plan;
 
-    // this unit's rows
-    const int qb = st.seg % C::kQ;
-    if (F8) mbar_wait(&M->q_full[qb], (st.seg / C::kQ) & 1u, ab);
-    if (tr < COLS) {
-        const int64_t rho = (int64_t)sg.j * kRowTile + coff + tr;
-        M->lim[u][tr] = coff + tr < sg.rows ? plan_seen(pl, sg.q, rho) : 0;
+    // this unit's rows (what the segment before left is no longer read)
+    if (F8) q_places(sg, [&](int k, uint32_t use) { wait_bar(&M->q_full[k], use & 1u, ab); });
+    if (tr < cols) {
+        int i, g;
+        plan_row(p.plan.group, sg.tok, sg.head, coff + tr, i, g);
+        M->lim[u][tr] = coff + tr < sg.rows ? plan_token_keys(sg.q, i) : 0;
+        M->ref[u][tr] = kFloorRef;
         M->nref[u][tr] = -kFloorRef;
-        if (F8) M->qm[u][tr] = M->q_scale[qb][coff + tr];
-    }
-    if (u == 0 && tr < kRowTile) {
-        const int64_t rho = (int64_t)sg.j * kRowTile + tr;
-        const int i = (int)(rho / pl.group), g = (int)(rho - (int64_t)i * pl.group);
-        M->row_at[parity][tr] = tr < sg.rows ? (int64_t)(sg.q.a + i) * p.heads + (int64_t)sg.h * pl.group + g : -1;
+        if (F8) M->qm[u][tr] = M->q_scale[(sg.qp == 1 ? C::kQRows : 0) + coff + tr];
     }
     named_sync(bar, 128);
-    if (F8 && lane == 0) mbar_arrive(&M->q_empty[qb]);        // the row scales are copied
+    if (F8 && lane == 0) q_places(sg, [&](int k, uint32_t) { mbar_arrive(&M->q_empty[k]); });   // the row scales are copied
 
-    uint64_t l2[COLS / 2];
+    uint64_t l2[kUnitRows / 2];
 #pragma unroll
-    for (int c = 0; c < COLS / 2; ++c) l2[c] = 0;
-    const int lim0 = plan_seen(pl, sg.q, (int64_t)sg.j * kRowTile);   // the first row sees the fewest keys
+    for (int c = 0; c < kUnitRows / 2; ++c) l2[c] = 0;
+    const int lim0 = plan_token_keys(sg.q, sg.tok);           // the first row sees the fewest keys
     const int n = sg.n, t0 = sg.t0;
+    const uint32_t line = sg.line;
+    const float scale2 = p.scale2;
 
-    for (int i = stream; i < n; i += sh.streams) {
+#pragma unroll 1
+    for (int i = (stream - sh.stream_at(sg, 0)) & (sh.streams - 1); i < n; i += sh.streams) {
         const int key = (t0 + i) * kKeyTile + tr;
-        const bool edge = (t0 + i + 1) * kKeyTile > lim0;  // some row does not see the whole tile
-        float mul = p.scale2, vs = 1.f;
+        const bool edge = (t0 + i + 1) * kKeyTile > lim0;     // some row does not see the whole tile
+        wait_bar(&M->s_full[u], st.tiles & 1u, ab);
+        tc_fence_after();
+        float mul = scale2, lvs = 0.f, ivs = 1.f;
         if (F8) {
-            const uint32_t at = st.line + (uint32_t)i;
+            // (the scores waited for the copy of these scales to be asked for)
+            const uint32_t at = line + (uint32_t)i;
             const int s = (int)(at % C::kScMod);
-            mbar_wait(&M->c_full[s], (at / C::kScMod) & 1u, ab);
-            const int bp = min(1 << p.page_log2, kKeyTile), pitch = max(bp * 4, 128);
-            const uint8_t* sc = smem + C::kOffSc + s * C::kScBytes + (tr / bp) * pitch + (tr % bp) * 4;
+            wait_bar(&M->c_full[s], (at / C::kScMod) & 1u, ab);
+            // (pages of 16 tokens lie 128 bytes apart, longer ones side by side)
+            const uint8_t* sc = smem + C::kOffSc + s * C::kScBytes +
+                                (p.page_log2 == 4 ? (tr >> 4) * 128 + (tr & 15) * 4 : tr * 4);
             mul *= *reinterpret_cast<const float*>(sc);
-            vs = *reinterpret_cast<const float*>(sc + C::kScBytes / 2);
+            float vs = *reinterpret_cast<const float*>(sc + C::kScBytes / 2);
             __syncwarp();
             // a wide tile's scales are read by two units
             if (lane == 0) mbar_arrive(&M->c_empty[s]);
             if (!sh.wide && lane == 0) mbar_arrive(&M->c_empty[s]);
+            if (edge && key >= sg.keys) vs = 1.f;             // no key here: any scale
+            if (vs < 7.888609e-31f) vs = 7.888609e-31f;       // 2^-100; a row of zeros has scale 0
+            lvs = lg2_approx(vs);
+            ivs = ex2_approx(-lvs);
         }
-        mbar_wait(&M->s_full[u], st.tiles & 1u, ab);
-        tc_fence_after();
 
-        // base-2 scores, minus the rows' references if `rel`
-        float t[COLS];
-        const uint64_t mul2 = pack2(mul, mul);
-        auto load_scores = [&](auto rel) {
-            tmem_ldn<COLS>(tS, t);
-            auto minus_ref = [&](int c) {
-                if constexpr (!decltype(rel)::value) return uint64_t(0);
-                const float2 r = *reinterpret_cast<const float2*>(&M->nref[u][c]);
-                return pack2(r.x, r.y);
-            };
-            if constexpr (F8) {
-                const uint64_t k16 = pack2(0.0625f, 0.0625f);
+        // base-2 exponents of the weights of 16 rows, relative to the references
+        // (or to 0); the scores stay in tensor memory and are formed again where
+        // they are needed again, which takes fewer registers than keeping them
+        const uint64_t mul2 = pack2(mul, mul), lvs2 = pack2(lvs, lvs);
+        auto exponents = [&](int c0, const float* nref, float (&t)[16]) {
+            tmem_ldn<16>(tS + (uint32_t)c0, t);
 #pragma unroll
-                for (int h = 0; h < COLS; h += 16) {
-                    float lo[16];
-                    tmem_ldn<16>(tS + (uint32_t)(sh.cols + h), lo);
-#pragma unroll
-                    for (int c = 0; c < 16; c += 2) {
-                        const uint64_t s = mul2x(fma2(pack2(lo[c], lo[c + 1]), k16, pack2(t[h + c], t[h + c + 1])), mul2);
-                        const float2 qm = *reinterpret_cast<const float2*>(&M->qm[u][h + c]);
-                        unpack2(fma2(s, pack2(qm.x, qm.y), minus_ref(h + c)), t[h + c], t[h + c + 1]);
-                    }
+            for (int c = 0; c < 16; c += 2) {
+                uint64_t x = pack2(t[c], t[c + 1]);
+                const float2 r = *reinterpret_cast<const float2*>(nref + c0 + c);
+                const uint64_t y = F8 ? add2(pack2(r.x, r.y), lvs2) : pack2(r.x, r.y);
+                if (F8) {
+                    const float2 qm = *reinterpret_cast<const float2*>(&M->qm[u][c0 + c]);
+                    x = mul2x(x, pack2(qm.x, qm.y));
                 }
-            } else {
-#pragma unroll
-                for (int c = 0; c < COLS; c += 2)
-                    unpack2(fma2(pack2(t[c], t[c + 1]), mul2, minus_ref(c)), t[c], t[c + 1]);
+                unpack2(fma2(x, mul2, y), t[c], t[c + 1]);
             }
             if (edge) {
 #pragma unroll
-                for (int c = 0; c < COLS; ++c)
-                    if (key >= M->lim[u][c]) t[c] = -INFINITY;
+                for (int c = 0; c < 16; ++c)
+                    if (key >= M->lim[u][c0 + c]) t[c] = -INFINITY;
             }
         };
-        for (bool raised = false;; raised = true) {
-            load_scores(std::true_type{});
-            if (raised) break;
+        bool over = false;
+#pragma unroll 1
+        for (int c0 = 0; c0 < cols; c0 += 16) {
+            float t[16];
+            exponents(c0, M->nref[u], t);
             float top = t[0];
 #pragma unroll
-            for (int c = 1; c < COLS; ++c) top = fmaxf(top, t[c]);
-            if (!named_any(bar, 128, top > kLazy)) break;
-            // raise the references to the largest scores so far, which happens
-            // once (scores of 2^28 and more round by more than the threshold)
-            load_scores(std::false_type{});
-            float mine = 0.f;
+            for (int c = 1; c < 16; ++c) top = fmaxf(top, t[c]);
+            over |= top > C::kLift + C::kLazy;
+        }
+        if (named_any(bar, 128, over)) {
+            // raise the references to the largest scores so far
+#pragma unroll 1
+            for (int c0 = 0; c0 < cols; c0 += 16) {
+                float t[16];
+                exponents(c0, M->zero, t);
+                float mine = 0.f;
 #pragma unroll
-            for (int c = 0; c < COLS; ++c) {
-                const float mx = redux_max(t[c]);
-                if (lane == c) mine = mx;
+                for (int c = 0; c < 16; ++c) {
+                    const float mx = redux_max(t[c]);
+                    if (lane == c) mine = mx;
+                }
+                if (lane < 16) M->red[u][wq][c0 + lane] = mine;
             }
-            if (lane < COLS) M->red[u][wq][lane] = mine;
             named_sync(bar, 128);
-            if (tr < COLS) {
-                const float old = -M->nref[u][tr];
+            if (tr < cols) {
+                const float old = M->ref[u][tr];
                 const float ref = fmaxf(fmaxf(fmaxf(M->red[u][0][tr], M->red[u][1][tr]),
                                               fmaxf(M->red[u][2][tr], M->red[u][3][tr])), old);
-                M->nref[u][tr] = -ref;
+                M->ref[u][tr] = ref;
+                M->nref[u][tr] = C::kLift - ref;
                 M->fac[u][tr] = ex2_approx(old - ref);
             }
             named_sync(bar, 128);
 #pragma unroll
-            for (int c = 0; c < COLS; c += 2) {
+            for (int c = 0; c < kUnitRows; c += 2) {
                 const float2 f = *reinterpret_cast<const float2*>(&M->fac[u][c]);
                 l2[c / 2] = mul2x(l2[c / 2], pack2(f.x, f.y));
             }
             if (i >= sh.streams) {                            // the accumulator holds earlier tiles
-                mbar_wait(&M->pv_done[u], (st.tiles - 1u) & 1u, ab);
+                wait_bar(&M->pv_done[u], (st.tiles - 1u) & 1u, ab);
                 tc_fence_after();
-                const uint32_t at = tO + sh.accum(stream) + (uint32_t)coff;
-#pragma unroll
-                for (int ch = 0; ch < COLS / 16; ++ch) {
+#pragma unroll 1
+                for (int c0 = 0; c0 < cols; c0 += 16) {
                     float o[16];
-                    tmem_ldn<16>(at + ch * 16, o);
+                    tmem_ldn<16>(tO + c0, o);
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) o[c] *= M->fac[u][ch * 16 + c];
-                    tmem_st16(at + ch * 16, o);
+                    for (int c = 0; c < 16; ++c) o[c] *= M->fac[u][c0 + c];
+                    tmem_st16(tO + c0, o);
                 }
                 tmem_st_wait();
             }
         }
         // the P buffer is free once this unit's previous product is done
-        if (st.tiles > 0) mbar_wait(&M->pv_done[u], (st.tiles - 1u) & 1u, ab);
+        if (st.tiles > 0) wait_bar(&M->pv_done[u], (st.tiles - 1u) & 1u, ab);
         ++st.tiles;
-        const uint64_t vs2 = pack2(vs, vs);
+        const uint64_t ivs2 = pack2(ivs, ivs);
 #pragma unroll
-        for (int c8 = 0; c8 < COLS / 8; ++c8) {
-            uint32_t pk[4];
+        for (int c0 = 0; c0 < kUnitRows; c0 += 16) {
+            if (c0 >= cols) break;
+            float t[16];
+            exponents(c0, M->nref[u], t);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int k = c8 * 8 + 2 * c;
-                float a = ex2_approx(t[k]), b = ex2_approx(t[k + 1]);
-                uint64_t w = pack2(a, b);
-                l2[k / 2] = add2(l2[k / 2], w);
-                if (F8) {
-                    unpack2(mul2x(w, vs2), a, b);
-                    if (edge) {
-                        // a hidden key's weight stays 0 whatever its place holds as a scale
-                        if (t[k] == -INFINITY) a = 0.f;
-                        if (t[k + 1] == -INFINITY) b = 0.f;
+            for (int c8 = 0; c8 < 2; ++c8) {
+                uint32_t pk[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int k = c8 * 8 + 2 * c, at = (c0 + k) / 2;
+                    const float a = ex2_approx(t[k]), b = ex2_approx(t[k + 1]);
+                    l2[at] = F8 ? fma2(pack2(a, b), ivs2, l2[at]) : add2(l2[at], pack2(a, b));
+                    // weights become 16-bit for the product with V (half a step: bf16
+                    // 2^-9, fp16 2^-12 of the binade); the sums keep them in float32
+                    if (F8) {
+                        const __half2 h = __floats2half2_rn(a, b);
+                        pk[c] = reinterpret_cast<const uint32_t&>(h);
+                    } else {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+                        pk[c] = reinterpret_cast<const uint32_t&>(h);
                     }
                 }
-                // weights become bf16 for the product with V (half a step: 2^-9 of
-                // each weight's binade); the sums keep them in float32
-                const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-                pk[c] = reinterpret_cast<const uint32_t&>(h);
+                *reinterpret_cast<uint4*>(P + (c0 / 8 + c8) * (kKeyTile * 16) + tr * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
             }
-            *reinterpret_cast<uint4*>(P + c8 * (kKeyTile * 16) + tr * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
         }
         if constexpr (F8) {
             // Widen V's e4m3 codes, 16 at a time; two units share a wide tile.
-            // (The widened tile two before this one has been multiplied, and so
+            // (The widened tile kW before this one has been multiplied, and so
             // has whatever the loaded tile's place held before.)
-            const uint32_t at = st.line + (uint32_t)i;
-            const int d = (int)(at % C::kWMod), s = (int)(at % C::kV);
-            mbar_wait(&M->w_empty[d], ((at / C::kWMod) & 1u) ^ 1u, ab);
-            mbar_wait(&M->v_full[s], (at / C::kV) & 1u, ab);
+            const uint32_t at = line + (uint32_t)i;
+            const int d = (int)(at % C::kW), s = (int)(at % C::kV);
+            wait_bar(&M->w_empty[d], ((at / C::kW) & 1u) ^ 1u, ab);
+            wait_bar(&M->v_full[s], (at / C::kV) & 1u, ab);
             const uint8_t* src = smem + C::kOffV + (size_t)s * C::kLoadBytes;
             uint8_t* dst = smem + C::kOffW + (size_t)d * C::kTileBytes;
             constexpr int kPieces = kKeyTile * HD / 16, kPer = HD / 16;
-            const int step = sh.wide ? 256 : 128;
-#pragma unroll 2
-            for (int x = coff * 4 + tr; x < kPieces; x += step) {
-                const uint4 v = *reinterpret_cast<const uint4*>(src + x * 16);
-                const uint2 a = e4m3x4_to_bf16x4(v.x), b = e4m3x4_to_bf16x4(v.y);
-                const uint2 c = e4m3x4_to_bf16x4(v.z), e = e4m3x4_to_bf16x4(v.w);
-                const int row = x / kPer, c0 = (x % kPer) * 2;
-                uint8_t* rowp = dst + (c0 / 8) * C::kHalfBytes + row * 128;
-                const int c8 = c0 & 7, sw = row & 7;
-                // lanes of the second half write their pieces in the other order: no bank conflicts
-                const bool flip = c0 >= 8;
-                const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(c.x, c.y, e.x, e.y);
-                *reinterpret_cast<uint4*>(rowp + ((c8 + (flip ? 1 : 0)) ^ sw) * 16) = flip ? hi : lo;
-                *reinterpret_cast<uint4*>(rowp + ((c8 + (flip ? 0 : 1)) ^ sw) * 16) = flip ? lo : hi;
-            }
+            const int valid = edge ? sg.keys - (t0 + i) * kKeyTile : kKeyTile;   // rows with a key
+            auto widen = [&](int x0, auto count, int step) {
+                constexpr int kN = decltype(count)::value, kB = 2;
+#pragma unroll 1
+                for (int h = 0; h < kN; h += kB) {
+                    uint4 v[kB];
+#pragma unroll
+                    for (int k = 0; k < kB; ++k) v[k] = *reinterpret_cast<const uint4*>(src + (x0 + (h + k) * step) * 16);
+#pragma unroll
+                    for (int k = 0; k < kB; ++k) {
+                        const int x = x0 + (h + k) * step;
+                        const int row = x / kPer, c0 = (x % kPer) * 2;
+                        if (row >= valid) v[k] = make_uint4(0u, 0u, 0u, 0u);
+                        uint8_t* rowp = dst + (c0 / 8) * C::kHalfBytes + row * 128;
+                        const int c8 = c0 & 7, sw = row & 7;
+                        // lanes of the second half write their pieces in the other order: no bank conflicts
+                        const bool flip = c0 >= 8;
+                        const uint4 lo = e4m3x8_to_half8(v[k].x, v[k].y), hi = e4m3x8_to_half8(v[k].z, v[k].w);
+                        *reinterpret_cast<uint4*>(rowp + ((c8 + (flip ? 1 : 0)) ^ sw) * 16) = flip ? hi : lo;
+                        *reinterpret_cast<uint4*>(rowp + ((c8 + (flip ? 0 : 1)) ^ sw) * 16) = flip ? lo : hi;
+                    }
+                }
+            };
+            if (sh.wide)
+                widen(coff * 4 + tr, std::integral_constant<int, kPieces / 256>{}, 256);
+            else
+                widen(tr, std::integral_constant<int, kPieces / 128>{}, 128);
         }
         fence_proxy_async();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&M->p_full[u]);
     }
-    st.line += (uint32_t)n;
-    ++st.seg;
 
-    // the units' sums, then one factor per row and stream
+    // hand the sums on; the segment before the last has been read
     {
-        float x[COLS];
+        float x[kUnitRows];
 #pragma unroll
-        for (int c = 0; c < COLS; c += 2) unpack2(l2[c / 2], x[c], x[c + 1]);
-        const float sum = lane_sums<COLS>(x);
-        if (lane < COLS) M->red[u][wq][lane] = sum;
+        for (int c = 0; c < kUnitRows; c += 2) unpack2(l2[c / 2], x[c], x[c + 1]);
+        M->red[u][wq][lane] = lane_sums(x);
+        wait_bar(&M->e_free[parity], ((st.seg >> 1) & 1u) ^ 1u, ab);
+        named_sync(bar, 128);
+        if (tr < cols) {
+            M->fin_l[parity][u][tr] = (M->red[u][0][tr] + M->red[u][1][tr]) + (M->red[u][2][tr] + M->red[u][3][tr]);
+            M->fin_m[parity][u][tr] = -M->nref[u][tr];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&M->l_done[parity]);
     }
-    if (st.tiles > 0) mbar_wait(&M->pv_done[u], (st.tiles - 1u) & 1u, ab);
-    tc_fence_after();
-    named_sync(5, kUnits * 128);
+    ++st.seg;
+}
+
+// Joins the streams of a finished segment and stores it (128 threads).
+template <int HD>
+__device__ __forceinline__ void finish_segment(const PagedParams& p, const SegInfo& sg, Misc* M, uint32_t tmem,
+                                               uint32_t seg) {
+    volatile WaitState* ab = &M->wst;
+    const Shape sh(sg.rows);
+    const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+    const int tr = wq * 32 + lane, parity = seg & 1;
+    const int n = sg.n, used = min(n, sh.streams);            // streams with an accumulator
     const bool whole = n == sg.tiles;
-    float* part = p.part + (size_t)(blockIdx.x * 2 + (t0 == 0 ? 1 : 0)) * piece_floats(HD);
+    float* part = p.part + (size_t)(blockIdx.x * 2 + (sg.t0 == 0 ? 1 : 0)) * piece_floats(HD);
+    int64_t at = -1;
+    if (tr < sg.rows) {
+        int i, g;
+        plan_row(p.plan.group, sg.tok, sg.head, tr, i, g);
+        at = (int64_t)(sg.q.a + i) * p.heads + (int64_t)sg.h * p.plan.group + g;
+    }
+    if (tr < kRowTile)
+        M->row_at[tr] = at < 0 ? nullptr
+                               : (whole ? reinterpret_cast<uint8_t*>(p.out + (size_t)at * HD)
+                                        : reinterpret_cast<uint8_t*>(part + 2 * kRowTile + tr * HD));
+    wait_bar(&M->l_done[parity], (seg >> 1) & 1u, ab);
+    wait_bar(&M->o_done[parity], (seg >> 1) & 1u, ab);
+    tc_fence_after();
     const bool store = !ab->abort;
-    const int used = min(n, sh.streams);                      // streams with an accumulator
-    if (u == 0 && tr < sh.cols) {
+    if (tr < sh.cols) {
         const int c = tr & 31;
-        auto unit = [&](int s) { return sh.wide ? 2 * s + (tr >> 5) : s; };
+        // the unit that holds this column of the segment's k-th stream
+        auto unit = [&](int k) {
+            const int s = sh.stream_at(sg, k);
+            return sh.wide ? 2 * s + (tr >> 5) : s;
+        };
         float m = kFloorRef;
-        for (int s = 0; s < used; ++s) m = fmaxf(m, -M->nref[unit(s)][c]);
+#pragma unroll 1
+        for (int k = 0; k < used; ++k) m = fmaxf(m, M->fin_m[parity][unit(k)][c]);
         float sum = 0.f;
-        for (int s = 0; s < used; ++s) {
-            const float* r = &M->red[unit(s)][0][c];
-            const float l = r[0] + r[kUnitRows] + r[2 * kUnitRows] + r[3 * kUnitRows];
-            const float f = ex2_approx(-M->nref[unit(s)][c] - m);
-            sum = fmaf(l, f, sum);
-            M->fac[unit(s)][c] = f;
+#pragma unroll 1
+        for (int k = 0; k < used; ++k) {
+            sum = fmaf(M->fin_l[parity][unit(k)][c], ex2_approx(M->fin_m[parity][unit(k)][c] - m), sum);
         }
         const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-        for (int s = 0; s < used; ++s) M->fac[unit(s)][c] *= inv;
-        const int64_t at = M->row_at[parity][tr];
+#pragma unroll 1
+        for (int k = 0; k < used; ++k) M->join[unit(k)][c] = ex2_approx(M->fin_m[parity][unit(k)][c] - m) * inv;
         if (store && whole && p.lse && at >= 0) p.lse[at] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
         if (store && !whole) {
             part[tr] = m;
             part[kRowTile + tr] = sum;
         }
     }
-    if (u == 0 && tr == 0 && t0 == 0 && !whole) {             // the last segment of the span
+    if (tr == 0 && sg.t0 == 0 && !whole) {                    // the last segment of the span
         const int spans = plan_spans(M->total, (int)gridDim.x);
         const int64_t last_tile = plan_cut(M->total, (int)blockIdx.x + 1, spans) - n + sg.tiles - 1;
         p.desc[blockIdx.x] = JoinDesc{sg.r, sg.j, sg.h, plan_owner(M->total, last_tile, spans)};
     }
-    named_sync(5, kUnits * 128);
-    const bool mine = store && tr < HD;
-    if (COLS == 32 && sh.wide)
-        store_columns<HD, 16>(p, M, sh, tO, u * 16, used, parity, whole, part, tr, mine);
-    else
-        store_columns<HD, COLS / 4>(p, M, sh, tO, u * (COLS / 4), used, parity, whole, part, tr, mine);
+    named_sync(5, 128);
+    const uint32_t tO = tmem + ((uint32_t)(wq * 32) << 16) + kColO * (1 + parity);
+#pragma unroll 1
+    for (int c0 = 0; c0 < sh.cols; c0 += 8) {
+        float o[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) o[c] = 0.f;
+#pragma unroll 1
+        for (int k = 0; k < used; ++k) {
+            float x[8];
+            const int st = sh.stream_at(sg, k);
+            const float* f = &M->join[sh.wide ? 2 * st + (c0 >> 5) : st][c0 & 31];
+            tmem_ldn<8>(tO + sh.column(st) + (uint32_t)c0, x);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) o[c] = fmaf(x[c], f[c], o[c]);
+        }
+        if (!store || tr >= HD) continue;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            uint8_t* row = M->row_at[c0 + c];
+            if (!row) break;                                  // rows come first
+            if (whole)
+                reinterpret_cast<uint16_t*>(row)[tr] = __bfloat16_as_ushort(__float2bfloat16_rn(o[c]));
+            else
+                reinterpret_cast<float*>(row)[tr] = o[c];
+        }
+    }
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&M->o_free);
+    if (lane == 0) mbar_arrive(&M->e_free[parity]);
+    named_sync(5, 128);                                       // row_at and join are no longer read
 }
 
 template <int HD, bool F8>
@@ -541,6 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int per = (pl.R + kThreads - 1) / kThreads;
     const int r0 = min((int)threadIdx.x * per, pl.R), r1 = min(r0 + per, pl.R);
     int64_t sum = 0;
+#pragma unroll 1
     for (int r = r0; r < r1; ++r) sum += plan_request_tiles(pl, r);
     int64_t upto = sum;
 #pragma unroll
@@ -550,34 +633,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane == 31) M->scan[warp] = upto;
     if (threadIdx.x == 0) {
+#pragma unroll 1
         for (int i = 0; i < C::kK; ++i) {
             mbar_init(&M->k_full[i], 1);
             mbar_init(&M->k_empty[i], 1);
         }
+#pragma unroll 1
         for (int i = 0; i < C::kV; ++i) {
             mbar_init(&M->v_full[i], 1);
             mbar_init(&M->v_empty[i], 1);
         }
+#pragma unroll 1
         for (int i = 0; i < C::kW; ++i) mbar_init(&M->w_empty[i], 1);
+#pragma unroll 1
         for (int i = 0; i < C::kSc; ++i) {
             mbar_init(&M->c_full[i], 1);
             mbar_init(&M->c_empty[i], 8);
         }
-        for (int i = 0; i < C::kQ; ++i) {
-            mbar_init(&M->q_full[i], 32);
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&M->q_full[i], 128);
             mbar_init(&M->q_empty[i], F8 ? 1 + 4 * kUnits : 1);
         }
+#pragma unroll 1
         for (int i = 0; i < kUnits; ++i) {
             mbar_init(&M->s_full[i], 1);
             mbar_init(&M->p_full[i], 4);
             mbar_init(&M->pv_done[i], 1);
         }
+#pragma unroll 1
         for (int i = 0; i < kSegs; ++i) {
             mbar_init(&M->seg_full[i], 1);
             mbar_init(&M->seg_empty[i], kReaders);
         }
-        mbar_init(&M->o_free, 4 * kUnits);
-        mbar_init(&M->done, 1);
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&M->o_done[i], 1);
+            mbar_init(&M->l_done[i], 4 * kUnits);
+            mbar_init(&M->e_free[i], 4);
+        }
+        mbar_init(&M->done, 2);
+#pragma unroll 1
+        for (int i = 0; i < kUnitRows; ++i) M->zero[i] = 0.f;
         M->wst.abort = 0;
         M->wst.limit = ws_wait_limit(p.ws);
         fence_mbar_init();
@@ -585,6 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     int64_t base = upto - sum, total = 0;
+#pragma unroll 1
     for (int i = 0; i < kThreads / 32; ++i) {
         if (i < warp) base += M->scan[i];
         total += M->scan[i];
@@ -595,6 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (base <= begin && begin < base + sum) {
         int64_t at = base;
         int r = r0;
+#pragma unroll 1
         for (;; ++r) {
             const int64_t t = plan_request_tiles(pl, r);
             if (begin < at + t) break;
@@ -604,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         M->start_skip = begin - at;
     }
     if (threadIdx.x == 0) M->total = total;
-    if (warp == 1) tmem_alloc(&M->tmem, C::kTmem);
+    if (warp == 1) tmem_alloc(&M->tmem, kTmem);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -615,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     SegInfo sg;
     auto next_segment = [&]() {
         const int at = nseg % kSegs;
-        if (!__all_sync(0xffffffffu, mbar_wait(&M->seg_full[at], (nseg / kSegs) & 1u, ab))) return false;
+        if (!__all_sync(0xffffffffu, wait_bar(&M->seg_full[at], (nseg / kSegs) & 1u, ab))) return false;
         sg = M->seg[at];
         return sg.rows > 0;
     };
@@ -628,250 +727,391 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int bp = min(1 << p.page_log2, kKeyTile);           // tokens of a page inside one tile
     const int ppt = kKeyTile / bp;                            // pages of a tile
 
+    // ---------------- loads of K (warp 0) and V (warp 2) tiles
+    // A place in the line of tiles: the next tile to load.
+    struct Place {
+        int tok, end, keys;                                   // first token of the tile, of the segment's end; keys
+        int at, now, next;                                    // page table: lane's entries of 32 pages from `at`, and the 32 after
+        int r, x;
+        uint32_t seg, slot, phase, count;                     // segment; ring place; tiles issued
+        uint64_t pol;
+        bool more;
+    };
+    const int pg = lane & 7;
+    const int lane_tok = pg < ppt ? pg * bp : 1 << 30;        // this lane's page of a tile, in tokens
+    bool ok = true;
+    auto entry = [&](const Place& c, int k) {
+        return (int64_t)k << p.page_log2 < c.keys ? __ldg(p.page_table + (size_t)c.r * p.max_pages + k) : -1;
+    };
+    auto enter = [&](Place& c) {
+        const int at = c.seg % kSegs;
+        ok = ok && __all_sync(0xffffffffu, wait_bar(&M->seg_full[at], (c.seg / kSegs) & 1u, ab));
+        const SegInfo& s = M->seg[at];
+        c.more = ok && s.rows > 0;
+        if (!c.more) return;
+        c.tok = s.t0 * kKeyTile;
+        c.end = (s.t0 + s.n) * kKeyTile;
+        c.keys = s.keys;
+        c.r = s.r;
+        c.x = s.h << p.page_log2;
+        // more than one row tile of a request reads its keys again
+        c.pol = (int64_t)s.q.q_len * pl.group > kRowTile ? policy_evict_normal() : policy_evict_first();
+        c.at = (c.tok >> p.page_log2) & ~31;
+        c.now = entry(c, c.at + lane);
+        c.next = entry(c, c.at + 32 + lane);
+    };
+    // this lane's page of the place's tile (pages past the keys: any)
+    auto page_of = [&](Place& c) {
+        int rel = (c.tok >> p.page_log2) - c.at;
+        if (rel >= 32) {
+            rel -= 32;
+            c.at += 32;
+            c.now = c.next;
+            c.next = entry(c, c.at + 32 + lane);
+        }
+        return __shfl_sync(0xffffffffu, c.now, (rel + pg) & 31);
+    };
+    // on to the next tile; true if it is another segment's
+    auto step = [&](Place& c) {
+        ++c.count;
+        c.tok += kKeyTile;
+        if (c.tok < c.end) return false;
+        ++c.seg;
+        return true;
+    };
+    auto load = [&](auto which, Place& c, int id) {
+        constexpr bool kIsV = decltype(which)::value;
+        constexpr uint32_t kRing = kIsV ? C::kV : C::kK;
+        uint64_t* full = (kIsV ? M->v_full : M->k_full) + c.slot;
+        ok = ok && __all_sync(0xffffffffu, wait_bar((kIsV ? M->v_empty : M->k_empty) + c.slot, c.phase ^ 1u, ab));
+        const uint32_t cs = c.count % C::kScMod;
+        if (F8 && !kIsV)
+            ok = ok && __all_sync(0xffffffffu, wait_bar(&M->c_empty[cs], ((c.count / C::kScMod) & 1u) ^ 1u, ab));
+        if (!ok) return;
+        const bool valid = lane_tok < c.keys - c.tok;
+        if (valid && (uint32_t)id >= (uint32_t)p.n_pages) {
+            raise_status(p.ws, kStatBadPage);
+            id = p.n_pages;                                   // past the tensor: zeros
+        }
+        const uint32_t pages = __popc(__ballot_sync(0xffffffffu, valid) & 0xFFu);
+        const int x = c.x + (ppt == 1 ? c.tok & ((1 << p.page_log2) - 1) : 0);        // a 256-token page is two tiles
+        if (elect_one()) {
+            mbar_expect_tx(full, pages * (uint32_t)(bp * (F8 ? HD : HD * 2)));
+            if (F8 && !kIsV) mbar_expect_tx(&M->c_full[cs], pages * (uint32_t)(bp * 8));
+        }
+        __syncwarp();
+        uint8_t* dst = smem + (kIsV ? C::kOffV : 0) + c.slot * C::kLoadBytes;
+        uint8_t* sc = smem + C::kOffSc + cs * C::kScBytes;
+#pragma unroll 1
+        for (uint32_t k = 0; k < pages; ++k) {
+            const int pid = __shfl_sync(0xffffffffu, id, k);
+            if (elect_one()) {
+#pragma unroll
+                for (int hf = 0; hf < (F8 ? 1 : C::kHalves); ++hf)
+                    tma_load_3d(dst + hf * C::kHalfBytes, kIsV ? &maps.v : &maps.k, full, hf * 64, x, pid, c.pol);
+                if (F8 && !kIsV) {
+                    tma_load_2d(sc, &maps.ks, &M->c_full[cs], x, pid, c.pol);
+                    tma_load_2d(sc + C::kScBytes / 2, &maps.vs, &M->c_full[cs], x, pid, c.pol);
+                }
+            }
+            dst += bp * (F8 ? HD : 128);
+            sc += max(bp * 4, 128);
+        }
+        __syncwarp();
+        if (++c.slot == kRing) {
+            c.slot = 0;
+            c.phase ^= 1u;
+        }
+    };
+    // copies in flight of a ring, after an abort
+    auto drain = [&](uint64_t* full, uint32_t ring, uint32_t count) {
+        if (ab->abort && lane == 0)
+#pragma unroll 1
+            for (uint32_t k = count > ring ? count - ring : 0; k < count; ++k)
+                mbar_wait_for(&full[k % ring], (k / ring) & 1u, ab->limit);
+        __syncwarp();
+    };
+
     if (warp == 0) {
-        // ---------------- producer
-        const uint64_t once = policy_evict_first(), again = policy_evict_normal();
-        uint32_t nk = 0, nv = 0;
-        const int pg = lane & 7, sub = lane >> 3;
-        bool ok = true;
-        for (; ok && next_segment(); done_segment()) {
-            // more than one row tile of a request reads its keys again
-            const uint64_t pol = (int64_t)sg.q.q_len * pl.group > kRowTile ? again : once;
-            const int32_t* table = p.page_table + (size_t)sg.r * p.max_pages;
-            const int n = sg.n, ahead = min(Shape(sg.rows).streams, n);
-            // the page of this lane's part of key tile i (-1: past the keys)
-            auto page_of = [&](int i) {
-                const int64_t tok = (int64_t)(sg.t0 + i) * kKeyTile + pg * bp;
-                if (i >= n || pg >= ppt || tok >= sg.keys) return -1;
-                int id = __ldg(table + (tok >> p.page_log2));
-                if (id < 0 || id >= p.n_pages) {
-                    raise_status(p.ws, kStatBadPage);
-                    id = p.n_pages;                           // past the tensor: zeros
-                }
-                return id;
-            };
-            auto issue = [&](bool is_v, int i, int id) {
-                const uint32_t g = is_v ? nv++ : nk++;
-                const int ring = is_v ? C::kV : C::kK, s = (int)(g % ring);
-                uint64_t *full = is_v ? M->v_full : M->k_full, *empty = is_v ? M->v_empty : M->k_empty;
-                ok = ok && __all_sync(0xffffffffu, mbar_wait(&empty[s], ((g / ring) & 1u) ^ 1u, ab));
-                const int c = (int)(g % C::kScMod);
-                if (F8 && !is_v)
-                    ok = ok && __all_sync(0xffffffffu, mbar_wait(&M->c_empty[c], ((g / C::kScMod) & 1u) ^ 1u, ab));
-                if (!ok) {
-                    (is_v ? nv : nk) -= 1;
-                    return;
-                }
-                const int pages = __popc(__ballot_sync(0xffffffffu, id >= 0 && lane < 8));
-                const int tok0 = ((sg.t0 + i) * kKeyTile) & ((1 << p.page_log2) - 1);   // place inside a 256-token page
-                const int x = (sg.h << p.page_log2) + (ppt == 1 ? tok0 : 0);
-                if (lane == 0) {
-                    mbar_expect_tx(&full[s], (uint32_t)(pages * bp * (F8 ? HD : HD * 2)));
-                    if (F8 && !is_v) mbar_expect_tx(&M->c_full[c], (uint32_t)(pages * bp * 8));
-                }
-                __syncwarp();
-                if (id < 0) return;
-                if (sub < (F8 ? 1 : C::kHalves))
-                    tma_load_3d(smem + (is_v ? C::kOffV : 0) + (size_t)s * C::kLoadBytes + (F8 ? 0 : sub * C::kHalfBytes) +
-                                    pg * bp * (F8 ? HD : 128),
-                                is_v ? &maps.v : &maps.k, &full[s], sub * 64, x, id, pol);
-                else if (F8 && !is_v && sub < 3)
-                    tma_load_2d(smem + C::kOffSc + c * C::kScBytes + (sub - 1) * (C::kScBytes / 2) + pg * max(bp * 4, 128),
-                                sub == 1 ? &maps.ks : &maps.vs, &M->c_full[c], x, id, pol);
-            };
-            // K runs `ahead` tiles before V; ids[k] is the page of tile i + k
-            int ids[6];
-#pragma unroll
-            for (int k = 0; k < 5; ++k) ids[k] = page_of(k);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (k < ahead) issue(false, k, ids[k]);
-            for (int i = 0; ok && i < n; ++i) {
-                ids[5] = page_of(i + 5);
-                if (i + ahead < n)
-                    issue(false, i + ahead, ahead == 4 ? ids[4] : (ahead == 3 ? ids[3] : (ahead == 2 ? ids[2] : ids[1])));
-                issue(true, i, ids[0]);
-#pragma unroll
-                for (int k = 0; k < 5; ++k) ids[k] = ids[k + 1];
+        // ---------------- K tiles
+        Place c = {};
+        enter(c);
+#pragma unroll 1
+        while (ok && c.more) {
+            load(std::false_type{}, c, page_of(c));
+            if (!ok) break;
+            const uint32_t seg = c.seg;
+            if (step(c)) {
+                if (lane == 0) mbar_arrive(&M->seg_empty[seg % kSegs]);
+                enter(c);
             }
         }
-        // every copy that was issued lands before the CTA may leave
-        __syncwarp();
-        if (ab->abort && lane == 0) {
-            for (uint32_t k = nk > C::kK ? nk - C::kK : 0; k < nk; ++k)
-                mbar_wait_for(&M->k_full[k % C::kK], (k / C::kK) & 1u, ab->limit);
-            for (uint32_t k = nv > C::kV ? nv - C::kV : 0; k < nv; ++k)
-                mbar_wait_for(&M->v_full[k % C::kV], (k / C::kV) & 1u, ab->limit);
-            if (F8)
-                for (uint32_t k = nk > (uint32_t)C::kSc ? nk - C::kSc : 0; k < nk; ++k)
-                    mbar_wait_for(&M->c_full[k % C::kScMod], (k / C::kScMod) & 1u, ab->limit);
-        }
+        drain(M->k_full, C::kK, c.count);
+        if (F8) drain(M->c_full, C::kScMod, c.count);
     } else if (warp == 1) {
-        // ---------------- MMA issuer
-        constexpr uint32_t a_lbo = HD == 128 ? C::kHalfBytes : 0;   // head_dim 64: rows 64..127 repeat 0..63
-        uint32_t nk = 0, nv = 0, np = 0;                      // np: parity of each unit's next p_full, by bit
-        bool ok = true;
-        auto wait = [&](uint64_t* bar, uint32_t par) {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, par, ab));
-            tc_fence_after();
-            return ok;
+        // ---------------- scores S^T = K Q^T
+        // A stream's columns are free once the weights of its tile before are
+        // made; at a change of shape, once all earlier weights are.
+        const uint64_t dk = F8 ? desc_f8<HD>(smem) : smem_desc_sw128(smem, 16, 1024);
+        const uint64_t dq = F8 ? desc_f8<HD>(smem + C::kOffQ) : smem_desc_sw128(smem + C::kOffQ, 16, 1024);
+        uint32_t ks = 0, kph = 0;
+        uint32_t made = 0, owed = 0;   // by unit: parity of its next p_full, and whether one is outstanding
+        uint32_t run = 0;
+        auto wait = [&](uint64_t* bar, uint32_t par) { ok = ok && __all_sync(0xffffffffu, wait_bar(bar, par, ab)); };
+        uint32_t used = 0;             // units that have had a tile
+        // waits for the outstanding weights of some units (done: and for their products)
+        auto settle = [&](uint32_t units, bool done) {
+#pragma unroll 1
+            for (int u = 0; u < kUnits; ++u) {
+                const uint32_t bit = 1u << u;
+                if (!(units & used & bit)) continue;
+                if (owed & bit) {
+                    wait(&M->p_full[u], (made >> u) & 1u);
+                    made ^= bit;
+                    owed ^= bit;
+                }
+                // pv_done's phases follow p_full's one by one
+                if (done) wait(&M->pv_done[u], ((made >> u) & 1u) ^ 1u);
+            }
         };
+#pragma unroll 1
         for (; ok && next_segment(); done_segment()) {
-            const int n = sg.n;
             const Shape sh(sg.rows);
-            const uint32_t id_qk = F8 ? idesc_e4m3_f32(128, 2 * sh.cols) : idesc_bf16_f32(128, sh.cols, false, false);
-            const uint32_t id_pv = idesc_bf16_f32(128, sh.cols, true, true);
-            const int qb = nseg % C::kQ;
-            const uint8_t* qt = smem + C::kOffQ + qb * C::kQBytes;
-            auto scores = [&](int i) {
-                const int s = (int)(nk % C::kK), st = i % sh.streams;
-                if (!wait(&M->k_full[s], (nk / C::kK) & 1u)) return;
-                if (lane == 0) {
-                    const uint8_t* kt = smem + (size_t)s * C::kLoadBytes;
-                    const uint32_t d = tmem + sh.scores<F8>(st);
+            const uint32_t id = F8 ? idesc_e4m3_f32(128, sh.cols) : idesc_bf16_f32(128, sh.cols, false, false);
+            const uint64_t b = dq + (sg.qp == 1 ? C::kQBytes / 16 : 0);
+            // rows between Q's halves along head_dim (bf16), or between hi and lo
+            const int q_rows = sg.qp == 2 ? 2 * C::kQRows : C::kQRows;
+            if (sg.run != run) settle(15u, true);             // columns and buffers change hands
+            run = sg.run;
+            q_places(sg, [&](int k, uint32_t use) { wait(&M->q_full[k], use & 1u); });
+#pragma unroll 1
+            for (int i = 0; ok && i < sg.n; ++i) {
+                const int st = sh.stream_at(sg, i);
+                const uint32_t units = sh.wide ? 3u << (2 * st) : 1u << st;
+                settle(units, false);
+                owed |= units;
+                used |= units;
+                wait(&M->k_full[ks], kph);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t d = tmem + sh.column(st);
+                    const uint64_t a = dk + ks * (C::kLoadBytes / 16);
                     if (F8) {
 #pragma unroll
-                        for (int kk = 0; kk < HD / 32; ++kk)
-                            umma_f8(d, desc_f8<HD>(kt + kk * 32), desc_f8<HD>(qt + kk * 32), id_qk, kk ? 1u : 0u);
+                        for (int kk = 0; kk < HD / 16; ++kk)   // hi, then lo
+                            umma_f8(d, a + (kk % (HD / 32)) * 2, b + (uint32_t)((kk / (HD / 32)) * (q_rows * HD / 16) + (kk % (HD / 32)) * 2),
+                                    id, kk ? 1u : 0u);
                     } else {
 #pragma unroll
                         for (int kk = 0; kk < HD / 16; ++kk)
-                            umma_bf16(d, smem_desc_sw128(kt + (kk / 4) * C::kHalfBytes + (kk % 4) * 32, 16, 1024),
-                                      smem_desc_sw128(qt + (kk / 4) * (kRowTile * 128) + (kk % 4) * 32, 16, 1024), id_qk,
-                                      kk ? 1u : 0u);
+                            umma_bf16(d, a + (kk / 4) * (C::kHalfBytes / 16) + (kk % 4) * 2,
+                                      b + (uint32_t)((kk / 4) * (q_rows * 8) + (kk % 4) * 2), id, kk ? 1u : 0u);
                     }
-                    umma_commit(&M->k_empty[s]);
                     umma_commit(&M->s_full[sh.wide ? 2 * st : st]);
                     if (sh.wide) umma_commit(&M->s_full[2 * st + 1]);
-                    if (i == n - 1) umma_commit(&M->q_empty[qb]);
+                    umma_commit(&M->k_empty[ks]);
+                    if (i == sg.n - 1) q_places(sg, [&](int k, uint32_t) { umma_commit(&M->q_empty[k]); });
                 }
                 __syncwarp();
-                ++nk;
-            };
-            if (!wait(&M->q_full[qb], (nseg / C::kQ) & 1u)) break;
-            for (int i = 0; ok && i < n && i < sh.streams; ++i) scores(i);
-            for (int i = 0; ok && i < n; ++i) {
-                const int st = i % sh.streams, u0 = sh.wide ? 2 * st : st;
-                if (!wait(&M->p_full[u0], (np >> u0) & 1u)) break;
-                if (sh.wide && !wait(&M->p_full[u0 + 1], (np >> (u0 + 1)) & 1u)) break;
-                np ^= (sh.wide ? 3u : 1u) << u0;
-                if (i + sh.streams < n) scores(i + sh.streams);
-                if (i == 0 && nseg > 0) wait(&M->o_free, (nseg - 1u) & 1u);
+                if (++ks == C::kK) {
+                    ks = 0;
+                    kph ^= 1u;
+                }
+            }
+        }
+        if (elect_one()) umma_commit(&M->done);
+        __syncwarp();
+    } else if (warp == 3) {
+        // ---------------- products O^T += V^T P^T
+        constexpr uint32_t a_lbo = HD == 128 ? C::kHalfBytes : 0;   // head_dim 64: rows 64..127 repeat 0..63
+        const uint64_t dv = smem_desc_sw128(smem + (F8 ? C::kOffW : C::kOffV), a_lbo, 1024);
+        const uint64_t dp = smem_desc_plain(smem + C::kOffP, 128, kKeyTile * 16);
+        uint32_t vs = 0, vph = 0, ws = 0;
+        uint32_t made = 0;                                    // parity of each unit's next p_full, by bit
+        auto wait = [&](uint64_t* bar, uint32_t par) { ok = ok && __all_sync(0xffffffffu, wait_bar(bar, par, ab)); };
+#pragma unroll 1
+        for (; ok && next_segment(); done_segment()) {
+            const Shape sh(sg.rows);
+            const uint32_t id = F8 ? idesc_f16_f32(128, sh.cols, true, true) : idesc_bf16_f32(128, sh.cols, true, true);
+            const uint32_t set = tmem + kColO * (1u + (nseg & 1u));
+#pragma unroll 1
+            for (int i = 0; ok && i < sg.n; ++i) {
+                const int st = sh.stream_at(sg, i), u0 = sh.wide ? 2 * st : st;
                 // bf16: the V tile as it was loaded; e4m3: the widened one, which
                 // p_full covers, as it does the end of the reads of the loaded one
-                const int s = (int)(nv % C::kV), d = (int)(nv % C::kWMod);
-                if (!F8) wait(&M->v_full[s], (nv / C::kV) & 1u);
-                if (!ok) break;
-                uint8_t* vt = smem + (F8 ? C::kOffW + (size_t)d * C::kTileBytes : C::kOffV + (size_t)s * C::kTileBytes);
-                const int valid = sg.keys - (sg.t0 + i) * kKeyTile;
-                if (!F8 && valid < kKeyTile) {
-                    // rows past the last key hold whatever the pages or this buffer held
-                    for (int x = max(valid, 0) * 8 + lane; x < kKeyTile * 8; x += 32)
+                if (!F8) {
+                    wait(&M->v_full[vs], vph);
+                    const int valid = sg.keys - (sg.t0 + i) * kKeyTile;
+                    if (ok && valid < kKeyTile) {
+                        // rows past the last key hold whatever the pages or this buffer held
+                        uint8_t* vt = smem + C::kOffV + (size_t)vs * C::kTileBytes;
+#pragma unroll 1
+                        for (int k = max(valid, 0) * 8 + lane; k < kKeyTile * 8; k += 32)
 #pragma unroll
-                        for (int hf = 0; hf < C::kHalves; ++hf)
-                            *reinterpret_cast<uint4*>(vt + hf * C::kHalfBytes + x * 16) = make_uint4(0u, 0u, 0u, 0u);
-                    fence_proxy_async();
-                    __syncwarp();
+                            for (int hf = 0; hf < C::kHalves; ++hf)
+                                *reinterpret_cast<uint4*>(vt + hf * C::kHalfBytes + k * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        fence_proxy_async();
+                        __syncwarp();
+                    }
                 }
-                if (lane == 0) {
-                    const uint8_t* pt = smem + C::kOffP + u0 * C::kPBytes;
+                wait(&M->p_full[u0], (made >> u0) & 1u);
+                if (sh.wide) wait(&M->p_full[u0 + 1], (made >> (u0 + 1)) & 1u);
+                made ^= (sh.wide ? 3u : 1u) << u0;
+                if (i == 0) wait(&M->e_free[nseg & 1], ((nseg >> 1) & 1u) ^ 1u);   // this set's last segment is stored
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t a = dv + (F8 ? ws : vs) * (C::kTileBytes / 16), b = dp + u0 * (C::kPBytes / 16);
+                    const uint32_t d = set + sh.column(st);
+                    umma_bf16(d, a, b, id, i >= sh.streams ? 1u : 0u);
 #pragma unroll
-                    for (int kk = 0; kk < kKeyTile / 16; ++kk)
-                        umma_bf16(tmem + C::kColO + sh.accum(st), smem_desc_sw128(vt + kk * 2048, a_lbo, 1024),
-                                  smem_desc_plain(pt + kk * 256, 128, kKeyTile * 16), id_pv,
-                                  (i >= sh.streams || kk) ? 1u : 0u);
-                    if (F8) mbar_arrive(&M->v_empty[s]);
-                    umma_commit(F8 ? &M->w_empty[d] : &M->v_empty[s]);
+                    for (int kk = 1; kk < kKeyTile / 16; ++kk) umma_bf16(d, a + kk * 128, b + kk * 16, id, 1u);
+                    if (F8) mbar_arrive(&M->v_empty[vs]);
+                    umma_commit(F8 ? &M->w_empty[ws] : &M->v_empty[vs]);
                     umma_commit(&M->pv_done[u0]);
                     if (sh.wide) umma_commit(&M->pv_done[u0 + 1]);
+                    if (i == sg.n - 1) umma_commit(&M->o_done[nseg & 1]);
                 }
                 __syncwarp();
-                ++nv;
+                if (++vs == C::kV) {
+                    vs = 0;
+                    vph ^= 1u;
+                }
+                if (F8 && ++ws == C::kW) ws = 0;
             }
         }
         // the tensor core is idle before its memory is given back
-        if (lane == 0) {
+        if (elect_one()) {
             umma_commit(&M->done);
             mbar_wait_for(&M->done, 0, ab->limit);
         }
         __syncwarp();
     } else if (warp == 2) {
-        // ---------------- Q rows
-        const uint64_t pol = policy_evict_normal();
-        constexpr int kLanes = HD / 8;                        // 8 values per lane
-        for (; next_segment(); done_segment()) {
-            const int qb = nseg % C::kQ;
-            if (!__all_sync(0xffffffffu, mbar_wait(&M->q_empty[qb], ((nseg / C::kQ) & 1u) ^ 1u, ab))) break;
-            const int cols = Shape(sg.rows).cols;
-            uint8_t* qt = smem + C::kOffQ + qb * C::kQBytes;
-            for (int x = lane; x < cols * kLanes; x += 32) {
-                const int row = x / kLanes, c = x % kLanes;
-                const int64_t rho = (int64_t)sg.j * kRowTile + row;
-                const int i = (int)(rho / pl.group), gq = (int)(rho - (int64_t)i * pl.group);
-                const bool in = row < sg.rows;
-                const uint16_t* src = in ? p.q + (int64_t)(sg.q.a + i) * p.q_stride +
-                                               ((int64_t)sg.h * pl.group + gq) * HD + c * 8
+        // ---------------- segments and V tiles: whatever can go on
+        Cursor cur;
+        cur.start(pl, M->start_r, M->start_skip, end - begin);
+        uint32_t made = 0, line = 0, run = 0;                 // segments listed, their key tiles
+        bool wide = false, more = true;
+        int place = 0;                                        // the next Q place
+        uint32_t use = 0;
+        Place c = {};
+        bool v_in = false;                                    // c stands in a segment
+        uint64_t t0 = sm_cycles();
+        auto test = [&](uint64_t* bar, uint32_t par) { return __all_sync(0xffffffffu, mbar_test(bar, par)) != 0; };
+#pragma unroll 1
+        for (;;) {
+            bool moved = false;
+            if (more && test(&M->seg_empty[made % kSegs], ((made / kSegs) & 1u) ^ 1u)) {
+                Segment s;
+                more = cur.next(pl, s);
+                if (more && Shape(s.rows).wide != wide) {
+                    wide = !wide;
+                    run = line;
+                }
+                const bool both = more && Shape(s.rows).cols > C::kQRows;
+                if (lane == 0) {
+                    SegInfo& o = M->seg[made % kSegs];
+                    o.rows = 0;
+                    if (more)
+                        o = SegInfo{s.r, s.j, s.h, s.t0, s.t1 - s.t0, s.tiles, s.keys, s.rows, s.tok, s.head, line, run,
+                                    both ? 2 : place, use, s.q};
+                    mbar_arrive(&M->seg_full[made % kSegs]);
+                }
+                __syncwarp();
+                if (more) line += (uint32_t)(s.t1 - s.t0);
+                use += (both || place == 0 ? 1u : 0u) + (both || place == 1 ? 0x10000u : 0u);
+                use &= 0x7FFF7FFFu;                           // parities are what counts
+                if (!both) place ^= 1;
+                ++made;
+                moved = true;
+            }
+            if (!v_in && c.seg < made) {
+                enter(c);
+                v_in = c.more;
+            }
+            if (v_in && test(&M->v_empty[c.slot], c.phase ^ 1u)) {
+                load(std::true_type{}, c, page_of(c));
+                if (!ok) break;
+                const uint32_t seg = c.seg;
+                if (step(c)) {
+                    if (lane == 0) mbar_arrive(&M->seg_empty[seg % kSegs]);
+                    v_in = false;
+                }
+                moved = true;
+            } else if (!more && !v_in && c.seg + 1 >= made) {
+                break;                                        // the last segment is loaded, its end listed
+            }
+            // bounded: give up when nothing moves for the wait limit
+            if (moved)
+                t0 = sm_cycles();
+            else if (sm_cycles() - t0 > ab->limit)
+                ab->abort = 1;
+            if (__any_sync(0xffffffffu, ab->abort != 0)) break;
+        }
+        drain(M->v_full, C::kV, c.count);
+    } else if (warp >= 4 + 4 * kUnits) {
+        // ---------------- Q rows of the segment to come, and the finished one
+        constexpr int kLanes = HD / 8, kStep = 128 / kLanes;  // 8 values per lane; rows per step
+        const int ft = threadIdx.x - 32 * (4 + 4 * kUnits);
+        // segment k's rows into its Q buffer; false at the end or when a wait ran out
+        auto bring = [&](uint32_t k) {
+            const SegInfo& s = M->seg[k % kSegs];
+            bool got = wait_bar(&M->seg_full[k % kSegs], (k / kSegs) & 1u, ab);
+            if (got && s.rows > 0)
+                q_places(s, [&](int b, uint32_t use) { got = got && wait_bar(&M->q_empty[b], (use & 1u) ^ 1u, ab); });
+            if (named_any(5, 128, !got)) return false;
+            if (s.rows == 0) return false;
+            const int cols = Shape(s.rows).cols, q_rows = s.qp == 2 ? 2 * C::kQRows : C::kQRows;
+            uint8_t* qt = smem + C::kOffQ + (s.qp == 1 ? C::kQBytes : 0);
+            const int x = ft % kLanes;
+#pragma unroll 1
+            for (int row = ft / kLanes; row < cols; row += kStep) {
+                int i, gq;
+                plan_row(pl.group, s.tok, s.head, row, i, gq);
+                const bool in = row < s.rows;
+                const uint16_t* src = in ? p.q + (int64_t)(s.q.a + i) * p.q_stride + ((int64_t)s.h * pl.group + gq) * HD + x * 8
                                          : p.q;
                 if (!F8) {
-                    cp_async16_zf(qt + (c / 8) * (kRowTile * 128) + row * 128 + ((c ^ row) & 7) * 16, src, in ? 16u : 0u,
-                                  pol);
-                    continue;
+                    cp_async16_zf(qt + (x / 8) * (q_rows * 128) + row * 128 + ((x ^ row) & 7) * 16, src, in ? 16u : 0u,
+                                  policy_evict_normal());
+                } else {
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if (in) v = __ldg(reinterpret_cast<const uint4*>(src));
+                    uint2 hi, lo;
+                    const float sc = split_e4m3<kLanes>(v, hi, lo);
+                    *reinterpret_cast<uint2*>(qt + swz_f8<HD>(row, x / 2) + (x & 1) * 8) = hi;
+                    *reinterpret_cast<uint2*>(qt + swz_f8<HD>(q_rows + row, x / 2) + (x & 1) * 8) = lo;
+                    if (x == 0) M->q_scale[(s.qp == 1 ? C::kQRows : 0) + row] = sc;
                 }
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (in) v = __ldg(reinterpret_cast<const uint4*>(src));
-                uint2 hi, lo;
-                const float s = split_e4m3<kLanes>(v, hi, lo);
-                const int at = swz_f8<HD>(row, c / 2) + (c & 1) * 8, at_lo = swz_f8<HD>(cols + row, c / 2) + (c & 1) * 8;
-                *reinterpret_cast<uint2*>(qt + at) = hi;
-                *reinterpret_cast<uint2*>(qt + at_lo) = lo;
-                if (c == 0) M->q_scale[qb][row] = s;
             }
             if (!F8) cp_async_wait_all();
             fence_proxy_async();
-            mbar_arrive(&M->q_full[qb]);
-        }
-    } else if (warp == 3) {
-        // ---------------- segments
-        if (lane == 0) {
-            Cursor cur;
-            cur.start(pl, M->start_r, M->start_skip, end - begin);
-            Segment s;
-            for (uint32_t k = 0;; ++k) {
-                const int at = k % kSegs;
-                const bool more = cur.next(pl, s);
-                if (!mbar_wait(&M->seg_empty[at], ((k / kSegs) & 1u) ^ 1u, ab)) break;
-                SegInfo& o = M->seg[at];
-                o.rows = more ? s.rows : 0;
-                if (more) {
-                    o.r = s.r;
-                    o.j = s.j;
-                    o.h = s.h;
-                    o.t0 = s.t0;
-                    o.n = s.t1 - s.t0;
-                    o.tiles = s.tiles;
-                    o.keys = s.keys;
-                    o.q = s.q;
-                }
-                mbar_arrive(&M->seg_full[at]);
-                if (!more) break;
-            }
+            q_places(s, [&](int b, uint32_t) { mbar_arrive(&M->q_full[b]); });
+            return true;
+        };
+        bool have = bring(0), after = have && bring(1);
+#pragma unroll 1
+        for (; have; ++nseg) {
+            finish_segment<HD>(p, M->seg[nseg % kSegs], M, tmem, nseg);
+            if (lane == 0) mbar_arrive(&M->seg_empty[nseg % kSegs]);
+            have = after;
+            after = after && bring(nseg + 2);
         }
     } else {
         // ---------------- softmax
         const int u = (warp - 4) >> 2;
-        SoftState st = {0, 0, 0};
+        SoftState st = {0, 0};
+#pragma unroll 1
         for (;; ++nseg) {
             const int at = nseg % kSegs;
-            const bool got = mbar_wait(&M->seg_full[at], (nseg / kSegs) & 1u, ab);
-            // all units agree on whether there is a segment; what the one
-            // before left in shared memory is no longer read
-            if (named_any(5, kUnits * 128, !got)) break;
+            const bool got = wait_bar(&M->seg_full[at], (nseg / kSegs) & 1u, ab);
+            // the unit agrees on whether there is a segment; what the one before
+            // left in its shared memory is no longer read
+            if (named_any(1 + u, 128, !got)) break;
             const SegInfo& s = M->seg[at];
             if (s.rows == 0) break;
-            if (s.rows <= 16)
-                soft_segment<HD, F8, 16>(p, s, M, smem, tmem, u, st);
-            else
-                soft_segment<HD, F8, 32>(p, s, M, smem, tmem, u, st);
+            soft_segment<HD, F8>(p, s, M, smem, tmem, u, st);
             __syncwarp();
             if (lane == 0) mbar_arrive(&M->seg_empty[at]);
         }
@@ -881,7 +1121,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0 && M->wst.abort) raise_status(p.ws, kStatTimeout);
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, C::kTmem);
+        tmem_dealloc(tmem, kTmem);
     }
 }
 
@@ -900,6 +1140,7 @@ __global__ void __launch_bounds__(256) attn_paged_join(const PagedParams p, int 
     if (rho >= (int64_t)q.q_len * pl.group) return;
     auto piece = [&](int i) { return p.part + (size_t)(i == c ? 2 * c + 1 : 2 * i) * piece_floats(HD); };
     float m = kFloorRef;
+#pragma unroll 1
     for (int i = c + lane; i <= d.last; i += 32) m = fmaxf(m, piece(i)[row]);
     m = warp_max(m);
     constexpr int N = HD / 32;

@@ -12,10 +12,14 @@
 
 #include <stdint.h>
 
+// The kernel's loops have to stay small enough for the instruction cache, so
+// what runs once per segment or less is a function of its own there.
 #if defined(__CUDACC__)
 #define DSPARK_HD __host__ __device__ __forceinline__
+#define DSPARK_HD_CALL static __host__ __device__ __noinline__
 #else
 #define DSPARK_HD inline
+#define DSPARK_HD_CALL static inline
 #endif
 
 namespace dspark {
@@ -48,12 +52,12 @@ DSPARK_HD int plan_seen(const PlanInput& p, const Request& q, int64_t rho) {
     return plan_clamp((int64_t)q.kv_len - q.q_len + rho / p.group + 1, q.kv_len);
 }
 // Keys that row tile j reads, and how many key tiles they take.
-DSPARK_HD int plan_tile_keys(const PlanInput& p, const Request& q, int j) {
+DSPARK_HD_CALL int plan_tile_keys(const PlanInput& p, const Request& q, int j) {
     const int64_t rows = (int64_t)q.q_len * p.group, end = (int64_t)(j + 1) * kRowTile;
     return plan_seen(p, q, (end < rows ? end : rows) - 1);
 }
 DSPARK_HD int plan_key_tiles(int keys) { return keys > 0 ? (keys - 1) / kKeyTile + 1 : 1; }
-DSPARK_HD int64_t plan_request_tiles(const PlanInput& p, int r) {
+DSPARK_HD_CALL int64_t plan_request_tiles(const PlanInput& p, int r) {
     const Request q = plan_request(p, r);
     const int n = plan_row_tiles(p, q);
     int64_t sum = 0;
@@ -66,7 +70,7 @@ DSPARK_HD int plan_spans(int64_t total, int grid) { return total < grid ? (int)t
 // First tile of CTA c of n = plan_spans() (c = n: the end).
 DSPARK_HD int64_t plan_cut(int64_t total, int c, int n) { return total / n * c + total % n * c / n; }
 // The CTA whose span holds tile g.
-DSPARK_HD int plan_owner(int64_t total, int64_t g, int n) {
+DSPARK_HD_CALL int plan_owner(int64_t total, int64_t g, int n) {
     int lo = 0, hi = n - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
@@ -82,8 +86,22 @@ struct Segment {
     int t0, t1, tiles;
     int keys;                      // keys the row tile reads
     int rows;                      // rows of the row tile
+    int tok, head;                 // the first row's new token, and its place in the group
     Request q;
 };
+
+// Row x of a row tile whose first row is (tok, head): its new token and its
+// place in the group, in 32 bits.
+DSPARK_HD void plan_row(int group, int tok, int head, int x, int& i, int& g) {
+    const unsigned y = (unsigned)(head + x), d = y / (unsigned)group;
+    i = tok + (int)d;
+    g = (int)(y - d * (unsigned)group);
+}
+// Keys that new token i of a request sees.
+DSPARK_HD int plan_token_keys(const Request& q, int i) {
+    const int64_t n = (int64_t)q.kv_len - q.q_len + i + 1;
+    return (int)(n < 0 ? 0 : n);                                  // i < q_len: at most kv_len
+}
 
 // Walks a span of the line of tiles.
 struct Cursor {
@@ -119,6 +137,8 @@ struct Cursor {
         s.keys = plan_tile_keys(p, q, j);
         s.tiles = plan_key_tiles(s.keys);
         s.rows = (int)(rows < kRowTile ? rows : kRowTile);
+        s.tok = (int)((int64_t)j * kRowTile / p.group);
+        s.head = (int)((int64_t)j * kRowTile - (int64_t)s.tok * p.group);
         s.t0 = t;
         s.t1 = (int)(s.tiles - t < left ? s.tiles : t + left);
         left -= s.t1 - s.t0;

@@ -73,4 +73,13 @@ __device__ __forceinline__ uint2 e4m3x4_to_bf16x4(uint32_t w) {
     return make_uint2(reinterpret_cast<const uint32_t&>(ra), reinterpret_cast<const uint32_t&>(rb));
 }
 
+// Eight e4m3 codes (bytes of a, then of b) as fp16, exactly.
+__device__ __forceinline__ uint4 e4m3x8_to_half8(uint32_t a, uint32_t b) {
+    auto two = [](uint32_t w) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w, __NV_E4M3);
+        return (uint32_t)h.x | ((uint32_t)h.y << 16);
+    };
+    return make_uint4(two(a & 0xFFFFu), two(a >> 16), two(b & 0xFFFFu), two(b >> 16));
+}
+
 }  // namespace dspark

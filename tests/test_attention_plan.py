@@ -74,6 +74,10 @@ int main() {
                 for (int x = 0; x < s.rows; ++x) {
                     const int seen = plan_seen(p, s.q, (int64_t)s.j * kRowTile + x);
                     CHECK(seen >= 0 && seen <= s.keys);
+                    int i, g;
+                    plan_row(group, s.tok, s.head, x, i, g);
+                    CHECK((int64_t)i * group + g == (int64_t)s.j * kRowTile + x && g < group && i < s.q.q_len);
+                    CHECK(plan_token_keys(s.q, i) == seen);
                 }
                 int& d = done[std::make_tuple(s.r, s.j, s.h)];
                 CHECK(d == s.t0);
