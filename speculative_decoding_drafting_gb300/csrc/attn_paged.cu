@@ -123,7 +123,6 @@ struct alignas(16) Misc {
     float qm[kUnits][kUnitRows];       // 2^e of a row's split
     float fac[kUnits][kUnitRows];      // factor of a raised reference
     float red[kUnits][4][kUnitRows];   // per-warp maxima, and sums
-    int lim[kUnits][kUnitRows];        // keys a row sees
     float q_scale[2 * kRowTile];       // 2^e of the Q places' rows
     // what a finished segment hands on, by its parity
     float fin_m[2][kUnits][kUnitRows];
@@ -305,9 +304,6 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
     // this unit's rows (what the segment before left is no longer read)
     if (F8) q_places(sg, [&](int k, uint32_t use) { wait_bar(&M->q_full[k], use & 1u, ab); });
     if (tr < cols) {
-        int i, g;
-        plan_row(p.plan.group, sg.tok, sg.head, coff + tr, i, g);
-        M->lim[u][tr] = coff + tr < sg.rows ? plan_token_keys(sg.q, i) : 0;
         M->ref[u][tr] = kFloorRef;
         M->nref[u][tr] = -kFloorRef;
         if (F8) M->qm[u][tr] = M->q_scale[(sg.qp == 1 ? C::kQRows : 0) + coff + tr];
@@ -327,6 +323,8 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
     for (int i = (stream - sh.stream_at(sg, 0)) & (sh.streams - 1); i < n; i += sh.streams) {
         const int key = (t0 + i) * kKeyTile + tr;
         const bool edge = (t0 + i + 1) * kKeyTile > lim0;     // some row does not see the whole tile
+        // new token k sees the key if kv_len - q_len + k >= key: from this row on
+        const int seen = !edge ? 0 : min(key - sg.q.kv_len + sg.q.q_len - sg.tok, kRowTile + 1) * p.plan.group - sg.head - coff;
         wait_bar(&M->s_full[u], st.tiles & 1u, ab);
         tc_fence_after();
         float mul = scale2, lvs = 0.f, ivs = 1.f;
@@ -350,14 +348,15 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
             ivs = ex2_approx(-lvs);
         }
 
-        // base-2 exponents of the weights of 16 rows, relative to the references
+        constexpr int kCh = F8 ? 8 : 16;                      // what fits the registers
+        // base-2 exponents of the weights of kCh rows, relative to the references
         // (or to 0); the scores stay in tensor memory and are formed again where
         // they are needed again, which takes fewer registers than keeping them
         const uint64_t mul2 = pack2(mul, mul), lvs2 = pack2(lvs, lvs);
-        auto exponents = [&](int c0, const float* nref, float (&t)[16]) {
-            tmem_ldn<16>(tS + (uint32_t)c0, t);
+        auto exponents = [&](int c0, const float* nref, float (&t)[kCh]) {
+            tmem_ldn<kCh>(tS + (uint32_t)c0, t);
 #pragma unroll
-            for (int c = 0; c < 16; c += 2) {
+            for (int c = 0; c < kCh; c += 2) {
                 uint64_t x = pack2(t[c], t[c + 1]);
                 const float2 r = *reinterpret_cast<const float2*>(nref + c0 + c);
                 const uint64_t y = F8 ? add2(pack2(r.x, r.y), lvs2) : pack2(r.x, r.y);
@@ -369,33 +368,33 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
             }
             if (edge) {
 #pragma unroll
-                for (int c = 0; c < 16; ++c)
-                    if (key >= M->lim[u][c0 + c]) t[c] = -INFINITY;
+                for (int c = 0; c < kCh; ++c)
+                    if (c0 + c < seen) t[c] = -INFINITY;
             }
         };
         bool over = false;
 #pragma unroll 1
-        for (int c0 = 0; c0 < cols; c0 += 16) {
-            float t[16];
+        for (int c0 = 0; c0 < cols; c0 += kCh) {
+            float t[kCh];
             exponents(c0, M->nref[u], t);
             float top = t[0];
 #pragma unroll
-            for (int c = 1; c < 16; ++c) top = fmaxf(top, t[c]);
+            for (int c = 1; c < kCh; ++c) top = fmaxf(top, t[c]);
             over |= top > C::kLift + C::kLazy;
         }
         if (named_any(bar, 128, over)) {
             // raise the references to the largest scores so far
 #pragma unroll 1
-            for (int c0 = 0; c0 < cols; c0 += 16) {
-                float t[16];
+            for (int c0 = 0; c0 < cols; c0 += kCh) {
+                float t[kCh];
                 exponents(c0, M->zero, t);
                 float mine = 0.f;
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
+                for (int c = 0; c < kCh; ++c) {
                     const float mx = redux_max(t[c]);
                     if (lane == c) mine = mx;
                 }
-                if (lane < 16) M->red[u][wq][c0 + lane] = mine;
+                if (lane < kCh) M->red[u][wq][c0 + lane] = mine;
             }
             named_sync(bar, 128);
             if (tr < cols) {
@@ -431,30 +430,30 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
         ++st.tiles;
         const uint64_t ivs2 = pack2(ivs, ivs);
 #pragma unroll
-        for (int c0 = 0; c0 < kUnitRows; c0 += 16) {
+        for (int c0 = 0; c0 < kUnitRows; c0 += kCh) {
             if (c0 >= cols) break;
-            float t[16];
+            float t[kCh];
             exponents(c0, M->nref[u], t);
+            uint32_t pk[kCh / 2];
 #pragma unroll
-            for (int c8 = 0; c8 < 2; ++c8) {
-                uint32_t pk[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int k = c8 * 8 + 2 * c, at = (c0 + k) / 2;
-                    const float a = ex2_approx(t[k]), b = ex2_approx(t[k + 1]);
-                    l2[at] = F8 ? fma2(pack2(a, b), ivs2, l2[at]) : add2(l2[at], pack2(a, b));
-                    // weights become 16-bit for the product with V (half a step: bf16
-                    // 2^-9, fp16 2^-12 of the binade); the sums keep them in float32
-                    if (F8) {
-                        const __half2 h = __floats2half2_rn(a, b);
-                        pk[c] = reinterpret_cast<const uint32_t&>(h);
-                    } else {
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-                        pk[c] = reinterpret_cast<const uint32_t&>(h);
-                    }
+            for (int c = 0; c < kCh / 2; ++c) {
+                const float a = ex2_approx(t[2 * c]), b = ex2_approx(t[2 * c + 1]);
+                const int at = c0 / 2 + c;
+                l2[at] = F8 ? fma2(pack2(a, b), ivs2, l2[at]) : add2(l2[at], pack2(a, b));
+                // weights become 16-bit for the product with V (half a step: bf16
+                // 2^-9, fp16 2^-12 of the binade); the sums keep them in float32
+                if (F8) {
+                    const __half2 h = __floats2half2_rn(a, b);
+                    pk[c] = reinterpret_cast<const uint32_t&>(h);
+                } else {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+                    pk[c] = reinterpret_cast<const uint32_t&>(h);
                 }
-                *reinterpret_cast<uint4*>(P + (c0 / 8 + c8) * (kKeyTile * 16) + tr * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
             }
+            uint8_t* dst = P + (c0 / 8) * (kKeyTile * 16) + tr * 16;
+#pragma unroll
+            for (int c = 0; c < kCh / 2; c += 4)
+                *reinterpret_cast<uint4*>(dst + (c / 4) * (kKeyTile * 16)) = make_uint4(pk[c], pk[c + 1], pk[c + 2], pk[c + 3]);
         }
         if constexpr (F8) {
             // Widen V's e4m3 codes, 16 at a time; two units share a wide tile.
@@ -519,6 +518,12 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
     ++st.seg;
 }
 
+// The CTA of the last piece of an item that this CTA's span ends inside of.
+__device__ __noinline__ int join_last(int64_t total, int n, int tiles) {
+    const int spans = plan_spans(total, (int)gridDim.x);
+    return plan_owner(total, plan_cut(total, (int)blockIdx.x + 1, spans) - n + tiles - 1, spans);
+}
+
 // Joins the streams of a finished segment and stores it (128 threads).
 template <int HD>
 __device__ __forceinline__ void finish_segment(const PagedParams& p, const SegInfo& sg, Misc* M, uint32_t tmem,
@@ -568,11 +573,7 @@ __device__ __forceinline__ void finish_segment(const PagedParams& p, const SegIn
             part[kRowTile + tr] = sum;
         }
     }
-    if (tr == 0 && sg.t0 == 0 && !whole) {                    // the last segment of the span
-        const int spans = plan_spans(M->total, (int)gridDim.x);
-        const int64_t last_tile = plan_cut(M->total, (int)blockIdx.x + 1, spans) - n + sg.tiles - 1;
-        p.desc[blockIdx.x] = JoinDesc{sg.r, sg.j, sg.h, plan_owner(M->total, last_tile, spans)};
-    }
+    if (tr == 0 && sg.t0 == 0 && !whole) p.desc[blockIdx.x] = JoinDesc{sg.r, sg.j, sg.h, join_last(M->total, n, sg.tiles)};
     named_sync(5, 128);
     const uint32_t tO = tmem + ((uint32_t)(wq * 32) << 16) + kColO * (1 + parity);
 #pragma unroll 1
@@ -611,7 +612,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_paged_kernel(const __grid_constant__ Maps maps, const PagedParams p) {
     using C = Cfg<HD, F8>;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // an offset, not an address rounded as an integer: the compiler keeps to
+    // shared-memory instructions
+    uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
     Misc* M = reinterpret_cast<Misc*>(smem + C::kOffMisc);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const PlanInput& pl = p.plan;

@@ -13,7 +13,8 @@
 #include <stdint.h>
 
 // The kernel's loops have to stay small enough for the instruction cache, so
-// what runs once per segment or less is a function of its own there.
+// what runs once per segment or less is a function of its own there (its
+// arguments by value: by reference they would live in local memory).
 #if defined(__CUDACC__)
 #define DSPARK_HD __host__ __device__ __forceinline__
 #define DSPARK_HD_CALL static __host__ __device__ __noinline__
@@ -52,12 +53,17 @@ DSPARK_HD int plan_seen(const PlanInput& p, const Request& q, int64_t rho) {
     return plan_clamp((int64_t)q.kv_len - q.q_len + rho / p.group + 1, q.kv_len);
 }
 // Keys that row tile j reads, and how many key tiles they take.
-DSPARK_HD_CALL int plan_tile_keys(const PlanInput& p, const Request& q, int j) {
+DSPARK_HD_CALL int plan_inner_keys(int group, int q_len, int kv_len, int j) {
+    const int64_t n = (int64_t)kv_len - q_len + (((int64_t)(j + 1) * kRowTile - 1) / group) + 1;
+    return plan_clamp(n, kv_len);
+}
+DSPARK_HD int plan_tile_keys(const PlanInput& p, const Request& q, int j) {
     const int64_t rows = (int64_t)q.q_len * p.group, end = (int64_t)(j + 1) * kRowTile;
-    return plan_seen(p, q, (end < rows ? end : rows) - 1);
+    // the last row tile's last row sees every key
+    return end < rows ? plan_inner_keys(p.group, q.q_len, q.kv_len, j) : q.kv_len;
 }
 DSPARK_HD int plan_key_tiles(int keys) { return keys > 0 ? (keys - 1) / kKeyTile + 1 : 1; }
-DSPARK_HD_CALL int64_t plan_request_tiles(const PlanInput& p, int r) {
+DSPARK_HD_CALL int64_t plan_request_tiles(PlanInput p, int r) {
     const Request q = plan_request(p, r);
     const int n = plan_row_tiles(p, q);
     int64_t sum = 0;
@@ -68,7 +74,7 @@ DSPARK_HD_CALL int64_t plan_request_tiles(const PlanInput& p, int r) {
 // since every CTA from an item's first to its last leaves a piece.
 DSPARK_HD int plan_spans(int64_t total, int grid) { return total < grid ? (int)total : grid; }
 // First tile of CTA c of n = plan_spans() (c = n: the end).
-DSPARK_HD int64_t plan_cut(int64_t total, int c, int n) { return total / n * c + total % n * c / n; }
+DSPARK_HD_CALL int64_t plan_cut(int64_t total, int c, int n) { return total / n * c + total % n * c / n; }
 // The CTA whose span holds tile g.
 DSPARK_HD_CALL int plan_owner(int64_t total, int64_t g, int n) {
     int lo = 0, hi = n - 1;

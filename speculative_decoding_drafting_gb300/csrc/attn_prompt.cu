@@ -206,7 +206,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_prompt_kernel(const __grid_constant__ Maps maps, const Params p) {
     using C = Cfg<HD>;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // an offset, not an address rounded as an integer: the compiler keeps to
+    // shared-memory instructions
+    uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
     Misc* M = reinterpret_cast<Misc*>(smem + C::kOffMisc);
     volatile WaitState* ab = &M->wst;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
