@@ -95,7 +95,8 @@ struct Cfg {
     static constexpr int kOffSc = kOffQ + 2 * kQBytes;
     static constexpr int kOffMisc = kOffSc + kSc * kScBytes;
 };
-constexpr uint32_t kColO = kUnits * kUnitRows;                             // TMEM: scores, then two sets of accumulators
+constexpr uint32_t kColO = kUnits * kUnitRows;         // TMEM: scores, two sets of accumulators, scores again
+constexpr uint32_t kColS1 = 3 * kUnits * kUnitRows;
 constexpr uint32_t kTmem = 512;
 constexpr int kThreads = 32 * (8 + 4 * kUnits);
 constexpr uint32_t kReaders = 8 + 4 * kUnits;                              // arrivals that free a segment's place
@@ -117,7 +118,6 @@ struct SegInfo {
 struct alignas(16) Misc {
     SegInfo seg[kSegs];
     uint64_t seg_full[kSegs], seg_empty[kSegs];
-    float zero[kUnitRows];
     float ref[kUnits][kUnitRows];      // reference of a row
     float nref[kUnits][kUnitRows];     // kLift minus it
     float qm[kUnits][kUnitRows];       // 2^e of a row's split
@@ -138,8 +138,9 @@ struct alignas(16) Misc {
     uint64_t w_empty[3];               // widened V tiles (p_full says that one is made)
     uint64_t c_full[4], c_empty[4];    // scales
     uint64_t q_full[2], q_empty[2];
-    uint64_t s_full[kUnits], p_full[kUnits], pv_done[kUnits];
+    uint64_t s_full[2][kUnits], s_free[2][kUnits], p_full[kUnits], pv_done[kUnits];
     uint64_t o_done[2], l_done[2], e_free[2];   // a segment's accumulators, its sums; both read
+    uint64_t r_done;                   // all products before a change of shape
     uint64_t done;
 };
 
@@ -197,11 +198,17 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
     return mbar_test(bar, parity) || wait_on(smem_u32(bar), parity, w);
 }
 
-// Sums over the 32 lanes of 32 values per lane; lane i gets the sum of value i.
+// Sums over the 32 lanes of the first N = 16 or 32 values per lane; lane i gets
+// the sum of value i % N.
+template <int N>
 __device__ __forceinline__ float lane_sums(float (&x)[32]) {
     const int lane = threadIdx.x & 31;
+    if constexpr (N == 16) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+        for (int i = 0; i < 16; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], 16);
+    }
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) {
         const bool up = lane & o;
 #pragma unroll
         for (int i = 0; i < o; ++i) {
@@ -271,6 +278,10 @@ struct Shape {
     __device__ __forceinline__ int stream_at(const SegInfo& s, int i) const {
         return (int)((s.line - s.run + (uint32_t)i) & (uint32_t)(streams - 1));
     }
+    // which of its two score tiles that stream uses for it
+    __device__ __forceinline__ uint32_t turn_at(const SegInfo& s, int i) const {
+        return ((s.line - s.run + (uint32_t)i) >> (wide ? 1 : 2)) & 1u;
+    }
     __device__ __forceinline__ int stream_of(int unit) const { return wide ? unit >> 1 : unit; }
     // first TMEM column of a stream's scores, and of its accumulator in a set
     __device__ __forceinline__ uint32_t column(int stream) const { return (uint32_t)stream * (wide ? 64u : 32u); }
@@ -279,6 +290,7 @@ struct Shape {
 // ------------------------------------------------------------------ softmax
 struct SoftState {
     uint32_t tiles;                    // key tiles this unit has taken
+    uint32_t phases;                   // parity of the next wait for each of its score tiles, by bit
     uint32_t seg;                      // segments so far
 };
 
@@ -297,7 +309,7 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
     const int bar = 1 + u, parity = st.seg & 1;
     const int stream = sh.stream_of(u), coff = sh.wide ? (u & 1) * kUnitRows : 0;
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
-    const uint32_t tS = tmem + lanes + (uint32_t)(u * kUnitRows);
+    const uint32_t tS0 = tmem + lanes + (uint32_t)(u * kUnitRows);
     const uint32_t tO = tmem + lanes + kColO * (1 + parity) + (uint32_t)(u * kUnitRows);
     uint8_t* P = smem + C::kOffP + u * C::kPBytes;
 
@@ -311,9 +323,7 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
     named_sync(bar, 128);
     if (F8 && lane == 0) q_places(sg, [&](int k, uint32_t) { mbar_arrive(&M->q_empty[k]); });   // the row scales are copied
 
-    uint64_t l2[kUnitRows / 2];
-#pragma unroll
-    for (int c = 0; c < kUnitRows / 2; ++c) l2[c] = 0;
+    float l = 0.f;                                            // this warp's sum of row `lane`
     const int lim0 = plan_token_keys(sg.q, sg.tok);           // the first row sees the fewest keys
     const int n = sg.n, t0 = sg.t0;
     const uint32_t line = sg.line;
@@ -325,8 +335,11 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
         const bool edge = (t0 + i + 1) * kKeyTile > lim0;     // some row does not see the whole tile
         // new token k sees the key if kv_len - q_len + k >= key: from this row on
         const int seen = !edge ? 0 : min(key - sg.q.kv_len + sg.q.q_len - sg.tok, kRowTile + 1) * p.plan.group - sg.head - coff;
-        wait_bar(&M->s_full[u], st.tiles & 1u, ab);
+        const uint32_t turn = sh.turn_at(sg, i);
+        wait_bar(&M->s_full[turn][u], (st.phases >> turn) & 1u, ab);
+        st.phases ^= 1u << turn;
         tc_fence_after();
+        const uint32_t tS = tS0 + (turn ? kColS1 : 0u);
         float mul = scale2, lvs = 0.f, ivs = 1.f;
         if (F8) {
             // (the scores waited for the copy of these scales to be asked for)
@@ -348,53 +361,52 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
             ivs = ex2_approx(-lvs);
         }
 
-        constexpr int kCh = F8 ? 8 : 16;                      // what fits the registers
-        // base-2 exponents of the weights of kCh rows, relative to the references
-        // (or to 0); the scores stay in tensor memory and are formed again where
-        // they are needed again, which takes fewer registers than keeping them
+        // base-2 exponents of the weights, relative to the references
+        float t[kUnitRows];
         const uint64_t mul2 = pack2(mul, mul), lvs2 = pack2(lvs, lvs);
-        auto exponents = [&](int c0, const float* nref, float (&t)[kCh]) {
-            tmem_ldn<kCh>(tS + (uint32_t)c0, t);
-#pragma unroll
-            for (int c = 0; c < kCh; c += 2) {
-                uint64_t x = pack2(t[c], t[c + 1]);
-                const float2 r = *reinterpret_cast<const float2*>(nref + c0 + c);
-                const uint64_t y = F8 ? add2(pack2(r.x, r.y), lvs2) : pack2(r.x, r.y);
-                if (F8) {
-                    const float2 qm = *reinterpret_cast<const float2*>(&M->qm[u][c0 + c]);
-                    x = mul2x(x, pack2(qm.x, qm.y));
-                }
-                unpack2(fma2(x, mul2, y), t[c], t[c + 1]);
-            }
-            if (edge) {
-#pragma unroll
-                for (int c = 0; c < kCh; ++c)
-                    if (c0 + c < seen) t[c] = -INFINITY;
-            }
-        };
-        bool over = false;
 #pragma unroll 1
-        for (int c0 = 0; c0 < cols; c0 += kCh) {
-            float t[kCh];
-            exponents(c0, M->nref[u], t);
-            float top = t[0];
+        for (bool raised = false;; raised = true) {
+            float top = -INFINITY;
 #pragma unroll
-            for (int c = 1; c < kCh; ++c) top = fmaxf(top, t[c]);
-            over |= top > C::kLift + C::kLazy;
-        }
-        if (named_any(bar, 128, over)) {
-            // raise the references to the largest scores so far
-#pragma unroll 1
-            for (int c0 = 0; c0 < cols; c0 += kCh) {
-                float t[kCh];
-                exponents(c0, M->zero, t);
-                float mine = 0.f;
+            for (int c0 = 0; c0 < kUnitRows; c0 += 16) {
+                if (c0 >= cols) break;
+                float x[16];
+                tmem_ldn<16>(tS + (uint32_t)c0, x);
 #pragma unroll
-                for (int c = 0; c < kCh; ++c) {
-                    const float mx = redux_max(t[c]);
-                    if (lane == c) mine = mx;
+                for (int c = 0; c < 16; c += 2) {
+                    uint64_t y = pack2(x[c], x[c + 1]);
+                    const float2 r = *reinterpret_cast<const float2*>(&M->nref[u][c0 + c]);
+                    if (F8) {
+                        const float2 qm = *reinterpret_cast<const float2*>(&M->qm[u][c0 + c]);
+                        y = fma2(mul2x(y, pack2(qm.x, qm.y)), mul2, add2(pack2(r.x, r.y), lvs2));
+                    } else {
+                        y = fma2(y, mul2, pack2(r.x, r.y));
+                    }
+                    unpack2(y, t[c0 + c], t[c0 + c + 1]);
                 }
-                if (lane < kCh) M->red[u][wq][c0 + lane] = mine;
+                if (edge) {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        if (c0 + c < seen) t[c0 + c] = -INFINITY;
+                }
+#pragma unroll
+                for (int c = 0; c < 16; ++c) top = fmaxf(top, t[c0 + c]);
+            }
+            // (raised once: scores of 2^28 and more round by more than the threshold)
+            if (raised || !named_any(bar, 128, top > C::kLift + C::kLazy)) break;
+            // one is too large: raise the references to the largest scores so far
+#pragma unroll 1
+            for (int c0 = 0; c0 < cols; c0 += 4) {
+                float x[4], mine = 0.f;
+                tmem_ldn<4>(tS + (uint32_t)c0, x);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float y = fmaf(F8 ? x[c] * M->qm[u][c0 + c] : x[c], mul, lvs);
+                    if (c0 + c < seen) y = -INFINITY;
+                    y = redux_max(y);
+                    if (lane == c) mine = y;
+                }
+                if (lane < 4) M->red[u][wq][c0 + lane] = mine;
             }
             named_sync(bar, 128);
             if (tr < cols) {
@@ -406,40 +418,37 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
                 M->fac[u][tr] = ex2_approx(old - ref);
             }
             named_sync(bar, 128);
-#pragma unroll
-            for (int c = 0; c < kUnitRows; c += 2) {
-                const float2 f = *reinterpret_cast<const float2*>(&M->fac[u][c]);
-                l2[c / 2] = mul2x(l2[c / 2], pack2(f.x, f.y));
-            }
+            if (lane < cols) l *= M->fac[u][lane];
             if (i >= sh.streams) {                            // the accumulator holds earlier tiles
                 wait_bar(&M->pv_done[u], (st.tiles - 1u) & 1u, ab);
                 tc_fence_after();
 #pragma unroll 1
-                for (int c0 = 0; c0 < cols; c0 += 16) {
-                    float o[16];
-                    tmem_ldn<16>(tO + c0, o);
+                for (int c0 = 0; c0 < cols; c0 += 8) {
+                    float o[8];
+                    tmem_ldn<8>(tO + c0, o);
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) o[c] *= M->fac[u][c0 + c];
-                    tmem_st16(tO + c0, o);
+                    for (int c = 0; c < 8; ++c) o[c] *= M->fac[u][c0 + c];
+                    tmem_st8(tO + c0, reinterpret_cast<const uint32_t(&)[8]>(o));
                 }
                 tmem_st_wait();
             }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&M->s_free[turn][u]);
         // the P buffer is free once this unit's previous product is done
         if (st.tiles > 0) wait_bar(&M->pv_done[u], (st.tiles - 1u) & 1u, ab);
         ++st.tiles;
-        const uint64_t ivs2 = pack2(ivs, ivs);
 #pragma unroll
-        for (int c0 = 0; c0 < kUnitRows; c0 += kCh) {
+        for (int c0 = 0; c0 < kUnitRows; c0 += 16) {
             if (c0 >= cols) break;
-            float t[kCh];
-            exponents(c0, M->nref[u], t);
-            uint32_t pk[kCh / 2];
+            uint32_t pk[8];
 #pragma unroll
-            for (int c = 0; c < kCh / 2; ++c) {
-                const float a = ex2_approx(t[2 * c]), b = ex2_approx(t[2 * c + 1]);
-                const int at = c0 / 2 + c;
-                l2[at] = F8 ? fma2(pack2(a, b), ivs2, l2[at]) : add2(l2[at], pack2(a, b));
+            for (int c = 0; c < 8; ++c) {
+                float& a = t[c0 + 2 * c];
+                float& b = t[c0 + 2 * c + 1];
+                a = ex2_approx(a);
+                b = ex2_approx(b);
                 // weights become 16-bit for the product with V (half a step: bf16
                 // 2^-9, fp16 2^-12 of the binade); the sums keep them in float32
                 if (F8) {
@@ -451,9 +460,8 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
                 }
             }
             uint8_t* dst = P + (c0 / 8) * (kKeyTile * 16) + tr * 16;
-#pragma unroll
-            for (int c = 0; c < kCh / 2; c += 4)
-                *reinterpret_cast<uint4*>(dst + (c / 4) * (kKeyTile * 16)) = make_uint4(pk[c], pk[c + 1], pk[c + 2], pk[c + 3]);
+            *reinterpret_cast<uint4*>(dst) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            *reinterpret_cast<uint4*>(dst + kKeyTile * 16) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
         }
         if constexpr (F8) {
             // Widen V's e4m3 codes, 16 at a time; two units share a wide tile.
@@ -498,14 +506,22 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&M->p_full[u]);
+        // the weights' sums (over w / scale for e4m3), while the product runs: a
+        // row's sum in one lane, since a sum per row and thread would not fit
+        // the registers
+        if (F8) {
+#pragma unroll
+            for (int c = 0; c < kUnitRows; ++c) t[c] *= ivs;
+        }
+        if (cols > 16)
+            l += lane_sums<32>(t);
+        else
+            l += lane_sums<16>(t);
     }
 
     // hand the sums on; the segment before the last has been read
     {
-        float x[kUnitRows];
-#pragma unroll
-        for (int c = 0; c < kUnitRows; c += 2) unpack2(l2[c / 2], x[c], x[c + 1]);
-        M->red[u][wq][lane] = lane_sums(x);
+        M->red[u][wq][lane] = l;
         wait_bar(&M->e_free[parity], ((st.seg >> 1) & 1u) ^ 1u, ab);
         named_sync(bar, 128);
         if (tr < cols) {
@@ -660,7 +676,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll 1
         for (int i = 0; i < kUnits; ++i) {
-            mbar_init(&M->s_full[i], 1);
+            mbar_init(&M->s_full[0][i], 1);
+            mbar_init(&M->s_full[1][i], 1);
+            mbar_init(&M->s_free[0][i], 4);
+            mbar_init(&M->s_free[1][i], 4);
             mbar_init(&M->p_full[i], 4);
             mbar_init(&M->pv_done[i], 1);
         }
@@ -675,9 +694,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&M->l_done[i], 4 * kUnits);
             mbar_init(&M->e_free[i], 4);
         }
+        mbar_init(&M->r_done, 1);
         mbar_init(&M->done, 2);
-#pragma unroll 1
-        for (int i = 0; i < kUnitRows; ++i) M->zero[i] = 0.f;
         M->wst.abort = 0;
         M->wst.limit = ws_wait_limit(p.ws);
         fence_mbar_init();
@@ -858,24 +876,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t dk = F8 ? desc_f8<HD>(smem) : smem_desc_sw128(smem, 16, 1024);
         const uint64_t dq = F8 ? desc_f8<HD>(smem + C::kOffQ) : smem_desc_sw128(smem + C::kOffQ, 16, 1024);
         uint32_t ks = 0, kph = 0;
-        uint32_t made = 0, owed = 0;   // by unit: parity of its next p_full, and whether one is outstanding
-        uint32_t run = 0;
+        uint32_t free_ph = 0xFFu;      // by score tile (turn, unit): parity of its next s_free
+        uint32_t run = 0, runs = 0;
         auto wait = [&](uint64_t* bar, uint32_t par) { ok = ok && __all_sync(0xffffffffu, wait_bar(bar, par, ab)); };
-        uint32_t used = 0;             // units that have had a tile
-        // waits for the outstanding weights of some units (done: and for their products)
-        auto settle = [&](uint32_t units, bool done) {
-#pragma unroll 1
-            for (int u = 0; u < kUnits; ++u) {
-                const uint32_t bit = 1u << u;
-                if (!(units & used & bit)) continue;
-                if (owed & bit) {
-                    wait(&M->p_full[u], (made >> u) & 1u);
-                    made ^= bit;
-                    owed ^= bit;
-                }
-                // pv_done's phases follow p_full's one by one
-                if (done) wait(&M->pv_done[u], ((made >> u) & 1u) ^ 1u);
-            }
+        auto give = [&](int u, uint32_t turn) {
+            wait(&M->s_free[turn][u], (free_ph >> (4 * turn + u)) & 1u);
+            free_ph ^= 1u << (4 * turn + u);
         };
 #pragma unroll 1
         for (; ok && next_segment(); done_segment()) {
@@ -884,21 +890,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t b = dq + (sg.qp == 1 ? C::kQBytes / 16 : 0);
             // rows between Q's halves along head_dim (bf16), or between hi and lo
             const int q_rows = sg.qp == 2 ? 2 * C::kQRows : C::kQRows;
-            if (sg.run != run) settle(15u, true);             // columns and buffers change hands
-            run = sg.run;
+            if (sg.run != run) {
+                // columns and buffers change hands: all products so far are done
+                wait(&M->r_done, runs++ & 1u);
+                run = sg.run;
+            }
             q_places(sg, [&](int k, uint32_t use) { wait(&M->q_full[k], use & 1u); });
 #pragma unroll 1
             for (int i = 0; ok && i < sg.n; ++i) {
                 const int st = sh.stream_at(sg, i);
-                const uint32_t units = sh.wide ? 3u << (2 * st) : 1u << st;
-                settle(units, false);
-                owed |= units;
-                used |= units;
+                const int u0 = sh.wide ? 2 * st : st;
+                const uint32_t turn = sh.turn_at(sg, i);
+                give(u0, turn);
+                if (sh.wide) give(u0 + 1, turn);
                 wait(&M->k_full[ks], kph);
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint32_t d = tmem + sh.column(st);
+                    const uint32_t d = tmem + sh.column(st) + (turn ? kColS1 : 0u);
                     const uint64_t a = dk + ks * (C::kLoadBytes / 16);
                     if (F8) {
 #pragma unroll
@@ -911,8 +920,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             umma_bf16(d, a + (kk / 4) * (C::kHalfBytes / 16) + (kk % 4) * 2,
                                       b + (uint32_t)((kk / 4) * (q_rows * 8) + (kk % 4) * 2), id, kk ? 1u : 0u);
                     }
-                    umma_commit(&M->s_full[sh.wide ? 2 * st : st]);
-                    if (sh.wide) umma_commit(&M->s_full[2 * st + 1]);
+                    umma_commit(&M->s_full[turn][u0]);
+                    if (sh.wide) umma_commit(&M->s_full[turn][u0 + 1]);
                     umma_commit(&M->k_empty[ks]);
                     if (i == sg.n - 1) q_places(sg, [&](int k, uint32_t) { umma_commit(&M->q_empty[k]); });
                 }
@@ -930,7 +939,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t a_lbo = HD == 128 ? C::kHalfBytes : 0;   // head_dim 64: rows 64..127 repeat 0..63
         const uint64_t dv = smem_desc_sw128(smem + (F8 ? C::kOffW : C::kOffV), a_lbo, 1024);
         const uint64_t dp = smem_desc_plain(smem + C::kOffP, 128, kKeyTile * 16);
-        uint32_t vs = 0, vph = 0, ws = 0;
+        uint32_t vs = 0, vph = 0, ws = 0, run = 0;
         uint32_t made = 0;                                    // parity of each unit's next p_full, by bit
         auto wait = [&](uint64_t* bar, uint32_t par) { ok = ok && __all_sync(0xffffffffu, wait_bar(bar, par, ab)); };
 #pragma unroll 1
@@ -938,6 +947,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Shape sh(sg.rows);
             const uint32_t id = F8 ? idesc_f16_f32(128, sh.cols, true, true) : idesc_bf16_f32(128, sh.cols, true, true);
             const uint32_t set = tmem + kColO * (1u + (nseg & 1u));
+            if (sg.run != run && elect_one()) umma_commit(&M->r_done);
+            __syncwarp();
+            run = sg.run;
 #pragma unroll 1
             for (int i = 0; ok && i < sg.n; ++i) {
                 const int st = sh.stream_at(sg, i), u0 = sh.wide ? 2 * st : st;
@@ -1104,7 +1116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ---------------- softmax
         const int u = (warp - 4) >> 2;
-        SoftState st = {0, 0};
+        SoftState st = {0, 0, 0};
 #pragma unroll 1
         for (;; ++nseg) {
             const int at = nseg % kSegs;
