@@ -1003,7 +1003,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp == 2) {
-        // ---------------- segments and V tiles: whatever can go on
+        // ---------------- segments and V tiles
         Cursor cur;
         cur.start(pl, M->start_r, M->start_skip, end - begin);
         uint32_t made = 0, line = 0, run = 0;                 // segments listed, their key tiles
@@ -1011,13 +1011,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         int place = 0;                                        // the next Q place
         uint32_t use = 0;
         Place c = {};
-        bool v_in = false;                                    // c stands in a segment
-        uint64_t t0 = sm_cycles();
-        auto test = [&](uint64_t* bar, uint32_t par) { return __all_sync(0xffffffffu, mbar_test(bar, par)) != 0; };
-#pragma unroll 1
         for (;;) {
-            bool moved = false;
-            if (more && test(&M->seg_empty[made % kSegs], ((made / kSegs) & 1u) ^ 1u)) {
+            // before each segment's tiles, list it and those after it that there is
+            // room for (the others never need more to get through this one)
+#pragma unroll 1
+            while (more) {
+                uint64_t* bar = &M->seg_empty[made % kSegs];
+                const uint32_t par = ((made / kSegs) & 1u) ^ 1u;
+                if (made == c.seg)
+                    ok = __all_sync(0xffffffffu, wait_bar(bar, par, ab));
+                else if (!__all_sync(0xffffffffu, mbar_test(bar, par)))
+                    break;
+                if (!ok) break;
                 Segment s;
                 more = cur.next(pl, s);
                 if (more && Shape(s.rows).wide != wide) {
@@ -1039,30 +1044,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 use &= 0x7FFF7FFFu;                           // parities are what counts
                 if (!both) place ^= 1;
                 ++made;
-                moved = true;
             }
-            if (!v_in && c.seg < made) {
-                enter(c);
-                v_in = c.more;
-            }
-            if (v_in && test(&M->v_empty[c.slot], c.phase ^ 1u)) {
+            if (!ok) break;
+            enter(c);
+            if (!c.more) break;
+            bool last = false;
+#pragma unroll 1
+            while (ok && !last) {
                 load(std::true_type{}, c, page_of(c));
-                if (!ok) break;
-                const uint32_t seg = c.seg;
-                if (step(c)) {
-                    if (lane == 0) mbar_arrive(&M->seg_empty[seg % kSegs]);
-                    v_in = false;
-                }
-                moved = true;
-            } else if (!more && !v_in && c.seg + 1 >= made) {
-                break;                                        // the last segment is loaded, its end listed
+                last = step(c);
             }
-            // bounded: give up when nothing moves for the wait limit
-            if (moved)
-                t0 = sm_cycles();
-            else if (sm_cycles() - t0 > ab->limit)
-                ab->abort = 1;
-            if (__any_sync(0xffffffffu, ab->abort != 0)) break;
+            if (!ok) break;
+            if (lane == 0) mbar_arrive(&M->seg_empty[(c.seg - 1) % kSegs]);
         }
         drain(M->v_full, C::kV, c.count);
     } else if (warp >= 4 + 4 * kUnits) {
