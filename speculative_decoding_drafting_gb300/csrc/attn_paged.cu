@@ -1176,7 +1176,7 @@ __global__ void __launch_bounds__(256) attn_paged_join(const PagedParams p, int 
 template <int HD, bool F8>
 cudaError_t launch(const Maps& maps, const PagedParams& p, int grid, cudaStream_t s) {
     const size_t smem = smem_bytes<HD, F8>();
-    cudaError_t e = cudaFuncSetAttribute(attn_paged_kernel<HD, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(attn_paged_kernel<HD, F8>, smem);
     if (e != cudaSuccess) return e;
     prof_begin(kPAttnPaged, s);
     e = launch_kernel(attn_paged_kernel<HD, F8>, dim3(grid), dim3(kThreads), smem, s, false, maps, p);

@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int HD>
 cudaError_t launch(const Maps& maps, const Params& p, cudaStream_t s) {
     const size_t smem = smem_bytes<HD>();
-    cudaError_t e = cudaFuncSetAttribute(attn_prompt_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(attn_prompt_kernel<HD>, smem);
     if (e != cudaSuccess) return e;
     prof_begin(kPAttnPromptPlan, s);
     e = launch_kernel(attn_prompt_plan, dim3(1), dim3(kPlanThreads), 0, s, false, p, const_cast<int2*>(p.list),

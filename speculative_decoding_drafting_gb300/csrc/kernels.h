@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/dspark.h"
 
 namespace dspark {
@@ -161,6 +163,28 @@ __host__ __device__ inline int gru_ldzb(int r, int d) { return (4 * r + d + 63) 
 int gru_tc_parts(int R, int r, int d);
 bool gru_tc_supported(const DraftArgs& a);
 cudaError_t launch_gru_tc(DraftArgs& a, int k, cudaStream_t s);
+
+// Let `kern` use `bytes` of dynamic shared memory; asked of the runtime once per
+// kernel and device (up to 64 devices).
+template <typename... KArgs>
+cudaError_t allow_smem(void (*kern)(KArgs...), size_t bytes) {
+    static std::atomic<const void*> done[64][8];             // kernels of this signature, per device
+    int dev = 0;
+    const cudaError_t g = cudaGetDevice(&dev);
+    if (g != cudaSuccess) return g;
+    const void* f = reinterpret_cast<const void*>(kern);
+    for (int i = 0; dev < 64 && i < 8; ++i) {
+        const void* have = done[dev][i].load(std::memory_order_acquire);
+        if (have == f) return cudaSuccess;
+        if (!have) break;
+    }
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    for (int i = 0; e == cudaSuccess && dev < 64 && i < 8; ++i) {
+        const void* none = nullptr;
+        if (done[dev][i].compare_exchange_strong(none, f, std::memory_order_acq_rel) || none == f) break;
+    }
+    return e;
+}
 
 // Launch `kern` on `s`.  With `pdl` set the launch may begin while the
 // previous kernel in the stream is still running (programmatic dependent
