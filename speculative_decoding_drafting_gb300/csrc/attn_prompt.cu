@@ -246,122 +246,170 @@ __global__ void __launch_bounds__(kThreads, 1)
     Item it;
 
     if (warp == 0) {
-        // ---------------- producer (one thread)
-        if (lane == 0) {
-            const uint64_t pol_q = policy_evict_first(), pol_kv = policy_evict_last();
-            uint32_t g = 0, nq[2] = {0, 0};
-            bool ok = true;
-            auto tile = [&](const CUtensorMap* m, int j) {
-                const int st = (int)(g % C::kStages);
-                ok = ok && mbar_wait(&M->empty[st], ((g / C::kStages) & 1u) ^ 1u, ab);
-                if (!ok) return;
+        // ---------------- producer
+        const uint64_t pol_q = policy_evict_first(), pol_kv = policy_evict_last();
+        uint32_t g = 0, st = 0, ph = 0, nq[2] = {0, 0};       // tiles issued; the next ring place and its phase
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, ab)); };
+        auto tile = [&](const CUtensorMap* m, int j) {
+            wait(&M->empty[st], ph ^ 1u);
+            if (!ok) return;
+            if (elect_one()) {
                 mbar_expect_tx(&M->full[st], (uint32_t)C::kTileBytes);
+#pragma unroll
                 for (int hf = 0; hf < C::kHalves; ++hf)
                     tma_load_3d(smem + st * C::kTileBytes + hf * C::kHalfBytes, m, &M->full[st], hf * 64, it.h,
                                 it.a + j * kKeys, pol_kv);
-                ++g;
-            };
-            auto query = [&](int s) {
-                if (!it.n[s]) return;
-                ok = ok && mbar_wait(&M->q_empty[s], (nq[s] & 1u) ^ 1u, ab);
-                if (!ok) return;
-                ++nq[s];
+            }
+            __syncwarp();
+            ++g;
+            if (++st == C::kStages) {
+                st = 0;
+                ph ^= 1u;
+            }
+        };
+        auto query = [&](int s) {
+            if (!it.n[s]) return;
+            wait(&M->q_empty[s], (nq[s] & 1u) ^ 1u);
+            if (!ok) return;
+            ++nq[s];
+            if (elect_one()) {
                 mbar_expect_tx(&M->q_full[s], (uint32_t)(p.toks * p.group * HD * 2));
+#pragma unroll
                 for (int hf = 0; hf < C::kHalves; ++hf)
                     tma_load_3d(smem + C::kOffQ + s * C::kTileBytes + hf * C::kHalfBytes, &maps.q, &M->q_full[s], hf * 64,
                                 it.h * p.group, it.a + it.tok0 + s * p.toks, pol_q);
-            };
-            for (int round = 0; ok && get_item(p, total, round, it); ++round) {
-                const int n = max(it.n[0], it.n[1]);
-                query(0);
-                tile(&maps.k, 0);
-                query(1);
-                tile(&maps.v, 0);
-                for (int j = 1; ok && j < n; ++j) {
-                    tile(&maps.k, j);
-                    tile(&maps.v, j);
-                }
             }
-            // copies in flight land before the CTA may leave
-            if (ab->abort) {
-                for (uint32_t k = g > C::kStages ? g - C::kStages : 0; k < g; ++k)
-                    mbar_wait_for(&M->full[k % C::kStages], (k / C::kStages) & 1u, ab->limit);
-                for (int s = 0; s < 2; ++s)
-                    if (nq[s]) mbar_wait_for(&M->q_full[s], (nq[s] - 1u) & 1u, ab->limit);
+            __syncwarp();
+        };
+#pragma unroll 1
+        for (int round = 0; ok && get_item(p, total, round, it); ++round) {
+            const int n = max(it.n[0], it.n[1]);
+            query(0);
+            tile(&maps.k, 0);
+            query(1);
+#pragma unroll 1
+            for (int j = 0; ok && j < n; ++j) {
+                if (j) tile(&maps.k, j);
+                tile(&maps.v, j);
             }
         }
+        // copies in flight land before the CTA may leave
+        if (ab->abort && lane == 0) {
+            for (uint32_t k = g > C::kStages ? g - C::kStages : 0; k < g; ++k)
+                mbar_wait_for(&M->full[k % C::kStages], (k / C::kStages) & 1u, ab->limit);
+            for (int s = 0; s < 2; ++s)
+                if (nq[s]) mbar_wait_for(&M->q_full[s], (nq[s] - 1u) & 1u, ab->limit);
+        }
+        __syncwarp();
     } else if (warp == 1) {
-        // ---------------- MMA issuer (one thread)
-        if (lane == 0) {
-            constexpr uint32_t id_qk = idesc_bf16_f32(128, 128, false, false);
-            constexpr uint32_t id_pv = idesc_bf16_f32(128, HD, false, true);
-            uint32_t g = 0, nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0}, nfix = 0;
-            bool ok = true;
-            auto wait = [&](uint64_t* bar, uint32_t parity) {
-                ok = ok && mbar_wait(bar, parity, ab);
-                tc_fence_after();
-                return ok;
-            };
-            auto scores = [&](int s, uint32_t at) {
-                const uint8_t* qt = smem + C::kOffQ + s * C::kTileBytes;
-                const uint8_t* kt = smem + (at % C::kStages) * C::kTileBytes;
+        // ---------------- MMA issuer
+        constexpr uint32_t id_qk = idesc_bf16_f32(128, 128, false, false);
+        constexpr uint32_t id_pv = idesc_bf16_f32(128, HD, false, true);
+        // descriptors of the first Q and ring tiles; others lie a constant number
+        // of 16-byte units on (addresses stay inside the 14-bit field)
+        const uint64_t dq = smem_desc_sw128(smem + C::kOffQ, 16, 1024);
+        const uint64_t dk = smem_desc_sw128(smem, 16, 1024);
+        const uint64_t dv = smem_desc_sw128(smem, C::kHalfBytes, 1024);
+        uint32_t nq = 0, np = 0, no = 0, started = 0, nfix = 0;   // parities of the next waits, by row tile's bit
+        uint32_t st = 0, ph = 0;                              // ring place of the next tile, and its phase
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, ab));
+            tc_fence_after();
+            return ok;
+        };
+        auto next = [&](uint32_t& at, uint32_t& phase) {
+            if (++at == C::kStages) {
+                at = 0;
+                phase ^= 1u;
+            }
+        };
+        auto scores = [&](int s, uint32_t at, bool last) {
+            if (elect_one()) {
+                const uint64_t a = dq + s * (C::kTileBytes / 16), b = dk + at * (C::kTileBytes / 16);
 #pragma unroll
                 for (int kk = 0; kk < HD / 16; ++kk) {
-                    const int off = (kk / 4) * C::kHalfBytes + (kk % 4) * 32;
-                    umma_bf16(tmem + (uint32_t)(s * 128), smem_desc_sw128(qt + off, 16, 1024),
-                              smem_desc_sw128(kt + off, 16, 1024), id_qk, kk ? 1u : 0u);
+                    const uint32_t off = (kk / 4) * (C::kHalfBytes / 16) + (kk % 4) * 2;
+                    umma_bf16(tmem + (uint32_t)(s * 128), a + off, b + off, id_qk, kk ? 1u : 0u);
                 }
                 umma_commit(&M->s_full[s]);
-            };
-            auto product = [&](int s, uint32_t at, bool first) {
-                const uint8_t* vt = smem + (at % C::kStages) * C::kTileBytes;
+                if (last) umma_commit(&M->q_empty[s]);
+            }
+            __syncwarp();
+        };
+        auto product = [&](int s, uint32_t at, bool first) {
+            if (elect_one()) {
+                const uint64_t b = dv + at * (C::kTileBytes / 16);
+                const uint32_t d = tmem + (uint32_t)(256 + s * HD), a = tmem + (uint32_t)(s * 128);
 #pragma unroll
                 for (int kk = 0; kk < kKeys / 16; ++kk)
-                    umma_bf16_ts(tmem + (uint32_t)(256 + s * HD), tmem + (uint32_t)(s * 128 + kk * 8),
-                                 smem_desc_sw128(vt + kk * 2048, C::kHalfBytes, 1024), id_pv, (!first || kk) ? 1u : 0u);
+                    umma_bf16_ts(d, a + kk * 8, b + kk * 128, id_pv, (!first || kk) ? 1u : 0u);
                 umma_commit(&M->pv_done[s]);
-            };
-            for (int round = 0; ok && get_item(p, total, round, it); ++round) {
-                const int n = max(it.n[0], it.n[1]);
-                // ring entries of this item: K_j at g + 2 j, V_j at g + 2 j + 1
-                if (!wait(&M->full[g % C::kStages], (g / C::kStages) & 1u)) break;
+            }
+            __syncwarp();
+        };
+#pragma unroll 1
+        for (int round = 0; ok && get_item(p, total, round, it); ++round) {
+            const int n = max(it.n[0], it.n[1]);
+            uint32_t kat = st, kph = ph;                      // K_j's place; V_j's is the next
+            if (!wait(&M->full[kat], kph)) break;
+#pragma unroll 1
+            for (int s = 0; ok && s < 2; ++s) {
+                if (!it.n[s]) continue;
+                if (!wait(&M->q_full[s], (nq >> s) & 1u)) break;
+                nq ^= 1u << s;
+                scores(s, kat, it.n[s] == 1);
+            }
+            if (!ok) break;
+            if (elect_one()) umma_commit(&M->empty[kat]);
+            __syncwarp();
+            next(st, ph);
+#pragma unroll 1
+            for (int j = 0; ok && j < n; ++j) {
+                const uint32_t vat = st;
+                if (!wait(&M->full[vat], ph)) break;
+                next(st, ph);
+                kat = st;
+                kph = ph;
+                if (j + 1 < n) next(st, ph);
+                bool fix = j == n - 1 && it.keys - j * kKeys < kKeys;
+                if (fix && lane == 0) mbar_arrive(&M->fix);   // warps 2 and 3 start while P is still being made
+#pragma unroll 1
                 for (int s = 0; s < 2; ++s) {
-                    if (!it.n[s]) continue;
-                    if (!wait(&M->q_full[s], nq[s]++ & 1u)) break;
-                    scores(s, g);
-                    if (it.n[s] == 1) umma_commit(&M->q_empty[s]);
+                    if (j >= it.n[s]) continue;
+                    if (j == 0) {
+                        if ((started >> s) & 1u) {            // the item before has been stored
+                            if (!wait(&M->o_free[s], (no >> s) & 1u)) break;
+                            no ^= 1u << s;
+                        }
+                        started |= 1u << s;
+                    }
+                    if (!wait(&M->p_full[s], (np >> s) & 1u)) break;
+                    np ^= 1u << s;
+                    if (fix && !wait(&M->fixed, nfix++ & 1u)) break;
+                    fix = false;
+                    product(s, vat, j == 0);
+                    if (j + 1 < it.n[s]) {
+                        // over P's columns: the tensor core runs a thread's MMAs in order
+                        if (!wait(&M->full[kat], kph)) break;
+                        scores(s, kat, j + 2 == it.n[s]);
+                    }
                 }
                 if (!ok) break;
-                umma_commit(&M->empty[g % C::kStages]);
-                for (int j = 0; ok && j < n; ++j) {
-                    const uint32_t vi = g + 2 * j + 1, ki = vi + 1;
-                    if (!wait(&M->full[vi % C::kStages], (vi / C::kStages) & 1u)) break;
-                    bool fix = j == n - 1 && it.keys - j * kKeys < kKeys;
-                    if (fix) mbar_arrive(&M->fix);            // warps 2 and 3 start while P is still being made
-                    for (int s = 0; s < 2; ++s) {
-                        if (j >= it.n[s]) continue;
-                        if (j == 0 && no[s] > 0 && !wait(&M->o_free[s], (no[s] - 1u) & 1u)) break;
-                        if (!wait(&M->p_full[s], np[s]++ & 1u)) break;
-                        if (fix && !wait(&M->fixed, nfix++ & 1u)) break;
-                        fix = false;
-                        product(s, vi, j == 0);
-                        if (j + 1 < it.n[s]) {
-                            if (!wait(&M->full[ki % C::kStages], (ki / C::kStages) & 1u)) break;
-                            scores(s, ki);
-                            if (j + 2 == it.n[s]) umma_commit(&M->q_empty[s]);
-                        }
-                    }
-                    if (!ok) break;
-                    umma_commit(&M->empty[vi % C::kStages]);
-                    if (j + 1 < n) umma_commit(&M->empty[ki % C::kStages]);
+                if (elect_one()) {
+                    umma_commit(&M->empty[vat]);
+                    if (j + 1 < n) umma_commit(&M->empty[kat]);
                 }
-                for (int s = 0; s < 2; ++s) no[s] += it.n[s] ? 1u : 0u;
-                g += 2 * n;
+                __syncwarp();
             }
-            // the tensor core is idle before its memory is given back
+        }
+        // the tensor core is idle before its memory is given back
+        if (elect_one()) {
             umma_commit(&M->done);
             mbar_wait_for(&M->done, 0, ab->limit);
         }
+        __syncwarp();
     } else if (warp < 4) {
         // ---------------- zero the last V tile's rows past the item's keys
         uint32_t g = 0, nfix = 0;
