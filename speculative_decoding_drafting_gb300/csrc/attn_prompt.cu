@@ -12,8 +12,10 @@
 // One persistent CTA per SM works on two row tiles at a time, so that one
 // tile's softmax runs beside the other's products:
 //   warp 0      TMA producer: the two Q tiles, then K and V tiles into a ring
-//   warp 1      MMA issuer: S_s and O_s in TMEM, P_s over S_s's columns (bf16)
-//   warps 2, 3  zero the rows of the last V tile that no row of the item may
+//   warps 1, 2  MMA issuers, one per row tile s: S_s and O_s in TMEM, P_s over
+//               S_s's columns (bf16).  (One warp for both left the tensor core
+//               idle for a third of the time, between its waits.)
+//   warp 3      zeroes the rows of the last V tile that no row of the item may
 //               see (0 times another sequence's NaN would be NaN)
 //   warps 4-11  softmax, one warpgroup per row tile, one row per thread: no
 //               exchange between threads; the reference m is raised only when
@@ -53,8 +55,8 @@ struct Cfg {
 
 struct Misc {
     uint64_t full[8], empty[8];
-    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], o_free[2];
-    uint64_t fix, fixed, done;
+    uint64_t q_full[2], q_empty[2], s_full[2], s_read[2], p_full[2][2], pv_done[2], o_free[2];
+    uint64_t fix, fixed[2], done;
     WaitState wst;
     uint32_t tmem;
 };
@@ -136,8 +138,10 @@ struct Item {
     int a, len;                         // the sequence's first row and its tokens
     int tok0;                           // first token of row tile 0
     int h;                              // key-value head
-    int n[2];                           // key tiles of each row tile (0: no rows)
+    int n0, n1;                         // key tiles of each row tile (0: no rows)
     int keys;                           // keys that the item's last token sees
+    __device__ __forceinline__ int n(int s) const { return s ? n1 : n0; }
+    __device__ __forceinline__ int tiles() const { return max(n0, n1); }
 };
 
 __device__ __forceinline__ bool get_item(const Params& p, int64_t total, int round, Item& it) {
@@ -150,11 +154,11 @@ __device__ __forceinline__ bool get_item(const Params& p, int64_t total, int rou
     it.a = r.a;
     it.len = r.b - r.a;
     it.tok0 = e.y * 2 * p.toks;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        const int first = it.tok0 + s * p.toks, last = min(it.len, first + p.toks);
-        it.n[s] = first < it.len ? (last + kKeys - 1) / kKeys : 0;
-    }
+    auto tiles = [&](int first) {
+        return first < it.len ? (min(it.len, first + p.toks) + kKeys - 1) / kKeys : 0;
+    };
+    it.n0 = tiles(it.tok0);
+    it.n1 = tiles(it.tok0 + p.toks);
     it.keys = min(it.len, it.tok0 + 2 * p.toks);
     return true;
 }
@@ -216,19 +220,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(&M->full[i], 1);
-            mbar_init(&M->empty[i], 1);
+            mbar_init(&M->empty[i], 2);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&M->q_full[s], 1);
             mbar_init(&M->q_empty[s], 1);
             mbar_init(&M->s_full[s], 1);
-            mbar_init(&M->p_full[s], 4);
+            mbar_init(&M->s_read[s], 4);
+            mbar_init(&M->p_full[s][0], 4);
+            mbar_init(&M->p_full[s][1], 4);
+            mbar_init(&M->fixed[s], 1);
             mbar_init(&M->pv_done[s], 1);
             mbar_init(&M->o_free[s], 4);
         }
         mbar_init(&M->fix, 1);
-        mbar_init(&M->fixed, 2);
-        mbar_init(&M->done, 1);
+        mbar_init(&M->done, 2);
         M->wst.abort = 0;
         M->wst.limit = ws_wait_limit(p.ws);
         fence_mbar_init();
@@ -245,192 +251,216 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t total = (int64_t)__ldcg(p.count) * p.kv_heads;
     Item it;
 
-    if (warp == 0) {
-        // ---------------- producer
-        const uint64_t pol_q = policy_evict_first(), pol_kv = policy_evict_last();
-        uint32_t g = 0, st = 0, ph = 0, nq[2] = {0, 0};       // tiles issued; the next ring place and its phase
-        bool ok = true;
-        auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, ab)); };
-        auto tile = [&](const CUtensorMap* m, int j) {
-            wait(&M->empty[st], ph ^ 1u);
-            if (!ok) return;
-            if (elect_one()) {
-                mbar_expect_tx(&M->full[st], (uint32_t)C::kTileBytes);
-#pragma unroll
-                for (int hf = 0; hf < C::kHalves; ++hf)
-                    tma_load_3d(smem + st * C::kTileBytes + hf * C::kHalfBytes, m, &M->full[st], hf * 64, it.h,
-                                it.a + j * kKeys, pol_kv);
-            }
-            __syncwarp();
-            ++g;
-            if (++st == C::kStages) {
-                st = 0;
-                ph ^= 1u;
-            }
-        };
-        auto query = [&](int s) {
-            if (!it.n[s]) return;
-            wait(&M->q_empty[s], (nq[s] & 1u) ^ 1u);
-            if (!ok) return;
-            ++nq[s];
-            if (elect_one()) {
-                mbar_expect_tx(&M->q_full[s], (uint32_t)(p.toks * p.group * HD * 2));
-#pragma unroll
-                for (int hf = 0; hf < C::kHalves; ++hf)
-                    tma_load_3d(smem + C::kOffQ + s * C::kTileBytes + hf * C::kHalfBytes, &maps.q, &M->q_full[s], hf * 64,
-                                it.h * p.group, it.a + it.tok0 + s * p.toks, pol_q);
-            }
-            __syncwarp();
-        };
-#pragma unroll 1
-        for (int round = 0; ok && get_item(p, total, round, it); ++round) {
-            const int n = max(it.n[0], it.n[1]);
-            query(0);
-            tile(&maps.k, 0);
-            query(1);
-#pragma unroll 1
-            for (int j = 0; ok && j < n; ++j) {
-                if (j) tile(&maps.k, j);
-                tile(&maps.v, j);
-            }
-        }
-        // copies in flight land before the CTA may leave
-        if (ab->abort && lane == 0) {
-            for (uint32_t k = g > C::kStages ? g - C::kStages : 0; k < g; ++k)
-                mbar_wait_for(&M->full[k % C::kStages], (k / C::kStages) & 1u, ab->limit);
-            for (int s = 0; s < 2; ++s)
-                if (nq[s]) mbar_wait_for(&M->q_full[s], (nq[s] - 1u) & 1u, ab->limit);
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        // ---------------- MMA issuer
-        constexpr uint32_t id_qk = idesc_bf16_f32(128, 128, false, false);
-        constexpr uint32_t id_pv = idesc_bf16_f32(128, HD, false, true);
-        // descriptors of the first Q and ring tiles; others lie a constant number
-        // of 16-byte units on (addresses stay inside the 14-bit field)
-        const uint64_t dq = smem_desc_sw128(smem + C::kOffQ, 16, 1024);
-        const uint64_t dk = smem_desc_sw128(smem, 16, 1024);
-        const uint64_t dv = smem_desc_sw128(smem, C::kHalfBytes, 1024);
-        uint32_t nq = 0, np = 0, no = 0, started = 0, nfix = 0;   // parities of the next waits, by row tile's bit
-        uint32_t st = 0, ph = 0;                              // ring place of the next tile, and its phase
-        bool ok = true;
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, ab));
-            tc_fence_after();
-            return ok;
-        };
-        auto next = [&](uint32_t& at, uint32_t& phase) {
-            if (++at == C::kStages) {
-                at = 0;
-                phase ^= 1u;
-            }
-        };
-        auto scores = [&](int s, uint32_t at, bool last) {
-            if (elect_one()) {
-                const uint64_t a = dq + s * (C::kTileBytes / 16), b = dk + at * (C::kTileBytes / 16);
-#pragma unroll
-                for (int kk = 0; kk < HD / 16; ++kk) {
-                    const uint32_t off = (kk / 4) * (C::kHalfBytes / 16) + (kk % 4) * 2;
-                    umma_bf16(tmem + (uint32_t)(s * 128), a + off, b + off, id_qk, kk ? 1u : 0u);
-                }
-                umma_commit(&M->s_full[s]);
-                if (last) umma_commit(&M->q_empty[s]);
-            }
-            __syncwarp();
-        };
-        auto product = [&](int s, uint32_t at, bool first) {
-            if (elect_one()) {
-                const uint64_t b = dv + at * (C::kTileBytes / 16);
-                const uint32_t d = tmem + (uint32_t)(256 + s * HD), a = tmem + (uint32_t)(s * 128);
-#pragma unroll
-                for (int kk = 0; kk < kKeys / 16; ++kk)
-                    umma_bf16_ts(d, a + kk * 8, b + kk * 128, id_pv, (!first || kk) ? 1u : 0u);
-                umma_commit(&M->pv_done[s]);
-            }
-            __syncwarp();
-        };
-#pragma unroll 1
-        for (int round = 0; ok && get_item(p, total, round, it); ++round) {
-            const int n = max(it.n[0], it.n[1]);
-            uint32_t kat = st, kph = ph;                      // K_j's place; V_j's is the next
-            if (!wait(&M->full[kat], kph)) break;
-#pragma unroll 1
-            for (int s = 0; ok && s < 2; ++s) {
-                if (!it.n[s]) continue;
-                if (!wait(&M->q_full[s], (nq >> s) & 1u)) break;
-                nq ^= 1u << s;
-                scores(s, kat, it.n[s] == 1);
-            }
-            if (!ok) break;
-            if (elect_one()) umma_commit(&M->empty[kat]);
-            __syncwarp();
-            next(st, ph);
-#pragma unroll 1
-            for (int j = 0; ok && j < n; ++j) {
-                const uint32_t vat = st;
-                if (!wait(&M->full[vat], ph)) break;
-                next(st, ph);
-                kat = st;
-                kph = ph;
-                if (j + 1 < n) next(st, ph);
-                bool fix = j == n - 1 && it.keys - j * kKeys < kKeys;
-                if (fix && lane == 0) mbar_arrive(&M->fix);   // warps 2 and 3 start while P is still being made
-#pragma unroll 1
-                for (int s = 0; s < 2; ++s) {
-                    if (j >= it.n[s]) continue;
-                    if (j == 0) {
-                        if ((started >> s) & 1u) {            // the item before has been stored
-                            if (!wait(&M->o_free[s], (no >> s) & 1u)) break;
-                            no ^= 1u << s;
-                        }
-                        started |= 1u << s;
-                    }
-                    if (!wait(&M->p_full[s], (np >> s) & 1u)) break;
-                    np ^= 1u << s;
-                    if (fix && !wait(&M->fixed, nfix++ & 1u)) break;
-                    fix = false;
-                    product(s, vat, j == 0);
-                    if (j + 1 < it.n[s]) {
-                        // over P's columns: the tensor core runs a thread's MMAs in order
-                        if (!wait(&M->full[kat], kph)) break;
-                        scores(s, kat, j + 2 == it.n[s]);
-                    }
-                }
-                if (!ok) break;
+    // registers: 384 x 168 at launch, then 128 x 104 + 256 x 200
+    if (warp < 4) {
+        regs_lower<104>();
+        if (warp == 0) {
+            // ---------------- producer
+            const uint64_t pol_q = policy_evict_first(), pol_kv = policy_evict_last();
+            uint32_t g = 0, st = 0, ph = 0, nq = 0, used = 0;     // tiles issued; the next ring place and its phase; Q's
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && __all_sync(0xffffffffu, wait_bar_here(bar, parity, ab)); };
+            auto tile = [&](const CUtensorMap* m, int j) {
+                wait(&M->empty[st], ph ^ 1u);
+                if (!ok) return;
                 if (elect_one()) {
-                    umma_commit(&M->empty[vat]);
-                    if (j + 1 < n) umma_commit(&M->empty[kat]);
+                    mbar_expect_tx(&M->full[st], (uint32_t)C::kTileBytes);
+#pragma unroll
+                    for (int hf = 0; hf < C::kHalves; ++hf)
+                        tma_load_3d(smem + st * C::kTileBytes + hf * C::kHalfBytes, m, &M->full[st], hf * 64, it.h,
+                                    it.a + j * kKeys, pol_kv);
                 }
                 __syncwarp();
+                ++g;
+                if (++st == C::kStages) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            };
+            auto query = [&](int s) {
+                if (!it.n(s)) return;
+                wait(&M->q_empty[s], ((nq >> s) & 1u) ^ 1u);
+                if (!ok) return;
+                nq ^= 1u << s;
+                used |= 1u << s;
+                if (elect_one()) {
+                    mbar_expect_tx(&M->q_full[s], (uint32_t)(p.toks * p.group * HD * 2));
+#pragma unroll
+                    for (int hf = 0; hf < C::kHalves; ++hf)
+                        tma_load_3d(smem + C::kOffQ + s * C::kTileBytes + hf * C::kHalfBytes, &maps.q, &M->q_full[s], hf * 64,
+                                    it.h * p.group, it.a + it.tok0 + s * p.toks, pol_q);
+                }
+                __syncwarp();
+            };
+#pragma unroll 1
+            for (int round = 0; ok && get_item(p, total, round, it); ++round) {
+                const int n = it.tiles();
+                query(0);
+                tile(&maps.k, 0);
+                query(1);
+#pragma unroll 1
+                for (int j = 0; ok && j < n; ++j) {
+                    if (j) tile(&maps.k, j);
+                    tile(&maps.v, j);
+                }
+            }
+            // copies in flight land before the CTA may leave
+            if (ab->abort && lane == 0) {
+                for (uint32_t k = g > C::kStages ? g - C::kStages : 0; k < g; ++k)
+                    mbar_wait_for(&M->full[k % C::kStages], (k / C::kStages) & 1u, ab->limit);
+                for (int s = 0; s < 2; ++s)
+                    if (used >> s & 1u) mbar_wait_for(&M->q_full[s], ((nq >> s) & 1u) ^ 1u, ab->limit);
+            }
+            __syncwarp();
+        } else if (warp < 3) {
+            // ---------------- MMA issuer of row tile s
+            const int s = warp - 1;
+            constexpr uint32_t id_qk = idesc_bf16_f32(128, 64, false, false);
+            constexpr uint32_t id_pv = idesc_bf16_f32(128, HD, false, true);
+            // descriptors of Q and of the first ring tile; others lie a constant number
+            // of 16-byte units on (addresses stay inside the 14-bit field)
+            const uint64_t dq = smem_desc_sw128(smem + C::kOffQ + s * C::kTileBytes, 16, 1024);
+            const uint64_t dk = smem_desc_sw128(smem, 16, 1024);
+            const uint64_t dv = smem_desc_sw128(smem, C::kHalfBytes, 1024);
+            const uint32_t tS = tmem + (uint32_t)(s * 128), tO = tmem + (uint32_t)(256 + s * HD);
+            uint32_t nq = 0, nr = 0, np = 0, no = 0, nfix = 0;    // parities of the next waits
+            uint32_t st = 0, ph = 0;                              // ring place of the next tile, and its phase
+            bool ok = true, started = false;
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                ok = ok && __all_sync(0xffffffffu, wait_bar_here(bar, parity, ab));
+                return ok;
+            };
+            auto next = [&]() {
+                if (++st == C::kStages) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            };
+            // Scores of 64 keys of the ring tile at `at`: half 1 goes to columns 64 to
+            // 127 and may start as soon as the scores there before have been read,
+            // half 0 to columns 0 to 63, over P, once P has been multiplied (the
+            // tensor core runs a thread's MMAs in order).
+            auto scores = [&](uint32_t at, int half, int j) {
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t b = dk + at * (C::kTileBytes / 16) + half * 512;
+#pragma unroll
+                    for (int kk = 0; kk < HD / 16; ++kk) {
+                        const uint32_t off = (kk / 4) * (C::kHalfBytes / 16) + (kk % 4) * 2;
+                        umma_bf16(tS + half * 64, dq + off, b + off, id_qk, kk ? 1u : 0u);
+                    }
+                    if (!half) {
+                        umma_commit(&M->s_full[s]);
+                        umma_commit(&M->empty[at]);
+                        if (j + 1 == it.n(s)) umma_commit(&M->q_empty[s]);
+                    }
+                }
+                __syncwarp();
+            };
+#pragma unroll 1
+            for (int round = 0; ok && get_item(p, total, round, it); ++round) {
+                const int n = it.tiles();
+                if (it.n(s)) {
+                    if (!wait(&M->q_full[s], nq & 1u)) break;
+                    nq ^= 1u;
+                }
+                if (!wait(&M->full[st], ph)) break;
+                if (it.n(s)) {
+                    // (the item before it has been read and multiplied)
+                    scores(st, 1, 0);
+                    scores(st, 0, 0);
+                } else if (lane == 0) {
+                    mbar_arrive(&M->empty[st]);
+                }
+                next();
+#pragma unroll 1
+                for (int j = 0; ok && j < n; ++j) {
+                    // V_j at st, K_{j+1} at the place after it
+                    const uint32_t vat = st, vph = ph;
+                    next();
+                    const uint32_t kat = st, kph = ph;
+                    if (j + 1 < n) next();
+                    if (j < it.n(s)) {
+                        if (!wait(&M->s_read[s], nr & 1u)) break;
+                        nr ^= 1u;
+                        if (j + 1 < it.n(s)) {
+                            if (!wait(&M->full[kat], kph)) break;
+                            scores(kat, 1, j + 1);
+                        }
+                    }
+                    if (!wait(&M->full[vat], vph)) break;
+                    const bool fix = j == n - 1 && it.keys - j * kKeys < kKeys;
+                    // warp 3 starts while P is still being made (row tile 1, where there
+                    // is one, sees the item's last tile)
+                    if (fix && lane == 0 && s == (it.n1 ? 1 : 0)) mbar_arrive(&M->fix);
+                    if (j < it.n(s)) {
+                        if (j == 0) {
+                            if (started) {                        // the item before has been stored
+                                if (!wait(&M->o_free[s], no & 1u)) break;
+                                no ^= 1u;
+                            }
+                            started = true;
+                        }
+                        if (fix && !wait(&M->fixed[s], nfix++ & 1u)) break;
+#pragma unroll 1
+                        for (int half = 0; half < 2; ++half) {    // 64 keys at a time
+                            if (!wait(&M->p_full[s][half], np & 1u)) break;
+                            tc_fence_after();
+                            if (elect_one()) {
+                                const uint64_t b = dv + vat * (C::kTileBytes / 16) + half * 512;
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    umma_bf16_ts(tO, tS + half * 32 + kk * 8, b + kk * 128, id_pv, (j | half | kk) ? 1u : 0u);
+                                if (half) {
+                                    umma_commit(&M->pv_done[s]);
+                                    umma_commit(&M->empty[vat]);
+                                }
+                            }
+                            __syncwarp();
+                        }
+                        if (!ok) break;
+                        np ^= 1u;
+                        if (j + 1 < it.n(s)) scores(kat, 0, j + 1);
+                    } else if (lane == 0) {
+                        mbar_arrive(&M->empty[vat]);
+                    }
+                    if (j + 1 < n && j + 1 >= it.n(s)) {          // a tile only the other row tile sees
+                        if (!wait(&M->full[kat], kph)) break;
+                        if (lane == 0) mbar_arrive(&M->empty[kat]);
+                    }
+                }
+            }
+            // the tensor core is idle before its memory is given back
+            if (elect_one()) {
+                umma_commit(&M->done);
+                mbar_wait_for(&M->done, 0, ab->limit);
+            }
+            __syncwarp();
+        } else if (warp == 3) {
+            // ---------------- zero the last V tile's rows past the item's keys
+            uint32_t g = 0, nfix = 0;
+#pragma unroll 1
+            for (int round = 0; get_item(p, total, round, it); ++round) {
+                const int n = it.tiles();
+                const int valid = it.keys - (n - 1) * kKeys;
+                const uint32_t vi = g + 2 * n - 1;
+                g += 2 * n;
+                if (valid >= kKeys) continue;
+                // an MMA issuer saw the tile arrive and asks for the zeros
+                if (!__all_sync(0xffffffffu, wait_bar_here(&M->fix, nfix++ & 1u, ab))) break;
+                uint8_t* vt = smem + (vi % C::kStages) * C::kTileBytes;
+#pragma unroll 1
+                for (int x = valid * 8 + lane; x < kKeys * 8; x += 32)
+#pragma unroll
+                    for (int hf = 0; hf < C::kHalves; ++hf)
+                        *reinterpret_cast<uint4*>(vt + hf * C::kHalfBytes + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+                fence_proxy_async();
+                __syncwarp();
+                if (lane < 2 && it.n(lane) == n) mbar_arrive(&M->fixed[lane]);
             }
         }
-        // the tensor core is idle before its memory is given back
-        if (elect_one()) {
-            umma_commit(&M->done);
-            mbar_wait_for(&M->done, 0, ab->limit);
-        }
-        __syncwarp();
-    } else if (warp < 4) {
-        // ---------------- zero the last V tile's rows past the item's keys
-        uint32_t g = 0, nfix = 0;
-        for (int round = 0; get_item(p, total, round, it); ++round) {
-            const int n = max(it.n[0], it.n[1]);
-            const int valid = it.keys - (n - 1) * kKeys;
-            const uint32_t vi = g + 2 * n - 1;
-            g += 2 * n;
-            if (valid >= kKeys) continue;
-            // the MMA issuer saw the tile arrive and asks for the zeros
-            if (!__all_sync(0xffffffffu, mbar_wait(&M->fix, nfix++ & 1u, ab))) break;
-            uint8_t* vt = smem + (vi % C::kStages) * C::kTileBytes;
-            for (int x = valid * 8 + (warp - 2) * 32 + lane; x < kKeys * 8; x += 64)
-#pragma unroll
-                for (int hf = 0; hf < C::kHalves; ++hf)
-                    *reinterpret_cast<uint4*>(vt + hf * C::kHalfBytes + x * 16) = make_uint4(0u, 0u, 0u, 0u);
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&M->fixed);
-        }
     } else {
+        regs_raise<200>();
         // ---------------- softmax: thread = row
         const int s = (warp - 4) >> 2, wq = warp & 3;
         const int row = wq * 32 + lane;
@@ -443,12 +473,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t ns = 0, npv = 0;
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
-            ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, ab));
+            ok = __all_sync(0xffffffffu, wait_bar_here(bar, parity, ab));
             tc_fence_after();
             return ok;
         };
         for (int round = 0; ok && get_item(p, total, round, it); ++round) {
-            const int n = it.n[s];
+            const int n = it.n(s);
             if (!n) continue;
             const int tok = it.tok0 + s * p.toks + rt;           // sees keys 0 .. tok
             const int first = it.tok0 + s * p.toks;
@@ -462,6 +492,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ready(x);
 #pragma unroll
                 for (int q = 1; q < 4; ++q) tmem_pin(x + q * 32);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&M->s_read[s]);
                 if ((j + 1) * kKeys - 1 > first) {               // a row of the tile does not see all keys
                     const int lim = tok - j * kKeys;
                     const float hidden = c < 0.f ? INFINITY : -INFINITY;
@@ -514,11 +547,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         pk[i] = reinterpret_cast<const uint32_t&>(h);
                     }
                     tmem_st32(tS + hf * 32, pk);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&M->p_full[s][hf]);
                 }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&M->p_full[s]);
                 ++npv;
             }
             if (!ok || !wait(&M->pv_done[s], (npv - 1u) & 1u)) break;

@@ -139,6 +139,62 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
     }
 }
 
+// mbar_wait in few instructions, of which there are many: the first try in
+// place, the rest in one function.
+static __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile WaitState* w) {
+    const uint64_t t0 = sm_cycles();
+    do {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok) return true;
+    } while (!w->abort && sm_cycles() - t0 <= w->limit);
+    w->abort = 1;
+    return false;
+}
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile WaitState* w) {
+    return mbar_test(bar, parity) || wait_on(smem_u32(bar), parity, w);
+}
+
+// Sums over the 32 lanes of the first N = 16 or 32 values per lane; lane i gets
+// the sum of value i % N.
+template <int N>
+__device__ __forceinline__ float lane_sums(float (&x)[32]) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (N == 16) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], 16);
+    }
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const float keep = up ? x[i + o] : x[i], give = up ? x[i] : x[i + o];
+            x[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+    }
+    return x[0];
+}
+
+// The same all in place and with a first try that may suspend the thread: about
+// 110 cycles from arrival to return, against 270 through the function, and no
+// call (registers cannot be moved between warpgroups around one).
+__device__ __forceinline__ bool wait_bar_here(uint64_t* bar, uint32_t parity, volatile WaitState* w) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = sm_cycles();
+    do {
+        if (mbar_try_wait(bar, parity)) return true;
+    } while (!w->abort && sm_cycles() - t0 <= w->limit);
+    w->abort = 1;
+    return false;
+}
+
 // Bounded wait that ignores the abort flag (used to drain copies in flight
 // after an abort).
 __device__ __forceinline__ bool mbar_wait_for(uint64_t* bar, uint32_t parity, uint64_t limit_cycles) {
