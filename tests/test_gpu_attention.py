@@ -225,6 +225,24 @@ def test_paged_many_requests():
 
 
 @pytest.mark.parametrize("dtype", [BF, F8])
+@pytest.mark.parametrize("heads,kv_heads,dim,most", [(24, 4, 64, 700), (16, 4, 128, 300), (32, 8, 64, 1500)])
+def test_paged_row_tiles_of_changing_shape(dtype, heads, kv_heads, dim, most):
+    """Several segments to a worker whose row tiles change between few and many
+    rows, with one key tile or several, and lengths of zero in between."""
+    g = torch.Generator().manual_seed(most)
+    n = 330
+    kv = torch.randint(0, most, (n,), generator=g).tolist()
+    q = torch.randint(0, 18, (n,), generator=g).tolist()
+    for i in range(0, n, 9):                     # long quiet runs of one shape, then a change
+        if i % 27:
+            q[i:i + 9] = [1] * len(q[i:i + 9])
+    s = Scene(kv, heads, kv_heads, dim, 16, dtype, seed=most)
+    _, first = s.check(q)
+    _, second = s.check(q[::-1])
+    assert not torch.equal(first["out"], second["out"])
+
+
+@pytest.mark.parametrize("dtype", [BF, F8])
 def test_paged_sharp_and_flat_scores(dtype):
     """Scores far apart (one key takes all the weight, the maximum moves late)
     and all equal."""
