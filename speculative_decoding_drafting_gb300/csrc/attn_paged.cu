@@ -54,6 +54,7 @@
 // a stale NaN would be NaN.
 #include <type_traits>
 
+#include <cstddef>
 #include <cuda.h>
 
 #include "attn_plan.h"
@@ -115,9 +116,45 @@ struct SegInfo {
     Request q;
 };
 
+struct Bars {
+    uint64_t seg_full[kSegs], seg_empty[kSegs];
+    uint64_t k_full[5], k_empty[5], v_full[6], v_empty[6];
+    uint64_t w_empty[3];               // widened V tiles (p_full says that one is made)
+    uint64_t c_full[4], c_empty[4];    // scales
+    uint64_t q_full[2], q_empty[2];
+    uint64_t s_full[2][kUnits], s_free[2][kUnits], p_full[kUnits], pv_done[kUnits];
+    uint64_t o_done[2], l_done[2], e_free[2];   // a segment's accumulators, its sums; both read
+    uint64_t r_done;                   // all products before a change of shape
+    uint64_t done;
+};
+
+// How many arrivals each of them takes, in the same order.
+struct BarCounts {
+    uint8_t n[sizeof(Bars) / sizeof(uint64_t)];
+};
+template <bool F8>
+constexpr BarCounts bar_counts() {
+    BarCounts c = {};
+    auto set = [&](size_t at, int n, int count) {
+        for (int i = 0; i < n; ++i) c.n[at / sizeof(uint64_t) + i] = (uint8_t)count;
+    };
+    set(0, sizeof(Bars) / sizeof(uint64_t), 1);
+    set(offsetof(Bars, c_empty), 4, 8);
+    set(offsetof(Bars, q_full), 2, 128);
+    set(offsetof(Bars, q_empty), 2, F8 ? 1 + 4 * kUnits : 1);
+    set(offsetof(Bars, s_free), 2 * kUnits, 4);
+    set(offsetof(Bars, p_full), kUnits, 4);
+    set(offsetof(Bars, seg_empty), kSegs, kReaders);
+    set(offsetof(Bars, l_done), 2, 4 * kUnits);
+    set(offsetof(Bars, e_free), 2, 4);
+    set(offsetof(Bars, done), 1, 2);
+    return c;
+}
+template <bool F8>
+__constant__ const BarCounts kBarCounts = bar_counts<F8>();
+
 struct alignas(16) Misc {
     SegInfo seg[kSegs];
-    uint64_t seg_full[kSegs], seg_empty[kSegs];
     float ref[kUnits][kUnitRows];      // reference of a row
     float nref[kUnits][kUnitRows];     // kLift minus it
     float qm[kUnits][kUnitRows];       // 2^e of a row's split
@@ -134,14 +171,7 @@ struct alignas(16) Misc {
     int start_r;
     uint32_t tmem;
     WaitState wst;
-    uint64_t k_full[5], k_empty[5], v_full[6], v_empty[6];
-    uint64_t w_empty[3];               // widened V tiles (p_full says that one is made)
-    uint64_t c_full[4], c_empty[4];    // scales
-    uint64_t q_full[2], q_empty[2];
-    uint64_t s_full[2][kUnits], s_free[2][kUnits], p_full[kUnits], pv_done[kUnits];
-    uint64_t o_done[2], l_done[2], e_free[2];   // a segment's accumulators, its sums; both read
-    uint64_t r_done;                   // all products before a change of shape
-    uint64_t done;
+    Bars b;
 };
 
 template <int HD, bool F8>
@@ -186,6 +216,21 @@ __device__ __forceinline__ uint64_t desc_f8(const void* p) {
 template <int HD>
 __device__ __forceinline__ int swz_f8(int r, int c) {
     return r * HD + (HD == 128 ? (c ^ (r & 7)) : (c ^ ((r >> 1) & 3))) * 16;
+}
+
+// Loads that may move past stores and barriers (nothing in the kernel writes
+// what they read) but, unlike the read-only path, see what the kernel before
+// this one wrote while this one had started: their addresses come from data
+// read after pdl_wait().
+__device__ __forceinline__ uint4 load16(const void* p) {
+    uint4 v;
+    asm("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ int load4(const int32_t* p) {
+    int v;
+    asm("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
 }
 
 // One lane's 8 values of a Q row that `LANES` lanes share: e4m3 codes of hi
@@ -271,14 +316,14 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
     uint8_t* P = smem + C::kOffP + u * C::kPBytes;
 
     // this unit's rows (what the segment before left is no longer read)
-    if (F8) q_places(sg, [&](int k, uint32_t use) { wait_bar(&M->q_full[k], use & 1u, ab); });
+    if (F8) q_places(sg, [&](int k, uint32_t use) { wait_bar(&M->b.q_full[k], use & 1u, ab); });
     if (tr < cols) {
         M->ref[u][tr] = kFloorRef;
         M->nref[u][tr] = -kFloorRef;
         if (F8) M->qm[u][tr] = M->q_scale[(sg.qp == 1 ? C::kQRows : 0) + coff + tr];
     }
     named_sync(bar, 128);
-    if (F8 && lane == 0) q_places(sg, [&](int k, uint32_t) { mbar_arrive(&M->q_empty[k]); });   // the row scales are copied
+    if (F8 && lane == 0) q_places(sg, [&](int k, uint32_t) { mbar_arrive(&M->b.q_empty[k]); });   // the row scales are copied
 
     float l = 0.f;                                            // this warp's sum of row `lane`
     const int lim0 = plan_token_keys(sg.q, sg.tok);           // the first row sees the fewest keys
@@ -293,7 +338,7 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
         // new token k sees the key if kv_len - q_len + k >= key: from this row on
         const int seen = !edge ? 0 : min(key - sg.q.kv_len + sg.q.q_len - sg.tok, kRowTile + 1) * p.plan.group - sg.head - coff;
         const uint32_t turn = sh.turn_at(sg, i);
-        wait_bar(&M->s_full[turn][u], (st.phases >> turn) & 1u, ab);
+        wait_bar(&M->b.s_full[turn][u], (st.phases >> turn) & 1u, ab);
         st.phases ^= 1u << turn;
         tc_fence_after();
         const uint32_t tS = tS0 + (turn ? kColS1 : 0u);
@@ -302,7 +347,7 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
             // (the scores waited for the copy of these scales to be asked for)
             const uint32_t at = line + (uint32_t)i;
             const int s = (int)(at % C::kScMod);
-            wait_bar(&M->c_full[s], (at / C::kScMod) & 1u, ab);
+            wait_bar(&M->b.c_full[s], (at / C::kScMod) & 1u, ab);
             // (pages of 16 tokens lie 128 bytes apart, longer ones side by side)
             const uint8_t* sc = smem + C::kOffSc + s * C::kScBytes +
                                 (p.page_log2 == 4 ? (tr >> 4) * 128 + (tr & 15) * 4 : tr * 4);
@@ -310,8 +355,8 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
             float vs = *reinterpret_cast<const float*>(sc + C::kScBytes / 2);
             __syncwarp();
             // a wide tile's scales are read by two units
-            if (lane == 0) mbar_arrive(&M->c_empty[s]);
-            if (!sh.wide && lane == 0) mbar_arrive(&M->c_empty[s]);
+            if (lane == 0) mbar_arrive(&M->b.c_empty[s]);
+            if (!sh.wide && lane == 0) mbar_arrive(&M->b.c_empty[s]);
             if (edge && key >= sg.keys) vs = 1.f;             // no key here: any scale
             if (vs < 7.888609e-31f) vs = 7.888609e-31f;       // 2^-100; a row of zeros has scale 0
             lvs = lg2_approx(vs);
@@ -377,7 +422,7 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
             named_sync(bar, 128);
             if (lane < cols) l *= M->fac[u][lane];
             if (i >= sh.streams) {                            // the accumulator holds earlier tiles
-                wait_bar(&M->pv_done[u], (st.tiles - 1u) & 1u, ab);
+                wait_bar(&M->b.pv_done[u], (st.tiles - 1u) & 1u, ab);
                 tc_fence_after();
 #pragma unroll 1
                 for (int c0 = 0; c0 < cols; c0 += 8) {
@@ -392,9 +437,9 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&M->s_free[turn][u]);
+        if (lane == 0) mbar_arrive(&M->b.s_free[turn][u]);
         // the P buffer is free once this unit's previous product is done
-        if (st.tiles > 0) wait_bar(&M->pv_done[u], (st.tiles - 1u) & 1u, ab);
+        if (st.tiles > 0) wait_bar(&M->b.pv_done[u], (st.tiles - 1u) & 1u, ab);
         ++st.tiles;
 #pragma unroll
         for (int c0 = 0; c0 < kUnitRows; c0 += 16) {
@@ -426,8 +471,8 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
             // has whatever the loaded tile's place held before.)
             const uint32_t at = line + (uint32_t)i;
             const int d = (int)(at % C::kW), s = (int)(at % C::kV);
-            wait_bar(&M->w_empty[d], ((at / C::kW) & 1u) ^ 1u, ab);
-            wait_bar(&M->v_full[s], (at / C::kV) & 1u, ab);
+            wait_bar(&M->b.w_empty[d], ((at / C::kW) & 1u) ^ 1u, ab);
+            wait_bar(&M->b.v_full[s], (at / C::kV) & 1u, ab);
             const uint8_t* src = smem + C::kOffV + (size_t)s * C::kLoadBytes;
             uint8_t* dst = smem + C::kOffW + (size_t)d * C::kTileBytes;
             constexpr int kPieces = kKeyTile * HD / 16, kPer = HD / 16;
@@ -462,7 +507,7 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
         fence_proxy_async();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&M->p_full[u]);
+        if (lane == 0) mbar_arrive(&M->b.p_full[u]);
         // the weights' sums (over w / scale for e4m3), while the product runs: a
         // row's sum in one lane, since a sum per row and thread would not fit
         // the registers
@@ -479,14 +524,14 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
     // hand the sums on; the segment before the last has been read
     {
         M->red[u][wq][lane] = l;
-        wait_bar(&M->e_free[parity], ((st.seg >> 1) & 1u) ^ 1u, ab);
+        wait_bar(&M->b.e_free[parity], ((st.seg >> 1) & 1u) ^ 1u, ab);
         named_sync(bar, 128);
         if (tr < cols) {
             M->fin_l[parity][u][tr] = (M->red[u][0][tr] + M->red[u][1][tr]) + (M->red[u][2][tr] + M->red[u][3][tr]);
             M->fin_m[parity][u][tr] = -M->nref[u][tr];
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&M->l_done[parity]);
+        if (lane == 0) mbar_arrive(&M->b.l_done[parity]);
     }
     ++st.seg;
 }
@@ -518,8 +563,8 @@ __device__ __forceinline__ void finish_segment(const PagedParams& p, const SegIn
         M->row_at[tr] = at < 0 ? nullptr
                                : (whole ? reinterpret_cast<uint8_t*>(p.out + (size_t)at * HD)
                                         : reinterpret_cast<uint8_t*>(part + 2 * kRowTile + tr * HD));
-    wait_bar(&M->l_done[parity], (seg >> 1) & 1u, ab);
-    wait_bar(&M->o_done[parity], (seg >> 1) & 1u, ab);
+    wait_bar(&M->b.l_done[parity], (seg >> 1) & 1u, ab);
+    wait_bar(&M->b.o_done[parity], (seg >> 1) & 1u, ab);
     tc_fence_after();
     const bool store = !ab->abort;
     if (tr < sh.cols) {
@@ -576,7 +621,7 @@ __device__ __forceinline__ void finish_segment(const PagedParams& p, const SegIn
     }
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&M->e_free[parity]);
+    if (lane == 0) mbar_arrive(&M->b.e_free[parity]);
     named_sync(5, 128);                                       // row_at and join are no longer read
 }
 
@@ -594,6 +639,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cta = (int)blockIdx.x;
     pdl_launch_dependents();
 
+    // ---------------- barriers and descriptors, beside the end of the kernel
+    // before this one
+    if (threadIdx.x < (int)(sizeof(Bars) / sizeof(uint64_t))) {
+        mbar_init(reinterpret_cast<uint64_t*>(&M->b) + threadIdx.x, kBarCounts<F8>.n[threadIdx.x]);
+        fence_mbar_init();
+    } else if (threadIdx.x == 21 * 32) {
+        M->wst.abort = 0;
+        prefetch_tmap(&maps.k);
+        prefetch_tmap(&maps.v);
+    }
+    pdl_wait();
+    if (threadIdx.x == 22 * 32) M->wst.limit = ws_wait_limit(p.ws);
+    if (threadIdx.x == 23 * 32) p.desc[cta] = JoinDesc{-1, 0, 0, 0};
     // ---------------- this CTA's span
     if (cta == 0) check_requests(pl.q_off, pl.kv_len, pl.R, pl.T, pl.most, p.ws);
     const int per = (pl.R + kThreads - 1) / kThreads;
@@ -608,71 +666,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane >= o) upto += x;
     }
     if (lane == 31) M->scan[warp] = upto;
-    if (threadIdx.x == 0) {
-#pragma unroll 1
-        for (int i = 0; i < C::kK; ++i) {
-            mbar_init(&M->k_full[i], 1);
-            mbar_init(&M->k_empty[i], 1);
-        }
-#pragma unroll 1
-        for (int i = 0; i < C::kV; ++i) {
-            mbar_init(&M->v_full[i], 1);
-            mbar_init(&M->v_empty[i], 1);
-        }
-#pragma unroll 1
-        for (int i = 0; i < C::kW; ++i) mbar_init(&M->w_empty[i], 1);
-#pragma unroll 1
-        for (int i = 0; i < C::kSc; ++i) {
-            mbar_init(&M->c_full[i], 1);
-            mbar_init(&M->c_empty[i], 8);
-        }
-#pragma unroll 1
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&M->q_full[i], 128);
-            mbar_init(&M->q_empty[i], F8 ? 1 + 4 * kUnits : 1);
-        }
-#pragma unroll 1
-        for (int i = 0; i < kUnits; ++i) {
-            mbar_init(&M->s_full[0][i], 1);
-            mbar_init(&M->s_full[1][i], 1);
-            mbar_init(&M->s_free[0][i], 4);
-            mbar_init(&M->s_free[1][i], 4);
-            mbar_init(&M->p_full[i], 4);
-            mbar_init(&M->pv_done[i], 1);
-        }
-#pragma unroll 1
-        for (int i = 0; i < kSegs; ++i) {
-            mbar_init(&M->seg_full[i], 1);
-            mbar_init(&M->seg_empty[i], kReaders);
-        }
-#pragma unroll 1
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&M->o_done[i], 1);
-            mbar_init(&M->l_done[i], 4 * kUnits);
-            mbar_init(&M->e_free[i], 4);
-        }
-        mbar_init(&M->r_done, 1);
-        mbar_init(&M->done, 2);
-        M->wst.abort = 0;
-        M->wst.limit = ws_wait_limit(p.ws);
-        fence_mbar_init();
-        p.desc[cta] = JoinDesc{-1, 0, 0, 0};
-    }
     __syncthreads();
-    int64_t base = upto - sum, total = 0;
-#pragma unroll 1
-    for (int i = 0; i < kThreads / 32; ++i) {
-        if (i < warp) base += M->scan[i];
-        total += M->scan[i];
+    const int64_t part = lane < kThreads / 32 ? M->scan[lane] : 0;
+    int64_t parts = part;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, parts, o);
+        if (lane >= o) parts += x;
     }
+    const int64_t total = __shfl_sync(0xffffffffu, parts, 31);
+    const int64_t base = upto - sum + __shfl_sync(0xffffffffu, parts - part, warp);
     const int spans = plan_spans(total, (int)gridDim.x);
     if (cta >= spans) return;                                 // the same for every thread of the CTA
-    const int64_t begin = plan_cut(total, cta, spans), end = plan_cut(total, cta + 1, spans);
+    const Span span = plan_span(total, cta, spans);
+    const int64_t begin = span.begin, end = span.end;
     if (base <= begin && begin < base + sum) {
         int64_t at = base;
         int r = r0;
 #pragma unroll 1
-        for (;; ++r) {
+        for (; r < r1 - 1; ++r) {                             // it is the last one, if none before it
             const int64_t t = plan_request_tiles(pl, r);
             if (begin < at + t) break;
             at += t;
@@ -692,13 +704,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     SegInfo sg;
     auto next_segment = [&]() {
         const int at = nseg % kSegs;
-        if (!__all_sync(0xffffffffu, wait_bar(&M->seg_full[at], (nseg / kSegs) & 1u, ab))) return false;
+        if (!__all_sync(0xffffffffu, wait_bar(&M->b.seg_full[at], (nseg / kSegs) & 1u, ab))) return false;
         sg = M->seg[at];
         return sg.rows > 0;
     };
     auto done_segment = [&]() {
         __syncwarp();
-        if (lane == 0) mbar_arrive(&M->seg_empty[nseg % kSegs]);
+        if (lane == 0) mbar_arrive(&M->b.seg_empty[nseg % kSegs]);
         ++nseg;
     };
 
@@ -719,11 +731,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lane_tok = pg < ppt ? pg * bp : 1 << 30;        // this lane's page of a tile, in tokens
     bool ok = true;
     auto entry = [&](const Place& c, int k) {
-        return (int64_t)k << p.page_log2 < c.keys ? __ldg(p.page_table + (size_t)c.r * p.max_pages + k) : -1;
+        return (int64_t)k << p.page_log2 < c.keys ? load4(p.page_table + (size_t)c.r * p.max_pages + k) : -1;
     };
     auto enter = [&](Place& c) {
         const int at = c.seg % kSegs;
-        ok = ok && __all_sync(0xffffffffu, wait_bar(&M->seg_full[at], (c.seg / kSegs) & 1u, ab));
+        ok = ok && __all_sync(0xffffffffu, wait_bar(&M->b.seg_full[at], (c.seg / kSegs) & 1u, ab));
         const SegInfo& s = M->seg[at];
         c.more = ok && s.rows > 0;
         if (!c.more) return;
@@ -760,11 +772,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto load = [&](auto which, Place& c, int id) {
         constexpr bool kIsV = decltype(which)::value;
         constexpr uint32_t kRing = kIsV ? C::kV : C::kK;
-        uint64_t* full = (kIsV ? M->v_full : M->k_full) + c.slot;
-        ok = ok && __all_sync(0xffffffffu, wait_bar((kIsV ? M->v_empty : M->k_empty) + c.slot, c.phase ^ 1u, ab));
+        uint64_t* full = (kIsV ? M->b.v_full : M->b.k_full) + c.slot;
+        ok = ok && __all_sync(0xffffffffu, wait_bar((kIsV ? M->b.v_empty : M->b.k_empty) + c.slot, c.phase ^ 1u, ab));
         const uint32_t cs = c.count % C::kScMod;
         if (F8 && !kIsV)
-            ok = ok && __all_sync(0xffffffffu, wait_bar(&M->c_empty[cs], ((c.count / C::kScMod) & 1u) ^ 1u, ab));
+            ok = ok && __all_sync(0xffffffffu, wait_bar(&M->b.c_empty[cs], ((c.count / C::kScMod) & 1u) ^ 1u, ab));
         if (!ok) return;
         const bool valid = lane_tok < c.keys - c.tok;
         if (valid && (uint32_t)id >= (uint32_t)p.n_pages) {
@@ -775,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int x = c.x + (ppt == 1 ? c.tok & ((1 << p.page_log2) - 1) : 0);        // a 256-token page is two tiles
         if (elect_one()) {
             mbar_expect_tx(full, pages * (uint32_t)(bp * (F8 ? HD : HD * 2)));
-            if (F8 && !kIsV) mbar_expect_tx(&M->c_full[cs], pages * (uint32_t)(bp * 8));
+            if (F8 && !kIsV) mbar_expect_tx(&M->b.c_full[cs], pages * (uint32_t)(bp * 8));
         }
         __syncwarp();
         uint8_t* dst = smem + (kIsV ? C::kOffV : 0) + c.slot * C::kLoadBytes;
@@ -788,8 +800,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int hf = 0; hf < (F8 ? 1 : C::kHalves); ++hf)
                     tma_load_3d(dst + hf * C::kHalfBytes, kIsV ? &maps.v : &maps.k, full, hf * 64, x, pid, c.pol);
                 if (F8 && !kIsV) {
-                    tma_load_2d(sc, &maps.ks, &M->c_full[cs], x, pid, c.pol);
-                    tma_load_2d(sc + C::kScBytes / 2, &maps.vs, &M->c_full[cs], x, pid, c.pol);
+                    tma_load_2d(sc, &maps.ks, &M->b.c_full[cs], x, pid, c.pol);
+                    tma_load_2d(sc + C::kScBytes / 2, &maps.vs, &M->b.c_full[cs], x, pid, c.pol);
                 }
             }
             dst += bp * (F8 ? HD : 128);
@@ -820,12 +832,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             const uint32_t seg = c.seg;
             if (step(c)) {
-                if (lane == 0) mbar_arrive(&M->seg_empty[seg % kSegs]);
+                if (lane == 0) mbar_arrive(&M->b.seg_empty[seg % kSegs]);
                 enter(c);
             }
         }
-        drain(M->k_full, C::kK, c.count);
-        if (F8) drain(M->c_full, C::kScMod, c.count);
+        drain(M->b.k_full, C::kK, c.count);
+        if (F8) drain(M->b.c_full, C::kScMod, c.count);
     } else if (warp == 1) {
         // ---------------- scores S^T = K Q^T
         // A stream's columns are free once the weights of its tile before are
@@ -837,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t run = 0, runs = 0;
         auto wait = [&](uint64_t* bar, uint32_t par) { ok = ok && __all_sync(0xffffffffu, wait_bar(bar, par, ab)); };
         auto give = [&](int u, uint32_t turn) {
-            wait(&M->s_free[turn][u], (free_ph >> (4 * turn + u)) & 1u);
+            wait(&M->b.s_free[turn][u], (free_ph >> (4 * turn + u)) & 1u);
             free_ph ^= 1u << (4 * turn + u);
         };
 #pragma unroll 1
@@ -849,10 +861,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int q_rows = sg.qp == 2 ? 2 * C::kQRows : C::kQRows;
             if (sg.run != run) {
                 // columns and buffers change hands: all products so far are done
-                wait(&M->r_done, runs++ & 1u);
+                wait(&M->b.r_done, runs++ & 1u);
                 run = sg.run;
             }
-            q_places(sg, [&](int k, uint32_t use) { wait(&M->q_full[k], use & 1u); });
+            q_places(sg, [&](int k, uint32_t use) { wait(&M->b.q_full[k], use & 1u); });
 #pragma unroll 1
             for (int i = 0; ok && i < sg.n; ++i) {
                 const int st = sh.stream_at(sg, i);
@@ -860,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t turn = sh.turn_at(sg, i);
                 give(u0, turn);
                 if (sh.wide) give(u0 + 1, turn);
-                wait(&M->k_full[ks], kph);
+                wait(&M->b.k_full[ks], kph);
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
@@ -877,10 +889,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             umma_bf16(d, a + (kk / 4) * (C::kHalfBytes / 16) + (kk % 4) * 2,
                                       b + (uint32_t)((kk / 4) * (q_rows * 8) + (kk % 4) * 2), id, kk ? 1u : 0u);
                     }
-                    umma_commit(&M->s_full[turn][u0]);
-                    if (sh.wide) umma_commit(&M->s_full[turn][u0 + 1]);
-                    umma_commit(&M->k_empty[ks]);
-                    if (i == sg.n - 1) q_places(sg, [&](int k, uint32_t) { umma_commit(&M->q_empty[k]); });
+                    umma_commit(&M->b.s_full[turn][u0]);
+                    if (sh.wide) umma_commit(&M->b.s_full[turn][u0 + 1]);
+                    umma_commit(&M->b.k_empty[ks]);
+                    if (i == sg.n - 1) q_places(sg, [&](int k, uint32_t) { umma_commit(&M->b.q_empty[k]); });
                 }
                 __syncwarp();
                 if (++ks == C::kK) {
@@ -889,7 +901,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        if (elect_one()) umma_commit(&M->done);
+        if (elect_one()) umma_commit(&M->b.done);
         __syncwarp();
     } else if (warp == 3) {
         // ---------------- products O^T += V^T P^T
@@ -904,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Shape sh(sg.rows);
             const uint32_t id = F8 ? idesc_f16_f32(128, sh.cols, true, true) : idesc_bf16_f32(128, sh.cols, true, true);
             const uint32_t set = tmem + kColO * (1u + (nseg & 1u));
-            if (sg.run != run && elect_one()) umma_commit(&M->r_done);
+            if (sg.run != run && elect_one()) umma_commit(&M->b.r_done);
             __syncwarp();
             run = sg.run;
 #pragma unroll 1
@@ -913,7 +925,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // bf16: the V tile as it was loaded; e4m3: the widened one, which
                 // p_full covers, as it does the end of the reads of the loaded one
                 if (!F8) {
-                    wait(&M->v_full[vs], vph);
+                    wait(&M->b.v_full[vs], vph);
                     const int valid = sg.keys - (sg.t0 + i) * kKeyTile;
                     if (ok && valid < kKeyTile) {
                         // rows past the last key hold whatever the pages or this buffer held
@@ -927,10 +939,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __syncwarp();
                     }
                 }
-                wait(&M->p_full[u0], (made >> u0) & 1u);
-                if (sh.wide) wait(&M->p_full[u0 + 1], (made >> (u0 + 1)) & 1u);
+                wait(&M->b.p_full[u0], (made >> u0) & 1u);
+                if (sh.wide) wait(&M->b.p_full[u0 + 1], (made >> (u0 + 1)) & 1u);
                 made ^= (sh.wide ? 3u : 1u) << u0;
-                if (i == 0) wait(&M->e_free[nseg & 1], ((nseg >> 1) & 1u) ^ 1u);   // this set's last segment is stored
+                if (i == 0) wait(&M->b.e_free[nseg & 1], ((nseg >> 1) & 1u) ^ 1u);   // this set's last segment is stored
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
@@ -939,11 +951,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     umma_bf16(d, a, b, id, i >= sh.streams ? 1u : 0u);
 #pragma unroll
                     for (int kk = 1; kk < kKeyTile / 16; ++kk) umma_bf16(d, a + kk * 128, b + kk * 16, id, 1u);
-                    if (F8) mbar_arrive(&M->v_empty[vs]);
-                    umma_commit(F8 ? &M->w_empty[ws] : &M->v_empty[vs]);
-                    umma_commit(&M->pv_done[u0]);
-                    if (sh.wide) umma_commit(&M->pv_done[u0 + 1]);
-                    if (i == sg.n - 1) umma_commit(&M->o_done[nseg & 1]);
+                    if (F8) mbar_arrive(&M->b.v_empty[vs]);
+                    umma_commit(F8 ? &M->b.w_empty[ws] : &M->b.v_empty[vs]);
+                    umma_commit(&M->b.pv_done[u0]);
+                    if (sh.wide) umma_commit(&M->b.pv_done[u0 + 1]);
+                    if (i == sg.n - 1) umma_commit(&M->b.o_done[nseg & 1]);
                 }
                 __syncwarp();
                 if (++vs == C::kV) {
@@ -955,8 +967,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // the tensor core is idle before its memory is given back
         if (elect_one()) {
-            umma_commit(&M->done);
-            mbar_wait_for(&M->done, 0, ab->limit);
+            umma_commit(&M->b.done);
+            mbar_wait_for(&M->b.done, 0, ab->limit);
         }
         __syncwarp();
     } else if (warp == 2) {
@@ -973,7 +985,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // room for (the others never need more to get through this one)
 #pragma unroll 1
             while (more) {
-                uint64_t* bar = &M->seg_empty[made % kSegs];
+                uint64_t* bar = &M->b.seg_empty[made % kSegs];
                 const uint32_t par = ((made / kSegs) & 1u) ^ 1u;
                 if (made == c.seg)
                     ok = __all_sync(0xffffffffu, wait_bar(bar, par, ab));
@@ -993,7 +1005,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (more)
                         o = SegInfo{s.r, s.j, s.h, s.t0, s.t1 - s.t0, s.tiles, s.keys, s.rows, s.tok, s.head, line, run,
                                     both ? 2 : place, use, s.q};
-                    mbar_arrive(&M->seg_full[made % kSegs]);
+                    mbar_arrive(&M->b.seg_full[made % kSegs]);
                 }
                 __syncwarp();
                 if (more) line += (uint32_t)(s.t1 - s.t0);
@@ -1012,9 +1024,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 last = step(c);
             }
             if (!ok) break;
-            if (lane == 0) mbar_arrive(&M->seg_empty[(c.seg - 1) % kSegs]);
+            if (lane == 0) mbar_arrive(&M->b.seg_empty[(c.seg - 1) % kSegs]);
         }
-        drain(M->v_full, C::kV, c.count);
+        drain(M->b.v_full, C::kV, c.count);
     } else if (warp >= 4 + 4 * kUnits) {
         // ---------------- Q rows of the segment to come, and the finished one
         constexpr int kLanes = HD / 8, kStep = 128 / kLanes;  // 8 values per lane; rows per step
@@ -1022,9 +1034,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // segment k's rows into its Q buffer; false at the end or when a wait ran out
         auto bring = [&](uint32_t k) {
             const SegInfo& s = M->seg[k % kSegs];
-            bool got = wait_bar(&M->seg_full[k % kSegs], (k / kSegs) & 1u, ab);
+            bool got = wait_bar(&M->b.seg_full[k % kSegs], (k / kSegs) & 1u, ab);
             if (got && s.rows > 0)
-                q_places(s, [&](int b, uint32_t use) { got = got && wait_bar(&M->q_empty[b], (use & 1u) ^ 1u, ab); });
+                q_places(s, [&](int b, uint32_t use) { got = got && wait_bar(&M->b.q_empty[b], (use & 1u) ^ 1u, ab); });
             if (named_any(5, 128, !got)) return false;
             if (s.rows == 0) return false;
             const int cols = Shape(s.rows).cols, q_rows = s.qp == 2 ? 2 * C::kQRows : C::kQRows;
@@ -1042,7 +1054,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   policy_evict_normal());
                 } else {
                     uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (in) v = __ldg(reinterpret_cast<const uint4*>(src));
+                    if (in) v = load16(src);
                     uint2 hi, lo;
                     const float sc = split_e4m3<kLanes>(v, hi, lo);
                     *reinterpret_cast<uint2*>(qt + swz_f8<HD>(row, x / 2) + (x & 1) * 8) = hi;
@@ -1052,14 +1064,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!F8) cp_async_wait_all();
             fence_proxy_async();
-            q_places(s, [&](int b, uint32_t) { mbar_arrive(&M->q_full[b]); });
+            q_places(s, [&](int b, uint32_t) { mbar_arrive(&M->b.q_full[b]); });
             return true;
         };
         bool have = bring(0), after = have && bring(1);
 #pragma unroll 1
         for (; have; ++nseg) {
             finish_segment<HD>(p, M->seg[nseg % kSegs], M, tmem, nseg);
-            if (lane == 0) mbar_arrive(&M->seg_empty[nseg % kSegs]);
+            if (lane == 0) mbar_arrive(&M->b.seg_empty[nseg % kSegs]);
             have = after;
             after = after && bring(nseg + 2);
         }
@@ -1070,7 +1082,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (;; ++nseg) {
             const int at = nseg % kSegs;
-            const bool got = wait_bar(&M->seg_full[at], (nseg / kSegs) & 1u, ab);
+            const bool got = wait_bar(&M->b.seg_full[at], (nseg / kSegs) & 1u, ab);
             // the unit agrees on whether there is a segment; what the one before
             // left in its shared memory is no longer read
             if (named_any(1 + u, 128, !got)) break;
@@ -1078,7 +1090,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (s.rows == 0) break;
             soft_segment<HD, F8>(p, s, M, smem, tmem, u, st);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&M->seg_empty[at]);
+            if (lane == 0) mbar_arrive(&M->b.seg_empty[at]);
         }
     }
     tc_fence_before();
@@ -1095,6 +1107,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // in a later one: a warp per row, pieces in the order of the keys.
 template <int HD>
 __global__ void __launch_bounds__(256) attn_paged_join(const PagedParams p, int grid) {
+    pdl_launch_dependents();
     pdl_wait();
     const JoinDesc d = p.desc[blockIdx.x];
     const int c = blockIdx.x, row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -1136,7 +1149,7 @@ cudaError_t launch(const Maps& maps, const PagedParams& p, int grid, cudaStream_
     cudaError_t e = allow_smem(attn_paged_kernel<HD, F8>, smem);
     if (e != cudaSuccess) return e;
     prof_begin(kPAttnPaged, s);
-    e = launch_kernel(attn_paged_kernel<HD, F8>, dim3(grid), dim3(kThreads), smem, s, false, maps, p);
+    e = launch_kernel(attn_paged_kernel<HD, F8>, dim3(grid), dim3(kThreads), smem, s, true, maps, p);
     prof_end(s);
     if (e != cudaSuccess) return e;
     prof_begin(kPAttnPagedJoin, s);

@@ -73,18 +73,19 @@ DSPARK_HD_CALL int64_t plan_request_tiles(PlanInput p, int r) {
 // How many of `grid` CTAs get a span: none is left empty between two others,
 // since every CTA from an item's first to its last leaves a piece.
 DSPARK_HD int plan_spans(int64_t total, int grid) { return total < grid ? (int)total : grid; }
-// First tile of CTA c of n = plan_spans() (c = n: the end).
-DSPARK_HD_CALL int64_t plan_cut(int64_t total, int c, int n) { return total / n * c + total % n * c / n; }
-// The CTA whose span holds tile g.
-DSPARK_HD_CALL int plan_owner(int64_t total, int64_t g, int n) {
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (plan_cut(total, mid, n) <= g) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
+// First tile of CTA c of n = plan_spans() (c = n: the end): floor(total c / n)
+// without the product, which could pass 64 bits.
+struct Span {
+    int64_t begin, end;
+};
+DSPARK_HD_CALL Span plan_span(int64_t total, int c, int n) {
+    const int64_t q = total / n;
+    const uint32_t rest = (uint32_t)(total - q * n), u = (uint32_t)n;      // rest (c + 1) <= n^2: grids are far below 2^16
+    return Span{q * c + rest * (uint32_t)c / u, q * (c + 1) + rest * ((uint32_t)c + 1u) / u};
 }
+DSPARK_HD int64_t plan_cut(int64_t total, int c, int n) { return c == n ? total : plan_span(total, c, n).begin; }
+// The CTA whose span holds tile g: the largest c with total c / n < g + 1.
+DSPARK_HD_CALL int plan_owner(int64_t total, int64_t g, int n) { return (int)(((g + 1) * n - 1) / total); }
 
 // One CTA's piece of an item: key tiles [t0, t1) of tiles.
 struct Segment {

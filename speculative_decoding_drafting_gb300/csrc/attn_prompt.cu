@@ -71,12 +71,19 @@ struct Params {
     const int2* list;                   // (sequence, pair of row tiles), longest first
     const int* count;                   // entries of the list
     int most;                           // entries that the workspace holds
+    int single;
     uint16_t* out;
     float* lse;
     void* ws;
     int B, T, heads, kv_heads, group, toks;   // toks: tokens of a row tile
     float scale2;                       // scale log2(e)
 };
+
+// Pairs of row tiles of a sequence.
+__device__ __forceinline__ int pairs_of(const Params& p, int b) {
+    const RowRange r = row_range(p.seq_off, b, p.T);
+    return (r.b - r.a + 2 * p.toks - 1) / (2 * p.toks);
+}
 
 // The list of (sequence, pair of row tiles) entries in descending order of
 // their length (the tile's place in its sequence), by a counting sort over
@@ -143,6 +150,33 @@ struct Item {
     __device__ __forceinline__ int n(int s) const { return s ? n1 : n0; }
     __device__ __forceinline__ int tiles() const { return max(n0, n1); }
 };
+
+// Entry k of the list in the order of the sequences, and how many there are,
+// by one warp.
+__device__ __forceinline__ int2 entry_of(const Params& p, int64_t k, int64_t& count) {
+    const int lane = threadIdx.x & 31;
+    int2 e = make_int2(0, 0);
+    count = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const int b = b0 + lane;
+        const int n = b < p.B ? pairs_of(p, b) : 0;
+        int64_t upto = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
+        }
+        const int64_t first = count + upto - n;
+        const uint32_t m = __ballot_sync(0xffffffffu, first <= k && k < first + n);
+        if (m) {
+            e.x = b0 + __ffs(m) - 1;
+            e.y = (int)(k - __shfl_sync(0xffffffffu, first, __ffs(m) - 1));
+        }
+        count += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return e;
+}
 
 __device__ __forceinline__ bool get_item(const Params& p, int64_t total, int round, Item& it) {
     const int64_t n = gridDim.x, c = blockIdx.x;
@@ -248,6 +282,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = M->tmem;
     pdl_wait();                                               // the list
+    if (p.single) {
+        if (blockIdx.x == 0) check_requests(p.seq_off, nullptr, p.B, p.T, 0, p.ws);
+        if (warp == 2) {
+            int64_t count;
+            const int2 e = entry_of(p, blockIdx.x / p.kv_heads, count);
+            if (lane == 0) {
+                const_cast<int2*>(p.list)[blockIdx.x / p.kv_heads] = e;
+                *const_cast<int*>(p.count) = (int)min(count, (int64_t)p.most);
+            }
+        }
+        __syncthreads();
+    }
     const int64_t total = (int64_t)__ldcg(p.count) * p.kv_heads;
     Item it;
 
@@ -596,11 +642,13 @@ cudaError_t launch(const Maps& maps, const Params& p, cudaStream_t s) {
     const size_t smem = smem_bytes<HD>();
     cudaError_t e = allow_smem(attn_prompt_kernel<HD>, smem);
     if (e != cudaSuccess) return e;
-    prof_begin(kPAttnPromptPlan, s);
-    e = launch_kernel(attn_prompt_plan, dim3(1), dim3(kPlanThreads), 0, s, false, p, const_cast<int2*>(p.list),
-                      const_cast<int*>(p.count));
-    prof_end(s);
-    if (e != cudaSuccess) return e;
+    if (!p.single) {
+        prof_begin(kPAttnPromptPlan, s);
+        e = launch_kernel(attn_prompt_plan, dim3(1), dim3(kPlanThreads), 0, s, false, p, const_cast<int2*>(p.list),
+                          const_cast<int*>(p.count));
+        prof_end(s);
+        if (e != cudaSuccess) return e;
+    }
     prof_begin(kPAttnPrompt, s);
     e = launch_kernel(attn_prompt_kernel<HD>, dim3(num_sms()), dim3(kThreads), smem, s, true, maps, p);
     prof_end(s);
@@ -634,6 +682,7 @@ cudaError_t launch_attn_prompt(const PromptArgs& a, cudaStream_t s) {
     p.group = a.n_heads / a.n_kv_heads;
     p.toks = tile_tokens(p.group);
     p.most = (int)list_entries(a.B, a.T, p.group);
+    p.single = (int64_t)p.most * p.kv_heads <= num_sms();
     // hidden keys are infinite before the scale: at scale 0 the smallest normal
     // number keeps them so, and every finite score still counts as 0
     p.scale2 = a.scale == 0.f ? FLT_MIN : a.scale * kLog2e;

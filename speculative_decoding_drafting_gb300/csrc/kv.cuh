@@ -10,16 +10,17 @@ namespace dspark {
 
 // Request r's rows [a, b) of a packed axis of T tokens; offsets outside
 // [0, T] are clamped and decreasing ones make the request empty, so that
-// every row index stays in range whatever the array holds.
+// every row index stays in range whatever the array holds.  (Plain loads: the
+// read-only path may not see what a kernel wrote that this one overlaps.)
 struct RowRange {
     int a, b;
 };
 __device__ __forceinline__ RowRange row_range(const int32_t* off, int r, int T) {
-    const int a = min(max(__ldg(off + r), 0), T), b = min(max(__ldg(off + r + 1), 0), T);
+    const int a = min(max(off[r], 0), T), b = min(max(off[r + 1], 0), T);
     return RowRange{a, max(a, b)};
 }
 __device__ __forceinline__ int clamped_len(const int32_t* kv_len, int r, int64_t most) {
-    return (int)min((int64_t)max(__ldg(kv_len + r), 0), most);
+    return (int)min((int64_t)max(kv_len[r], 0), most);
 }
 
 // The last request whose offset is <= t (0 if none), by all 32 lanes of a
@@ -47,10 +48,10 @@ __device__ __forceinline__ void check_requests(const int32_t* off, const int32_t
                                                void* ws) {
     bool bad = false;
     for (int r = threadIdx.x; r < R; r += blockDim.x) {
-        const int a = __ldg(off + r), b = __ldg(off + r + 1);
+        const int a = off[r], b = off[r + 1];
         bad |= a < 0 || b > T || b < a;
         if (kv_len) {
-            const int n = __ldg(kv_len + r);
+            const int n = kv_len[r];
             bad |= n < 0 || n > most;
         }
     }
