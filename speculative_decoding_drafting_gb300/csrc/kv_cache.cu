@@ -4,9 +4,12 @@
 // Both move each row once: a row is head_dim values of one token and head, 8
 // or 16 lanes hold 8 values each (16 bytes of bf16), and a warp takes one
 // token with all its heads, K and V, so that its loads are in flight together.
+#include <type_traits>
+
 #include "kernels.h"
 #include "kv.cuh"
 #include "profile.h"
+#include "sm100.cuh"
 
 namespace dspark {
 
@@ -27,22 +30,40 @@ __device__ __forceinline__ uint32_t bf16x2_abs_bits(uint32_t w) { return w & 0x7
 // value across one.
 __device__ __forceinline__ uint2 quantise8(uint4 w, float inv) {
     const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-    uint32_t out[2];
+    const uint64_t k = pack2(513.f, 513.f), i2 = pack2(inv, inv), minus = pack2(-1.f, -1.f);
+    uint32_t half[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint32_t half[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t x = in[2 * h + i];
-            float2 t = make_float2(bf16_bits_to_float(x & 0xFFFFu) * inv, bf16_bits_to_float(x >> 16) * inv);
-            const float cx = t.x * 513.f, cy = t.y * 513.f;
-            t.x = __fsub_rn(cx, __fsub_rn(cx, t.x));
-            t.y = __fsub_rn(cy, __fsub_rn(cy, t.y));
-            half[i] = __nv_cvt_float2_to_fp8x2(t, __NV_SATFINITE, __NV_E4M3);
-        }
-        out[h] = half[0] | (half[1] << 16);
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t t = mul2x(pack2(bf16_bits_to_float(in[i] & 0xFFFFu), bf16_bits_to_float(in[i] >> 16)), i2);
+        const uint64_t c = mul2x(t, k);
+        float2 y;
+        unpack2(fma2(fma2(t, minus, c), minus, c), y.x, y.y);             // c - (c - t)
+        half[i] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
     }
-    return make_uint2(out[0], out[1]);
+    return make_uint2(half[0] | (half[1] << 16), half[2] | (half[3] << 16));
+}
+
+// A warp's row vectors of one step: kSteps of K, then kSteps of V.
+constexpr int kSteps = 4, kVecs = 2 * kSteps;
+
+// The largest of each of the kVecs values over the LANES lanes of a row: lane
+// part holds the one of vector vec_of(part) afterwards.  Each exchange halves
+// the vectors instead of repeating the reduction for each (LANES / 8 * 8
+// exchanges against 8 log2(LANES)).
+template <int LANES>
+__device__ __forceinline__ uint32_t row_maxima(uint32_t (&m)[kVecs], int part) {
+#pragma unroll
+    for (int n = kVecs / 2, o = LANES / 2; n > 0; n >>= 1, o >>= 1) {
+        const bool upper = part & o;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const uint32_t give = upper ? m[i] : m[i + n], keep = upper ? m[i + n] : m[i];
+            m[i] = __vmaxu2(keep, __shfl_xor_sync(0xffffffffu, give, o));
+        }
+    }
+#pragma unroll
+    for (int o = LANES / 16; o > 0; o >>= 1) m[0] = __vmaxu2(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
+    return m[0];
 }
 
 struct WriteParams {
@@ -78,50 +99,59 @@ __global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(WriteParams p) {
     }
     const int slot = pos & ((1 << p.page_log2) - 1);
     const size_t row0 = (((size_t)page * p.heads) << p.page_log2) + slot;    // head 0's row of the cache
+    for (int h0 = 0; h0 < p.heads; h0 += kSteps * kRows) {
+        // K's and V's loads are all in flight before the first is used
+        uint4 w[kVecs];
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-        const uint16_t* src = p.src[kv] + (size_t)t * p.stride[kv];
-#pragma unroll 4
-        for (int h0 = 0; h0 < p.heads; h0 += kRows) {
-            const int h = h0 + sub;
-            const bool in = h < p.heads;
-            uint4 w = make_uint4(0u, 0u, 0u, 0u);
-            if (in) w = __ldcs(reinterpret_cast<const uint4*>(src + (size_t)h * HD + part * 8));
+        for (int i = 0; i < kVecs; ++i) {
+            const int kv = i / kSteps, h = h0 + (i % kSteps) * kRows + sub;
+            w[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (h < p.heads)
+                w[i] = __ldcs(reinterpret_cast<const uint4*>(p.src[kv] + (size_t)t * p.stride[kv] + (size_t)h * HD + part * 8));
+        }
+        float inv = 0.f;
+        if (F8) {
+            // largest magnitude of a row: bf16 magnitudes order as their bits do
+            // (a NaN's lie above infinity's)
+            uint32_t m[kVecs];
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i)
+                m[i] = __vmaxu2(__vmaxu2(bf16x2_abs_bits(w[i].x), bf16x2_abs_bits(w[i].y)),
+                                __vmaxu2(bf16x2_abs_bits(w[i].z), bf16x2_abs_bits(w[i].w)));
+            // each lane now takes one row: one scale and one reciprocal for all the
+            // warp's rows, where every lane would divide for its own vectors
+            const uint32_t big = row_maxima<kLanes>(m, part);
+            const float a = bf16_bits_to_float(max(big & 0xFFFFu, big >> 16));
+            const int i = part / (kLanes / kVecs), kv = i / kSteps, h = h0 + (i % kSteps) * kRows + sub;
+            if (part % (kLanes / kVecs) == 0 && h < p.heads) p.scale[kv][row0 + ((size_t)h << p.page_log2)] = __fdiv_rn(a, 448.f);
+            // below 2^-100 the reciprocal would overflow float32: such rows (a
+            // negative sign marks them) are scaled up by 2^64 first, which changes
+            // no quotient; rows that are zero or not finite get codes of zero
+            if (a > 0.f && a < INFINITY)
+                inv = a < 7.888609e-31f ? -__fdiv_rn(448.f, a * 1.8446744e19f) : __fdiv_rn(448.f, a);
+        }
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const int kv = i / kSteps, h = h0 + (i % kSteps) * kRows + sub;
             const size_t row = row0 + ((size_t)h << p.page_log2);
             if (!F8) {
-                if (in) *reinterpret_cast<uint4*>(p.dst[kv] + (row * HD + part * 8) * 2) = w;
+                if (h < p.heads) *reinterpret_cast<uint4*>(p.dst[kv] + (row * HD + part * 8) * 2) = w[i];
                 continue;
             }
-            // largest magnitude of the row: bf16 magnitudes order as their bits do
-            // (a NaN's lie above infinity's)
-            uint32_t m = __vmaxu2(__vmaxu2(bf16x2_abs_bits(w.x), bf16x2_abs_bits(w.y)),
-                                  __vmaxu2(bf16x2_abs_bits(w.z), bf16x2_abs_bits(w.w)));
+            const float f = __shfl_sync(0xffffffffu, inv, sub * kLanes + i * (kLanes / kVecs));
+            if (f < 0.f) {
+                uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                const __nv_bfloat162 up = __floats2bfloat162_rn(1.8446744e19f, 1.8446744e19f);
 #pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float a = bf16_bits_to_float(max(m & 0xFFFFu, m >> 16));
-            const float scale = __fdiv_rn(a, 448.f);
-            uint2 code = make_uint2(0u, 0u);
-            // below 2^-100 the reciprocal would overflow float32: such rows are
-            // scaled up by 2^64 first, which changes no quotient
-            const bool tiny = a < 7.888609e-31f;
-            if (a > 0.f && a < INFINITY) {
-                if (!tiny) {
-                    code = quantise8(w, __fdiv_rn(448.f, a));
-                } else {
-                    uint32_t x[4] = {w.x, w.y, w.z, w.w};
-                    const __nv_bfloat162 up = __floats2bfloat162_rn(1.8446744e19f, 1.8446744e19f);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const __nv_bfloat162 y = __hmul2(reinterpret_cast<const __nv_bfloat162&>(x[i]), up);
-                        x[i] = reinterpret_cast<const uint32_t&>(y);
-                    }
-                    code = quantise8(make_uint4(x[0], x[1], x[2], x[3]), __fdiv_rn(448.f, a * 1.8446744e19f));
+                for (int e = 0; e < 4; ++e) {
+                    const __nv_bfloat162 y = __hmul2(reinterpret_cast<const __nv_bfloat162&>(x[e]), up);
+                    x[e] = reinterpret_cast<const uint32_t&>(y);
                 }
+                w[i] = make_uint4(x[0], x[1], x[2], x[3]);
             }
-            if (in) {
-                *reinterpret_cast<uint2*>(p.dst[kv] + row * HD + part * 8) = code;
-                if (part == 0) p.scale[kv][row] = scale;
-            }
+            uint2 code = quantise8(w[i], fabsf(f));
+            if (f == 0.f) code = make_uint2(0u, 0u);
+            if (h < p.heads) *reinterpret_cast<uint2*>(p.dst[kv] + row * HD + part * 8) = code;
         }
     }
 }
@@ -161,31 +191,41 @@ __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(ReadParams p) {
     if (!ok && lane == 0) raise_status(p.ws, kStatBadPage);
     const int slot = pos & ((1 << p.page_log2) - 1);
     const size_t row0 = (((size_t)(ok ? page : 0) * p.heads) << p.page_log2) + slot;
+    for (int h0 = 0; h0 < p.heads; h0 += kSteps * kRows) {
+        // K's and V's loads are all in flight before the first is used
+        using Vec = std::conditional_t<F8, uint2, uint4>;
+        Vec w[kVecs];
+        float scale[kVecs];
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-        uint16_t* dst = p.dst[kv] + (size_t)t * p.heads * HD;
-#pragma unroll 4
-        for (int h0 = 0; h0 < p.heads; h0 += kRows) {
-            const int h = h0 + sub;
-            if (h >= p.heads) continue;
+        for (int i = 0; i < kVecs; ++i) {
+            const int kv = i / kSteps, h = h0 + (i % kSteps) * kRows + sub;
             const size_t row = row0 + ((size_t)h << p.page_log2);
-            uint4 o = make_uint4(0u, 0u, 0u, 0u);
-            if (ok && !F8) o = __ldcs(reinterpret_cast<const uint4*>(p.src[kv] + (row * HD + part * 8) * 2));
-            if (ok && F8) {
-                const uint2 c = __ldcs(reinterpret_cast<const uint2*>(p.src[kv] + row * HD + part * 8));
-                const float s = __ldg(p.scale[kv] + row);
-                const uint2 a = e4m3x4_to_bf16x4(c.x), b = e4m3x4_to_bf16x4(c.y);
+            w[i] = Vec{};
+            scale[i] = 0.f;
+            if (!ok || h >= p.heads) continue;
+            w[i] = __ldcs(reinterpret_cast<const Vec*>(p.src[kv] + row * HD * (F8 ? 1 : 2) + part * sizeof(Vec)));
+            if (F8) scale[i] = __ldg(p.scale[kv] + row);
+        }
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const int kv = i / kSteps, h = h0 + (i % kSteps) * kRows + sub;
+            if (h >= p.heads) continue;
+            uint4 o;
+            if constexpr (F8) {
+                const uint2 a = e4m3x4_to_bf16x4(w[i].x), b = e4m3x4_to_bf16x4(w[i].y);
                 const uint32_t x[4] = {a.x, a.y, b.x, b.y};
                 uint32_t y[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const __nv_bfloat162 v = __floats2bfloat162_rn(bf16_bits_to_float(x[i] & 0xFFFFu) * s,
-                                                                   bf16_bits_to_float(x[i] >> 16) * s);
-                    y[i] = reinterpret_cast<const uint32_t&>(v);
+                for (int e = 0; e < 4; ++e) {
+                    const __nv_bfloat162 v = __floats2bfloat162_rn(bf16_bits_to_float(x[e] & 0xFFFFu) * scale[i],
+                                                                   bf16_bits_to_float(x[e] >> 16) * scale[i]);
+                    y[e] = reinterpret_cast<const uint32_t&>(v);
                 }
                 o = make_uint4(y[0], y[1], y[2], y[3]);
+            } else {
+                o = w[i];
             }
-            __stcs(reinterpret_cast<uint4*>(dst + (size_t)h * HD + part * 8), o);
+            __stcs(reinterpret_cast<uint4*>(p.dst[kv] + ((size_t)t * p.heads + h) * HD + part * 8), o);
         }
     }
 }
