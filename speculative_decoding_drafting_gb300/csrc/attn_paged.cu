@@ -299,7 +299,7 @@ struct SoftState {
 // One segment's key tiles of unit u.  The unit's threads all
 // walk the same barriers even after a wait ran out (the results are then not
 // stored), so that no named barrier is left waiting.
-template <int HD, bool F8>
+template <int HD, bool F8, int N>
 __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo& sg, Misc* M, uint8_t* smem,
                                              uint32_t tmem, int u, SoftState& st) {
     using C = Cfg<HD, F8>;
@@ -307,9 +307,11 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
     const Shape sh(sg.rows);
     const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
     const int tr = wq * 32 + lane;                            // key of the tile; head_dim index of O^T
-    const int cols = min(sh.cols, kUnitRows);                 // 16 or 32 rows of this unit
+    constexpr int kB = N < 16 ? N : 16;                       // columns loaded at a time
+    const bool wide = N == kUnitRows && sh.wide;
+    const int streams = N == kUnitRows ? sh.streams : kUnits;
     const int bar = 1 + u, parity = st.seg & 1;
-    const int stream = sh.stream_of(u), coff = sh.wide ? (u & 1) * kUnitRows : 0;
+    const int stream = wide ? u >> 1 : u, coff = wide ? (u & 1) * kUnitRows : 0;
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
     const uint32_t tS0 = tmem + lanes + (uint32_t)(u * kUnitRows);
     const uint32_t tO = tmem + lanes + kColO * (1 + parity) + (uint32_t)(u * kUnitRows);
@@ -317,7 +319,7 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
 
     // this unit's rows (what the segment before left is no longer read)
     if (F8) q_places(sg, [&](int k, uint32_t use) { wait_bar(&M->b.q_full[k], use & 1u, ab); });
-    if (tr < cols) {
+    if (tr < N) {
         M->ref[u][tr] = kFloorRef;
         M->nref[u][tr] = -kFloorRef;
         if (F8) M->qm[u][tr] = M->q_scale[(sg.qp == 1 ? C::kQRows : 0) + coff + tr];
@@ -332,7 +334,7 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
     const float scale2 = p.scale2;
 
 #pragma unroll 1
-    for (int i = (stream - sh.stream_at(sg, 0)) & (sh.streams - 1); i < n; i += sh.streams) {
+    for (int i = (stream - sh.stream_at(sg, 0)) & (streams - 1); i < n; i += streams) {
         const int key = (t0 + i) * kKeyTile + tr;
         const bool edge = (t0 + i + 1) * kKeyTile > lim0;     // some row does not see the whole tile
         // new token k sees the key if kv_len - q_len + k >= key: from this row on
@@ -356,7 +358,7 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
             __syncwarp();
             // a wide tile's scales are read by two units
             if (lane == 0) mbar_arrive(&M->b.c_empty[s]);
-            if (!sh.wide && lane == 0) mbar_arrive(&M->b.c_empty[s]);
+            if (!wide && lane == 0) mbar_arrive(&M->b.c_empty[s]);
             if (edge && key >= sg.keys) vs = 1.f;             // no key here: any scale
             if (vs < 7.888609e-31f) vs = 7.888609e-31f;       // 2^-100; a row of zeros has scale 0
             lvs = lg2_approx(vs);
@@ -364,18 +366,17 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
         }
 
         // base-2 exponents of the weights, relative to the references
-        float t[kUnitRows];
+        float t[32];
         const uint64_t mul2 = pack2(mul, mul), lvs2 = pack2(lvs, lvs);
 #pragma unroll 1
         for (bool raised = false;; raised = true) {
             float top = -INFINITY;
 #pragma unroll
-            for (int c0 = 0; c0 < kUnitRows; c0 += 16) {
-                if (c0 >= cols) break;
-                float x[16];
-                tmem_ldn<16>(tS + (uint32_t)c0, x);
+            for (int c0 = 0; c0 < N; c0 += kB) {
+                float x[kB];
+                tmem_ldn<kB>(tS + (uint32_t)c0, x);
 #pragma unroll
-                for (int c = 0; c < 16; c += 2) {
+                for (int c = 0; c < kB; c += 2) {
                     uint64_t y = pack2(x[c], x[c + 1]);
                     const float2 r = *reinterpret_cast<const float2*>(&M->nref[u][c0 + c]);
                     if (F8) {
@@ -388,17 +389,17 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
                 }
                 if (edge) {
 #pragma unroll
-                    for (int c = 0; c < 16; ++c)
+                    for (int c = 0; c < kB; ++c)
                         if (c0 + c < seen) t[c0 + c] = -INFINITY;
                 }
 #pragma unroll
-                for (int c = 0; c < 16; ++c) top = fmaxf(top, t[c0 + c]);
+                for (int c = 0; c < kB; ++c) top = fmaxf(top, t[c0 + c]);
             }
             // (raised once: scores of 2^28 and more round by more than the threshold)
             if (raised || !named_any(bar, 128, top > C::kLift + C::kLazy)) break;
             // one is too large: raise the references to the largest scores so far
 #pragma unroll 1
-            for (int c0 = 0; c0 < cols; c0 += 4) {
+            for (int c0 = 0; c0 < N; c0 += 4) {
                 float x[4], mine = 0.f;
                 tmem_ldn<4>(tS + (uint32_t)c0, x);
 #pragma unroll
@@ -411,7 +412,7 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
                 if (lane < 4) M->red[u][wq][c0 + lane] = mine;
             }
             named_sync(bar, 128);
-            if (tr < cols) {
+            if (tr < N) {
                 const float old = M->ref[u][tr];
                 const float ref = fmaxf(fmaxf(fmaxf(M->red[u][0][tr], M->red[u][1][tr]),
                                               fmaxf(M->red[u][2][tr], M->red[u][3][tr])), old);
@@ -420,12 +421,12 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
                 M->fac[u][tr] = ex2_approx(old - ref);
             }
             named_sync(bar, 128);
-            if (lane < cols) l *= M->fac[u][lane];
-            if (i >= sh.streams) {                            // the accumulator holds earlier tiles
+            if (lane < N) l *= M->fac[u][lane];
+            if (i >= streams) {                            // the accumulator holds earlier tiles
                 wait_bar(&M->b.pv_done[u], (st.tiles - 1u) & 1u, ab);
                 tc_fence_after();
 #pragma unroll 1
-                for (int c0 = 0; c0 < cols; c0 += 8) {
+                for (int c0 = 0; c0 < N; c0 += 8) {
                     float o[8];
                     tmem_ldn<8>(tO + c0, o);
 #pragma unroll
@@ -442,11 +443,10 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
         if (st.tiles > 0) wait_bar(&M->b.pv_done[u], (st.tiles - 1u) & 1u, ab);
         ++st.tiles;
 #pragma unroll
-        for (int c0 = 0; c0 < kUnitRows; c0 += 16) {
-            if (c0 >= cols) break;
-            uint32_t pk[8];
+        for (int c0 = 0; c0 < N; c0 += 8) {
+            uint32_t pk[4];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
+            for (int c = 0; c < 4; ++c) {
                 float& a = t[c0 + 2 * c];
                 float& b = t[c0 + 2 * c + 1];
                 a = ex2_approx(a);
@@ -461,9 +461,7 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
                     pk[c] = reinterpret_cast<const uint32_t&>(h);
                 }
             }
-            uint8_t* dst = P + (c0 / 8) * (kKeyTile * 16) + tr * 16;
-            *reinterpret_cast<uint4*>(dst) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-            *reinterpret_cast<uint4*>(dst + kKeyTile * 16) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+            *reinterpret_cast<uint4*>(P + (c0 / 8) * (kKeyTile * 16) + tr * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
         }
         if constexpr (F8) {
             // Widen V's e4m3 codes, 16 at a time; two units share a wide tile.
@@ -477,32 +475,50 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
             uint8_t* dst = smem + C::kOffW + (size_t)d * C::kTileBytes;
             constexpr int kPieces = kKeyTile * HD / 16, kPer = HD / 16;
             const int valid = edge ? sg.keys - (t0 + i) * kKeyTile : kKeyTile;   // rows with a key
-            auto widen = [&](int x0, auto count, int step) {
-                constexpr int kN = decltype(count)::value, kB = 2;
+            // A thread's pieces lie `step` pieces, a multiple of 8 rows, apart: their
+            // swizzle is the same.  It reads the two 8-byte halves of a piece in an
+            // order that differs between lanes, so that neither the loads nor the
+            // stores of a quarter warp meet in a bank.
+            auto widen = [&](int x0, auto count, auto step) {
+                constexpr int kN = decltype(count)::value, kStep = decltype(step)::value, kB = 2;
+                const int row0 = x0 / kPer, c0 = (x0 % kPer) * 2, sw = row0 & 7;
+                const int flip = HD == 128 ? ((tr >> 2) ^ (tr >> 3)) & 1 : (tr >> 3) & 1;
+                const uint8_t* from = src + x0 * 16;
+                uint8_t* to = dst + (c0 / 8) * C::kHalfBytes + row0 * 128;
+                const int a = flip * 8, b = 8 - a;
+                const int ta = (((c0 & 7) + flip) ^ sw) * 16, tb = (((c0 & 7) + 1 - flip) ^ sw) * 16;
 #pragma unroll 1
                 for (int h = 0; h < kN; h += kB) {
-                    uint4 v[kB];
-#pragma unroll
-                    for (int k = 0; k < kB; ++k) v[k] = *reinterpret_cast<const uint4*>(src + (x0 + (h + k) * step) * 16);
+                    uint2 v[2 * kB];
 #pragma unroll
                     for (int k = 0; k < kB; ++k) {
-                        const int x = x0 + (h + k) * step;
-                        const int row = x / kPer, c0 = (x % kPer) * 2;
-                        if (row >= valid) v[k] = make_uint4(0u, 0u, 0u, 0u);
-                        uint8_t* rowp = dst + (c0 / 8) * C::kHalfBytes + row * 128;
-                        const int c8 = c0 & 7, sw = row & 7;
-                        // lanes of the second half write their pieces in the other order: no bank conflicts
-                        const bool flip = c0 >= 8;
-                        const uint4 lo = e4m3x8_to_half8(v[k].x, v[k].y), hi = e4m3x8_to_half8(v[k].z, v[k].w);
-                        *reinterpret_cast<uint4*>(rowp + ((c8 + (flip ? 1 : 0)) ^ sw) * 16) = flip ? hi : lo;
-                        *reinterpret_cast<uint4*>(rowp + ((c8 + (flip ? 0 : 1)) ^ sw) * 16) = flip ? lo : hi;
+                        v[2 * k] = *reinterpret_cast<const uint2*>(from + k * kStep * 16 + a);
+                        v[2 * k + 1] = *reinterpret_cast<const uint2*>(from + k * kStep * 16 + b);
+                    }
+#pragma unroll
+                    for (int k = 0; k < kB; ++k) {
+                        *reinterpret_cast<uint4*>(to + k * (kStep / kPer) * 128 + ta) = e4m3x8_to_half8(v[2 * k].x, v[2 * k].y);
+                        *reinterpret_cast<uint4*>(to + k * (kStep / kPer) * 128 + tb) =
+                            e4m3x8_to_half8(v[2 * k + 1].x, v[2 * k + 1].y);
+                    }
+                    from += kB * kStep * 16;
+                    to += kB * (kStep / kPer) * 128;
+                }
+                // rows without a key become zeros, whatever their places hold
+                if (valid < kKeyTile) {
+#pragma unroll 1
+                    for (int h = kN; h > 0; --h) {
+                        to -= (kStep / kPer) * 128;
+                        if (row0 + (h - 1) * (kStep / kPer) < valid) break;
+                        *reinterpret_cast<uint4*>(to + ta) = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4*>(to + tb) = make_uint4(0u, 0u, 0u, 0u);
                     }
                 }
             };
-            if (sh.wide)
-                widen(coff * 4 + tr, std::integral_constant<int, kPieces / 256>{}, 256);
+            if (wide)
+                widen(coff * 4 + tr, std::integral_constant<int, kPieces / 256>{}, std::integral_constant<int, 256>{});
             else
-                widen(tr, std::integral_constant<int, kPieces / 128>{}, 128);
+                widen(tr, std::integral_constant<int, kPieces / 128>{}, std::integral_constant<int, 128>{});
         }
         fence_proxy_async();
         tc_fence_before();
@@ -513,12 +529,9 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
         // the registers
         if (F8) {
 #pragma unroll
-            for (int c = 0; c < kUnitRows; ++c) t[c] *= ivs;
+            for (int c = 0; c < N; ++c) t[c] *= ivs;
         }
-        if (cols > 16)
-            l += lane_sums<32>(t);
-        else
-            l += lane_sums<16>(t);
+        l += lane_sums<N>(t);
     }
 
     // hand the sums on; the segment before the last has been read
@@ -526,7 +539,7 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
         M->red[u][wq][lane] = l;
         wait_bar(&M->b.e_free[parity], ((st.seg >> 1) & 1u) ^ 1u, ab);
         named_sync(bar, 128);
-        if (tr < cols) {
+        if (tr < N) {
             M->fin_l[parity][u][tr] = (M->red[u][0][tr] + M->red[u][1][tr]) + (M->red[u][2][tr] + M->red[u][3][tr]);
             M->fin_m[parity][u][tr] = -M->nref[u][tr];
         }
@@ -1088,7 +1101,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (named_any(1 + u, 128, !got)) break;
             const SegInfo& s = M->seg[at];
             if (s.rows == 0) break;
-            soft_segment<HD, F8>(p, s, M, smem, tmem, u, st);
+            if (s.rows <= 8)
+                soft_segment<HD, F8, 8>(p, s, M, smem, tmem, u, st);
+            else if (s.rows <= 16)
+                soft_segment<HD, F8, 16>(p, s, M, smem, tmem, u, st);
+            else
+                soft_segment<HD, F8, 32>(p, s, M, smem, tmem, u, st);
             __syncwarp();
             if (lane == 0) mbar_arrive(&M->b.seg_empty[at]);
         }

@@ -161,15 +161,12 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
     return mbar_test(bar, parity) || wait_on(smem_u32(bar), parity, w);
 }
 
-// Sums over the 32 lanes of the first N = 16 or 32 values per lane; lane i gets
-// the sum of value i % N.
+// Sums over the 32 lanes of the first N = 8, 16 or 32 values per lane; lane i
+// gets the sum of value i % N.  (Each exchange halves the values; what is left
+// of the lanes is summed for one value.)
 template <int N>
 __device__ __forceinline__ float lane_sums(float (&x)[32]) {
     const int lane = threadIdx.x & 31;
-    if constexpr (N == 16) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], 16);
-    }
 #pragma unroll
     for (int o = N / 2; o > 0; o >>= 1) {
         const bool up = lane & o;
@@ -179,6 +176,8 @@ __device__ __forceinline__ float lane_sums(float (&x)[32]) {
             x[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
         }
     }
+#pragma unroll
+    for (int o = N; o < 32; o <<= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], o);
     return x[0];
 }
 
