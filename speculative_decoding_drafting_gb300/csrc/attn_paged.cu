@@ -81,7 +81,7 @@ struct Cfg {
     static constexpr int kV = F8 ? (HD == 128 ? 4 : 6) : (HD == 128 ? 3 : 5);       // V tiles
     static constexpr int kW = F8 ? (HD == 128 ? 2 : 3) : 0;                // widened V tiles
     static constexpr int kSc = F8 ? 4 : 0;                                 // scales of a tile (K, V)
-    static constexpr int kScBytes = 2048;                                  // 2 x 128 scales, 16-token pages at 128-byte pitch
+    static constexpr int kScBytes = 2 * kKeyTile * 4;                      // K's scales, then V's
     static constexpr int kPBytes = kKeyTile * kUnitRows * 2;               // a unit's P^T
     // two Q places; at head_dim 128 an item of more than 32 rows takes both
     static constexpr int kQRows = HD == 128 ? 32 : 64;
@@ -139,6 +139,7 @@ constexpr BarCounts bar_counts() {
         for (int i = 0; i < n; ++i) c.n[at / sizeof(uint64_t) + i] = (uint8_t)count;
     };
     set(0, sizeof(Bars) / sizeof(uint64_t), 1);
+    set(offsetof(Bars, c_full), 4, 32);
     set(offsetof(Bars, c_empty), 4, 8);
     set(offsetof(Bars, q_full), 2, 128);
     set(offsetof(Bars, q_empty), 2, F8 ? 1 + 4 * kUnits : 1);
@@ -191,6 +192,7 @@ struct PagedParams {
     int64_t q_stride;
     PlanInput plan;
     const int32_t* page_table;
+    const float *k_scale, *v_scale;    // e4m3 only
     uint16_t* out;
     float* lse;
     void* ws;
@@ -203,7 +205,7 @@ struct PagedParams {
 __device__ __forceinline__ size_t piece_floats(int hd) { return (size_t)kRowTile * (hd + 2); }
 
 struct Maps {
-    CUtensorMap k, v, ks, vs;
+    CUtensorMap k, v;
 };
 
 // Shared-memory operand of e4m3 rows of HD bytes: 128-byte swizzle at
@@ -284,7 +286,6 @@ struct Shape {
     __device__ __forceinline__ uint32_t turn_at(const SegInfo& s, int i) const {
         return ((s.line - s.run + (uint32_t)i) >> (wide ? 1 : 2)) & 1u;
     }
-    __device__ __forceinline__ int stream_of(int unit) const { return wide ? unit >> 1 : unit; }
     // first TMEM column of a stream's scores, and of its accumulator in a set
     __device__ __forceinline__ uint32_t column(int stream) const { return (uint32_t)stream * (wide ? 64u : 32u); }
 };
@@ -346,13 +347,10 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
         const uint32_t tS = tS0 + (turn ? kColS1 : 0u);
         float mul = scale2, lvs = 0.f, ivs = 1.f;
         if (F8) {
-            // (the scores waited for the copy of these scales to be asked for)
             const uint32_t at = line + (uint32_t)i;
             const int s = (int)(at % C::kScMod);
             wait_bar(&M->b.c_full[s], (at / C::kScMod) & 1u, ab);
-            // (pages of 16 tokens lie 128 bytes apart, longer ones side by side)
-            const uint8_t* sc = smem + C::kOffSc + s * C::kScBytes +
-                                (p.page_log2 == 4 ? (tr >> 4) * 128 + (tr & 15) * 4 : tr * 4);
+            const uint8_t* sc = smem + C::kOffSc + s * C::kScBytes + tr * 4;
             mul *= *reinterpret_cast<const float*>(sc);
             float vs = *reinterpret_cast<const float*>(sc + C::kScBytes / 2);
             __syncwarp();
@@ -800,11 +798,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int x = c.x + (ppt == 1 ? c.tok & ((1 << p.page_log2) - 1) : 0);        // a 256-token page is two tiles
         if (elect_one()) {
             mbar_expect_tx(full, pages * (uint32_t)(bp * (F8 ? HD : HD * 2)));
-            if (F8 && !kIsV) mbar_expect_tx(&M->b.c_full[cs], pages * (uint32_t)(bp * 8));
         }
         __syncwarp();
         uint8_t* dst = smem + (kIsV ? C::kOffV : 0) + c.slot * C::kLoadBytes;
-        uint8_t* sc = smem + C::kOffSc + cs * C::kScBytes;
+        if (F8 && !kIsV) {
+            // the tile's 2 x 128 scales, 4 tokens to a lane: a tensor copy per page,
+            // 64 bytes each at 16 tokens, took 248 us where this takes 216 (64
+            // requests of 8192 tokens, 8 heads of 128)
+            const int tk = lane * 4;
+            const uint32_t pid = (uint32_t)__shfl_sync(0xffffffffu, id, tk >> (p.page_log2 < 7 ? p.page_log2 : 7));
+            const bool in = tk < c.keys - c.tok && pid < (uint32_t)p.n_pages;
+            const size_t at = in ? (((size_t)pid * pl.kv_heads) << p.page_log2) + x + (tk & (bp - 1)) : 0;
+            uint8_t* sc = smem + C::kOffSc + cs * C::kScBytes + lane * 16;
+            cp_async16_zf(sc, p.k_scale + at, in ? 16u : 0u);
+            cp_async16_zf(sc + C::kScBytes / 2, p.v_scale + at, in ? 16u : 0u);
+            cp_async_arrive(&M->b.c_full[cs]);
+        }
 #pragma unroll 1
         for (uint32_t k = 0; k < pages; ++k) {
             const int pid = __shfl_sync(0xffffffffu, id, k);
@@ -812,13 +821,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int hf = 0; hf < (F8 ? 1 : C::kHalves); ++hf)
                     tma_load_3d(dst + hf * C::kHalfBytes, kIsV ? &maps.v : &maps.k, full, hf * 64, x, pid, c.pol);
-                if (F8 && !kIsV) {
-                    tma_load_2d(sc, &maps.ks, &M->b.c_full[cs], x, pid, c.pol);
-                    tma_load_2d(sc + C::kScBytes / 2, &maps.vs, &M->b.c_full[cs], x, pid, c.pol);
-                }
             }
             dst += bp * (F8 ? HD : 128);
-            sc += max(bp * 4, 128);
         }
         __syncwarp();
         if (++c.slot == kRing) {
@@ -1063,8 +1067,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint16_t* src = in ? p.q + (int64_t)(s.q.a + i) * p.q_stride + ((int64_t)s.h * pl.group + gq) * HD + x * 8
                                          : p.q;
                 if (!F8) {
-                    cp_async16_zf(qt + (x / 8) * (q_rows * 128) + row * 128 + ((x ^ row) & 7) * 16, src, in ? 16u : 0u,
-                                  policy_evict_normal());
+                    cp_async16_zf(qt + (x / 8) * (q_rows * 128) + row * 128 + ((x ^ row) & 7) * 16, src, in ? 16u : 0u);
                 } else {
                     uint4 v = make_uint4(0u, 0u, 0u, 0u);
                     if (in) v = load16(src);
@@ -1193,6 +1196,8 @@ cudaError_t launch_attn_paged(const void* q, int64_t q_stride, const dspark_kv_c
     p.q_stride = q_stride;
     p.plan = PlanInput{b.q_off, b.kv_len, b.R, b.T, n_heads / c.n_kv_heads, c.n_kv_heads, (int64_t)b.max_pages * c.page};
     p.page_table = b.page_table;
+    p.k_scale = c.k_scale;
+    p.v_scale = c.v_scale;
     p.out = static_cast<uint16_t*>(out);
     p.lse = lse;
     p.ws = ws;
@@ -1217,17 +1222,8 @@ cudaError_t launch_attn_paged(const void* q, int64_t q_stride, const dspark_kv_c
     // e4m3: K feeds the tensor core in rows of head_dim bytes, V the widening
     const CUtensorMapSwizzle swz_k = f8 && hd == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
     const CUtensorMapSwizzle swz_v = f8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
-    bool ok = make_tensor_map(&maps.k, dt, 3, c.k, dims, str, box, swz_k) &&
+    const bool ok = make_tensor_map(&maps.k, dt, 3, c.k, dims, str, box, swz_k) &&
               make_tensor_map(&maps.v, dt, 3, c.v, dims, str, box, swz_v);
-    if (f8) {
-        const cuuint64_t sd[2] = {rows, pages}, ss[1] = {rows * 4};
-        const cuuint32_t sb[2] = {bp, 1};
-        ok = ok && make_tensor_map(&maps.ks, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, c.k_scale, sd, ss, sb, CU_TENSOR_MAP_SWIZZLE_NONE) &&
-             make_tensor_map(&maps.vs, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, c.v_scale, sd, ss, sb, CU_TENSOR_MAP_SWIZZLE_NONE);
-    } else {
-        maps.ks = maps.k;
-        maps.vs = maps.v;
-    }
     if (!ok) return cudaErrorInvalidValue;
     if (c.head_dim == 64) return f8 ? launch<64, true>(maps, p, grid, s) : launch<64, false>(maps, p, grid, s);
     return f8 ? launch<128, true>(maps, p, grid, s) : launch<128, false>(maps, p, grid, s);
