@@ -277,7 +277,9 @@ struct Shape {
     int cols, streams;
     bool wide;
     __device__ __forceinline__ explicit Shape(int rows)
-        : cols(rows <= 16 ? 16 : (rows <= 32 ? 32 : 64)), streams(rows > 32 ? 2 : 4), wide(rows > 32) {}
+        : cols(max((rows + 15) & ~15, 16)), streams(rows > 32 ? 2 : 4), wide(rows > 32) {}
+    // columns of a unit
+    __device__ __forceinline__ int width() const { return wide ? cols / 2 : kUnitRows; }
     // stream of key tile i of a segment
     __device__ __forceinline__ int stream_at(const SegInfo& s, int i) const {
         return (int)((s.line - s.run + (uint32_t)i) & (uint32_t)(streams - 1));
@@ -300,7 +302,7 @@ struct SoftState {
 // One segment's key tiles of unit u.  The unit's threads all
 // walk the same barriers even after a wait ran out (the results are then not
 // stored), so that no named barrier is left waiting.
-template <int HD, bool F8, int N>
+template <int HD, bool F8, int kMost>
 __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo& sg, Misc* M, uint8_t* smem,
                                              uint32_t tmem, int u, SoftState& st) {
     using C = Cfg<HD, F8>;
@@ -308,15 +310,15 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
     const Shape sh(sg.rows);
     const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
     const int tr = wq * 32 + lane;                            // key of the tile; head_dim index of O^T
-    constexpr int kB = N < 16 ? N : 16;                       // columns loaded at a time
-    const bool wide = N == kUnitRows && sh.wide;
-    const int streams = N == kUnitRows ? sh.streams : kUnits;
+    // columns of this unit: a half of a wide row tile
+    constexpr bool wide = kMost > kUnitRows;
+    constexpr int N = wide ? kMost / 2 : kMost, streams = wide ? kUnits / 2 : kUnits;
     const int bar = 1 + u, parity = st.seg & 1;
-    const int stream = wide ? u >> 1 : u, coff = wide ? (u & 1) * kUnitRows : 0;
+    const int stream = wide ? u >> 1 : u, coff = wide ? (u & 1) * N : 0;
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
-    const uint32_t tS0 = tmem + lanes + (uint32_t)(u * kUnitRows);
-    const uint32_t tO = tmem + lanes + kColO * (1 + parity) + (uint32_t)(u * kUnitRows);
-    uint8_t* P = smem + C::kOffP + u * C::kPBytes;
+    const uint32_t tS0 = tmem + lanes + sh.column(stream) + (uint32_t)coff;
+    const uint32_t tO = tS0 + kColO * (1 + parity);
+    uint8_t* P = smem + C::kOffP + (wide ? 2 * stream : u) * C::kPBytes + (coff / 8) * (kKeyTile * 16);
 
     // this unit's rows (what the segment before left is no longer read)
     if (F8) q_places(sg, [&](int k, uint32_t use) { wait_bar(&M->b.q_full[k], use & 1u, ab); });
@@ -369,8 +371,8 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
 #pragma unroll 1
         for (bool raised = false;; raised = true) {
             float top = -INFINITY;
-#pragma unroll
-            for (int c0 = 0; c0 < N; c0 += kB) {
+            auto part = [&](auto first, auto count) {
+                constexpr int c0 = decltype(first)::value, kB = decltype(count)::value;
                 float x[kB];
                 tmem_ldn<kB>(tS + (uint32_t)c0, x);
 #pragma unroll
@@ -392,7 +394,9 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
                 }
 #pragma unroll
                 for (int c = 0; c < kB; ++c) top = fmaxf(top, t[c0 + c]);
-            }
+            };
+            part(std::integral_constant<int, 0>{}, std::integral_constant<int, (N < 16 ? N : 16)>{});
+            if constexpr (N > 16) part(std::integral_constant<int, 16>{}, std::integral_constant<int, N - 16>{});
             // (raised once: scores of 2^28 and more round by more than the threshold)
             if (raised || !named_any(bar, 128, top > C::kLift + C::kLazy)) break;
             // one is too large: raise the references to the largest scores so far
@@ -513,8 +517,8 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
                     }
                 }
             };
-            if (wide)
-                widen(coff * 4 + tr, std::integral_constant<int, kPieces / 256>{}, std::integral_constant<int, 256>{});
+            if constexpr (wide)
+                widen((u & 1) * 128 + tr, std::integral_constant<int, kPieces / 256>{}, std::integral_constant<int, 256>{});
             else
                 widen(tr, std::integral_constant<int, kPieces / 128>{}, std::integral_constant<int, 128>{});
         }
@@ -529,7 +533,13 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
 #pragma unroll
             for (int c = 0; c < N; ++c) t[c] *= ivs;
         }
-        l += lane_sums<N>(t);
+        if constexpr (N == 24) {
+            float* rest = t + 16;
+            const float a = lane_sums<16>(t), b = lane_sums<8>(rest);
+            l += lane < 16 ? a : b;
+        } else {
+            l += lane_sums<N>(t);
+        }
     }
 
     // hand the sums on; the segment before the last has been read
@@ -579,11 +589,11 @@ __device__ __forceinline__ void finish_segment(const PagedParams& p, const SegIn
     tc_fence_after();
     const bool store = !ab->abort;
     if (tr < sh.cols) {
-        const int c = tr & 31;
+        const int c = tr >= sh.width() ? tr - sh.width() : tr;
         // the unit that holds this column of the segment's k-th stream
         auto unit = [&](int k) {
             const int s = sh.stream_at(sg, k);
-            return sh.wide ? 2 * s + (tr >> 5) : s;
+            return sh.wide ? 2 * s + (tr >= sh.width() ? 1 : 0) : s;
         };
         float m = kFloorRef;
 #pragma unroll 1
@@ -614,7 +624,8 @@ __device__ __forceinline__ void finish_segment(const PagedParams& p, const SegIn
         for (int k = 0; k < used; ++k) {
             float x[8];
             const int st = sh.stream_at(sg, k);
-            const float* f = &M->join[sh.wide ? 2 * st + (c0 >> 5) : st][c0 & 31];
+            const bool second = c0 >= sh.width();
+            const float* f = &M->join[sh.wide ? 2 * st + second : st][second ? c0 - sh.width() : c0];
             tmem_ldn<8>(tO + sh.column(st) + (uint32_t)c0, x);
 #pragma unroll
             for (int c = 0; c < 8; ++c) o[c] = fmaf(x[c], f[c], o[c]);
@@ -1104,12 +1115,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (named_any(1 + u, 128, !got)) break;
             const SegInfo& s = M->seg[at];
             if (s.rows == 0) break;
+            // a loop for each number of rows: e4m3 decoding of 8 rows took 138 us with
+            // one loop for 16 and 32, and takes 118; 48 rows over long e4m3 caches
+            // 157 and 141.  (bf16 has no loop for 24: such items are bound by the
+            // cache's bytes, and one shape more cost mixed lengths 3 %.)
             if (s.rows <= 8)
                 soft_segment<HD, F8, 8>(p, s, M, smem, tmem, u, st);
             else if (s.rows <= 16)
                 soft_segment<HD, F8, 16>(p, s, M, smem, tmem, u, st);
-            else
+            else if (F8 && s.rows <= 24)
+                soft_segment<HD, F8, F8 ? 24 : 32>(p, s, M, smem, tmem, u, st);
+            else if (s.rows <= 32)
                 soft_segment<HD, F8, 32>(p, s, M, smem, tmem, u, st);
+            else if (s.rows <= 48)
+                soft_segment<HD, F8, 48>(p, s, M, smem, tmem, u, st);
+            else
+                soft_segment<HD, F8, 64>(p, s, M, smem, tmem, u, st);
             __syncwarp();
             if (lane == 0) mbar_arrive(&M->b.seg_empty[at]);
         }

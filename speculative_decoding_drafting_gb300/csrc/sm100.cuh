@@ -165,7 +165,7 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
 // gets the sum of value i % N.  (Each exchange halves the values; what is left
 // of the lanes is summed for one value.)
 template <int N>
-__device__ __forceinline__ float lane_sums(float (&x)[32]) {
+__device__ __forceinline__ float lane_sums(float* x) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = N / 2; o > 0; o >>= 1) {
