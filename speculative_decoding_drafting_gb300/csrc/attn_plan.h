@@ -4,8 +4,10 @@
 // An item is one row tile of one request and one key-value head: up to
 // kRowTile of the request's rows (row = new token x query heads of the group,
 // heads fastest) over the keys that its last row sees, in tiles of kKeyTile
-// keys, at least one.  Items are numbered request, row tile, head; the tiles
-// of all items form one line, which is cut into equal spans, one per CTA, so
+// keys, at least one.  Items are numbered request, row tile, head and laid one
+// after another on a line, each as long as it is expected to take: `start` and
+// a length per key tile that depends on its rows.  The line is cut into equal
+// spans, one per CTA, and a CTA takes the key tiles that begin in its span, so
 // that requests of any mix of lengths load the device evenly.  An item that a
 // cut goes through leaves one partial result per piece.
 #pragma once
@@ -33,7 +35,14 @@ struct PlanInput {
     const int32_t* kv_len;
     int R, T, group, kv_heads;
     int64_t most;                  // max_pages * page
+    int start;                     // length of an item besides its tiles
+    uint32_t lengths;              // length of a tile, 5 bits each: up to 8, 16, 24, 32, 48, 64 rows (1 .. 31)
 };
+DSPARK_HD int plan_length(const PlanInput& p, int rows) {
+    return (int)(p.lengths >> 5 * (rows <= 32 ? (rows - 1) / 8 : (rows <= 48 ? 4 : 5))) & 31;
+}
+// The longest tile that row tiles of up to `rows` rows have (lengths grow with them).
+DSPARK_HD int plan_longest(const PlanInput& p, int64_t rows) { return plan_length(p, (int)(rows < kRowTile ? rows : kRowTile)); }
 
 // A request's first row of the token axis, its new tokens and its keys, with
 // values out of range clamped.
@@ -63,17 +72,35 @@ DSPARK_HD int plan_tile_keys(const PlanInput& p, const Request& q, int j) {
     return end < rows ? plan_inner_keys(p.group, q.q_len, q.kv_len, j) : q.kv_len;
 }
 DSPARK_HD int plan_key_tiles(int keys) { return keys > 0 ? (keys - 1) / kKeyTile + 1 : 1; }
-DSPARK_HD_CALL int64_t plan_request_tiles(PlanInput p, int r) {
+DSPARK_HD int plan_rows(const PlanInput& p, const Request& q, int j) {
+    const int64_t rows = (int64_t)q.q_len * p.group - (int64_t)j * kRowTile;
+    return (int)(rows < kRowTile ? rows : kRowTile);
+}
+// Where key tile t of an item begins, from the item's beginning (t = tiles:
+// the item's length).
+DSPARK_HD int64_t plan_place(const PlanInput& p, int length, int t) { return p.start + (int64_t)t * length; }
+// The first key tile that begins at or after place x of an item.
+DSPARK_HD int plan_tile_at(const PlanInput& p, int length, int64_t x, int tiles) {
+    if (x <= p.start) return 0;
+    const int64_t t = (x - p.start + length - 1) / length;
+    return (int)(t < tiles ? t : tiles);
+}
+DSPARK_HD_CALL int64_t plan_request_length(PlanInput p, int r) {
     const Request q = plan_request(p, r);
     const int n = plan_row_tiles(p, q);
     int64_t sum = 0;
-    for (int j = 0; j < n; ++j) sum += plan_key_tiles(plan_tile_keys(p, q, j));
+    for (int j = 0; j < n; ++j)
+        sum += plan_place(p, plan_length(p, plan_rows(p, q, j)), plan_key_tiles(plan_tile_keys(p, q, j)));
     return sum * p.kv_heads;
 }
-// How many of `grid` CTAs get a span: none is left empty between two others,
-// since every CTA from an item's first to its last leaves a piece.
-DSPARK_HD int plan_spans(int64_t total, int grid) { return total < grid ? (int)total : grid; }
-// First tile of CTA c of n = plan_spans() (c = n: the end): floor(total c / n)
+// How many of `grid` CTAs get a span: each span is at least as long as the
+// widest gap between two tiles' beginnings, so that one begins in each (every
+// CTA from an item's first to its last leaves a piece).
+DSPARK_HD int plan_spans(const PlanInput& p, int64_t total, int grid) {
+    const int64_t n = total / (p.start + plan_longest(p, (int64_t)p.T * p.group));
+    return total == 0 ? 0 : (n < 1 ? 1 : (n < grid ? (int)n : grid));
+}
+// Where CTA c's span of n = plan_spans() begins (c = n: the end): floor(total c / n)
 // without the product, which could pass 64 bits.
 struct Span {
     int64_t begin, end;
@@ -84,7 +111,7 @@ DSPARK_HD_CALL Span plan_span(int64_t total, int c, int n) {
     return Span{q * c + rest * (uint32_t)c / u, q * (c + 1) + rest * ((uint32_t)c + 1u) / u};
 }
 DSPARK_HD int64_t plan_cut(int64_t total, int c, int n) { return c == n ? total : plan_span(total, c, n).begin; }
-// The CTA whose span holds tile g: the largest c with total c / n < g + 1.
+// The CTA whose span holds place g of the line: the largest c with total c / n < g + 1.
 DSPARK_HD_CALL int plan_owner(int64_t total, int64_t g, int n) { return (int)(((g + 1) * n - 1) / total); }
 
 // One CTA's piece of an item: key tiles [t0, t1) of tiles.
@@ -94,6 +121,7 @@ struct Segment {
     int keys;                      // keys the row tile reads
     int rows;                      // rows of the row tile
     int tok, head;                 // the first row's new token, and its place in the group
+    int rest;                      // from the span's end to the beginning of the item's last tile (an unfinished item's: >= 0)
     Request q;
 };
 
@@ -110,55 +138,62 @@ DSPARK_HD int plan_token_keys(const Request& q, int i) {
     return (int)(n < 0 ? 0 : n);                                  // i < q_len: at most kv_len
 }
 
-// Walks a span of the line of tiles.
+// Walks a span of the line.
 struct Cursor {
     int r, j, h, t;
-    int64_t left;
+    int64_t end;                   // of the span, from the item's beginning
     Request q;
 
-    // start inside request r, `skip` tiles after its first
+    // start inside request r, at place `skip` of its items, for a span of n
     DSPARK_HD void start(const PlanInput& p, int r_, int64_t skip, int64_t n) {
         r = r_;
         j = h = t = 0;
-        left = n;
+        end = 0;
         if (n <= 0) return;
         q = plan_request(p, r);
         for (;; ++j) {
-            const int tiles = plan_key_tiles(plan_tile_keys(p, q, j));
-            if (skip < (int64_t)tiles * p.kv_heads) {
-                h = (int)(skip / tiles);
-                t = (int)(skip % tiles);
+            const int tiles = plan_key_tiles(plan_tile_keys(p, q, j)), length = plan_length(p, plan_rows(p, q, j));
+            const int64_t item = plan_place(p, length, tiles);
+            if (skip < item * p.kv_heads) {
+                h = (int)(skip / item);
+                skip -= h * item;
+                t = plan_tile_at(p, length, skip, tiles);
+                end = skip + n;
                 return;
             }
-            skip -= (int64_t)tiles * p.kv_heads;
+            skip -= item * p.kv_heads;
         }
     }
     DSPARK_HD bool next(const PlanInput& p, Segment& s) {
-        if (left <= 0) return false;
-        while (q.q_len == 0) q = plan_request(p, ++r);     // left > 0: a request with rows follows
-        const int64_t rows = (int64_t)q.q_len * p.group - (int64_t)j * kRowTile;
-        s.r = r;
-        s.j = j;
-        s.h = h;
-        s.q = q;
-        s.keys = plan_tile_keys(p, q, j);
-        s.tiles = plan_key_tiles(s.keys);
-        s.rows = (int)(rows < kRowTile ? rows : kRowTile);
-        s.tok = (int)((int64_t)j * kRowTile / p.group);
-        s.head = (int)((int64_t)j * kRowTile - (int64_t)s.tok * p.group);
-        s.t0 = t;
-        s.t1 = (int)(s.tiles - t < left ? s.tiles : t + left);
-        left -= s.t1 - s.t0;
-        t = 0;
-        if (left > 0 && ++h == p.kv_heads) {
-            h = 0;
-            if (++j == plan_row_tiles(p, q)) {
-                j = 0;
-                ++r;
-                q = plan_request(p, r);
+        while (end > p.start) {                            // else no further tile begins in the span
+            while (q.q_len == 0) q = plan_request(p, ++r); // the span goes on: a request with rows follows
+            s.keys = plan_tile_keys(p, q, j);
+            s.tiles = plan_key_tiles(s.keys);
+            s.rows = plan_rows(p, q, j);
+            const int length = plan_length(p, s.rows);
+            s.r = r;
+            s.j = j;
+            s.h = h;
+            s.q = q;
+            s.tok = (int)((int64_t)j * kRowTile / p.group);
+            s.head = (int)((int64_t)j * kRowTile - (int64_t)s.tok * p.group);
+            s.t0 = t;
+            s.t1 = plan_tile_at(p, length, end, s.tiles);
+            s.rest = (int)(plan_place(p, length, s.tiles - 1) - end);
+            end -= plan_place(p, length, s.tiles);
+            t = 0;
+            if (end > 0 && ++h == p.kv_heads) {
+                h = 0;
+                if (++j == plan_row_tiles(p, q)) {
+                    j = 0;
+                    ++r;
+                    q = Request{0, 0, 0};                  // read when the span reaches it
+                    if (end > p.start) q = plan_request(p, r);
+                }
             }
+            if (s.t0 < s.t1) return true;
         }
-        return true;
+        return false;
     }
 };
 

@@ -40,28 +40,39 @@ int main() {
             len[r] = (int)pick(0, trial % 2 ? most : (most < 300 ? most : 300));
             if (wild && pick(0, 3) == 0) len[r] = pick(0, 1) ? (int)pick(-2147483647 - 1ll, -1) : (int)pick(most, 2147483647);
         }
-        const PlanInput p{off.data(), len.data(), R, T, group, kv_heads, most};
+        // any lengths that grow with the rows
+        int start = (int)pick(0, 9), length = (int)pick(1, 5);
+        uint32_t lengths = 0;
+        for (int k = 0; k < 6; ++k) {
+            lengths |= (uint32_t)length << (5 * k);
+            length += (int)pick(0, 5);
+        }
+        if (trial % 6 == 5) {                               // every tile as long as another, as the simplest case
+            start = 0;
+            lengths = 0x02108421u;
+        }
+        const PlanInput p{off.data(), len.data(), R, T, group, kv_heads, most, start, lengths};
         int64_t total = 0;
         std::vector<int64_t> first(R);
         for (int r = 0; r < R; ++r) {
             first[r] = total;
-            total += plan_request_tiles(p, r);
+            total += plan_request_length(p, r);
         }
-        const int n = plan_spans(total, (int)pick(1, 152));
+        const int n = plan_spans(p, total, (int)pick(1, 152));
         if (total == 0) { CHECK(n == 0); continue; }
         CHECK(plan_cut(total, 0, n) == 0 && plan_cut(total, n, n) == total);
-        std::map<std::tuple<int, int, int>, int> done;
+        std::map<std::tuple<int, int, int>, int> done, last;
         int64_t seen_tiles = 0;
         for (int c = 0; c < n; ++c) {
             const int64_t b = plan_cut(total, c, n), e = plan_cut(total, c + 1, n);
             CHECK(b < e && e - b <= total / n + 1);
             int r = 0;
-            while (!(first[r] <= b && b < first[r] + plan_request_tiles(p, r))) CHECK(++r < R);
+            while (!(first[r] <= b && b < first[r] + plan_request_length(p, r))) CHECK(++r < R);
             Cursor cur;
             cur.start(p, r, b - first[r], e - b);
             Segment s;
-            int64_t line = b;
             bool tail = false;
+            int pieces = 0;
             while (cur.next(p, s)) {
                 CHECK(!tail);
                 CHECK(s.r >= 0 && s.r < R && s.h >= 0 && s.h < kv_heads);
@@ -82,18 +93,22 @@ int main() {
                 int& d = done[std::make_tuple(s.r, s.j, s.h)];
                 CHECK(d == s.t0);
                 d = s.t1;
+                ++pieces;
+                CHECK(s.t0 == 0 || pieces == 1);            // only a span's first piece begins inside its item
                 if (s.t0 == 0 && s.t1 < s.tiles) {          // the piece that describes the join
-                    const int64_t last = e - (s.t1 - s.t0) + s.tiles - 1;
-                    const int owner = plan_owner(total, last, n);
-                    CHECK(line == e - (s.t1 - s.t0));
+                    CHECK(s.rest >= 0);
+                    const int owner = plan_owner(total, e + s.rest, n);
                     CHECK(owner > c && owner < n);
-                    CHECK(plan_cut(total, owner, n) <= last && last < plan_cut(total, owner + 1, n));
-                    for (int k = c + 1; k <= owner; ++k) CHECK(plan_cut(total, k, n) < plan_cut(total, k + 1, n));
+                    CHECK(plan_cut(total, owner, n) <= e + s.rest && e + s.rest < plan_cut(total, owner + 1, n));
+                    last[std::make_tuple(s.r, s.j, s.h)] = owner;
+                }
+                if (s.t0 > 0) {                             // every CTA from the first to the last has a piece
+                    CHECK(c <= last[std::make_tuple(s.r, s.j, s.h)]);
+                    CHECK((s.t1 == s.tiles) == (c == last[std::make_tuple(s.r, s.j, s.h)]));
                 }
                 tail = s.t1 < s.tiles;
-                line += s.t1 - s.t0;
             }
-            CHECK(line == e);
+            CHECK(pieces > 0);
             seen_tiles += e - b;
         }
         CHECK(seen_tiles == total);
