@@ -1,9 +1,13 @@
 // kv_cache.cu -- writing new tokens' keys and values into the paged cache
 // (bf16, or e4m3 with a float32 scale per token and head) and reading them back.
 //
-// Both move each row once: a row is head_dim values of one token and head, 8
-// or 16 lanes hold 8 values each (16 bytes of bf16), and a warp takes one
-// token with all its heads, K and V, so that its loads are in flight together.
+// Both move each row once and are bound by its bytes: a row is head_dim values
+// of one token and head, 8 or 16 lanes hold 8 values each (16 bytes of bf16),
+// and a warp takes one token with all its heads, K and V, so that its loads
+// are in flight together.  Measured (GB300, against 6.68 TB/s of a plain copy;
+// 8 heads of 128): 47386 tokens into an e4m3 cache 52.4 us, 5.6 TB/s; 109747
+// tokens out of one 104.6 us, 6.5 TB/s.  (With K's rows used up before V's were
+// loaded and a division per lane it was 69.8 and 127 us.)
 #include <type_traits>
 
 #include "kernels.h"
@@ -47,9 +51,8 @@ __device__ __forceinline__ uint2 quantise8(uint4 w, float inv) {
 constexpr int kSteps = 4, kVecs = 2 * kSteps;
 
 // The largest of each of the kVecs values over the LANES lanes of a row: lane
-// part holds the one of vector vec_of(part) afterwards.  Each exchange halves
-// the vectors instead of repeating the reduction for each (LANES / 8 * 8
-// exchanges against 8 log2(LANES)).
+// `part` gets the one of vector part / (LANES / kVecs).  Each exchange halves
+// the vectors, 7 or 8 exchanges where one reduction per vector takes 24 or 32.
 template <int LANES>
 __device__ __forceinline__ uint32_t row_maxima(uint32_t (&m)[kVecs], int part) {
 #pragma unroll
