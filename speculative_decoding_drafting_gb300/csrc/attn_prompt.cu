@@ -68,6 +68,10 @@ struct Misc {
     uint64_t fix, fixed[2], done;
     WaitState wst;
     uint32_t tmem;
+    // this CTA's entry and the number of entries, where there is no list (a
+    // CTA past the last entry has none, and the workspace no room for one)
+    int2 own;
+    int entries;
 };
 
 template <int HD>
@@ -187,11 +191,12 @@ __device__ __forceinline__ int2 entry_of(const Params& p, int64_t k, int64_t& co
     return e;
 }
 
-__device__ __forceinline__ bool get_item(const Params& p, int64_t total, int round, Item& it) {
+__device__ __forceinline__ bool get_item(const Params& p, const Misc* M, int64_t total, int round, Item& it) {
     const int64_t n = gridDim.x, c = blockIdx.x;
     const int64_t k = (int64_t)round * n + ((round & 1) ? n - 1 - c : c);
     if (k >= total) return false;
-    const int2 e = __ldcg(p.list + k / p.kv_heads);          // written by the kernel before this one
+    // the list was written by the kernel before this one
+    const int2 e = p.single ? M->own : __ldcg(p.list + k / p.kv_heads);
     it.h = (int)(k % p.kv_heads);
     const RowRange r = row_range(p.seq_off, e.x, p.T);
     it.a = r.a;
@@ -291,19 +296,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = M->tmem;
     pdl_wait();                                               // the list
-    if (p.single) {                                           // every CTA writes what it reads, all the same values
+    if (p.single) {
         if (blockIdx.x == 0) check_requests(p.seq_off, nullptr, p.B, p.T, 0, p.ws);
         if (warp == 2) {
             int64_t count;
             const int2 e = entry_of(p, blockIdx.x / p.kv_heads, count);
             if (lane == 0) {
-                const_cast<int2*>(p.list)[blockIdx.x / p.kv_heads] = e;
-                *const_cast<int*>(p.count) = (int)min(count, (int64_t)p.most);
+                M->own = e;
+                M->entries = (int)min(count, (int64_t)p.most);
             }
         }
         __syncthreads();
     }
-    const int64_t total = (int64_t)__ldcg(p.count) * p.kv_heads;
+    const int64_t total = (int64_t)(p.single ? M->entries : __ldcg(p.count)) * p.kv_heads;
     Item it;
 
     // registers: 384 x 168 at launch, then 128 x 104 + 256 x 200
@@ -348,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
             };
 #pragma unroll 1
-            for (int round = 0; ok && get_item(p, total, round, it); ++round) {
+            for (int round = 0; ok && get_item(p, M, total, round, it); ++round) {
                 const int n = it.tiles();
                 query(0);
                 tile(&maps.k, 0);
@@ -413,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
             };
 #pragma unroll 1
-            for (int round = 0; ok && get_item(p, total, round, it); ++round) {
+            for (int round = 0; ok && get_item(p, M, total, round, it); ++round) {
                 const int n = it.tiles();
                 if (it.n(s)) {
                     if (!wait(&M->q_full[s], nq & 1u)) break;
@@ -495,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---------------- zero the last V tile's rows past the item's keys
             uint32_t g = 0, nfix = 0;
 #pragma unroll 1
-            for (int round = 0; get_item(p, total, round, it); ++round) {
+            for (int round = 0; get_item(p, M, total, round, it); ++round) {
                 const int n = it.tiles();
                 const int valid = it.keys - (n - 1) * kKeys;
                 const uint32_t vi = g + 2 * n - 1;
@@ -532,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             return ok;
         };
-        for (int round = 0; ok && get_item(p, total, round, it); ++round) {
+        for (int round = 0; ok && get_item(p, M, total, round, it); ++round) {
             const int n = it.n(s);
             if (!n) continue;
             const int tok = it.tok0 + s * p.toks + rt;           // sees keys 0 .. tok
