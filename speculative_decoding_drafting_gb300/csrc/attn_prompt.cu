@@ -284,18 +284,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&M->fix, 1);
         mbar_init(&M->done, 2);
         M->wst.abort = 0;
-        M->wst.limit = ws_wait_limit(p.ws);
         fence_mbar_init();
         prefetch_tmap(&maps.q);
         prefetch_tmap(&maps.k);
         prefetch_tmap(&maps.v);
     }
     if (warp == 1) tmem_alloc(&M->tmem, 512);
+    // the kernel before this one: the list, or whatever the caller queued (the
+    // workspace's header may be its work)
+    pdl_wait();
+    if (threadIdx.x == 0) M->wst.limit = ws_wait_limit(p.ws);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = M->tmem;
-    pdl_wait();                                               // the list
     if (p.single) {
         if (blockIdx.x == 0) check_requests(p.seq_off, nullptr, p.B, p.T, 0, p.ws);
         if (warp == 2) {
