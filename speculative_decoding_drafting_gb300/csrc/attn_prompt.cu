@@ -544,6 +544,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!n) continue;
             const int tok = it.tok0 + s * p.toks + rt;           // sees keys 0 .. tok
             const int first = it.tok0 + s * p.toks;
+            // rows of no token (unused rows of the tile, tokens of the next
+            // sequence) have scores of whatever is there: they raise nothing
+            const bool valid = row < p.toks * p.group && tok < it.len;
+            const float lazy = valid ? kLazy : INFINITY;
             float ref = kFloorRef;
             uint64_t l2 = 0;                                     // two partial sums
             for (int j = 0; ok && j < n; ++j) {
@@ -575,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const float top = c >= 0.f ? fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c
                                            : fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3])) * c;
-                if (__any_sync(0xffffffffu, top > ref + kLazy)) {
+                if (__any_sync(0xffffffffu, top > ref + lazy)) {
                     const float m = fmaxf(ref, top), f = ex2_approx(ref - m);
                     ref = m;
                     float a, b;
@@ -620,7 +624,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             float a, b;
             unpack2(l2, a, b);
             const float l = a + b, inv = 1.f / l;
-            const bool valid = row < p.toks * p.group && tok < it.len;
             const size_t at = (size_t)(it.a + tok) * p.heads + (size_t)it.h * p.group + rg;
 #pragma unroll
             for (int q = 0; q < HD / 16; ++q) {
