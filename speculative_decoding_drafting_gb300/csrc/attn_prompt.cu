@@ -284,20 +284,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&M->fix, 1);
         mbar_init(&M->done, 2);
         M->wst.abort = 0;
+        M->wst.limit = 1ull << 32;                            // until the workspace's own is read
         fence_mbar_init();
         prefetch_tmap(&maps.q);
         prefetch_tmap(&maps.k);
         prefetch_tmap(&maps.v);
     }
     if (warp == 1) tmem_alloc(&M->tmem, 512);
-    // the kernel before this one: the list, or whatever the caller queued (the
-    // workspace's header may be its work)
-    pdl_wait();
-    if (threadIdx.x == 0) M->wst.limit = ws_wait_limit(p.ws);
+    // rows of Q that no token of an item fills are zeros (these for the whole
+    // kernel, the rest item by item): their scores are 0 whatever ran before and
+    // whatever the next sequence holds, so they never raise the references of
+    // the rows beside them.  (Left as they were and kept from voting instead,
+    // they cost 5 %: the softmax loop has no register to spare.)
+    for (int x = p.toks * p.group * 8 + threadIdx.x; x < kRows * 8; x += kThreads)
+#pragma unroll
+        for (int k = 0; k < 2 * C::kHalves; ++k)
+            *reinterpret_cast<uint4*>(smem + C::kOffQ + k * C::kHalfBytes + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = M->tmem;
+    // the kernel before this one: the list, or whatever the caller queued (the
+    // workspace's header may be its work).  Waits read the limit anew each time
+    // round, so no barrier follows; with one, or with this before the barrier
+    // above, the softmax loop came out differently and 859 us were 868 to 929.
+    pdl_wait();
+    if (threadIdx.x == 96) M->wst.limit = ws_wait_limit(p.ws);
     if (p.single) {
         if (blockIdx.x == 0) check_requests(p.seq_off, nullptr, p.B, p.T, 0, p.ws);
         if (warp == 2) {
@@ -425,6 +438,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (it.n(s)) {
                     if (!wait(&M->q_full[s], nq & 1u)) break;
                     nq ^= 1u;
+                    // a last row tile's rows of the next sequence
+                    const int first = it.tok0 + s * p.toks;
+                    if (it.len - first < p.toks) {
+                        uint8_t* qt = smem + C::kOffQ + s * C::kTileBytes;
+#pragma unroll 1
+                        for (int x = (it.len - first) * p.group * 8 + lane; x < p.toks * p.group * 8; x += 32)
+#pragma unroll
+                            for (int hf = 0; hf < C::kHalves; ++hf)
+                                *reinterpret_cast<uint4*>(qt + hf * C::kHalfBytes + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        fence_proxy_async();
+                        __syncwarp();
+                    }
                 }
                 if (!wait(&M->full[st], ph)) break;
                 if (it.n(s)) {
@@ -544,10 +569,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!n) continue;
             const int tok = it.tok0 + s * p.toks + rt;           // sees keys 0 .. tok
             const int first = it.tok0 + s * p.toks;
-            // rows of no token (unused rows of the tile, tokens of the next
-            // sequence) have scores of whatever is there: they raise nothing
-            const bool valid = row < p.toks * p.group && tok < it.len;
-            const float lazy = valid ? kLazy : INFINITY;
             float ref = kFloorRef;
             uint64_t l2 = 0;                                     // two partial sums
             for (int j = 0; ok && j < n; ++j) {
@@ -579,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const float top = c >= 0.f ? fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c
                                            : fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3])) * c;
-                if (__any_sync(0xffffffffu, top > ref + lazy)) {
+                if (__any_sync(0xffffffffu, top > ref + kLazy)) {
                     const float m = fmaxf(ref, top), f = ex2_approx(ref - m);
                     ref = m;
                     float a, b;
@@ -624,6 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float a, b;
             unpack2(l2, a, b);
             const float l = a + b, inv = 1.f / l;
+            const bool valid = row < p.toks * p.group && tok < it.len;
             const size_t at = (size_t)(it.a + tok) * p.heads + (size_t)it.h * p.group + rg;
 #pragma unroll
             for (int q = 0; q < HD / 16; ++q) {
