@@ -350,8 +350,11 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
     for (int i = (stream - sh.stream_at(sg, 0)) & (streams - 1); i < n; i += streams) {
         const int key = (t0 + i) * kKeyTile + tr;
         const bool edge = (t0 + i + 1) * kKeyTile > lim0;     // some row does not see the whole tile
-        // new token k sees the key if kv_len - q_len + k >= key: from this row on
-        const int seen = !edge ? 0 : min(key - sg.q.kv_len + sg.q.q_len - sg.tok, kRowTile + 1) * p.plan.group - sg.head - coff;
+        // new token k sees the key if kv_len - q_len + k >= key: from this row on.
+        // Past the last key no column sees it, the unused ones neither: what
+        // lies there must not raise the other columns' references.
+        const int seen = !edge ? 0 : (key >= sg.keys ? kRowTile
+                                      : (key - sg.q.kv_len + sg.q.q_len - sg.tok) * p.plan.group - sg.head - coff);
         const uint32_t turn = sh.turn_at(sg, i);
         wait_bar(&M->b.s_full[turn][u], (st.phases >> turn) & 1u, ab);
         st.phases ^= 1u << turn;

@@ -68,3 +68,37 @@ def test_prompt_rows_do_not_depend_on_the_next_sequence(heads, kv_heads, dim):
             r = binding.attn_prompt(*x, _off(lens), lse=True)
             for s in rest:
                 assert torch.equal(r["out"][s], first["out"][s]) and torch.equal(r["lse"][s], first["lse"][s])
+
+
+@pytest.mark.parametrize("dtype", [BF, F8])
+@pytest.mark.parametrize("heads,kv_heads,dim,new", [(3, 1, 128, 1), (10, 2, 64, 3), (8, 2, 128, 6), (40, 1, 64, 1), (4, 4, 128, 1)])
+def test_paged_values_past_the_end_do_not_matter(dtype, heads, kv_heads, dim, new):
+    """Whatever codes and scales stand behind a request's last token, its bits
+    are the same (enough requests that a CTA takes several tiles of one, the
+    last of them cut)."""
+    g = torch.Generator().manual_seed(heads + dim)
+    kv, page = [600 + (i * 37) % 700 for i in range(300 // kv_heads)] + [65, 5], 64
+    counts = [-(-n // page) for n in kv]
+    table = torch.full((len(kv), max(counts)), -1, dtype=torch.int32)
+    for r, c in enumerate(counts):
+        table[r, :c] = torch.arange(sum(counts[:r]), sum(counts[:r]) + c)
+    table = table.to(DEV)
+    shape = (sum(counts), kv_heads, page, dim)
+    K, V = (_rand(g, sum(kv), kv_heads, dim) for _ in range(2))
+    q = _rand(g, len(kv) * new, heads, dim)
+    first = None
+    nan, inf = float("nan"), float("inf")
+    for code, scale in ((0x00, 1.0), (0x7F, nan), (0x38, 1.0), (0x7E, 3e38), (0x7E, inf), (0xF0, -2.0), (0x01, 1e-40)):
+        if dtype == BF:
+            bits = torch.tensor([code * 256 + 0x80], dtype=torch.int32).to(torch.int16).view(BF).item() if scale == scale else nan
+            if scale == inf:
+                bits = inf
+            cache = binding.KvCache(*(torch.full(shape, bits, dtype=BF, device=DEV) for _ in range(2)))
+        else:
+            cache = binding.KvCache(*(torch.full(shape, code, dtype=torch.uint8, device=DEV).view(F8) for _ in range(2)),
+                                    *(torch.full(shape[:3], scale, device=DEV) for _ in range(2)))
+        binding.kv_write(cache, K, V, _off(kv), _i32(kv), table)
+        r = binding.attn_paged(q, cache, _off([new] * len(kv)), _i32(kv), table, lse=True)
+        assert torch.isfinite(r["out"].float()).all()
+        first = first or r
+        assert _same(r, first), (code, scale)
