@@ -469,7 +469,7 @@ int dspark_sts_apply(const float* c, int N, int gamma, const double* t, float* o
  * slot j % page; heads are separate planes of a page.
  *   k, v       [n_pages, n_kv_heads, page, head_dim]  dtype
  *   k_scale, v_scale  [n_pages, n_kv_heads, page]     float, DSPARK_E4M3 only (else NULL):
- *                     the stored row is code * scale
+ *                     the stored row is code * scale; not negative
  *   dtype      DSPARK_BF16 or DSPARK_E4M3
  * Requirements: n_pages >= 1, page in {16, 32, 64, 128, 256}, n_kv_heads in
  * [1, 4096], head_dim 64 or 128 (SHAPE); k, v and the scales 16-byte aligned
@@ -558,7 +558,8 @@ size_t dspark_attn_paged_workspace_size(int R, int T, int n_heads, int n_kv_head
  * (exact but for values below 2^-10 of their row's largest, which are off by
  * 2^-18 of it at most), V's codes are widened exactly to fp16 and the weights
  * rounded to fp16 (11 bits down to 2^-24 of the row's largest); scales
- * multiply scores and weights in float32.  The order of all sums depends on
+ * multiply scores and weights in float32.  V rows whose scale is below 2^-100
+ * (values below 2^-91) count as zeros.  The order of all sums depends on
  * the sizes and the device only, so reruns agree bit for bit.
  * Cached values past kv_len[r] never matter, whatever bits they hold; K and V
  * of the kv_len[r] tokens themselves must be finite.

@@ -373,7 +373,10 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
             if (lane == 0) mbar_arrive(&M->b.c_empty[s]);
             if (!wide && lane == 0) mbar_arrive(&M->b.c_empty[s]);
             if (edge && key >= sg.keys) vs = 1.f;             // no key here: any scale
-            if (vs < 7.888609e-31f) vs = 7.888609e-31f;       // 2^-100; a row of zeros has scale 0
+            // Below 2^-100 (a row of zeros has scale 0) 1 / scale would take the sum
+            // out of float32's range: there the sum counts the key with 2^-101, and
+            // its weight for V is 0 (values below 2^-91 are dropped, not raised).
+            if (vs < 3.944305e-31f) vs = 3.944305e-31f;
             lvs = lg2_approx(vs);
             ivs = ex2_approx(-lvs);
         }
@@ -477,6 +480,11 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
                 }
             }
             *reinterpret_cast<uint4*>(P + (c0 / 8) * (kKeyTile * 16) + tr * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        }
+        if (F8 && ivs > 1.2676506e30f) {                      // 2^100
+#pragma unroll 1
+            for (int c0 = 0; c0 < N; c0 += 8)
+                *reinterpret_cast<uint4*>(P + (c0 / 8) * (kKeyTile * 16) + tr * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
         if constexpr (F8) {
             // Widen V's e4m3 codes, 16 at a time; two units share a wide tile.
