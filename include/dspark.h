@@ -515,7 +515,8 @@ size_t dspark_kv_workspace_size(void);
  *   K, V     [T, n_kv_heads, head_dim] bfloat16; k_stride and v_stride are the
  *            elements from one token to the next (a slice of a fused
  *            projection needs no copy): multiples of 8, at least
- *            n_kv_heads * head_dim; K and V 16-byte aligned
+ *            n_kv_heads * head_dim; K and V 16-byte aligned device memory of
+ *            the current device
  * DSPARK_BF16: the rows are copied.  DSPARK_E4M3: with a = max |x| over a row
  * (one token, one head), scale = a / 448 and each code is the e4m3 value
  * nearest to x * 448 / a (ties to even, decided as in exact arithmetic);
@@ -548,6 +549,7 @@ size_t dspark_attn_paged_workspace_size(int R, int T, int n_heads, int n_kv_head
  *   s_j = scale * (q . k_j),  out = sum_j softmax(s)_j v_j,  lse = ln sum_j exp(s_j)
  *   q    [T, n_heads, head_dim] bfloat16, q_stride elements from token to token
  *        (a multiple of 8, at least n_heads * head_dim); 16-byte aligned
+ *        device memory of the current device
  *   out  [T, n_heads, head_dim] bfloat16, 16-byte aligned
  *   lse  [T, n_heads] float, may be NULL
  * A token that sees no key (its position is negative) gets out = 0 and

@@ -1,5 +1,7 @@
 """What the cache and attention calls leave alone: the bytes around every
 buffer that they write, with workspaces of exactly the stated size."""
+import ctypes
+
 import pytest
 import torch
 
@@ -111,3 +113,34 @@ def test_cache_calls_write_their_buffers_only(dtype, heads, kv_heads, dim, page)
     mem.check()
     assert binding.workspace_status(ws) == 0 and binding.workspace_status(small) == 0
     assert torch.equal(out["out"], want["out"]) and torch.equal(out["lse"], want["lse"])
+
+
+def test_rows_that_are_not_device_memory_are_refused():
+    """Pinned host memory (which a kernel could read) in the place of each input:
+    the same refusal in all the calls that take rows, before anything is enqueued."""
+    L = binding.load()
+    T, heads, kv_heads, dim = 3, 4, 2, 64
+    cache = binding.KvCache.empty(2, kv_heads, 16, dim, BF, DEV)
+    b = binding._batch(_i32([0, T]), _i32([T]), _i32([[0, 1]]), T)
+    c, b = ctypes.byref(cache._struct()), ctypes.byref(b)
+    dev = {n: torch.zeros((T, h, dim), dtype=BF, device=DEV) for n, h in (("q", heads), ("K", kv_heads), ("V", kv_heads), ("out", heads))}
+    host = {n: torch.zeros(t.shape, dtype=BF).pin_memory() for n, t in dev.items()}
+    ws = binding._workspace(1 << 24, DEV)
+    off = _i32([0, T])
+    torch.cuda.synchronize()
+
+    def at(name, moved):
+        return (host if name == moved else dev)[name].data_ptr()
+
+    calls = {
+        "write": (("K", "V"), lambda m: L.dspark_kv_write(c, b, at("K", m), at("V", m), 128, 128, ws.data_ptr(), 256, None)),
+        "paged": (("q",), lambda m: L.dspark_attn_paged(at("q", m), 256, c, b, heads, 0.125, at("out", m), None,
+                                                              ws.data_ptr(), 1 << 24, None)),
+        "prompt": (("q", "K", "V"), lambda m: L.dspark_attn_prompt(
+            at("q", m), at("K", m), at("V", m), 256, 128, 128, off.data_ptr(), 1, T, heads, kv_heads, dim, 0.125,
+            at("out", m), None, ws.data_ptr(), 1 << 24, None))}
+    for name, (arrays, call) in calls.items():
+        assert call(None) == 0, name
+        for moved in arrays:
+            assert call(moved) == -1, (name, moved)
+    torch.cuda.synchronize()
