@@ -85,13 +85,42 @@ DSPARK_HD int plan_tile_at(const PlanInput& p, int length, int64_t x, int tiles)
     const int64_t t = (x - p.start + length - 1) / length;
     return (int)(t < tiles ? t : tiles);
 }
+// Length of a request's first n row tiles, all of them full and none its last:
+// row tile j reads kv_len - q_len + floor((64 j + 63) / group) + 1 keys, so it
+// takes max(0, floor((j + b) / 2 group)) + 1 key tiles, b = floor((63 +
+// (kv_len - q_len) group) / 64), and the floors of a run from 0 sum in closed
+// form.  (A walk over the row tiles, on every CTA before its first load, grew
+// with a request's new tokens: 2048 of them, 32 heads to a group, over 4096 keys
+// took 806 us and take 392; blocks of 1 to 17 tokens take the same.)
+DSPARK_HD int64_t plan_floor_sum(int64_t y, uint32_t m) {                  // of floor(x / m), 0 <= x < y
+    if (y <= 0) return 0;
+    const uint32_t u = (uint32_t)y, d = u / m;                             // y <= 2 kv_len: 32 bits
+    return (int64_t)d * (int32_t)(d - 1) / 2 * m + (int64_t)d * (u - d * m);
+}
+DSPARK_HD_CALL int64_t plan_before(int group, int start, int length, int q_len, int kv_len, int n) {
+    const int64_t b = (63 + ((int64_t)kv_len - q_len) * group) >> 6;
+    const uint32_t m = 2u * (uint32_t)group;
+    return (int64_t)n * start + (n + plan_floor_sum(b + n, m) - plan_floor_sum(b, m)) * length;
+}
+DSPARK_HD int64_t plan_tiles_before(const PlanInput& p, const Request& q, int n) {
+    return plan_before(p.group, p.start, plan_length(p, kRowTile), q.q_len, q.kv_len, n);
+}
 DSPARK_HD_CALL int64_t plan_request_length(PlanInput p, int r) {
     const Request q = plan_request(p, r);
     const int n = plan_row_tiles(p, q);
-    int64_t sum = 0;
-    for (int j = 0; j < n; ++j)
-        sum += plan_place(p, plan_length(p, plan_rows(p, q, j)), plan_key_tiles(plan_tile_keys(p, q, j)));
-    return sum * p.kv_heads;
+    if (n == 0) return 0;
+    const int64_t last = plan_place(p, plan_length(p, plan_rows(p, q, n - 1)), plan_key_tiles(q.kv_len));
+    return (plan_tiles_before(p, q, n - 1) + last) * p.kv_heads;
+}
+// The row tile that holds place x of request r's items: the last that begins at or before it.
+DSPARK_HD int plan_tile_of(const PlanInput& p, const Request& q, int64_t x) {
+    int j = 0, upto = plan_row_tiles(p, q);
+    while (upto - j > 1) {
+        const int mid = j + (upto - j) / 2;
+        if (plan_tiles_before(p, q, mid) * p.kv_heads <= x) j = mid;
+        else upto = mid;
+    }
+    return j;
 }
 // How many of `grid` CTAs get a span: each span is at least as long as the
 // widest gap between two tiles' beginnings, so that one begins in each (every
@@ -151,18 +180,14 @@ struct Cursor {
         end = 0;
         if (n <= 0) return;
         q = plan_request(p, r);
-        for (;; ++j) {
-            const int tiles = plan_key_tiles(plan_tile_keys(p, q, j)), length = plan_length(p, plan_rows(p, q, j));
-            const int64_t item = plan_place(p, length, tiles);
-            if (skip < item * p.kv_heads) {
-                h = (int)(skip / item);
-                skip -= h * item;
-                t = plan_tile_at(p, length, skip, tiles);
-                end = skip + n;
-                return;
-            }
-            skip -= item * p.kv_heads;
-        }
+        j = plan_tile_of(p, q, skip);
+        const int tiles = plan_key_tiles(plan_tile_keys(p, q, j)), length = plan_length(p, plan_rows(p, q, j));
+        const int64_t item = plan_place(p, length, tiles);
+        skip -= plan_tiles_before(p, q, j) * p.kv_heads;
+        h = (int)(skip / item);
+        skip -= h * item;
+        t = plan_tile_at(p, length, skip, tiles);
+        end = skip + n;
     }
     DSPARK_HD bool next(const PlanInput& p, Segment& s) {
         while (end > p.start) {                            // else no further tile begins in the span
