@@ -65,7 +65,13 @@ struct Cfg {
 struct Misc {
     uint64_t full[8], empty[8];
     uint64_t q_full[2], q_empty[2], s_full[2], s_read[2], p_full[2][2], pv_done[2], o_free[2];
-    uint64_t fix, fixed[2], done;
+    // A V tile for warp 3 to clear, asked for by row tile s's issuer, and, by ring
+    // place, cleared.  (One barrier for both issuers' requests took the request
+    // of an item that one of them had reached for the item before it; one per
+    // issuer for the answers could be two phases ahead of its reader.  Either
+    // ended in a wait that ran out, with many sequences of a few tiles.)
+    uint64_t asked[2], fixed[8];
+    uint64_t done;
     WaitState wst;
     uint32_t tmem;
     // this CTA's entry and the number of entries, where there is no list (a
@@ -269,6 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(&M->full[i], 1);
             mbar_init(&M->empty[i], 2);
+            mbar_init(&M->fixed[i], 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&M->q_full[s], 1);
@@ -277,11 +284,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&M->s_read[s], 4);
             mbar_init(&M->p_full[s][0], 4);
             mbar_init(&M->p_full[s][1], 4);
-            mbar_init(&M->fixed[s], 1);
+            mbar_init(&M->asked[s], 1);
             mbar_init(&M->pv_done[s], 1);
             mbar_init(&M->o_free[s], 4);
         }
-        mbar_init(&M->fix, 1);
         mbar_init(&M->done, 2);
         M->wst.abort = 0;
         M->wst.limit = 1ull << 32;                            // until the workspace's own is read
@@ -398,7 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t dk = smem_desc_sw128(smem, 16, 1024);
             const uint64_t dv = smem_desc_sw128(smem, C::kHalfBytes, 1024);
             const uint32_t tS = tmem + (uint32_t)(s * 128), tO = tmem + (uint32_t)(256 + s * HD);
-            uint32_t nq = 0, nr = 0, np = 0, no = 0, nfix = 0;    // parities of the next waits
+            uint32_t nq = 0, nr = 0, np = 0, no = 0;      // parities of the next waits
+            uint32_t nfix = 0;                                    // the same for each ring place's `fixed`, by bit
             uint32_t st = 0, ph = 0;                              // ring place of the next tile, and its phase
             bool ok = true, started = false;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -478,8 +485,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!wait(&M->full[vat], vph)) break;
                     const bool fix = j == n - 1 && it.keys - j * kKeys < kKeys;
                     // warp 3 starts while P is still being made (row tile 1, where there
-                    // is one, sees the item's last tile)
-                    if (fix && lane == 0 && s == (it.n1 ? 1 : 0)) mbar_arrive(&M->fix);
+                    // is one, sees the item's last tile and does not pass it uncleared)
+                    if (fix && lane == 0 && s == (it.n1 ? 1 : 0)) mbar_arrive(&M->asked[s]);
                     if (j < it.n(s)) {
                         if (j == 0) {
                             if (started) {                        // the item before has been stored
@@ -488,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             started = true;
                         }
-                        if (fix && !wait(&M->fixed[s], nfix++ & 1u)) break;
+                        if (fix && !wait(&M->fixed[vat], (nfix >> vat) & 1u)) break;
 #pragma unroll 1
                         for (int half = 0; half < 2; ++half) {    // 64 keys at a time
                             if (!wait(&M->p_full[s][half], np & 1u)) break;
@@ -511,6 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else if (lane == 0) {
                         mbar_arrive(&M->empty[vat]);
                     }
+                    if (fix) nfix ^= 1u << vat;
                     if (j + 1 < n && j + 1 >= it.n(s)) {          // a tile only the other row tile sees
                         if (!wait(&M->full[kat], kph)) break;
                         if (lane == 0) mbar_arrive(&M->empty[kat]);
@@ -525,17 +533,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         } else if (warp == 3) {
             // ---------------- zero the last V tile's rows past the item's keys
-            uint32_t g = 0, nfix = 0;
+            uint32_t g = 0, nasked = 0;                           // nasked: parity of each issuer's next request, by bit
 #pragma unroll 1
             for (int round = 0; get_item(p, M, total, round, it); ++round) {
                 const int n = it.tiles();
                 const int valid = it.keys - (n - 1) * kKeys;
-                const uint32_t vi = g + 2 * n - 1;
+                const uint32_t vat = (g + 2 * n - 1) % C::kStages;
                 g += 2 * n;
                 if (valid >= kKeys) continue;
                 // an MMA issuer saw the tile arrive and asks for the zeros
-                if (!__all_sync(0xffffffffu, wait_bar_here(&M->fix, nfix++ & 1u, ab))) break;
-                uint8_t* vt = smem + (vi % C::kStages) * C::kTileBytes;
+                const int s = it.n1 ? 1 : 0;
+                if (!__all_sync(0xffffffffu, wait_bar_here(&M->asked[s], (nasked >> s) & 1u, ab))) break;
+                nasked ^= 1u << s;
+                uint8_t* vt = smem + vat * C::kTileBytes;
 #pragma unroll 1
                 for (int x = valid * 8 + lane; x < kKeys * 8; x += 32)
 #pragma unroll
@@ -543,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         *reinterpret_cast<uint4*>(vt + hf * C::kHalfBytes + x * 16) = make_uint4(0u, 0u, 0u, 0u);
                 fence_proxy_async();
                 __syncwarp();
-                if (lane < 2 && it.n(lane) == n) mbar_arrive(&M->fixed[lane]);
+                if (lane == 0) mbar_arrive(&M->fixed[vat]);
             }
         }
     } else {
