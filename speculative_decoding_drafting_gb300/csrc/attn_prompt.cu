@@ -269,7 +269,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
     Misc* M = reinterpret_cast<Misc*>(smem + C::kOffMisc);
     volatile WaitState* ab = &M->wst;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // by a shuffle: the compiler then knows that the warp's number, and what the
+    // roles derive from it, is the same in every lane.  Without it changes that do
+    // not touch the loops moved 12001 tokens between 855 and 932 us; with it they
+    // take 796.
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
@@ -300,8 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // rows of Q that no token of an item fills are zeros (these for the whole
     // kernel, the rest item by item): their scores are 0 whatever ran before and
     // whatever the next sequence holds, so they never raise the references of
-    // the rows beside them.  (Left as they were and kept from voting instead,
-    // they cost 5 %: the softmax loop has no register to spare.)
+    // the rows beside them.
     for (int x = p.toks * p.group * 8 + threadIdx.x; x < kRows * 8; x += kThreads)
 #pragma unroll
         for (int k = 0; k < 2 * C::kHalves; ++k)
@@ -313,8 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = M->tmem;
     // the kernel before this one: the list, or whatever the caller queued (the
     // workspace's header may be its work).  Waits read the limit anew each time
-    // round, so no barrier follows; with one, or with this before the barrier
-    // above, the softmax loop came out differently and 859 us were 868 to 929.
+    // round, so no barrier follows.
     pdl_wait();
     if (threadIdx.x == 96) M->wst.limit = ws_wait_limit(p.ws);
     if (p.single) {
