@@ -587,8 +587,10 @@ size_t dspark_attn_prompt_workspace_size(int B, int T, int n_heads, int n_kv_hea
  *        the nearest in range; the status word records DSPARK_ERR_BAD_PAGE)
  *   out  [T, n_heads, head_dim] bfloat16, lse [T, n_heads] float or NULL; rows
  *        that belong to no sequence stay untouched
- * Sequences never mix: values of one, finite or not, cannot reach another's
- * rows.  B >= 1, T >= 0 (T = 0 returns OK at once), head_dim 64 or 128,
+ * Values that are not finite reach the rows that see them and no others: not
+ * another sequence's, and not those of earlier tokens (a NaN or an infinity in v
+ * is added to the rows it belongs to; such a call takes about twice the time).
+ * B >= 1, T >= 0 (T = 0 returns OK at once), head_dim 64 or 128,
  * n_heads / n_kv_heads <= 128.
  */
 int dspark_attn_prompt(const void* q, const void* k, const void* v,
