@@ -557,12 +557,14 @@ size_t dspark_attn_paged_workspace_size(int R, int T, int n_heads, int n_kv_head
  * Products are summed in float32; the softmax's sum, maximum and lse are
  * float32.  DSPARK_BF16: factors are bf16, the weights rounded to it for the
  * product with V.  DSPARK_E4M3: K's codes meet q as the sum of two e4m3 terms
- * (exact but for values below 2^-10 of their row's largest, which are off by
- * 2^-18 of it at most), V's codes are widened exactly to fp16 and the weights
+ * (exact but for values below 2^-9 of their row's largest, which are off by
+ * 2^-17 of it at most), V's codes are widened exactly to fp16 and the weights
  * rounded to fp16 (11 bits down to 2^-24 of the row's largest); scales
  * multiply scores and weights in float32.  V rows whose scale is below 2^-100
  * (values below 2^-91) count as zeros.  The order of all sums depends on
  * the sizes and the device only, so reruns agree bit for bit.
+ * Scores (scale q.k) stay below 2^26 in magnitude: float32 rounds them by 4
+ * there, and far beyond a row may come out as NaN or as one without keys.
  * Cached values past kv_len[r] never matter, whatever bits they hold; K and V
  * of the kv_len[r] tokens themselves must be finite.
  * n_heads is a multiple of n_kv_heads, n_heads / n_kv_heads <= 128, scale

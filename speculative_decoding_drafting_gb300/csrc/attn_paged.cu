@@ -49,9 +49,10 @@
 // e4m3 caches: K tiles go to the tensor core as they are.  Each row of Q is
 // split into 2^e (hi + lo), both e4m3, 2^e such that the row's largest value is
 // in [128, 256): bf16's 8 significant bits are two times e4m3's 4, and e4m3
-// holds a value of 128's rounding error (1 .. 8) down to 2^-9, so the split is
-// exact except for values below 2^-10 of the row's largest, which are off by
-// 2^-18 of it at most.  hi and lo follow one another along K.
+// holds what the first term leaves down to 2^-9, so the split is exact except
+// for values below 2^-9 of the row's largest (0.25 of 128), which are off by
+// half of that step, 2^-17 of the largest, at most.  hi and lo follow one another
+// along K.
 // V tiles are widened to fp16 (one instruction for two values) by the units
 // that made the tile's weights, the one shared-memory pass that e4m3 costs.
 // V's scale joins the exponent, w = 2^(score + log2 scale - m + 10), so that
