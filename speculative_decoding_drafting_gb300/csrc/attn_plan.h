@@ -58,18 +58,17 @@ DSPARK_HD int plan_row_tiles(const PlanInput& p, const Request& q) {
     return (int)(((int64_t)q.q_len * p.group + kRowTile - 1) / kRowTile);
 }
 // Keys that row rho (of q_len * group) sees.
+DSPARK_HD_CALL int plan_row_keys(int group, int q_len, int kv_len, int64_t rho) {
+    return plan_clamp((int64_t)kv_len - q_len + rho / group + 1, kv_len);
+}
 DSPARK_HD int plan_seen(const PlanInput& p, const Request& q, int64_t rho) {
-    return plan_clamp((int64_t)q.kv_len - q.q_len + rho / p.group + 1, q.kv_len);
+    return plan_row_keys(p.group, q.q_len, q.kv_len, rho);
 }
-// Keys that row tile j reads, and how many key tiles they take.
-DSPARK_HD_CALL int plan_inner_keys(int group, int q_len, int kv_len, int j) {
-    const int64_t n = (int64_t)kv_len - q_len + (((int64_t)(j + 1) * kRowTile - 1) / group) + 1;
-    return plan_clamp(n, kv_len);
-}
+// Keys that row tile j reads (those of its last row), and how many key tiles they take.
 DSPARK_HD int plan_tile_keys(const PlanInput& p, const Request& q, int j) {
     const int64_t rows = (int64_t)q.q_len * p.group, end = (int64_t)(j + 1) * kRowTile;
     // the last row tile's last row sees every key
-    return end < rows ? plan_inner_keys(p.group, q.q_len, q.kv_len, j) : q.kv_len;
+    return end < rows ? plan_seen(p, q, end - 1) : q.kv_len;
 }
 DSPARK_HD int plan_key_tiles(int keys) { return keys > 0 ? (keys - 1) / kKeyTile + 1 : 1; }
 DSPARK_HD int plan_rows(const PlanInput& p, const Request& q, int j) {

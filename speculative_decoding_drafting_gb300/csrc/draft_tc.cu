@@ -499,21 +499,6 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-bool make_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, void* base, const cuuint64_t* dims,
-              const cuuint64_t* strides_bytes, const cuuint32_t* box,
-              CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    // host-side guard: a swizzled box row must fit the 128-byte swizzle span
-    const cuuint32_t es = dt == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 4u : (dt == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? 1u : 2u);
-    if (swz != CU_TENSOR_MAP_SWIZZLE_NONE && box[0] * es > 128u) return false;
-    if ((box[0] * es) % 16u) return false;
-    cuuint32_t estr[3] = {1, 1, 1};
-    return fn(m, dt, (cuuint32_t)rank, base, dims, strides_bytes, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // M-groups per cluster: pairs when the number of M-groups is even, else one.
 // Clusters of four placed 36 at a time on a 152-SM GB300 (144 CTAs, against
 // 76 pairs), and the 512-request sweep took 64.6 us per launch with them
@@ -594,7 +579,7 @@ cudaError_t launch_typed(DraftArgs& a, int k, cudaStream_t s) {
         cuuint64_t dims[2] = {(cuuint64_t)a.V, (cuuint64_t)a.r};
         cuuint64_t str[1] = {(cuuint64_t)a.V * 2};
         cuuint32_t box[2] = {64, (cuuint32_t)(pl.cs > 1 ? 128 / pl.cs : 64)};
-        if (!make_map(&tmB, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(a.W2), dims, str, box))
+        if (!make_tensor_map(&tmB, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.W2, dims, str, box))
             return cudaErrorInvalidValue;
     }
     TcParams p;
@@ -651,12 +636,16 @@ bool draft_tc_encode_available() { return encode_fn() != nullptr; }
 
 bool make_tensor_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base, const cuuint64_t* dims,
                      const cuuint64_t* strides_bytes, const cuuint32_t* box, CUtensorMapSwizzle swz) {
-    return make_map(m, dt, rank, const_cast<void*>(base), dims, strides_bytes, box, swz);
-}
-
-bool draft_tc_make_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, void* base, const cuuint64_t* dims,
-                       const cuuint64_t* strides_bytes, const cuuint32_t* box) {
-    return make_map(m, dt, rank, base, dims, strides_bytes, box);
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    // host-side guard: a swizzled box row must fit the 128-byte swizzle span
+    const cuuint32_t es = dt == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 4u : (dt == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? 1u : 2u);
+    if (swz != CU_TENSOR_MAP_SWIZZLE_NONE && box[0] * es > 128u) return false;
+    if ((box[0] * es) % 16u) return false;
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, dt, (cuuint32_t)rank, const_cast<void*>(base), dims, strides_bytes, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool draft_tc_supported(const DraftArgs& a) {

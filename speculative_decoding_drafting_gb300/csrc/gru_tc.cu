@@ -30,8 +30,6 @@
 namespace dspark {
 
 bool draft_tc_encode_available();
-bool draft_tc_make_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, void* base, const cuuint64_t* dims,
-                       const cuuint64_t* strides_bytes, const cuuint32_t* box);
 
 namespace {
 
@@ -233,7 +231,7 @@ cudaError_t launch_gru_tc(DraftArgs& a, int k, cudaStream_t s) {
         cuuint64_t dims[2] = {(cuuint64_t)ldzb, (cuuint64_t)a.R};
         cuuint64_t str[1] = {(cuuint64_t)ldzb * 2};
         cuuint32_t box[2] = {64, (cuuint32_t)kGM};
-        if (!draft_tc_make_map(&tmA, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.zb, dims, str, box))
+        if (!make_tensor_map(&tmA, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.zb, dims, str, box))
             return cudaErrorInvalidValue;
     }
     {
@@ -241,7 +239,7 @@ cudaError_t launch_gru_tc(DraftArgs& a, int k, cudaStream_t s) {
         cuuint64_t dims[2] = {(cuuint64_t)(3 * a.r), (cuuint64_t)(2 * a.r + a.d)};
         cuuint64_t str[1] = {(cuuint64_t)(3 * a.r) * 2};
         cuuint32_t box[2] = {64, 64};
-        if (!draft_tc_make_map(&tmB, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(a.Wgco), dims, str, box))
+        if (!make_tensor_map(&tmB, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.Wgco, dims, str, box))
             return cudaErrorInvalidValue;
     }
     GruParams p;

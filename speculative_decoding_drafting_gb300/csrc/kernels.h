@@ -189,9 +189,12 @@ cudaError_t allow_smem(void (*kern)(KArgs...), size_t bytes) {
 // Launch `kern` on `s`.  With `pdl` set the launch may begin while the
 // previous kernel in the stream is still running (programmatic dependent
 // launch); such a kernel executes griddepcontrol.wait (pdl_wait) before it
-// touches anything that kernel writes or reads.  The first kernel of every
-// entry point is launched without it, so work the caller queued before the
-// call is complete and visible as usual.
+// touches anything that kernel writes or reads.  The first kernel of an entry
+// point is launched without it, so work the caller queued before the call is
+// complete and visible as usual; but for attn_paged and, where there is no list
+// to sort, attn_prompt: their first kernel starts beside the caller's last one
+// (barriers and descriptors are ready by its end) and touches no device memory
+// before pdl_wait.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, bool pdl,
                           Args... args) {

@@ -12,7 +12,8 @@ namespace dspark {
 // Host side: a tiled tensor map of rank 1 to 3 (draft_tc.cu); false if the
 // driver refuses it.
 bool make_tensor_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base, const cuuint64_t* dims,
-                     const cuuint64_t* strides_bytes, const cuuint32_t* box, CUtensorMapSwizzle swz);
+                     const cuuint64_t* strides_bytes, const cuuint32_t* box,
+                     CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B);
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -29,8 +29,6 @@
 namespace dspark {
 
 bool draft_tc_encode_available();
-bool draft_tc_make_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, void* base, const cuuint64_t* dims,
-                       const cuuint64_t* strides_bytes, const cuuint32_t* box);
 
 namespace {
 
@@ -488,7 +486,7 @@ cudaError_t launch_typed(VerifyArgs& a, cudaStream_t s) {
         cuuint64_t dims[2] = {(cuuint64_t)a.V, (cuuint64_t)a.r};
         cuuint64_t str[1] = {(cuuint64_t)a.V * 2};
         cuuint32_t box[2] = {kBN, (cuuint32_t)(64 / cs)};
-        if (!draft_tc_make_map(&tmB, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(a.W2), dims, str, box))
+        if (!make_tensor_map(&tmB, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.W2, dims, str, box))
             return cudaErrorInvalidValue;
     }
     ResParams p;
