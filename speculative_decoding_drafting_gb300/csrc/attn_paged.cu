@@ -38,7 +38,7 @@
 //               others run.  Thread = key, registers = rows.  The reference of
 //               a row is raised only when a score exceeds it by more than 8
 //               binary orders (a vote per tile; weights up to 2^8 are far
-//               inside bf16 and float32; 4 orders above the lift for e4m3), so
+//               inside bf16 and float32; 5.5 orders above the lift for e4m3), so
 //               a tile costs no maximum over its keys.
 //   warps 20-23 bring the next segment's Q rows, then join the streams of the
 //               finished one and store it, while the units are at the next
@@ -56,7 +56,7 @@
 // V tiles are widened to fp16 (one instruction for two values) by the units
 // that made the tile's weights, the one shared-memory pass that e4m3 costs.
 // V's scale joins the exponent, w = 2^(score + log2 scale - m + 10), so that
-// the weights, whatever the scales, lie below 2^14 with fp16's 11 bits down to
+// the weights, whatever the scales, lie below 2^15.5 with fp16's 11 bits down to
 // 2^-24 of the row's largest; the sum takes w / scale.
 //
 // Keys a row must not see get weight 0 by selection, not by multiplication;
@@ -97,8 +97,9 @@ struct Cfg {
     static constexpr int kQRows = HD == 128 ? 32 : 64;
     static constexpr int kQBytes = kQRows * HD * 2;                        // bf16 rows, or hi and lo
     static constexpr int kScMod = kSc ? kSc : 1;                           // divisor (unused without e4m3)
-    // bits by which a weight's exponent is lifted, and may exceed that
-    static constexpr float kLift = F8 ? 10.f : 0.f, kLazy = F8 ? 4.f : 8.f;
+    // bits by which a weight's exponent is lifted, and may exceed that (fp16 ends
+    // at 2^16; with 4 instead of 5.5 the long e4m3 case took 149 us for 138)
+    static constexpr float kLift = F8 ? 10.f : 0.f, kLazy = F8 ? 5.5f : 8.f;
     static constexpr int kOffV = kK * kLoadBytes;
     static constexpr int kOffW = kOffV + kV * kLoadBytes;
     static constexpr int kOffP = kOffW + kW * kTileBytes;
@@ -416,7 +417,7 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
             if constexpr (N > 16) part(std::integral_constant<int, 16>{}, std::integral_constant<int, N - 16>{});
             // (raised once: scores of 2^28 and more round by more than the threshold)
             if (raised || !named_any(bar, 128, top > C::kLift + C::kLazy)) break;
-            // one is too large: raise the references to the largest scores so far
+            // one is too large: raise its reference to its largest score so far
 #pragma unroll 1
             for (int c0 = 0; c0 < N; c0 += 4) {
                 float x[4], mine = 0.f;
@@ -433,8 +434,9 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
             named_sync(bar, 128);
             if (tr < N) {
                 const float old = M->ref[u][tr];
-                const float ref = fmaxf(fmaxf(fmaxf(M->red[u][0][tr], M->red[u][1][tr]),
-                                              fmaxf(M->red[u][2][tr], M->red[u][3][tr])), old);
+                const float most = fmaxf(fmaxf(M->red[u][0][tr], M->red[u][1][tr]), fmaxf(M->red[u][2][tr], M->red[u][3][tr]));
+                // each row by its own scores alone: the others' do not reach its bits
+                const float ref = most > old + C::kLazy ? most : old;
                 M->ref[u][tr] = ref;
                 M->nref[u][tr] = C::kLift - ref;
                 M->fac[u][tr] = ex2_approx(old - ref);

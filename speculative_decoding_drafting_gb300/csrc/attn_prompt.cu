@@ -669,7 +669,8 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint32_t 
             const float top = c >= 0.f ? fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c
                                        : fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3])) * c;
             if (__any_sync(0xffffffffu, top > ref + kLazy)) {
-                const float m = fmaxf(ref, top), f = ex2_approx(ref - m);
+                // each row by its own scores alone: the others' do not reach its bits
+                const float m = top > ref + kLazy ? top : ref, f = ex2_approx(ref - m);
                 ref = m;
                 float a, b;
                 unpack2(l2, a, b);

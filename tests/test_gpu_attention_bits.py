@@ -102,3 +102,56 @@ def test_paged_values_past_the_end_do_not_matter(dtype, heads, kv_heads, dim, ne
         assert torch.isfinite(r["out"].float()).all()
         first = first or r
         assert _same(r, first), (code, scale)
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim", [(8, 2, 128), (4, 4, 64), (7, 1, 128), (16, 1, 64)])
+def test_prompt_rows_do_not_depend_on_later_tokens(heads, kv_heads, dim):
+    """Large values in the later tokens of the same sequence, infinities among
+    them, do not change a bit of the rows before."""
+    g = torch.Generator().manual_seed(dim + heads)
+    lens = [700, 90, 333]
+    T = sum(lens)
+    q, k, v = (_rand(g, T, h, dim) for h in (heads, kv_heads, kv_heads))
+    first = binding.attn_prompt(q, k, v, _off(lens), lse=True)
+    for keep in ((600, 50, 1), (129, 1, 300), (640, 89, 332)):
+        good = torch.zeros(T, dtype=torch.bool)
+        for i, n in enumerate(keep):
+            good[sum(lens[:i]):sum(lens[:i]) + n] = True
+        good = good.to(DEV)
+        for size in (20.0, 400.0, float("inf"), float("nan")):
+            x = [t.clone() for t in (q, k, v)]
+            for t in x:
+                t[~good] *= size
+            r = binding.attn_prompt(*x, _off(lens), lse=True)
+            assert torch.equal(r["out"][good], first["out"][good]) and torch.equal(r["lse"][good], first["lse"][good])
+
+
+@pytest.mark.parametrize("dtype", [BF, F8])
+@pytest.mark.parametrize("heads,kv_heads,dim", [(8, 2, 128), (4, 4, 64), (12, 2, 128), (3, 1, 64)])
+def test_paged_rows_do_not_depend_on_later_tokens(dtype, heads, kv_heads, dim):
+    """The same for the new tokens of a block: large queries, keys and values of
+    the later ones leave the first ones' bits alone."""
+    g = torch.Generator().manual_seed(dim + heads)
+    kv, new, page = [300 + (i * 29) % 500 for i in range(240 // kv_heads)], 6, 16
+    R = len(kv)
+    counts = [-(-n // page) for n in kv]
+    table = torch.full((R, max(counts)), -1, dtype=torch.int32)
+    for r, c in enumerate(counts):
+        table[r, :c] = torch.arange(sum(counts[:r]), sum(counts[:r]) + c)
+    table = table.to(DEV)
+    K, V = (_rand(g, sum(kv), kv_heads, dim) for _ in range(2))
+    q = _rand(g, R * new, heads, dim)
+    last = torch.tensor([n - 1 for n in torch.tensor(kv).cumsum(0).tolist()], device=DEV)
+    good = torch.arange(R * new, device=DEV) % new < 3
+    first = None
+    for size in (1.0, 20.0, 300.0):
+        k2, v2, q2 = K.clone(), V.clone(), q.clone()
+        for back in range(3):
+            k2[last - back] *= size
+            v2[last - back] *= size
+        q2[~good] *= size
+        cache = binding.KvCache.empty(sum(counts), kv_heads, page, dim, dtype, DEV)
+        binding.kv_write(cache, k2, v2, _off(kv), _i32(kv), table)
+        r = binding.attn_paged(q2, cache, _off([new] * R), _i32(kv), table, lse=True)
+        first = first or r
+        assert torch.equal(r["out"][good], first["out"][good]) and torch.equal(r["lse"][good], first["lse"][good]), size
