@@ -12,10 +12,10 @@
 // bound by the cache's bytes: 64 KB of bf16 per key tile take the SM about
 // 2800 cycles at the measured copy rate, its two products under 600.
 // Measured (GB300, against 6.68 TB/s of a plain copy): 256 requests of 200 to
-// 4000 keys, blocks of 1 to 6 tokens, 32 heads over 8 of 128, bf16: 333 us,
-// 6.7 TB/s; 64 requests of 500 to 8000 e4m3 keys, one token, 64 heads over 8:
-// 116 us, 5.0 TB/s (5.7 TB/s at 8192 keys each); two requests of 150001 and
-// 260001 e4m3 keys at most, blocks of 6, 32 heads over 4: 140 us, 3.8 TB/s.
+// 4000 keys, blocks of 1 to 6 tokens, 32 heads over 8 of 128, bf16: 330 to 335
+// us, 6.7 TB/s; 64 requests of 500 to 8000 e4m3 keys, one token, 64 heads over 8:
+// 113 us, 5.1 TB/s (5.6 TB/s at 8192 keys each); two requests of 150001 and
+// 260001 e4m3 keys at most, blocks of 6, 32 heads over 4: 138 us, 3.8 TB/s.
 //
 // One persistent CTA per SM walks an equal span of the line of all items' key
 // tiles (attn_plan.h); pieces of split items go to the workspace and a second
@@ -840,8 +840,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t* dst = smem + (kIsV ? C::kOffV : 0) + c.slot * C::kLoadBytes;
         if (F8 && !kIsV) {
             // the tile's 2 x 128 scales, 4 tokens to a lane: a tensor copy per page,
-            // 64 bytes each at 16 tokens, took 248 us where this takes 216 (64
-            // requests of 8192 tokens, 8 heads of 128)
+            // 64 bytes each at 16 tokens, took 248 us where this took 216 (64
+            // requests of 8192 tokens, 8 heads of 128; 208 by now)
             const int tk = lane * 4;
             const uint32_t pid = (uint32_t)__shfl_sync(0xffffffffu, id, tk >> (p.page_log2 < 7 ? p.page_log2 : 7));
             const bool in = tk < c.keys - c.tok && pid < (uint32_t)p.n_pages;
@@ -1141,10 +1141,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (named_any(1 + u, 128, !got)) break;
             const SegInfo& s = M->seg[at];
             if (s.rows == 0) break;
-            // a loop for each number of rows: e4m3 decoding of 8 rows took 138 us with
-            // one loop for 16 and 32, and takes 118; 48 rows over long e4m3 caches
-            // 157 and 141.  (bf16 has no loop for 24: such items are bound by the
-            // cache's bytes, and one shape more cost mixed lengths 3 %.)
+            // a loop for each number of rows: without the one for 48, e4m3 blocks of 1
+            // to 17 tokens take 229 us where they take 180, and 48 rows over long e4m3
+            // caches 146 and 138; without the one for 8, e4m3 decoding 115.4 and 113.5.
+            // (bf16 has no loop for 24: such items are bound by the cache's bytes, and
+            // one shape more cost blocks of 1 to 17 tokens 4 %.)
             if (s.rows <= 8)
                 soft_segment<HD, F8, 8>(p, s, M, smem, tmem, u, st);
             else if (s.rows <= 16)
@@ -1215,12 +1216,13 @@ __global__ void __launch_bounds__(256) attn_paged_join(const PagedParams p, int 
 }
 
 // PlanInput::lengths.  The lengths stand for the time a CTA takes, fitted to
-// mixed batches (an item costs about what two tiles do, between its Q rows and
-// its stored rows; e4m3 tiles of many rows cost more than they bring in bytes).
-// With every tile as long as another, e4m3 blocks of 1 to 17 tokens (64
-// requests of 1000 to 6001 keys, 48 heads of 64) took 220 us and take 194,
-// e4m3 blocks of 1 to 6 (256 requests of 200 to 4000 keys) 350 and 323, short
-// bf16 ones (50 to 1000 keys) 134 and 128.
+// mixed batches of both head sizes, by the rows and the cache's type alone (an
+// item costs about what two tiles do, between its Q rows and its stored rows;
+// e4m3 tiles of many rows cost more than they bring in bytes).  With every tile
+// as long as another, blocks of 1 to 17 tokens (64 requests of 1000 to 6001
+// keys, 48 heads of 64) take 196 us where they take 180 over e4m3 caches, and 127
+// and 120 over bf16; blocks of 1 to 6 tokens (256 requests of 200 to 4000, or of
+// 50 to 1000 keys) take the same.
 constexpr uint32_t tile_lengths(uint32_t r8, uint32_t r16, uint32_t r24, uint32_t r32, uint32_t r48, uint32_t r64) {
     return r8 | r16 << 5 | r24 << 10 | r32 << 15 | r48 << 20 | r64 << 25;
 }

@@ -34,12 +34,12 @@
 //
 // Bound by the tensor core and the softmax beside it: the two products of a
 // tile of 128 x 128 scores take it about 1024 cycles at head_dim 128.
-// Measured (GB300): one sequence of 12001 tokens, 32 heads over 8 of 128: 851
-// us, 1386 TFLOP/s of the causal half (a plain bf16 product of 8192^3 runs at
-// 1902 in a burst and 1733 under the power cap); 16 sequences of 100 to 4000
-// tokens: 604 us, 1122 TFLOP/s.  (Taking a quarter of the exponentials from
-// the XU pipe to a polynomial on the FMA pipe made the first 1012 us: its
-// instructions cost more than the pipe it relieves.)
+// Measured (GB300): one sequence of 12001 tokens, 32 heads over 8 of 128: 789
+// to 847 us, 1.39 to 1.50 PFLOP/s of the causal half (a plain bf16 product of
+// 8192^3 runs at 1.90 in a burst and 1.73 under the power cap), of 64: 676 us; 16
+// sequences of 100 to 4000 tokens: 590 to 612 us, 1.11 to 1.15 PFLOP/s.  (Taking
+// a quarter of the exponentials from the XU pipe to a polynomial on the FMA pipe
+// cost 18 %: its instructions cost more than the pipe it relieves.)
 #include <cfloat>
 
 #include <cuda.h>
