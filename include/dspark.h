@@ -600,6 +600,99 @@ int dspark_attn_prompt(const void* q, const void* k, const void* v,
                        const int32_t* seq_off, int B, int T, int n_heads, int n_kv_heads, int head_dim,
                        float scale, void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------- head norms and rotary positions */
+
+/*
+ * What stands between a layer's projections and the attention above (no
+ * counterpart on the pages): each query and key head is normed and turned to
+ * its token's position.
+ *
+ * Rotary positions.  The first `rot` values of a head are turned in pairs:
+ *   a' = amplitude (a cos t - b sin t),  b' = amplitude (b cos t + a sin t)
+ * where pair i (i < rot / 2) is (x_i, x_{i + rot/2}), or (x_2i, x_{2i+1}) if
+ * interleaved, and t = position[axis[i]] * inv_freq[i].  The values after
+ * the first `rot` pass as they are.  One axis is the usual position in a text;
+ * images and video take several (time, height, width), each frequency following
+ * one of them, in any pattern.
+ *   rot         a multiple of 8, 8 .. head_dim (SHAPE)
+ *   n_axes      1 .. 4 (SHAPE)
+ *   axis        [rot / 2] below n_axes (INVALID_ARG)
+ *   inv_freq    [rot / 2] radians per position, finite (INVALID_ARG)
+ *   amplitude   finite (INVALID_ARG); 1 as a rule
+ * The angle's fraction of a turn is formed in 64-bit integers: cosine and sine are
+ * off by less than 2^-22, and by 2^-52 of the whole angle (inv_freq / 2 pi is
+ * rounded to 53 bits), at any position.  The struct is read on the host during
+ * the call.
+ */
+typedef struct {
+    int rot, interleaved, n_axes;
+    float amplitude;
+    uint8_t axis[64];
+    double inv_freq[64];
+} dspark_rope_t;
+
+/*
+ * RMS norm of each head before the rotation: y = x w / sqrt(mean x^2 + eps).
+ *   q_w, k_w   [head_dim] w_dtype (DSPARK_F32 or DSPARK_BF16), device, 16-byte
+ *              aligned; NULL: queries (keys) are not normed
+ *   eps        at least 1e-30 and finite (INVALID_ARG)
+ * The sum of squares is float32: values up to 2^60 in magnitude.
+ */
+typedef struct {
+    const void* q_w;
+    const void* k_w;
+    int w_dtype;
+    float eps;
+} dspark_head_norm_t;
+
+/*
+ * Norm and rotation of packed rows:
+ *   q         [T, n_heads, head_dim] bfloat16,  k [T, n_kv_heads, head_dim]
+ *             bfloat16 or NULL with n_kv_heads = 0; q_stride, k_stride elements
+ *             from token to token (multiples of 8, at least the heads times
+ *             head_dim)
+ *   positions [T, n_axes] int32, any values; may be NULL if rope is
+ *   rope, norm  either may be NULL: no rotation, no norm
+ *   q_out, k_out  bfloat16 in the shapes of q and k, with strides of their own.
+ *             They may be q and k themselves, with the same strides; otherwise
+ *             nothing of inputs and outputs may overlap.
+ * All of float32 up to one rounding per value.  q, k, q_out and k_out are
+ * 16-byte aligned device memory of the current device.  head_dim 64 or 128,
+ * n_heads in [1, 2^19], n_kv_heads in [0, 4096], T >= 0 (SHAPE; T = 0 returns OK
+ * at once).  No workspace.
+ */
+int dspark_qk_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride, const int32_t* positions,
+                   int T, int n_heads, int n_kv_heads, int head_dim,
+                   const dspark_rope_t* rope, const dspark_head_norm_t* norm,
+                   void* q_out, void* k_out, int64_t q_out_stride, int64_t k_out_stride, void* stream);
+
+/*
+ * The same on the way into the cache: queries are normed and turned into q_out,
+ * keys are normed, turned and written to their places, values are written as
+ * dspark_kv_write writes them.
+ *   q         [T, n_heads, head_dim] bfloat16, or NULL with n_heads = 0
+ *   K, V      [T, n_kv_heads, head_dim] bfloat16
+ *   positions NULL: a token's position in its request, on every axis; else
+ *             [T, n_axes] int32 for the angles alone (its place in the cache
+ *             follows from the batch)
+ *   k_out     [T, n_kv_heads, head_dim] bfloat16 or NULL: the turned keys, for
+ *             dspark_attn_prompt
+ * DSPARK_BF16 caches hold the bits of k_out.  DSPARK_E4M3: scale = a / 448 with a
+ * the largest magnitude of the float32 row, each code the e4m3 value nearest
+ * to x 448 / a in float32 (values, and keys that are neither normed nor turned, to
+ * the exact quotient); zero rows and rows that are not finite as dspark_kv_write.
+ * Tokens of no request leave their rows of q_out and k_out untouched; tokens
+ * without a place in the cache (a negative position, a bad page) get theirs.
+ * Strides, alignment and sizes as above (n_heads may be 0), workspace of
+ * dspark_kv_workspace_size() bytes.
+ */
+int dspark_rope_write(const dspark_kv_cache_t* cache, const dspark_kv_batch_t* batch,
+                      const void* q, const void* K, const void* V,
+                      int64_t q_stride, int64_t k_stride, int64_t v_stride, int n_heads, const int32_t* positions,
+                      const dspark_rope_t* rope, const dspark_head_norm_t* norm,
+                      void* q_out, void* k_out, int64_t q_out_stride, int64_t k_out_stride,
+                      void* ws, size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------- random */
 
 /*

@@ -97,6 +97,8 @@ def load(build_if_missing: bool = True):
         L.dspark_kv_read.argtypes = [P, P, P, P, P, sz, P]
         L.dspark_attn_paged.argtypes = [P, i64, P, P, i32, f32, P, P, P, sz, P]
         L.dspark_attn_prompt.argtypes = [P, P, P, i64, i64, i64, P, i32, i32, i32, i32, i32, f32, P, P, P, sz, P]
+        L.dspark_qk_rope.argtypes = [P, P, i64, i64, P, i32, i32, i32, i32, P, P, P, P, i64, i64, P]
+        L.dspark_rope_write.argtypes = [P, P, P, P, P, i64, i64, i64, i32, P, P, P, P, P, i64, i64, P, sz, P]
         L.dspark_workspace_set_wait.argtypes = [P, u64, i32, P]
         L.dspark_profile_enable.argtypes = [i32]
         L.dspark_profile_collect.argtypes = [P, P, i32]
@@ -108,7 +110,8 @@ def load(build_if_missing: bool = True):
                      "dspark_sts_fit",
                      "dspark_sts_apply", "dspark_philox4x32_10", "dspark_workspace_set_wait",
                      "dspark_workspace_status", "dspark_profile_enable", "dspark_profile_collect",
-                     "dspark_kv_write", "dspark_kv_read", "dspark_attn_paged", "dspark_attn_prompt"):
+                     "dspark_kv_write", "dspark_kv_read", "dspark_attn_paged", "dspark_attn_prompt",
+                     "dspark_qk_rope", "dspark_rope_write"):
             getattr(L, name).restype = i32
         _lib = L
         return _lib
@@ -617,6 +620,142 @@ def attn_prompt(q, k, v, seq_off, scale: Optional[float] = None, lse: bool = Fal
                                 float(dim ** -0.5 if scale is None else scale), _p(out["out"]), _p(out.get("lse")),
                                 _p(ws), ws.numel(), _stream(stream))
     _check("dspark_attn_prompt", code)
+    out["ws"] = ws
+    return out
+
+
+class _Rope(ctypes.Structure):
+    """dspark_rope_t."""
+    _fields_ = [("rot", ctypes.c_int), ("interleaved", ctypes.c_int), ("n_axes", ctypes.c_int),
+                ("amplitude", ctypes.c_float), ("axis", ctypes.c_uint8 * 64), ("inv_freq", ctypes.c_double * 64)]
+
+
+class _HeadNorm(ctypes.Structure):
+    """dspark_head_norm_t."""
+    _fields_ = [("q_w", ctypes.c_void_p), ("k_w", ctypes.c_void_p), ("w_dtype", ctypes.c_int), ("eps", ctypes.c_float)]
+
+
+class Rope:
+    """Rotary positions: the first ``2 * len(inv_freq)`` values of a head are
+    turned, pair i by position[axis[i]] * inv_freq[i] radians (``dspark_rope_t``).
+    ``axis`` None: one axis.  ``interleaved`` pairs neighbours instead of the two
+    halves; ``amplitude`` multiplies what is turned.  ``n_axes`` None: as many as
+    ``axis`` names."""
+
+    def __init__(self, inv_freq, axis=None, interleaved: bool = False, amplitude: float = 1.0,
+                 n_axes: Optional[int] = None):
+        inv_freq = [float(f) for f in inv_freq]
+        axis = [0] * len(inv_freq) if axis is None else [int(a) for a in axis]
+        if not 1 <= len(inv_freq) <= 64:
+            raise ValueError(f"1 to 64 frequencies, got {len(inv_freq)}")
+        if len(axis) != len(inv_freq) or min(axis) < 0 or max(axis) > 3:
+            raise ValueError("axis must hold a number from 0 to 3 for each frequency")
+        self.n_axes = max(axis) + 1 if n_axes is None else int(n_axes)
+        self._c = _Rope(2 * len(inv_freq), int(interleaved), self.n_axes, amplitude, (ctypes.c_uint8 * 64)(*axis),
+                        (ctypes.c_double * 64)(*inv_freq))
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def from_theta(cls, rot: int, theta: float = 10000.0, **kw) -> "Rope":
+        """The usual frequencies theta^(-2 i / rot), i < rot / 2."""
+        return cls([theta ** (-2.0 * i / rot) for i in range(rot // 2)], **kw)
+
+
+class HeadNorm:
+    """RMS norm of each query and key head with weights ``q`` and ``k``
+    [head_dim], float32 or bfloat16 CUDA tensors (None: that side is not normed)."""
+
+    def __init__(self, q=None, k=None, eps: float = 1e-6):
+        given = [w for w in (q, k) if w is not None]
+        if not given:
+            raise ValueError("HeadNorm takes weights for queries, keys or both")
+        if any(w.dtype != given[0].dtype or w.dim() != 1 for w in given):
+            raise ValueError("the weights must be vectors of one dtype")
+        self.q, self.k, self.eps = q, k, eps
+        self._c = _HeadNorm(_p(q), _p(k), _dt(given[0]), eps)
+        self._ref = ctypes.byref(self._c)
+
+    def _check(self, dim):
+        _shape("the norm's q", self.q, (dim,))
+        _shape("the norm's k", self.k, (dim,))
+
+
+def _turn_args(rope, norm, positions, T, dim):
+    """Checks of what both calls share; the positions' and the structs' addresses."""
+    if norm is not None:
+        norm._check(dim)
+    if positions is not None:
+        if rope is None:
+            raise ValueError("positions go with a rope")
+        _shape("positions", positions, (T,) if rope.n_axes == 1 and positions.dim() == 1 else (T, rope.n_axes), torch.int32)
+    return _p(positions), rope and rope._ref, norm and norm._ref
+
+
+def _rows_out(out, name, T, heads, dim, dev):
+    """The output rows of that name, made if need be, with their address and stride."""
+    if out.get(name) is None:
+        t = out[name] = torch.empty((T, heads, dim), dtype=torch.bfloat16, device=dev)
+        return t.data_ptr(), heads * dim
+    return _token_rows(name, out[name], T, heads, dim)
+
+
+def qk_rope(q, k, positions, rope: Optional[Rope] = None, norm: Optional[HeadNorm] = None, out=None, stream=None):
+    """Norm and rotation of query and key heads (``dspark_qk_rope``): q [T,
+    n_heads, head_dim] and k [T, n_kv_heads, head_dim] (or None) in bf16,
+    positions int32 [T] or [T, axes].  Returns a dict with ``q`` and ``k``;
+    ``out=dict(q=q, k=k)`` works in place."""
+    L = load()
+    T, heads, dim = q.shape
+    pos, rp, np_ = _turn_args(rope, norm, positions, T, dim)
+    if rope is not None and positions is None:
+        raise ValueError("a rope takes positions")
+    out = {} if out is None else out
+    qp, qs = _token_rows("q", q, T, heads, dim)
+    qo, qos = _rows_out(out, "q", T, heads, dim, q.device)
+    kv_heads = kp = ks = ko = kos = 0
+    if k is not None:
+        if k.dim() != 3:
+            raise ValueError("k must have shape (T, n_kv_heads, head_dim)")
+        kv_heads = k.shape[1]
+        kp, ks = _token_rows("k", k, T, kv_heads, dim)
+        ko, kos = _rows_out(out, "k", T, kv_heads, dim, q.device)
+    code = L.dspark_qk_rope(qp, kp or None, qs, ks, pos, T, heads, kv_heads, dim, rp, np_, qo, ko or None, qos, kos,
+                            _stream(stream))
+    _check("dspark_qk_rope", code)
+    return out
+
+
+def rope_write(cache: KvCache, q, K, V, q_off, kv_len, page_table, rope: Optional[Rope] = None,
+               norm: Optional[HeadNorm] = None, positions=None, keep: bool = False, ws=None, out=None, stream=None):
+    """Norm and rotation on the way into the cache (``dspark_rope_write``): K and V
+    go to their pages as ``kv_write`` takes them, K normed and turned; q (None:
+    keys and values alone) comes back in the dict's ``q``, with ``keep`` the turned
+    keys in ``k``.  ``positions`` None: a token's place in its request; else
+    [T] or [T, axes].  ``ws`` holds the status word, as for ``kv_write``."""
+    L = load()
+    T, dim = K.shape[0], cache.head_dim
+    b = _batch(q_off, kv_len, page_table, T)
+    pos, rp, np_ = _turn_args(rope, norm, positions, T, dim)
+    out = {} if out is None else out
+    dev = cache.k.device
+    kp, ks = _token_rows("K", K, T, cache.n_kv_heads, dim)
+    vp, vs = _token_rows("V", V, T, cache.n_kv_heads, dim)
+    heads = qs = qos = kos = 0
+    qp = qo = ko = None
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must have shape (T, n_heads, head_dim)")
+        heads = q.shape[1]
+        qp, qs = _token_rows("q", q, T, heads, dim)
+        qo, qos = _rows_out(out, "q", T, heads, dim, dev)
+    if keep or out.get("k") is not None:
+        ko, kos = _rows_out(out, "k", T, cache.n_kv_heads, dim, dev)
+    c = cache._struct()
+    if ws is None:
+        ws = _workspace(L.dspark_kv_workspace_size(), dev)
+    code = L.dspark_rope_write(ctypes.byref(c), ctypes.byref(b), qp, kp, vp, qs, ks, vs, heads, pos, rp, np_, qo, ko, qos, kos,
+                               _p(ws), ws.numel(), _stream(stream))
+    _check("dspark_rope_write", code)
     out["ws"] = ws
     return out
 

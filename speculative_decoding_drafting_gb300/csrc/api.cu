@@ -453,4 +453,84 @@ int dspark_attn_prompt(const void* q, const void* k, const void* v, int64_t q_st
     return cuda_status(launch_attn_prompt(a, static_cast<cudaStream_t>(stream)));
 }
 
+// The rotation's and the norm's own checks.
+static int check_rope(const dspark_rope_t* r, int head_dim) {
+    if (!r) return DSPARK_OK;
+    if (r->rot < 8 || r->rot > head_dim || r->rot % 8 || r->n_axes < 1 || r->n_axes > 4) return DSPARK_ERR_SHAPE;
+    if (!std::isfinite(r->amplitude)) return DSPARK_ERR_INVALID_ARG;
+    for (int i = 0; i < r->rot / 2; ++i)
+        if (r->axis[i] >= r->n_axes || !std::isfinite(r->inv_freq[i])) return DSPARK_ERR_INVALID_ARG;
+    return DSPARK_OK;
+}
+
+static int check_norm(const dspark_head_norm_t* n) {
+    if (!n) return DSPARK_OK;
+    if (!dtype_ok(n->w_dtype)) return DSPARK_ERR_UNSUPPORTED_DTYPE;
+    if (!(n->eps >= 1e-30f) || !std::isfinite(n->eps) || !aligned16(n->q_w) || !aligned16(n->k_w))
+        return DSPARK_ERR_INVALID_ARG;
+    return DSPARK_OK;
+}
+
+static bool rows_ok(const void* p, int64_t stride, int heads, int dim) {
+    return p && aligned16(p) && stride_ok(stride, heads, dim);
+}
+
+int dspark_qk_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride, const int32_t* positions, int T,
+                   int n_heads, int n_kv_heads, int head_dim, const dspark_rope_t* rope, const dspark_head_norm_t* norm,
+                   void* q_out, void* k_out, int64_t q_out_stride, int64_t k_out_stride, void* stream) {
+    if ((head_dim != 64 && head_dim != 128) || n_heads < 1 || n_heads > 1 << 19 || n_kv_heads < 0 || n_kv_heads > 4096 || T < 0)
+        return DSPARK_ERR_SHAPE;
+    int st = check_rope(rope, head_dim);
+    if (st) return st;
+    st = check_norm(norm);
+    if (st) return st;
+    if (T == 0) return DSPARK_OK;
+    if (!rows_ok(q, q_stride, n_heads, head_dim) || !rows_ok(q_out, q_out_stride, n_heads, head_dim) || (rope && !positions))
+        return DSPARK_ERR_INVALID_ARG;
+    if (n_kv_heads > 0 && (!rows_ok(k, k_stride, n_kv_heads, head_dim) || !rows_ok(k_out, k_out_stride, n_kv_heads, head_dim)))
+        return DSPARK_ERR_INVALID_ARG;
+    if (!on_current_device(q) || !on_current_device(q_out) ||
+        (n_kv_heads > 0 && (!on_current_device(k) || !on_current_device(k_out))))
+        return DSPARK_ERR_INVALID_ARG;
+    RopeArgs a = {};
+    a.q = q; a.k = k; a.q_stride = q_stride; a.k_stride = k_stride;
+    a.n_heads = n_heads; a.n_kv_heads = n_kv_heads; a.head_dim = head_dim; a.T = T;
+    a.positions = positions; a.rope = rope; a.norm = norm;
+    a.q_out = q_out; a.k_out = k_out; a.q_out_stride = q_out_stride; a.k_out_stride = k_out_stride;
+    return cuda_status(launch_rope(a, static_cast<cudaStream_t>(stream)));
+}
+
+int dspark_rope_write(const dspark_kv_cache_t* cache, const dspark_kv_batch_t* batch, const void* q, const void* K,
+                      const void* V, int64_t q_stride, int64_t k_stride, int64_t v_stride, int n_heads,
+                      const int32_t* positions, const dspark_rope_t* rope, const dspark_head_norm_t* norm, void* q_out,
+                      void* k_out, int64_t q_out_stride, int64_t k_out_stride, void* ws, size_t ws_bytes, void* stream) {
+    int st = check_cache(cache);
+    if (st) return st;
+    st = check_batch_sizes(batch);
+    if (st) return st;
+    if (n_heads < 0 || n_heads > 1 << 19) return DSPARK_ERR_SHAPE;
+    st = check_rope(rope, cache->head_dim);
+    if (st) return st;
+    st = check_norm(norm);
+    if (st) return st;
+    if (batch->T == 0) return DSPARK_OK;
+    const int hk = cache->n_kv_heads, dim = cache->head_dim;
+    if (!batch->q_off || !batch->kv_len || !batch->page_table || !rows_ok(K, k_stride, hk, dim) || !rows_ok(V, v_stride, hk, dim))
+        return DSPARK_ERR_INVALID_ARG;
+    if (n_heads > 0 && (!rows_ok(q, q_stride, n_heads, dim) || !rows_ok(q_out, q_out_stride, n_heads, dim)))
+        return DSPARK_ERR_INVALID_ARG;
+    if (k_out && !rows_ok(k_out, k_out_stride, hk, dim)) return DSPARK_ERR_INVALID_ARG;
+    if (!ws || !aligned256(ws) || ws_bytes < sizeof(WsHeader)) return DSPARK_ERR_WORKSPACE;
+    if (!cache_on_device(cache) || !on_current_device(K) || !on_current_device(V) ||
+        (n_heads > 0 && (!on_current_device(q) || !on_current_device(q_out))) || (k_out && !on_current_device(k_out)))
+        return DSPARK_ERR_INVALID_ARG;
+    RopeArgs a = {};
+    a.q = q; a.k = K; a.v = V; a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
+    a.n_heads = n_heads; a.n_kv_heads = hk; a.head_dim = dim; a.T = batch->T;
+    a.positions = positions; a.rope = rope; a.norm = norm;
+    a.q_out = q_out; a.k_out = k_out; a.q_out_stride = q_out_stride; a.k_out_stride = k_out_stride;
+    a.cache = cache; a.batch = batch; a.ws = ws;
+    return cuda_status(launch_rope(a, static_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -145,6 +145,24 @@ struct PromptArgs {
     void* ws;
 };
 
+struct RopeArgs {
+    const void* q;
+    const void* k;
+    const void* v;                          // with a cache only
+    int64_t q_stride, k_stride, v_stride;   // elements from one token to the next
+    int n_heads, n_kv_heads, head_dim, T;
+    const int32_t* positions;
+    const dspark_rope_t* rope;
+    const dspark_head_norm_t* norm;
+    void* q_out;
+    void* k_out;
+    int64_t q_out_stride, k_out_stride;
+    const dspark_kv_cache_t* cache;         // null: rows in and out
+    const dspark_kv_batch_t* batch;
+    void* ws;
+};
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s);
+
 cudaError_t launch_kv_write(const dspark_kv_cache_t& c, const dspark_kv_batch_t& b, const void* K, const void* V,
                             int64_t k_stride, int64_t v_stride, void* ws, cudaStream_t s);
 cudaError_t launch_kv_read(const dspark_kv_cache_t& c, const dspark_kv_batch_t& b, void* K, void* V, void* ws,

@@ -5,6 +5,7 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "sm100.cuh"
 
 namespace dspark {
 
@@ -56,6 +57,33 @@ __device__ __forceinline__ void check_requests(const int32_t* off, const int32_t
         }
     }
     if (bad) raise_status(ws, kStatBadPage);
+}
+
+// e4m3 codes of two values y: bf16 values x times (448 / a) in float32 (packed
+// pairs x, inv), the row's largest magnitude a (finite, above zero).  The code is the
+// e4m3 value nearest to the exact quotient x 448 / a.  x and a have 8 significant
+// bits and 448 = 7 2^6, so the quotient either lies on a midpoint of two e4m3
+// values (5 significant bits) or at a relative distance above 2^-13 of it.
+// t = x (448 / a) in float32 is within 2^-22 of the quotient; rounding t to 15
+// significant bits (Veltkamp's splitting, T. J. Dekker, "A floating-point
+// technique for extending the available precision", 1971) restores exact
+// midpoints and moves no other value across one.
+__device__ __forceinline__ uint32_t quantise2(uint64_t x, uint64_t inv) {
+    const uint64_t k = pack2(513.f, 513.f), minus = pack2(-1.f, -1.f);
+    const uint64_t t = mul2x(x, inv);
+    const uint64_t c = mul2x(t, k);
+    float2 y;
+    unpack2(fma2(fma2(t, minus, c), minus, c), y.x, y.y);                 // c - (c - t)
+    return __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+}
+// The same of 8 bf16 values (w).
+__device__ __forceinline__ uint2 quantise8(uint4 w, float inv) {
+    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+    const uint64_t i2 = pack2(inv, inv);
+    uint32_t half[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) half[i] = quantise2(pack2(bf16_bits_to_float(in[i] & 0xFFFFu), bf16_bits_to_float(in[i] >> 16)), i2);
+    return make_uint2(half[0] | (half[1] << 16), half[2] | (half[3] << 16));
 }
 
 // bf16 bits of four e4m3 codes (bytes of w), exactly.  An e4m3 value with its

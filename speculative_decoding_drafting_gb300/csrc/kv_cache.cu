@@ -23,30 +23,6 @@ constexpr int kWarps = 4;          // tokens per CTA
 
 __device__ __forceinline__ uint32_t bf16x2_abs_bits(uint32_t w) { return w & 0x7FFF7FFFu; }
 
-// Codes of 8 bf16 values (w) with the row's largest magnitude a (float bits
-// of a finite value > 0).  The code is the e4m3 value nearest to the exact
-// quotient x 448 / a.  x and a have 8 significant bits and 448 = 7 2^6, so the
-// quotient either lies on a midpoint of two e4m3 values (5 significant bits)
-// or at a relative distance above 2^-13 of it.  t = x (448 / a) in float32 is
-// within 2^-22 of the quotient; rounding t to 15 significant bits (Veltkamp's
-// splitting, T. J. Dekker, "A floating-point technique for extending the
-// available precision", 1971) restores exact midpoints and moves no other
-// value across one.
-__device__ __forceinline__ uint2 quantise8(uint4 w, float inv) {
-    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-    const uint64_t k = pack2(513.f, 513.f), i2 = pack2(inv, inv), minus = pack2(-1.f, -1.f);
-    uint32_t half[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint64_t t = mul2x(pack2(bf16_bits_to_float(in[i] & 0xFFFFu), bf16_bits_to_float(in[i] >> 16)), i2);
-        const uint64_t c = mul2x(t, k);
-        float2 y;
-        unpack2(fma2(fma2(t, minus, c), minus, c), y.x, y.y);             // c - (c - t)
-        half[i] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
-    }
-    return make_uint2(half[0] | (half[1] << 16), half[2] | (half[3] << 16));
-}
-
 // A warp's row vectors of one step: kSteps of K, then kSteps of V.
 constexpr int kSteps = 4, kVecs = 2 * kSteps;
 

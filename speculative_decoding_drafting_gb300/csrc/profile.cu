@@ -24,7 +24,8 @@ const char* const kNames[] = {"draft_prep",      "draft_sweep_generic", "draft_s
                               "schedule_threshold", "sts_hist",           "sts_ece",          "sts_advance",
                               "sts_apply",          "sts_fix",
                               "draft_rnn_gru_finish", "kv_write",        "kv_read",          "attn_paged",
-                              "attn_paged_join",    "attn_prompt",     "attn_prompt_plan"};
+                              "attn_paged_join",    "attn_prompt",     "attn_prompt_plan",
+                              "qk_rope",            "rope_write"};
 
 cudaEvent_t take() {
     if (!g_pool.empty()) {

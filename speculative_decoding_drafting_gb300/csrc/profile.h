@@ -29,6 +29,8 @@ enum ProfName : int {
     kPAttnPagedJoin = 21,
     kPAttnPrompt = 22,
     kPAttnPromptPlan = 23,
+    kPQkRope = 24,
+    kPRopeWrite = 25,
 };
 
 void prof_begin(int name, cudaStream_t s);
