@@ -600,6 +600,30 @@ int dspark_attn_prompt(const void* q, const void* k, const void* v,
                        const int32_t* seq_off, int B, int T, int n_heads, int n_kv_heads, int head_dim,
                        float scale, void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------- attention with a window */
+
+/*
+ * The two calls above for a local layer: a token at position p of its request
+ * (or sequence) sees the keys j <= p with p - j < window, the last `window`
+ * tokens with its own among them, and those with j < sinks, the first tokens,
+ * which stay visible.  Everything else as dspark_attn_paged and
+ * dspark_attn_prompt, workspaces of the same size among it.  window >= 1 and
+ * sinks >= 0 (INVALID_ARG); a window of all tokens is none.
+ * Paged: a page of which no new token of the request sees a key is not read, may
+ * hold anything and may have any id in the table (a server may have given it
+ * away).  Keys and values that no new token sees need not be finite.  Where
+ * window is below max_pages * page, that is at most 2^30 (SHAPE).
+ * Prompt: values that are not finite reach the rows that see them and no others.
+ */
+int dspark_attn_paged_window(const void* q, int64_t q_stride, const dspark_kv_cache_t* cache,
+                             const dspark_kv_batch_t* batch, int n_heads, float scale, int window, int sinks,
+                             void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+int dspark_attn_prompt_window(const void* q, const void* k, const void* v,
+                              int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                              const int32_t* seq_off, int B, int T, int n_heads, int n_kv_heads, int head_dim,
+                              float scale, int window, int sinks, void* out, float* lse, void* ws, size_t ws_bytes,
+                              void* stream);
+
 /* ------------------------------------------- head norms and rotary positions */
 
 /*

@@ -97,6 +97,9 @@ def load(build_if_missing: bool = True):
         L.dspark_kv_read.argtypes = [P, P, P, P, P, sz, P]
         L.dspark_attn_paged.argtypes = [P, i64, P, P, i32, f32, P, P, P, sz, P]
         L.dspark_attn_prompt.argtypes = [P, P, P, i64, i64, i64, P, i32, i32, i32, i32, i32, f32, P, P, P, sz, P]
+        L.dspark_attn_paged_window.argtypes = [P, i64, P, P, i32, f32, i32, i32, P, P, P, sz, P]
+        L.dspark_attn_prompt_window.argtypes = [P, P, P, i64, i64, i64, P, i32, i32, i32, i32, i32, f32, i32, i32,
+                                                P, P, P, sz, P]
         L.dspark_qk_rope.argtypes = [P, P, i64, i64, P, i32, i32, i32, i32, P, P, P, P, i64, i64, P]
         L.dspark_rope_write.argtypes = [P, P, P, P, P, i64, i64, i64, i32, P, P, P, P, P, i64, i64, P, sz, P]
         L.dspark_workspace_set_wait.argtypes = [P, u64, i32, P]
@@ -111,7 +114,7 @@ def load(build_if_missing: bool = True):
                      "dspark_sts_apply", "dspark_philox4x32_10", "dspark_workspace_set_wait",
                      "dspark_workspace_status", "dspark_profile_enable", "dspark_profile_collect",
                      "dspark_kv_write", "dspark_kv_read", "dspark_attn_paged", "dspark_attn_prompt",
-                     "dspark_qk_rope", "dspark_rope_write"):
+                     "dspark_attn_paged_window", "dspark_attn_prompt_window", "dspark_qk_rope", "dspark_rope_write"):
             getattr(L, name).restype = i32
         _lib = L
         return _lib
@@ -578,11 +581,23 @@ def _attn_out(out, lse, T, heads, dim, dev):
     return out
 
 
+def _window(window, sinks):
+    """The extra arguments of a call with a window."""
+    if window is None:
+        if sinks:
+            raise ValueError("sinks go with a window")
+        return ()
+    # longer than any request is as good as the longest the ABI can say
+    return min(int(window), 0x7FFFFFFF), min(int(sinks), 0x7FFFFFFF)
+
+
 def attn_paged(q, cache: KvCache, q_off, kv_len, page_table, scale: Optional[float] = None, lse: bool = False,
-               ws=None, out=None, stream=None):
+               ws=None, out=None, stream=None, window: Optional[int] = None, sinks: int = 0):
     """Attention of the new tokens q [T, n_heads, head_dim] over the paged
-    cache (``dspark_attn_paged``); ``scale`` None: 1 / sqrt(head_dim).  Returns
-    a dict with ``out`` and, on request, ``lse`` [T, n_heads]."""
+    cache (``dspark_attn_paged``); ``scale`` None: 1 / sqrt(head_dim).  With a
+    ``window`` a token sees the last ``window`` tokens and the first ``sinks``
+    alone (``dspark_attn_paged_window``).  Returns a dict with ``out`` and, on
+    request, ``lse`` [T, n_heads]."""
     L = load()
     T, heads, dim = q.shape
     b = _batch(q_off, kv_len, page_table, T)
@@ -591,18 +606,21 @@ def attn_paged(q, cache: KvCache, q_off, kv_len, page_table, scale: Optional[flo
     c = cache._struct()
     if ws is None:
         ws = _workspace(L.dspark_attn_paged_workspace_size(b.R, T, heads, cache.n_kv_heads, dim), q.device)
-    code = L.dspark_attn_paged(qp, qs, ctypes.byref(c), ctypes.byref(b), heads,
-                               float(dim ** -0.5 if scale is None else scale), _p(out["out"]), _p(out.get("lse")),
-                               _p(ws), ws.numel(), _stream(stream))
-    _check("dspark_attn_paged", code)
+    local = _window(window, sinks)
+    name = "dspark_attn_paged_window" if local else "dspark_attn_paged"
+    code = getattr(L, name)(qp, qs, ctypes.byref(c), ctypes.byref(b), heads, float(dim ** -0.5 if scale is None else scale),
+                            *local, _p(out["out"]), _p(out.get("lse")), _p(ws), ws.numel(), _stream(stream))
+    _check(name, code)
     out["ws"] = ws
     return out
 
 
-def attn_prompt(q, k, v, seq_off, scale: Optional[float] = None, lse: bool = False, ws=None, out=None, stream=None):
-    """Causal attention over whole packed prompts (``dspark_attn_prompt``):
-    q [T, n_heads, head_dim], k and v [T, n_kv_heads, head_dim], sequence b the
-    tokens seq_off[b] .. seq_off[b+1].  Returns a dict as ``attn_paged``."""
+def attn_prompt(q, k, v, seq_off, scale: Optional[float] = None, lse: bool = False, ws=None, out=None, stream=None,
+                window: Optional[int] = None, sinks: int = 0):
+    """Causal attention over whole packed prompts (``dspark_attn_prompt``, with a
+    ``window`` ``dspark_attn_prompt_window``): q [T, n_heads, head_dim], k and v
+    [T, n_kv_heads, head_dim], sequence b the tokens seq_off[b] ..
+    seq_off[b+1].  Window and result as ``attn_paged``."""
     L = load()
     T, heads, dim = q.shape
     if k.dim() != 3:
@@ -616,10 +634,12 @@ def attn_prompt(q, k, v, seq_off, scale: Optional[float] = None, lse: bool = Fal
     out = _attn_out(out, lse, T, heads, dim, q.device)
     if ws is None:
         ws = _workspace(L.dspark_attn_prompt_workspace_size(B, T, heads, kv_heads, dim), q.device)
-    code = L.dspark_attn_prompt(qp, kp, vp, qs, ks, vs, _p(seq_off), B, T, heads, kv_heads, dim,
-                                float(dim ** -0.5 if scale is None else scale), _p(out["out"]), _p(out.get("lse")),
-                                _p(ws), ws.numel(), _stream(stream))
-    _check("dspark_attn_prompt", code)
+    local = _window(window, sinks)
+    name = "dspark_attn_prompt_window" if local else "dspark_attn_prompt"
+    code = getattr(L, name)(qp, kp, vp, qs, ks, vs, _p(seq_off), B, T, heads, kv_heads, dim,
+                            float(dim ** -0.5 if scale is None else scale), *local, _p(out["out"]), _p(out.get("lse")),
+                            _p(ws), ws.numel(), _stream(stream))
+    _check(name, code)
     out["ws"] = ws
     return out
 

@@ -403,9 +403,10 @@ size_t dspark_attn_paged_workspace_size(int R, int T, int n_heads, int n_kv_head
     return attn_paged_workspace_bytes(R, T, n_heads, n_kv_heads, head_dim);
 }
 
-int dspark_attn_paged(const void* q, int64_t q_stride, const dspark_kv_cache_t* cache,
-                      const dspark_kv_batch_t* batch, int n_heads, float scale, void* out, float* lse, void* ws,
-                      size_t ws_bytes, void* stream) {
+// window = 0: none.
+static int attn_paged(const void* q, int64_t q_stride, const dspark_kv_cache_t* cache, const dspark_kv_batch_t* batch,
+                      int n_heads, float scale, int window, int sinks, void* out, float* lse, void* ws, size_t ws_bytes,
+                      void* stream) {
     int st = check_cache(cache);
     if (st) return st;
     st = check_batch_sizes(batch);
@@ -413,6 +414,8 @@ int dspark_attn_paged(const void* q, int64_t q_stride, const dspark_kv_cache_t* 
     st = check_heads(n_heads, cache->n_kv_heads, cache->head_dim);
     if (st) return st;
     if (!std::isfinite(scale)) return DSPARK_ERR_INVALID_ARG;
+    const int64_t most = (int64_t)batch->max_pages * cache->page;
+    if (window > 0 && window < most && most > int64_t(1) << 30) return DSPARK_ERR_SHAPE;
     if (batch->T == 0) return DSPARK_OK;
     if (!q || !out || !aligned16(q) || !aligned16(out) || !batch->q_off || !batch->kv_len || !batch->page_table)
         return DSPARK_ERR_INVALID_ARG;
@@ -421,8 +424,21 @@ int dspark_attn_paged(const void* q, int64_t q_stride, const dspark_kv_cache_t* 
         ws_bytes < attn_paged_workspace_bytes(batch->R, batch->T, n_heads, cache->n_kv_heads, cache->head_dim))
         return DSPARK_ERR_WORKSPACE;
     if (!cache_on_device(cache) || !on_current_device(q)) return DSPARK_ERR_INVALID_ARG;
-    return cuda_status(launch_attn_paged(q, q_stride, *cache, *batch, n_heads, scale, out, lse, ws,
+    return cuda_status(launch_attn_paged(q, q_stride, *cache, *batch, n_heads, scale, window, sinks, out, lse, ws,
                                          static_cast<cudaStream_t>(stream)));
+}
+
+int dspark_attn_paged(const void* q, int64_t q_stride, const dspark_kv_cache_t* cache,
+                      const dspark_kv_batch_t* batch, int n_heads, float scale, void* out, float* lse, void* ws,
+                      size_t ws_bytes, void* stream) {
+    return attn_paged(q, q_stride, cache, batch, n_heads, scale, 0, 0, out, lse, ws, ws_bytes, stream);
+}
+
+int dspark_attn_paged_window(const void* q, int64_t q_stride, const dspark_kv_cache_t* cache,
+                             const dspark_kv_batch_t* batch, int n_heads, float scale, int window, int sinks, void* out,
+                             float* lse, void* ws, size_t ws_bytes, void* stream) {
+    if (window < 1 || sinks < 0) return DSPARK_ERR_INVALID_ARG;
+    return attn_paged(q, q_stride, cache, batch, n_heads, scale, window, sinks, out, lse, ws, ws_bytes, stream);
 }
 
 size_t dspark_attn_prompt_workspace_size(int B, int T, int n_heads, int n_kv_heads, int head_dim) {
@@ -430,9 +446,11 @@ size_t dspark_attn_prompt_workspace_size(int B, int T, int n_heads, int n_kv_hea
     return attn_prompt_workspace_bytes(B, T, n_heads, n_kv_heads, head_dim);
 }
 
-int dspark_attn_prompt(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+// window = 0: none.
+static int attn_prompt(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
                        int64_t v_stride, const int32_t* seq_off, int B, int T, int n_heads, int n_kv_heads,
-                       int head_dim, float scale, void* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+                       int head_dim, float scale, int window, int sinks, void* out, float* lse, void* ws,
+                       size_t ws_bytes, void* stream) {
     if (B < 1 || T < 0) return DSPARK_ERR_SHAPE;
     int st = check_heads(n_heads, n_kv_heads, head_dim);
     if (st) return st;
@@ -449,8 +467,24 @@ int dspark_attn_prompt(const void* q, const void* k, const void* v, int64_t q_st
     PromptArgs a;
     a.q = q; a.k = k; a.v = v; a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
     a.seq_off = seq_off; a.B = B; a.T = T; a.n_heads = n_heads; a.n_kv_heads = n_kv_heads; a.head_dim = head_dim;
-    a.scale = scale; a.out = out; a.lse = lse; a.ws = ws;
+    a.scale = scale; a.window = window; a.sinks = sinks; a.out = out; a.lse = lse; a.ws = ws;
     return cuda_status(launch_attn_prompt(a, static_cast<cudaStream_t>(stream)));
+}
+
+int dspark_attn_prompt(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                       int64_t v_stride, const int32_t* seq_off, int B, int T, int n_heads, int n_kv_heads,
+                       int head_dim, float scale, void* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+    return attn_prompt(q, k, v, q_stride, k_stride, v_stride, seq_off, B, T, n_heads, n_kv_heads, head_dim, scale, 0, 0,
+                       out, lse, ws, ws_bytes, stream);
+}
+
+int dspark_attn_prompt_window(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                              int64_t v_stride, const int32_t* seq_off, int B, int T, int n_heads, int n_kv_heads,
+                              int head_dim, float scale, int window, int sinks, void* out, float* lse, void* ws,
+                              size_t ws_bytes, void* stream) {
+    if (window < 1 || sinks < 0) return DSPARK_ERR_INVALID_ARG;
+    return attn_prompt(q, k, v, q_stride, k_stride, v_stride, seq_off, B, T, n_heads, n_kv_heads, head_dim, scale, window,
+                       sinks, out, lse, ws, ws_bytes, stream);
 }
 
 // The rotation's and the norm's own checks.

@@ -62,6 +62,7 @@
 // Keys a row must not see get weight 0 by selection, not by multiplication;
 // V rows past the item's last key are zeroed in shared memory, since 0 times
 // a stale NaN would be NaN.
+#include <algorithm>
 #include <type_traits>
 
 #include <cstddef>
@@ -126,6 +127,7 @@ struct SegInfo {
     int qp;                            // its Q place: 0, 1, or 2 for both
     uint32_t q_use;                    // how often place 0 (low half) and 1 have been used before
     Request q;
+    int skip;                          // key tiles left out behind the sinks' (0 without a window)
 };
 
 struct Bars {
@@ -202,7 +204,7 @@ struct JoinDesc {
 struct PagedParams {
     const uint16_t* q;
     int64_t q_stride;
-    PlanInput plan;
+    WindowPlan plan;                   // the window and what follows from it: only with one
     const int32_t* page_table;
     const float *k_scale, *v_scale;    // e4m3 only
     uint16_t* out;
@@ -219,6 +221,19 @@ __device__ __forceinline__ size_t piece_floats(int hd) { return (size_t)kRowTile
 struct Maps {
     CUtensorMap k, v;
 };
+
+template <bool kWindow>
+using Plan = std::conditional_t<kWindow, WindowPlan, PlanInput>;
+// The key tile that tile t of an item stands for.
+template <bool kWindow>
+__device__ __forceinline__ int key_tile(const PagedParams& p, const SegInfo& s, int t) {
+    return kWindow && t >= p.plan.sink_tiles ? t + s.skip : t;
+}
+// With a window: the first key that the first row of a row tile sees behind the
+// sinks (0 where its window reaches the beginning).
+__device__ __forceinline__ int first_low(const PagedParams& p, const SegInfo& s) {
+    return (int)max((int64_t)s.q.kv_len - s.q.q_len + s.tok - p.plan.window + 1, (int64_t)0);
+}
 
 // Shared-memory operand of e4m3 rows of HD bytes: 128-byte swizzle at
 // head_dim 128, 64-byte at 64.
@@ -314,7 +329,7 @@ struct SoftState {
 // One segment's key tiles of unit u.  The unit's threads all
 // walk the same barriers even after a wait ran out (the results are then not
 // stored), so that no named barrier is left waiting.
-template <int HD, bool F8, int kMost>
+template <int HD, bool F8, bool kWindow, int kMost>
 __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo& sg, Misc* M, uint8_t* smem,
                                              uint32_t tmem, int u, SoftState& st) {
     using C = Cfg<HD, F8>;
@@ -350,13 +365,26 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
 
 #pragma unroll 1
     for (int i = (stream - sh.stream_at(sg, 0)) & (streams - 1); i < n; i += streams) {
-        const int key = (t0 + i) * kKeyTile + tr;
-        const bool edge = (t0 + i + 1) * kKeyTile > lim0;     // some row does not see the whole tile
+        const int kt = key_tile<kWindow>(p, sg, t0 + i), key = kt * kKeyTile + tr;
+        bool edge = (kt + 1) * kKeyTile > lim0;               // some row does not see the whole tile
+        // with a window, columns from this one on do not see the key either, since
+        // their windows begin behind it (of all rows: hidden_rows from the tile's first)
+        int hid = kRowTile, hidden_rows = kRowTile;
+        if (kWindow && kt * kKeyTile < sg.keys - p.plan.window && (kt + 1) * kKeyTile > p.plan.sinks) {
+            edge = true;
+            if (key >= p.plan.sinks) {
+                // the first token (from the tile's) that does not
+                const int64_t d = (int64_t)key + p.plan.window - sg.q.kv_len + sg.q.q_len - sg.tok;
+                hidden_rows = (int)min(max(d, (int64_t)0), (int64_t)kRowTile + 1) * p.plan.group - sg.head;
+                hid = hidden_rows - coff;
+            }
+        }
         // new token k sees the key if kv_len - q_len + k >= key: from this row on.
         // Past the last key no column sees it, the unused ones neither: what
         // lies there must not raise the other columns' references.
+        const int behind = key - sg.q.kv_len + sg.q.q_len - sg.tok;
         const int seen = !edge ? 0 : (key >= sg.keys ? kRowTile
-                                      : (key - sg.q.kv_len + sg.q.q_len - sg.tok) * p.plan.group - sg.head - coff);
+                                      : (kWindow ? max(behind, -1) : behind) * p.plan.group - sg.head - coff);
         const uint32_t turn = sh.turn_at(sg, i);
         wait_bar(&M->b.s_full[turn][u], (st.phases >> turn) & 1u, ab);
         st.phases ^= 1u << turn;
@@ -374,7 +402,7 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
             // a wide tile's scales are read by two units
             if (lane == 0) mbar_arrive(&M->b.c_empty[s]);
             if (!wide && lane == 0) mbar_arrive(&M->b.c_empty[s]);
-            if (edge && key >= sg.keys) vs = 1.f;             // no key here: any scale
+            if (edge && (key >= sg.keys || (kWindow && hidden_rows <= 0))) vs = 1.f;   // no key here: any scale
             // Below 2^-100 (a row of zeros has scale 0) 1 / scale would take the sum
             // out of float32's range: there the sum counts the key with 2^-101, and
             // its weight for V is 0 (values below 2^-91 are dropped, not raised).
@@ -408,7 +436,7 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
                 if (edge) {
 #pragma unroll
                     for (int c = 0; c < kB; ++c)
-                        if (c0 + c < seen) t[c0 + c] = -INFINITY;
+                        if (c0 + c < seen || (kWindow && c0 + c >= hid)) t[c0 + c] = -INFINITY;
                 }
 #pragma unroll
                 for (int c = 0; c < kB; ++c) top = fmaxf(top, t[c0 + c]);
@@ -425,7 +453,7 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     float y = fmaf(F8 ? x[c] * M->qm[u][c0 + c] : x[c], mul, lvs);
-                    if (c0 + c < seen) y = -INFINITY;
+                    if (c0 + c < seen || (kWindow && c0 + c >= hid)) y = -INFINITY;
                     y = redux_max(y);
                     if (lane == c) mine = y;
                 }
@@ -500,7 +528,10 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
             const uint8_t* src = smem + C::kOffV + (size_t)s * C::kLoadBytes;
             uint8_t* dst = smem + C::kOffW + (size_t)d * C::kTileBytes;
             constexpr int kPieces = kKeyTile * HD / 16, kPer = HD / 16;
-            const int valid = edge ? sg.keys - (t0 + i) * kKeyTile : kKeyTile;   // rows with a key
+            const int valid = edge ? sg.keys - kt * kKeyTile : kKeyTile;         // rows with a key
+            // with a window, rows [gap0, gap1) hold keys that no row of the item sees
+            const int gap0 = kWindow ? max(p.plan.sinks - kt * kKeyTile, 0) : 0;
+            const int gap1 = kWindow ? first_low(p, sg) - kt * kKeyTile : 0;
             // A thread's pieces lie `step` pieces, a multiple of 8 rows, apart: their
             // swizzle is the same.  It reads the two 8-byte halves of a piece in an
             // order that differs between lanes, so that neither the loads nor the
@@ -531,6 +562,15 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
                     to += kB * (kStep / kPer) * 128;
                 }
                 // rows without a key become zeros, whatever their places hold
+                if (kWindow && gap0 < gap1) {
+#pragma unroll 1
+                    for (int h = 1; h <= kN; ++h) {
+                        const int row = row0 + (kN - h) * (kStep / kPer);
+                        if (row < gap0 || row >= gap1) continue;
+                        *reinterpret_cast<uint4*>(to - h * (kStep / kPer) * 128 + ta) = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4*>(to - h * (kStep / kPer) * 128 + tb) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
                 if (valid < kKeyTile) {
 #pragma unroll 1
                     for (int h = kN; h > 0; --h) {
@@ -671,7 +711,7 @@ __device__ __forceinline__ void finish_segment(const PagedParams& p, const SegIn
     named_sync(5, 128);                                       // row_at and join are no longer read
 }
 
-template <int HD, bool F8>
+template <int HD, bool F8, bool kWindow>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_paged_kernel(const __grid_constant__ Maps maps, const PagedParams p) {
     using C = Cfg<HD, F8>;
@@ -683,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // by a shuffle, so that the compiler knows it to be the same in every lane:
     // e4m3 blocks of 1 to 17 tokens 195 -> 184 us, e4m3 decoding 115.7 -> 113.5
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-    const PlanInput& pl = p.plan;
+    const Plan<kWindow>& pl = p.plan;
     const int cta = (int)blockIdx.x;
     pdl_launch_dependents();
 
@@ -771,6 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int tok, end, keys;                                   // first token of the tile, of the segment's end; keys
         int at, now, next;                                    // page table: lane's entries of 32 pages from `at`, and the 32 after
         int r, x;
+        int low, gap, far;                                    // with a window: its first key, the tokens left out, lane's page there
         uint32_t seg, slot, phase, count;                     // segment; ring place; tiles issued
         uint64_t pol;
         bool more;
@@ -787,8 +828,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const SegInfo& s = M->seg[at];
         c.more = ok && s.rows > 0;
         if (!c.more) return;
-        c.tok = s.t0 * kKeyTile;
-        c.end = (s.t0 + s.n) * kKeyTile;
+        c.tok = key_tile<kWindow>(p, s, s.t0) * kKeyTile;
+        c.end = (key_tile<kWindow>(p, s, s.t0 + s.n - 1) + 1) * kKeyTile;
         c.keys = s.keys;
         c.r = s.r;
         c.x = s.h << p.page_log2;
@@ -797,6 +838,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         c.at = (c.tok >> p.page_log2) & ~31;
         c.now = entry(c, c.at + lane);
         c.next = entry(c, c.at + 32 + lane);
+        if (kWindow) {
+            c.low = first_low(p, s);
+            c.gap = s.skip * kKeyTile;
+            // the pages behind the gap, if the segment comes to it
+            const int to = p.plan.sink_tiles * kKeyTile + c.gap;
+            if (c.gap > 0 && c.tok < to && to < c.end) c.far = entry(c, ((to >> p.page_log2) & ~31) + lane);
+        }
     };
     // this lane's page of the place's tile (pages past the keys: any)
     auto page_of = [&](Place& c) {
@@ -813,6 +861,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto step = [&](Place& c) {
         ++c.count;
         c.tok += kKeyTile;
+        if (kWindow && c.gap > 0 && c.tok == p.plan.sink_tiles * kKeyTile) {
+            c.tok += c.gap;
+            c.at = (c.tok >> p.page_log2) & ~31;
+            c.now = c.far;
+            if (c.tok < c.end) c.next = entry(c, c.at + 32 + lane);
+        }
         if (c.tok < c.end) return false;
         ++c.seg;
         return true;
@@ -827,7 +881,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = ok && __all_sync(0xffffffffu, wait_bar(&M->b.c_empty[cs], ((c.count / C::kScMod) & 1u) ^ 1u, ab));
         if (!ok) return;
         const bool valid = lane_tok < c.keys - c.tok;
-        if (valid && (uint32_t)id >= (uint32_t)p.n_pages) {
+        // a page that no row of the item sees is not read, whatever its id
+        const bool unseen = kWindow && c.tok + lane_tok >= p.plan.sinks && c.tok + lane_tok + bp <= c.low;
+        if (valid && unseen) {
+            id = p.n_pages;
+        } else if (valid && (uint32_t)id >= (uint32_t)p.n_pages) {
             raise_status(p.ws, kStatBadPage);
             id = p.n_pages;                                   // past the tensor: zeros
         }
@@ -980,17 +1038,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // p_full covers, as it does the end of the reads of the loaded one
                 if (!F8) {
                     wait(&M->b.v_full[vs], vph);
-                    const int valid = sg.keys - (sg.t0 + i) * kKeyTile;
-                    if (ok && valid < kKeyTile) {
-                        // rows past the last key hold whatever the pages or this buffer held
-                        uint8_t* vt = smem + C::kOffV + (size_t)vs * C::kTileBytes;
+                    const int first = key_tile<kWindow>(p, sg, sg.t0 + i) * kKeyTile, valid = sg.keys - first;
+                    uint8_t* vt = smem + C::kOffV + (size_t)vs * C::kTileBytes;
+                    auto clear = [&](int from, int to) {
 #pragma unroll 1
-                        for (int k = max(valid, 0) * 8 + lane; k < kKeyTile * 8; k += 32)
+                        for (int k = from * 8 + lane; k < to * 8; k += 32)
 #pragma unroll
                             for (int hf = 0; hf < C::kHalves; ++hf)
                                 *reinterpret_cast<uint4*>(vt + hf * C::kHalfBytes + k * 16) = make_uint4(0u, 0u, 0u, 0u);
                         fence_proxy_async();
                         __syncwarp();
+                    };
+                    // rows past the last key hold whatever the pages or this buffer held
+                    if (ok && valid < kKeyTile) clear(max(valid, 0), kKeyTile);
+                    if (kWindow && ok) {                      // and those of keys that no row of the item sees anything
+                        const int gap0 = max(p.plan.sinks - first, 0), gap1 = min(first_low(p, sg) - first, kKeyTile);
+                        if (gap0 < gap1) clear(gap0, gap1);
                     }
                 }
                 wait(&M->b.p_full[u0], (made >> u0) & 1u);
@@ -1058,7 +1121,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     o.rows = 0;
                     if (more)
                         o = SegInfo{s.r, s.j, s.h, s.t0, s.t1 - s.t0, s.tiles, s.keys, s.rows, s.tok, s.head, s.rest, line, run,
-                                    both ? 2 : place, use, s.q};
+                                    both ? 2 : place, use, s.q, s.skip};
                     mbar_arrive(&M->b.seg_full[made % kSegs]);
                 }
                 __syncwarp();
@@ -1147,17 +1210,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (bf16 has no loop for 24: such items are bound by the cache's bytes, and
             // one shape more cost blocks of 1 to 17 tokens 4 %.)
             if (s.rows <= 8)
-                soft_segment<HD, F8, 8>(p, s, M, smem, tmem, u, st);
+                soft_segment<HD, F8, kWindow, 8>(p, s, M, smem, tmem, u, st);
             else if (s.rows <= 16)
-                soft_segment<HD, F8, 16>(p, s, M, smem, tmem, u, st);
+                soft_segment<HD, F8, kWindow, 16>(p, s, M, smem, tmem, u, st);
             else if (F8 && s.rows <= 24)
-                soft_segment<HD, F8, F8 ? 24 : 32>(p, s, M, smem, tmem, u, st);
+                soft_segment<HD, F8, kWindow, F8 ? 24 : 32>(p, s, M, smem, tmem, u, st);
             else if (s.rows <= 32)
-                soft_segment<HD, F8, 32>(p, s, M, smem, tmem, u, st);
+                soft_segment<HD, F8, kWindow, 32>(p, s, M, smem, tmem, u, st);
             else if (s.rows <= 48)
-                soft_segment<HD, F8, 48>(p, s, M, smem, tmem, u, st);
+                soft_segment<HD, F8, kWindow, 48>(p, s, M, smem, tmem, u, st);
             else
-                soft_segment<HD, F8, 64>(p, s, M, smem, tmem, u, st);
+                soft_segment<HD, F8, kWindow, 64>(p, s, M, smem, tmem, u, st);
             __syncwarp();
             if (lane == 0) mbar_arrive(&M->b.seg_empty[at]);
         }
@@ -1227,13 +1290,13 @@ constexpr uint32_t tile_lengths(uint32_t r8, uint32_t r16, uint32_t r24, uint32_
     return r8 | r16 << 5 | r24 << 10 | r32 << 15 | r48 << 20 | r64 << 25;
 }
 
-template <int HD, bool F8>
+template <int HD, bool F8, bool kWindow>
 cudaError_t launch(const Maps& maps, const PagedParams& p, int grid, cudaStream_t s) {
     const size_t smem = smem_bytes<HD, F8>();
-    cudaError_t e = allow_smem(attn_paged_kernel<HD, F8>, smem);
+    cudaError_t e = allow_smem(attn_paged_kernel<HD, F8, kWindow>, smem);
     if (e != cudaSuccess) return e;
     prof_begin(kPAttnPaged, s);
-    e = launch_kernel(attn_paged_kernel<HD, F8>, dim3(grid), dim3(kThreads), smem, s, true, maps, p);
+    e = launch_kernel(attn_paged_kernel<HD, F8, kWindow>, dim3(grid), dim3(kThreads), smem, s, true, maps, p);
     prof_end(s);
     if (e != cudaSuccess) return e;
     prof_begin(kPAttnPagedJoin, s);
@@ -1251,7 +1314,8 @@ size_t attn_paged_workspace_bytes(int, int, int, int, int head_dim) {
 }
 
 cudaError_t launch_attn_paged(const void* q, int64_t q_stride, const dspark_kv_cache_t& c, const dspark_kv_batch_t& b,
-                              int n_heads, float scale, void* out, float* lse, void* ws, cudaStream_t s) {
+                              int n_heads, float scale, int window, int sinks, void* out, float* lse, void* ws,
+                              cudaStream_t s) {
     const int grid = num_sms();
     uint8_t* w = static_cast<uint8_t*>(ws) + sizeof(WsHeader);
     PagedParams p;
@@ -1262,8 +1326,17 @@ cudaError_t launch_attn_paged(const void* q, int64_t q_stride, const dspark_kv_c
     // it is of, and short spans let more CTAs in (one request of 777 keys, 8
     // heads: 13.2 us on the device against 14.0)
     const bool few = (b.R + (int64_t)b.T * (n_heads / c.n_kv_heads) / kRowTile) * c.n_kv_heads <= grid;
-    p.plan = PlanInput{b.q_off, b.kv_len, b.R, b.T, n_heads / c.n_kv_heads, c.n_kv_heads, (int64_t)b.max_pages * c.page,
-                       few ? 0 : (f8 ? 12 : 8), f8 ? tile_lengths(4, 4, 4, 5, 6, 7) : tile_lengths(4, 4, 4, 4, 5, 6)};
+    const int64_t most = (int64_t)b.max_pages * c.page;
+    p.plan = WindowPlan{{b.q_off, b.kv_len, b.R, b.T, n_heads / c.n_kv_heads, c.n_kv_heads, most,
+                         few ? 0 : (f8 ? 12 : 8), f8 ? tile_lengths(4, 4, 4, 5, 6, 7) : tile_lengths(4, 4, 4, 4, 5, 6)},
+                        0, 0, 0};
+    // a window of all that a request may hold is none
+    const bool windowed = window > 0 && window < most;
+    if (windowed) {
+        p.plan.window = window;
+        p.plan.sinks = (int)std::min((int64_t)sinks, most);
+        p.plan.sink_tiles = (p.plan.sinks + kKeyTile - 1) / kKeyTile;
+    }
     p.page_table = b.page_table;
     p.k_scale = c.k_scale;
     p.v_scale = c.v_scale;
@@ -1293,8 +1366,12 @@ cudaError_t launch_attn_paged(const void* q, int64_t q_stride, const dspark_kv_c
     const bool ok = make_tensor_map(&maps.k, dt, 3, c.k, dims, str, box, swz_k) &&
               make_tensor_map(&maps.v, dt, 3, c.v, dims, str, box, swz_v);
     if (!ok) return cudaErrorInvalidValue;
-    if (c.head_dim == 64) return f8 ? launch<64, true>(maps, p, grid, s) : launch<64, false>(maps, p, grid, s);
-    return f8 ? launch<128, true>(maps, p, grid, s) : launch<128, false>(maps, p, grid, s);
+    auto go = [&](auto w) {
+        constexpr bool kW = decltype(w)::value;
+        if (c.head_dim == 64) return f8 ? launch<64, true, kW>(maps, p, grid, s) : launch<64, false, kW>(maps, p, grid, s);
+        return f8 ? launch<128, true, kW>(maps, p, grid, s) : launch<128, false, kW>(maps, p, grid, s);
+    };
+    return windowed ? go(std::true_type{}) : go(std::false_type{});
 }
 
 }  // namespace dspark

@@ -10,6 +10,11 @@
 // spans, one per CTA, and a CTA takes the key tiles that begin in its span, so
 // that requests of any mix of lengths load the device evenly.  An item that a
 // cut goes through leaves one partial result per piece.
+//
+// With a window (WindowPlan) an item's tiles are the sinks' and, from the first
+// that its first row's window reaches, those up to its end: the tiles between
+// are left out of the count, and tile t of an item is key tile t, or t + skip
+// from the sinks' end on.
 #pragma once
 
 #include <stdint.h>
@@ -37,6 +42,11 @@ struct PlanInput {
     int64_t most;                  // max_pages * page
     int start;                     // length of an item besides its tiles
     uint32_t lengths;              // length of a tile, 5 bits each: up to 8, 16, 24, 32, 48, 64 rows (1 .. 31)
+};
+// Tokens that see the last `window` tokens, their own among them, and the first
+// sink_tiles key tiles' (some of them: that is the kernel's matter).
+struct WindowPlan : PlanInput {
+    int window, sinks, sink_tiles;
 };
 DSPARK_HD int plan_length(const PlanInput& p, int rows) {
     return (int)(p.lengths >> 5 * (rows <= 32 ? (rows - 1) / 8 : (rows <= 48 ? 4 : 5))) & 31;
@@ -69,6 +79,17 @@ DSPARK_HD int plan_tile_keys(const PlanInput& p, const Request& q, int j) {
     const int64_t rows = (int64_t)q.q_len * p.group, end = (int64_t)(j + 1) * kRowTile;
     // the last row tile's last row sees every key
     return end < rows ? plan_seen(p, q, end - 1) : q.kv_len;
+}
+// The first key that a window ending with row tile j's first row holds (may be negative).
+DSPARK_HD int64_t plan_low(const WindowPlan& p, const Request& q, int j) {
+    return (int64_t)q.kv_len - q.q_len + (int64_t)j * kRowTile / p.group - p.window + 1;
+}
+// Key tiles between the sinks' and the window's.
+DSPARK_HD int plan_skip(const PlanInput&, const Request&, int) { return 0; }
+DSPARK_HD int plan_skip(const WindowPlan& p, const Request& q, int j) {
+    const int64_t low = plan_low(p, q, j);
+    const int n = low > 0 ? (int)low / kKeyTile - p.sink_tiles : 0;       // low <= kv_len
+    return n > 0 ? n : 0;
 }
 DSPARK_HD int plan_key_tiles(int keys) { return keys > 0 ? (keys - 1) / kKeyTile + 1 : 1; }
 DSPARK_HD int plan_rows(const PlanInput& p, const Request& q, int j) {
@@ -104,15 +125,29 @@ DSPARK_HD_CALL int64_t plan_before(int group, int start, int length, int q_len, 
 DSPARK_HD int64_t plan_tiles_before(const PlanInput& p, const Request& q, int n) {
     return plan_before(p.group, p.start, plan_length(p, kRowTile), q.q_len, q.kv_len, n);
 }
-DSPARK_HD_CALL int64_t plan_request_length(PlanInput p, int r) {
+// Tiles that the first n row tiles skip, each max(0, floor((j + b) / 2 group)) of
+// them: the same sum, with b from the beginning of the first row's window less the
+// sinks' tiles.
+DSPARK_HD_CALL int64_t plan_skipped_before(int group, int64_t ahead, int sink_tiles, int n) {
+    const uint32_t m = 2u * (uint32_t)group;
+    const int64_t b = (ahead * group >> 6) - (int64_t)m * sink_tiles;
+    return plan_floor_sum(b + n, m) - plan_floor_sum(b, m);
+}
+DSPARK_HD int64_t plan_tiles_before(const WindowPlan& p, const Request& q, int n) {
+    return plan_before(p.group, p.start, plan_length(p, kRowTile), q.q_len, q.kv_len, n) -
+           plan_skipped_before(p.group, plan_low(p, q, 0), p.sink_tiles, n) * plan_length(p, kRowTile);
+}
+template <typename P>
+DSPARK_HD_CALL int64_t plan_request_length(P p, int r) {
     const Request q = plan_request(p, r);
     const int n = plan_row_tiles(p, q);
     if (n == 0) return 0;
-    const int64_t last = plan_place(p, plan_length(p, plan_rows(p, q, n - 1)), plan_key_tiles(q.kv_len));
+    const int64_t last = plan_place(p, plan_length(p, plan_rows(p, q, n - 1)), plan_key_tiles(q.kv_len) - plan_skip(p, q, n - 1));
     return (plan_tiles_before(p, q, n - 1) + last) * p.kv_heads;
 }
 // The row tile that holds place x of request r's items: the last that begins at or before it.
-DSPARK_HD int plan_tile_of(const PlanInput& p, const Request& q, int64_t x) {
+template <typename P>
+DSPARK_HD int plan_tile_of(const P& p, const Request& q, int64_t x) {
     int j = 0, upto = plan_row_tiles(p, q);
     while (upto - j > 1) {
         const int mid = j + (upto - j) / 2;
@@ -151,6 +186,7 @@ struct Segment {
     int tok, head;                 // the first row's new token, and its place in the group
     int rest;                      // from the span's end to the beginning of the item's last tile (an unfinished item's: >= 0)
     Request q;
+    int skip;                      // key tiles left out behind the sinks' (0 without a window)
 };
 
 // Row x of a row tile whose first row is (tok, head): its new token and its
@@ -173,14 +209,15 @@ struct Cursor {
     Request q;
 
     // start inside request r, at place `skip` of its items, for a span of n
-    DSPARK_HD void start(const PlanInput& p, int r_, int64_t skip, int64_t n) {
+    template <typename P>
+    DSPARK_HD void start(const P& p, int r_, int64_t skip, int64_t n) {
         r = r_;
         j = h = t = 0;
         end = 0;
         if (n <= 0) return;
         q = plan_request(p, r);
         j = plan_tile_of(p, q, skip);
-        const int tiles = plan_key_tiles(plan_tile_keys(p, q, j)), length = plan_length(p, plan_rows(p, q, j));
+        const int tiles = plan_key_tiles(plan_tile_keys(p, q, j)) - plan_skip(p, q, j), length = plan_length(p, plan_rows(p, q, j));
         const int64_t item = plan_place(p, length, tiles);
         skip -= plan_tiles_before(p, q, j) * p.kv_heads;
         h = (int)(skip / item);
@@ -188,11 +225,13 @@ struct Cursor {
         t = plan_tile_at(p, length, skip, tiles);
         end = skip + n;
     }
-    DSPARK_HD bool next(const PlanInput& p, Segment& s) {
+    template <typename P>
+    DSPARK_HD bool next(const P& p, Segment& s) {
         while (end > p.start) {                            // else no further tile begins in the span
             while (q.q_len == 0) q = plan_request(p, ++r); // the span goes on: a request with rows follows
             s.keys = plan_tile_keys(p, q, j);
-            s.tiles = plan_key_tiles(s.keys);
+            s.skip = plan_skip(p, q, j);
+            s.tiles = plan_key_tiles(s.keys) - s.skip;
             s.rows = plan_rows(p, q, j);
             const int length = plan_length(p, s.rows);
             s.r = r;

@@ -114,6 +114,11 @@ struct Params {
     float* lse;
     void* ws;
     int B, T, heads, kv_heads, group, toks;   // toks: tokens of a row tile
+    // with a window: its tokens, the first tokens that stay visible and their key
+    // tiles; v as it lies in memory (for values that are not finite)
+    int window, sinks, sink_tiles;
+    const uint16_t* v;
+    int64_t v_stride;
     float scale2;                       // scale log2(e)
 };
 
@@ -179,19 +184,42 @@ __global__ void __launch_bounds__(kPlanThreads) attn_prompt_plan(Params p, int2*
     });
 }
 
+// With a window an item goes over the sinks' key tiles and those from the first
+// that row tile 0's first window reaches (`from`), in an order in which each row
+// tile's own stand together: those that only row tile 0 sees (`lead`, one at
+// most), the sinks', the rest.  Where nothing lies between the sinks' and the
+// window's, the order is the keys'.
+template <bool kWindow>
 struct Item {
     int a, len;                         // the sequence's first row and its tokens
     int tok0;                           // first token of row tile 0
     int h;                              // key-value head
     int n0, n1;                         // key tiles of each row tile (0: no rows)
     int keys;                           // keys that the item's last token sees
-    // first V tile to clear: with rows past the item's keys (none: tiles()), or,
-    // the second time, with a key that some row of the item does not see
-    __device__ __forceinline__ int edge(bool second) const {
-        return second ? min((tok0 + 1) / kKeys, tiles() - 1) : keys / kKeys;
-    }
+    int from, lead, sinks;              // with a window; sinks: their tiles in the order (0: the keys' own order)
     __device__ __forceinline__ int n(int s) const { return s ? n1 : n0; }
     __device__ __forceinline__ int tiles() const { return max(n0, n1); }
+    // row tile s goes over tiles begin(s) to n(s)
+    __device__ __forceinline__ int begin(int s) const { return kWindow && s && n1 ? lead : 0; }
+    // the key tile that tile j of the item stands for
+    __device__ __forceinline__ int key_tile(int j) const {
+        if (!kWindow) return j;
+        return j < lead ? from + j : (j < lead + sinks ? j - lead : from + j - sinks);
+    }
+    // V tiles to clear: with rows past the item's keys, or, the second time, with a
+    // key that some row of the item does not see
+    __device__ __forceinline__ bool clears_key_tile(const Params& p, int t, bool second) const {
+        if (!second) return t >= keys / kKeys;
+        if (t >= min((tok0 + 1) / kKeys, (keys - 1) / kKeys)) return true;
+        return kWindow && t * kKeys < keys - p.window && (t + 1) * kKeys > p.sinks;
+    }
+    __device__ __forceinline__ bool clears(const Params& p, int j, bool second) const {
+        return clears_key_tile(p, key_tile(j), second);
+    }
+    // no tile before this one is cleared
+    __device__ __forceinline__ int first_cleared(bool second) const {
+        return kWindow ? 0 : (second ? min((tok0 + 1) / kKeys, tiles() - 1) : keys / kKeys);
+    }
 };
 
 // Entry k of the list in the order of the sequences, and how many there are,
@@ -221,7 +249,8 @@ __device__ __forceinline__ int2 entry_of(const Params& p, int64_t k, int64_t& co
     return e;
 }
 
-__device__ __forceinline__ bool get_item(const Params& p, const Misc* M, int64_t total, int round, Item& it) {
+template <bool kWindow>
+__device__ __forceinline__ bool get_item(const Params& p, const Misc* M, int64_t total, int round, Item<kWindow>& it) {
     const int64_t n = gridDim.x, c = blockIdx.x;
     const int64_t k = (int64_t)round * n + ((round & 1) ? n - 1 - c : c);
     if (k >= total) return false;
@@ -238,6 +267,16 @@ __device__ __forceinline__ bool get_item(const Params& p, const Misc* M, int64_t
     it.n0 = tiles(it.tok0);
     it.n1 = tiles(it.tok0 + p.toks);
     it.keys = min(it.len, it.tok0 + 2 * p.toks);
+    if (kWindow) {
+        const int from = max(it.tok0 - p.window + 1, 0) / kKeys;
+        const bool gap = from > p.sink_tiles;
+        it.from = gap ? from : 0;
+        it.sinks = gap ? p.sink_tiles : 0;
+        it.lead = gap && it.n1 ? max(it.tok0 + p.toks - p.window + 1, 0) / kKeys - from : 0;
+        const int less = it.from - it.sinks;
+        it.n0 -= less;
+        if (it.n1) it.n1 -= less;
+    }
     return true;
 }
 
@@ -307,13 +346,13 @@ __device__ __forceinline__ void init_bars(Bars* B) {
 }
 
 // One time over the CTA's items: warps 0 to 3.
-template <int HD, bool kSecond>
+template <int HD, bool kWindow, bool kSecond>
 __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Misc* M, uint8_t* smem, uint32_t tmem,
                                           int64_t total, int warp, int lane) {
     using C = Cfg<HD>;
     Bars* B = &M->b[kSecond];
     volatile WaitState* ab = &M->wst;
-    Item it;
+    Item<kWindow> it;
 
     if (warp == 0) {
         // ---------------- producer
@@ -322,6 +361,7 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && __all_sync(0xffffffffu, wait_bar_here(bar, parity, ab)); };
         auto tile = [&](const CUtensorMap* m, int j) {
+            const int t = it.key_tile(j);
             wait(&B->empty[st], ph ^ 1u);
             if (!ok) return;
             if (elect_one()) {
@@ -329,7 +369,7 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
 #pragma unroll
                 for (int hf = 0; hf < C::kHalves; ++hf)
                     tma_load_3d(smem + st * C::kTileBytes + hf * C::kHalfBytes, m, &B->full[st], hf * 64, it.h,
-                                it.a + j * kKeys, pol_kv);
+                                it.a + t * kKeys, pol_kv);
             }
             __syncwarp();
             ++g;
@@ -438,17 +478,26 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
                     __syncwarp();
                 }
             }
+            const int j0 = it.begin(s);
+            // tiles that only the other row tile sees, before this one's
+#pragma unroll 1
+            for (int j = 0; kWindow && ok && j < 2 * j0; ++j) {
+                if (!wait(&B->full[st], ph)) break;
+                if (lane == 0) mbar_arrive(&B->empty[st]);
+                if ((j & 1) && it.clears(p, j >> 1, kSecond)) nfix ^= 1u << st;
+                next();
+            }
             if (!wait(&B->full[st], ph)) break;
             if (it.n(s)) {
                 // (the item before it has been read and multiplied)
-                scores(st, 1, 0);
-                scores(st, 0, 0);
+                scores(st, 1, j0);
+                scores(st, 0, j0);
             } else if (lane == 0) {
                 mbar_arrive(&B->empty[st]);
             }
             next();
 #pragma unroll 1
-            for (int j = 0; ok && j < n; ++j) {
+            for (int j = j0; ok && j < n; ++j) {
                 // V_j at st, K_{j+1} at the place after it
                 const uint32_t vat = st, vph = ph;
                 next();
@@ -463,11 +512,11 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
                     }
                 }
                 if (!wait(&B->full[vat], vph)) break;
-                const bool fix = j >= it.edge(kSecond);
+                const bool fix = kWindow ? it.clears(p, j, kSecond) : j >= it.first_cleared(kSecond);
                 if (j < it.n(s)) {
                     // warp 3 starts while P is still being made
                     if (fix && lane == 0) mbar_arrive(&B->asked[s]);
-                    if (j == 0) {
+                    if (j == j0) {
                         if (started) {                        // the item before has been stored
                             if (!wait(&B->o_free[s], no & 1u)) break;
                             no ^= 1u;
@@ -483,7 +532,7 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
                             const uint64_t b = dv + vat * (C::kTileBytes / 16) + half * 512;
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                umma_bf16_ts(tO, tS + half * 32 + kk * 8, b + kk * 128, id_pv, (j | half | kk) ? 1u : 0u);
+                                umma_bf16_ts(tO, tS + half * 32 + kk * 8, b + kk * 128, id_pv, ((j - j0) | half | kk) ? 1u : 0u);
                             if (half) {
                                 umma_commit(&B->pv_done[s]);
                                 umma_commit(&B->empty[vat]);
@@ -527,21 +576,42 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
             const int n = it.tiles();
             uint32_t add = 0;                                 // row tiles that the table matters to, by bit
 #pragma unroll 1
-            for (int j = it.edge(kSecond); j < n; ++j) {
+            for (int j = it.first_cleared(kSecond); j < n; ++j) {
+                if (kWindow && !it.clears(p, j, kSecond)) continue;
+                const int key0 = it.key_tile(j) * kKeys;
                 // the issuers that use the tile have seen it arrive (its parity alone
                 // could be an earlier tile's), and the rows of the items before are stored
                 const uint32_t vi = g + 2 * j + 1, vat = vi % C::kStages;
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    if (j >= it.n(s)) continue;
+                    if (j < it.begin(s) || j >= it.n(s)) continue;
                     wait(&B->asked[s], (asked >> s) & 1u);
                     asked ^= 1u << s;
                 }
                 if (!wait(&B->full[vat], (vi / C::kStages) & 1u)) break;
                 uint8_t* vt = smem + vat * C::kTileBytes + (piece / 8) * C::kHalfBytes;
                 auto at = [&](int row) { return reinterpret_cast<uint4*>(vt + row * 128 + ((piece ^ row) & 7) * 16); };
-                const int valid = min(it.keys - j * kKeys, kKeys);
-                if (kSecond) {
+                const int valid = min(it.keys - key0, kKeys);
+                if (kSecond && kWindow) {
+                    // whatever is not finite goes; which rows see it is worked out below
+                    bool found = false;
+#pragma unroll 1
+                    for (int row = sub; row < valid; row += kStep) {
+                        uint4 w = *at(row);
+                        uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                        bool bad = false;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t m = x[e] & 0x7FFF7FFFu;
+                            if ((m & 0xFFFFu) >= 0x7F80u) x[e] &= 0xFFFF0000u, bad = true;
+                            if (m >= 0x7F800000u) x[e] &= 0xFFFFu, bad = true;
+                        }
+                        if (bad) *at(row) = make_uint4(x[0], x[1], x[2], x[3]);
+                        found |= bad;
+                    }
+                    if (__any_sync(0xffffffffu, found))
+                        add |= (it.begin(0) <= j && j < it.n0 ? 1u : 0u) | (it.begin(1) <= j && j < it.n1 ? 2u : 0u);
+                } else if (kSecond) {
                     if (!add) {
 #pragma unroll 1
                         for (int x = lane; x < 256; x += 32) (&M->since[0][0])[x] = 0xFFFFu;
@@ -590,16 +660,63 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
             for (int s = 0; s < 2; ++s) {
                 if ((add >> s & 1u) && wait(&B->o_free[s], (stored >> s) & 1u)) {
                     const int first = it.tok0 + s * p.toks, end = min(first + p.toks, it.len);
+                    if constexpr (kWindow) {
+                        // the cleared tiles' keys in their order, each when the first token
+                        // that sees it comes: the latest that holds an infinity (a NaN
+                        // counts as both) and the first among the sinks decide a token
 #pragma unroll 1
-                    for (int d = lane; d < HD; d += 32) {
-                        const int plus = it.tok0 + M->since[0][d], minus = it.tok0 + M->since[1][d];
+                        for (int d = lane; d < HD; d += 32) {
+                            const uint16_t* v = p.v + (int64_t)it.a * p.v_stride + (int64_t)it.h * HD + d;
+                            int plus = -1, minus = -1, plus_sink = 0x7FFFFFFF, minus_sink = 0x7FFFFFFF, k = 0;
 #pragma unroll 1
-                        for (int tok = max(first, min(plus, minus)); tok < end; ++tok) {
-                            const float inf = tok < plus ? -INFINITY : (tok < minus ? INFINITY : NAN);
-                            uint16_t* x = p.out + ((size_t)(it.a + tok) * p.heads + (size_t)it.h * p.group) * HD + d;
+                            for (int tok = first; tok < end; ++tok) {
 #pragma unroll 1
-                            for (int q = 0; q < p.group; ++q)
-                                x[q * HD] = __bfloat16_as_ushort(__float2bfloat16_rn(bf16_bits_to_float(x[q * HD]) + inf));
+                                while (k <= tok) {
+                                    const int t = k / kKeys;
+                                    if (t >= it.sinks && t < it.from) {
+                                        k = it.from * kKeys;
+                                        continue;
+                                    }
+                                    if (!it.clears_key_tile(p, t, true)) {
+                                        k = (t + 1) * kKeys;
+                                        continue;
+                                    }
+                                    const uint32_t x = v[(int64_t)k * p.v_stride];
+                                    if ((x & 0x7F80u) == 0x7F80u) {
+                                        if ((x & 0x7Fu) || !(x & 0x8000u)) {
+                                            plus = k;
+                                            if (k < p.sinks) plus_sink = min(plus_sink, k);
+                                        }
+                                        if ((x & 0x7Fu) || (x & 0x8000u)) {
+                                            minus = k;
+                                            if (k < p.sinks) minus_sink = min(minus_sink, k);
+                                        }
+                                    }
+                                    ++k;
+                                }
+                                const int low = tok - p.window;
+                                const bool up = (plus >= 0 && plus > low) || plus_sink <= tok;
+                                const bool down = (minus >= 0 && minus > low) || minus_sink <= tok;
+                                if (!up && !down) continue;
+                                const float inf = up ? (down ? NAN : INFINITY) : -INFINITY;
+                                uint16_t* x = p.out + ((size_t)(it.a + tok) * p.heads + (size_t)it.h * p.group) * HD + d;
+#pragma unroll 1
+                                for (int q = 0; q < p.group; ++q)
+                                    x[q * HD] = __bfloat16_as_ushort(__float2bfloat16_rn(bf16_bits_to_float(x[q * HD]) + inf));
+                            }
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int d = lane; d < HD; d += 32) {
+                            const int plus = it.tok0 + M->since[0][d], minus = it.tok0 + M->since[1][d];
+#pragma unroll 1
+                            for (int tok = max(first, min(plus, minus)); tok < end; ++tok) {
+                                const float inf = tok < plus ? -INFINITY : (tok < minus ? INFINITY : NAN);
+                                uint16_t* x = p.out + ((size_t)(it.a + tok) * p.heads + (size_t)it.h * p.group) * HD + d;
+#pragma unroll 1
+                                for (int q = 0; q < p.group; ++q)
+                                    x[q * HD] = __bfloat16_as_ushort(__float2bfloat16_rn(bf16_bits_to_float(x[q * HD]) + inf));
+                            }
                         }
                     }
                 }
@@ -610,11 +727,11 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
 }
 
 // One time over the CTA's items: the softmax warps.
-template <int HD, bool kSecond>
+template <int HD, bool kWindow, bool kSecond>
 __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint32_t tmem, int64_t total, int warp, int lane) {
     Bars* B = &M->b[kSecond];
     volatile WaitState* ab = &M->wst;
-    Item it;
+    Item<kWindow> it;
 
     // ---------------- softmax: thread = row
     const int s = (warp - 4) >> 2, wq = warp & 3;
@@ -633,14 +750,15 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint32_t 
         return ok;
     };
     for (int round = 0; ok && get_item(p, M, total, round, it); ++round) {
-        const int n = it.n(s);
+        const int n = it.n(s), j0 = it.begin(s);
         if (!n) continue;
         const int tok = it.tok0 + s * p.toks + rt;           // sees keys 0 .. tok
         const int first = it.tok0 + s * p.toks;
         float ref = kFloorRef;
         uint64_t l2 = 0;                                     // two partial sums
-        for (int j = 0; ok && j < n; ++j) {
+        for (int j = j0; ok && j < n; ++j) {
             if (!wait(&B->s_full[s], ns++ & 1u)) break;
+            const int key0 = it.key_tile(j) * kKeys;
             float x[128];
 #pragma unroll
             for (int q = 0; q < 4; ++q) tmem_ld32_async(tS + q * 32, x + q * 32);
@@ -650,12 +768,19 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint32_t 
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&B->s_read[s]);
-            if ((j + 1) * kKeys - 1 > first) {               // a row of the tile does not see all keys
-                const int lim = tok - j * kKeys;
-                const float hidden = c < 0.f ? INFINITY : -INFINITY;
+            const float hidden = c < 0.f ? INFINITY : -INFINITY;
+            if (key0 + kKeys - 1 > first) {                  // a row of the tile does not see all keys
+                const int lim = tok - key0;
 #pragma unroll
                 for (int i = 0; i < 128; ++i)
                     if (i > lim) x[i] = hidden;
+            }
+            // nor the keys before its window and behind the sinks
+            if (kWindow && key0 < first + p.toks - p.window && key0 + kKeys > p.sinks) {
+                const int low = tok - p.window - key0, sink = p.sinks - key0;
+#pragma unroll
+                for (int i = 0; i < 128; ++i)
+                    if (i <= low && i >= sink) x[i] = hidden;
             }
             // the row's largest score (a negative scale makes it the smallest product)
             float mx[4] = {x[0], x[1], x[2], x[3]};
@@ -675,7 +800,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint32_t 
                 float a, b;
                 unpack2(l2, a, b);
                 l2 = pack2(a * f, b * f);
-                if (j > 0) {
+                if (j > j0) {
                     if (!wait(&B->pv_done[s], (npv - 1u) & 1u)) break;
 #pragma unroll
                     for (int q = 0; q < HD / 16; ++q) {
@@ -742,7 +867,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint32_t 
     }
 }
 
-template <int HD>
+template <int HD, bool kWindow>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_prompt_kernel(const __grid_constant__ Maps maps, const Params p) {
     using C = Cfg<HD>;
@@ -809,12 +934,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // registers: 384 x 168 at launch, then 128 x 104 + 256 x 200
     if (warp < 4) {
         regs_lower<104>();
-        few_roles<HD, false>(maps, p, M, smem, tmem, total, warp, lane);
-        if (again()) few_roles<HD, true>(maps, p, M, smem, tmem, total, warp, lane);
+        few_roles<HD, kWindow, false>(maps, p, M, smem, tmem, total, warp, lane);
+        if (again()) few_roles<HD, kWindow, true>(maps, p, M, smem, tmem, total, warp, lane);
     } else {
         regs_raise<200>();
-        softmax_role<HD, false>(p, M, tmem, total, warp, lane);
-        if (again()) softmax_role<HD, true>(p, M, tmem, total, warp, lane);
+        softmax_role<HD, kWindow, false>(p, M, tmem, total, warp, lane);
+        if (again()) softmax_role<HD, kWindow, true>(p, M, tmem, total, warp, lane);
     }
     tc_fence_before();
     __syncthreads();
@@ -825,10 +950,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int HD>
+template <int HD, bool kWindow>
 cudaError_t launch(const Maps& maps, const Params& p, cudaStream_t s) {
     const size_t smem = smem_bytes<HD>();
-    cudaError_t e = allow_smem(attn_prompt_kernel<HD>, smem);
+    cudaError_t e = allow_smem(attn_prompt_kernel<HD, kWindow>, smem);
     if (e != cudaSuccess) return e;
     if (!p.single) {
         prof_begin(kPAttnPromptPlan, s);
@@ -838,7 +963,7 @@ cudaError_t launch(const Maps& maps, const Params& p, cudaStream_t s) {
         if (e != cudaSuccess) return e;
     }
     prof_begin(kPAttnPrompt, s);
-    e = launch_kernel(attn_prompt_kernel<HD>, dim3(num_sms()), dim3(kThreads), smem, s, true, maps, p);
+    e = launch_kernel(attn_prompt_kernel<HD, kWindow>, dim3(num_sms()), dim3(kThreads), smem, s, true, maps, p);
     prof_end(s);
     return e;
 }
@@ -856,7 +981,7 @@ size_t attn_prompt_workspace_bytes(int B, int T, int n_heads, int n_kv_heads, in
 
 cudaError_t launch_attn_prompt(const PromptArgs& a, cudaStream_t s) {
     uint8_t* w = static_cast<uint8_t*>(a.ws) + sizeof(WsHeader);
-    Params p;
+    Params p = {};
     p.seq_off = a.seq_off;
     p.count = reinterpret_cast<const int*>(w);
     p.list = reinterpret_cast<const int2*>(w + 256);
@@ -887,7 +1012,16 @@ cudaError_t launch_attn_prompt(const PromptArgs& a, cudaStream_t s) {
     if (!map(&maps.q, a.q, a.n_heads, a.q_stride, (cuuint32_t)p.group, (cuuint32_t)p.toks) ||
         !map(&maps.k, a.k, a.n_kv_heads, a.k_stride, 1, kKeys) || !map(&maps.v, a.v, a.n_kv_heads, a.v_stride, 1, kKeys))
         return cudaErrorInvalidValue;
-    return a.head_dim == 64 ? launch<64>(maps, p, s) : launch<128>(maps, p, s);
+    // a window of every token is none
+    if (a.window > 0 && a.window < a.T) {
+        p.window = a.window;
+        p.sinks = a.sinks < a.T ? a.sinks : a.T;
+        p.sink_tiles = (int)(((int64_t)p.sinks + kKeys - 1) / kKeys);
+        p.v = static_cast<const uint16_t*>(a.v);
+        p.v_stride = a.v_stride;
+        return a.head_dim == 64 ? launch<64, true>(maps, p, s) : launch<128, true>(maps, p, s);
+    }
+    return a.head_dim == 64 ? launch<64, false>(maps, p, s) : launch<128, false>(maps, p, s);
 }
 
 }  // namespace dspark

@@ -140,6 +140,7 @@ struct PromptArgs {
     const int32_t* seq_off;
     int B, T, n_heads, n_kv_heads, head_dim;
     float scale;
+    int window, sinks;                      // window 0: none
     void* out;
     float* lse;
     void* ws;
@@ -169,7 +170,7 @@ cudaError_t launch_kv_read(const dspark_kv_cache_t& c, const dspark_kv_batch_t& 
                            cudaStream_t s);
 size_t attn_paged_workspace_bytes(int R, int T, int n_heads, int n_kv_heads, int head_dim);
 cudaError_t launch_attn_paged(const void* q, int64_t q_stride, const dspark_kv_cache_t& c, const dspark_kv_batch_t& b,
-                              int n_heads, float scale, void* out, float* lse, void* ws, cudaStream_t s);
+                              int n_heads, float scale, int window, int sinks, void* out, float* lse, void* ws, cudaStream_t s);
 size_t attn_prompt_workspace_bytes(int B, int T, int n_heads, int n_kv_heads, int head_dim);
 cudaError_t launch_attn_prompt(const PromptArgs& a, cudaStream_t s);
 
