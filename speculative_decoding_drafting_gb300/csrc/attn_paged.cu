@@ -127,7 +127,6 @@ struct SegInfo {
     int qp;                            // its Q place: 0, 1, or 2 for both
     uint32_t q_use;                    // how often place 0 (low half) and 1 have been used before
     Request q;
-    int skip;                          // key tiles left out behind the sinks' (0 without a window)
 };
 
 struct Bars {
@@ -224,16 +223,20 @@ struct Maps {
 
 template <bool kWindow>
 using Plan = std::conditional_t<kWindow, WindowPlan, PlanInput>;
-// The key tile that tile t of an item stands for.
+// A segment's window: the first key that the row tile's first row sees behind the
+// sinks (0 where its window reaches the beginning), and the key tiles left out.
 template <bool kWindow>
-__device__ __forceinline__ int key_tile(const PagedParams& p, const SegInfo& s, int t) {
-    return kWindow && t >= p.plan.sink_tiles ? t + s.skip : t;
-}
-// With a window: the first key that the first row of a row tile sees behind the
-// sinks (0 where its window reaches the beginning).
-__device__ __forceinline__ int first_low(const PagedParams& p, const SegInfo& s) {
-    return (int)max((int64_t)s.q.kv_len - s.q.q_len + s.tok - p.plan.window + 1, (int64_t)0);
-}
+struct Window {
+    int low, skip, sink_tiles;
+    __device__ __forceinline__ Window(const PagedParams& p, const SegInfo& s) {
+        if (!kWindow) return;
+        low = (int)max((int64_t)s.q.kv_len - s.q.q_len + s.tok - p.plan.window + 1, (int64_t)0);
+        sink_tiles = p.plan.sink_tiles;
+        skip = max(low / kKeyTile - sink_tiles, 0);
+    }
+    // the key tile that tile t of the item stands for
+    __device__ __forceinline__ int key_tile(int t) const { return kWindow && t >= sink_tiles ? t + skip : t; }
+};
 
 // Shared-memory operand of e4m3 rows of HD bytes: 128-byte swizzle at
 // head_dim 128, 64-byte at 64.
@@ -359,13 +362,14 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
 
     float l = 0.f;                                            // this warp's sum of row `lane`
     const int lim0 = plan_token_keys(sg.q, sg.tok);           // the first row sees the fewest keys
+    const Window<kWindow> win(p, sg);
     const int n = sg.n, t0 = sg.t0;
     const uint32_t line = sg.line;
     const float scale2 = p.scale2;
 
 #pragma unroll 1
     for (int i = (stream - sh.stream_at(sg, 0)) & (streams - 1); i < n; i += streams) {
-        const int kt = key_tile<kWindow>(p, sg, t0 + i), key = kt * kKeyTile + tr;
+        const int kt = win.key_tile(t0 + i), key = kt * kKeyTile + tr;
         bool edge = (kt + 1) * kKeyTile > lim0;               // some row does not see the whole tile
         // with a window, columns from this one on do not see the key either, since
         // their windows begin behind it (of all rows: hidden_rows from the tile's first)
@@ -531,7 +535,7 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
             const int valid = edge ? sg.keys - kt * kKeyTile : kKeyTile;         // rows with a key
             // with a window, rows [gap0, gap1) hold keys that no row of the item sees
             const int gap0 = kWindow ? max(p.plan.sinks - kt * kKeyTile, 0) : 0;
-            const int gap1 = kWindow ? first_low(p, sg) - kt * kKeyTile : 0;
+            const int gap1 = kWindow ? win.low - kt * kKeyTile : 0;
             // A thread's pieces lie `step` pieces, a multiple of 8 rows, apart: their
             // swizzle is the same.  It reads the two 8-byte halves of a piece in an
             // order that differs between lanes, so that neither the loads nor the
@@ -828,8 +832,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const SegInfo& s = M->seg[at];
         c.more = ok && s.rows > 0;
         if (!c.more) return;
-        c.tok = key_tile<kWindow>(p, s, s.t0) * kKeyTile;
-        c.end = (key_tile<kWindow>(p, s, s.t0 + s.n - 1) + 1) * kKeyTile;
+        const Window<kWindow> win(p, s);
+        c.tok = win.key_tile(s.t0) * kKeyTile;
+        c.end = (win.key_tile(s.t0 + s.n - 1) + 1) * kKeyTile;
         c.keys = s.keys;
         c.r = s.r;
         c.x = s.h << p.page_log2;
@@ -839,8 +844,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         c.now = entry(c, c.at + lane);
         c.next = entry(c, c.at + 32 + lane);
         if (kWindow) {
-            c.low = first_low(p, s);
-            c.gap = s.skip * kKeyTile;
+            c.low = win.low;
+            c.gap = win.skip * kKeyTile;
             // the pages behind the gap, if the segment comes to it
             const int to = p.plan.sink_tiles * kKeyTile + c.gap;
             if (c.gap > 0 && c.tok < to && to < c.end) c.far = entry(c, ((to >> p.page_log2) & ~31) + lane);
@@ -1028,6 +1033,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Shape sh(sg.rows);
             const uint32_t id = F8 ? idesc_f16_f32(128, sh.cols, true, true) : idesc_bf16_f32(128, sh.cols, true, true);
             const uint32_t set = tmem + kColO * (1u + (nseg & 1u));
+            const Window<kWindow> win(p, sg);
             if (sg.run != run && elect_one()) umma_commit(&M->b.r_done);
             __syncwarp();
             run = sg.run;
@@ -1038,9 +1044,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // p_full covers, as it does the end of the reads of the loaded one
                 if (!F8) {
                     wait(&M->b.v_full[vs], vph);
-                    const int first = key_tile<kWindow>(p, sg, sg.t0 + i) * kKeyTile, valid = sg.keys - first;
-                    uint8_t* vt = smem + C::kOffV + (size_t)vs * C::kTileBytes;
+                    const int first = win.key_tile(sg.t0 + i) * kKeyTile, valid = sg.keys - first;
                     auto clear = [&](int from, int to) {
+                        uint8_t* vt = smem + C::kOffV + (size_t)vs * C::kTileBytes;
 #pragma unroll 1
                         for (int k = from * 8 + lane; k < to * 8; k += 32)
 #pragma unroll
@@ -1052,7 +1058,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // rows past the last key hold whatever the pages or this buffer held
                     if (ok && valid < kKeyTile) clear(max(valid, 0), kKeyTile);
                     if (kWindow && ok) {                      // and those of keys that no row of the item sees anything
-                        const int gap0 = max(p.plan.sinks - first, 0), gap1 = min(first_low(p, sg) - first, kKeyTile);
+                        const int gap0 = max(p.plan.sinks - first, 0), gap1 = min(win.low - first, kKeyTile);
                         if (gap0 < gap1) clear(gap0, gap1);
                     }
                 }
@@ -1121,7 +1127,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     o.rows = 0;
                     if (more)
                         o = SegInfo{s.r, s.j, s.h, s.t0, s.t1 - s.t0, s.tiles, s.keys, s.rows, s.tok, s.head, s.rest, line, run,
-                                    both ? 2 : place, use, s.q, s.skip};
+                                    both ? 2 : place, use, s.q};
                     mbar_arrive(&M->b.seg_full[made % kSegs]);
                 }
                 __syncwarp();
