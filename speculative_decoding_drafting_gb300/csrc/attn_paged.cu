@@ -224,18 +224,20 @@ struct Maps {
 template <bool kWindow>
 using Plan = std::conditional_t<kWindow, WindowPlan, PlanInput>;
 // A segment's window: the first key that the row tile's first row sees behind the
-// sinks (0 where its window reaches the beginning), and the key tiles left out.
+// sinks (0 where its window reaches the beginning), and what lies before it on the
+// line of the item's keys.
 template <bool kWindow>
 struct Window {
-    int low, skip, sink_tiles;
+    int low = 0, gap = 0, head = 0;
+    __device__ __forceinline__ Window() {}
     __device__ __forceinline__ Window(const PagedParams& p, const SegInfo& s) {
         if (!kWindow) return;
         low = (int)max((int64_t)s.q.kv_len - s.q.q_len + s.tok - p.plan.window + 1, (int64_t)0);
-        sink_tiles = p.plan.sink_tiles;
-        skip = max(low / kKeyTile - sink_tiles, 0);
+        gap = plan_gap(p.plan, s.q, s.j);
+        head = p.plan.head;
     }
-    // the key tile that tile t of the item stands for
-    __device__ __forceinline__ int key_tile(int t) const { return kWindow && t >= sink_tiles ? t + skip : t; }
+    // the key that place v of the item's keys stands for
+    __device__ __forceinline__ int key(int v) const { return kWindow && v >= head ? v + gap : v; }
 };
 
 // Shared-memory operand of e4m3 rows of HD bytes: 128-byte swizzle at
@@ -369,12 +371,12 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
 
 #pragma unroll 1
     for (int i = (stream - sh.stream_at(sg, 0)) & (streams - 1); i < n; i += streams) {
-        const int kt = win.key_tile(t0 + i), key = kt * kKeyTile + tr;
-        bool edge = (kt + 1) * kKeyTile > lim0;               // some row does not see the whole tile
+        const int v0 = (t0 + i) * kKeyTile, key = win.key(v0 + tr);
+        bool edge = win.key(v0 + kKeyTile - 1) >= lim0;       // some row does not see the whole tile
         // with a window, columns from this one on do not see the key either, since
         // their windows begin behind it (of all rows: hidden_rows from the tile's first)
         int hid = kRowTile, hidden_rows = kRowTile;
-        if (kWindow && kt * kKeyTile < sg.keys - p.plan.window && (kt + 1) * kKeyTile > p.plan.sinks) {
+        if (kWindow && (v0 < win.head ? p.plan.sinks : v0 + win.gap) < sg.keys - p.plan.window && v0 + kKeyTile > p.plan.sinks) {
             edge = true;
             if (key >= p.plan.sinks) {
                 // the first token (from the tile's) that does not
@@ -389,6 +391,10 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
         const int behind = key - sg.q.kv_len + sg.q.q_len - sg.tok;
         const int seen = !edge ? 0 : (key >= sg.keys ? kRowTile
                                       : (kWindow ? max(behind, -1) : behind) * p.plan.group - sg.head - coff);
+        // the columns that do not see the key, by bit: one test per score for both ends
+        uint32_t out_of_sight = 0;
+        if (kWindow && edge)
+            out_of_sight = (seen <= 0 ? 0u : 0xFFFFFFFFu >> (32 - min(seen, 32))) | (hid >= 32 ? 0u : 0xFFFFFFFFu << max(hid, 0));
         const uint32_t turn = sh.turn_at(sg, i);
         wait_bar(&M->b.s_full[turn][u], (st.phases >> turn) & 1u, ab);
         st.phases ^= 1u << turn;
@@ -440,7 +446,7 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
                 if (edge) {
 #pragma unroll
                     for (int c = 0; c < kB; ++c)
-                        if (c0 + c < seen || (kWindow && c0 + c >= hid)) t[c0 + c] = -INFINITY;
+                        if (kWindow ? (out_of_sight >> (c0 + c)) & 1u : c0 + c < seen) t[c0 + c] = -INFINITY;
                 }
 #pragma unroll
                 for (int c = 0; c < kB; ++c) top = fmaxf(top, t[c0 + c]);
@@ -457,7 +463,7 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     float y = fmaf(F8 ? x[c] * M->qm[u][c0 + c] : x[c], mul, lvs);
-                    if (c0 + c < seen || (kWindow && c0 + c >= hid)) y = -INFINITY;
+                    if (kWindow ? (out_of_sight >> (c0 + c)) & 1u : c0 + c < seen) y = -INFINITY;
                     y = redux_max(y);
                     if (lane == c) mine = y;
                 }
@@ -532,10 +538,9 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
             const uint8_t* src = smem + C::kOffV + (size_t)s * C::kLoadBytes;
             uint8_t* dst = smem + C::kOffW + (size_t)d * C::kTileBytes;
             constexpr int kPieces = kKeyTile * HD / 16, kPer = HD / 16;
-            const int valid = edge ? sg.keys - kt * kKeyTile : kKeyTile;         // rows with a key
+            const int valid = edge ? sg.keys - win.gap - v0 : kKeyTile;          // rows with a key
             // with a window, rows [gap0, gap1) hold keys that no row of the item sees
-            const int gap0 = kWindow ? max(p.plan.sinks - kt * kKeyTile, 0) : 0;
-            const int gap1 = kWindow ? win.low - kt * kKeyTile : 0;
+            const int gap0 = kWindow ? p.plan.sinks - v0 : 0, gap1 = kWindow ? win.low - win.gap - v0 : 0;
             // A thread's pieces lie `step` pieces, a multiple of 8 rows, apart: their
             // swizzle is the same.  It reads the two 8-byte halves of a piece in an
             // order that differs between lanes, so that neither the loads nor the
@@ -566,20 +571,13 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
                     to += kB * (kStep / kPer) * 128;
                 }
                 // rows without a key become zeros, whatever their places hold
-                if (kWindow && gap0 < gap1) {
-#pragma unroll 1
-                    for (int h = 1; h <= kN; ++h) {
-                        const int row = row0 + (kN - h) * (kStep / kPer);
-                        if (row < gap0 || row >= gap1) continue;
-                        *reinterpret_cast<uint4*>(to - h * (kStep / kPer) * 128 + ta) = make_uint4(0u, 0u, 0u, 0u);
-                        *reinterpret_cast<uint4*>(to - h * (kStep / kPer) * 128 + tb) = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                }
-                if (valid < kKeyTile) {
+                if (valid < kKeyTile || (kWindow && max(gap0, 0) < gap1)) {
 #pragma unroll 1
                     for (int h = kN; h > 0; --h) {
                         to -= (kStep / kPer) * 128;
-                        if (row0 + (h - 1) * (kStep / kPer) < valid) break;
+                        const int row = row0 + (h - 1) * (kStep / kPer);
+                        if (kWindow && row < valid && !(row >= gap0 && row < gap1)) continue;
+                        if (!kWindow && row < valid) break;
                         *reinterpret_cast<uint4*>(to + ta) = make_uint4(0u, 0u, 0u, 0u);
                         *reinterpret_cast<uint4*>(to + tb) = make_uint4(0u, 0u, 0u, 0u);
                     }
@@ -815,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int tok, end, keys;                                   // first token of the tile, of the segment's end; keys
         int at, now, next;                                    // page table: lane's entries of 32 pages from `at`, and the 32 after
         int r, x;
-        int low, gap, far;                                    // with a window: its first key, the tokens left out, lane's page there
+        Window<kWindow> win;
         uint32_t seg, slot, phase, count;                     // segment; ring place; tiles issued
         uint64_t pol;
         bool more;
@@ -823,7 +821,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int pg = lane & 7;
     const int lane_tok = pg < ppt ? pg * bp : 1 << 30;        // this lane's page of a tile, in tokens
     bool ok = true;
+    // pages, or with a window what is left out together
+    const int unit_log2 = kWindow ? min(p.page_log2, 7) : p.page_log2;
     auto entry = [&](const Place& c, int k) {
+        if (kWindow) {
+            const int64_t v = (int64_t)k << unit_log2;
+            return v < c.keys ? load4(p.page_table + (size_t)c.r * p.max_pages + (c.win.key((int)v) >> p.page_log2)) : -1;
+        }
         return (int64_t)k << p.page_log2 < c.keys ? load4(p.page_table + (size_t)c.r * p.max_pages + k) : -1;
     };
     auto enter = [&](Place& c) {
@@ -832,28 +836,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         const SegInfo& s = M->seg[at];
         c.more = ok && s.rows > 0;
         if (!c.more) return;
-        const Window<kWindow> win(p, s);
-        c.tok = win.key_tile(s.t0) * kKeyTile;
-        c.end = (win.key_tile(s.t0 + s.n - 1) + 1) * kKeyTile;
-        c.keys = s.keys;
+        c.win = Window<kWindow>(p, s);
+        c.tok = s.t0 * kKeyTile;
+        c.end = (s.t0 + s.n) * kKeyTile;
+        c.keys = s.keys - c.win.gap;
         c.r = s.r;
         c.x = s.h << p.page_log2;
         // more than one row tile of a request reads its keys again
         c.pol = (int64_t)s.q.q_len * pl.group > kRowTile ? policy_evict_normal() : policy_evict_first();
-        c.at = (c.tok >> p.page_log2) & ~31;
+        c.at = (c.tok >> unit_log2) & ~31;
         c.now = entry(c, c.at + lane);
         c.next = entry(c, c.at + 32 + lane);
-        if (kWindow) {
-            c.low = win.low;
-            c.gap = win.skip * kKeyTile;
-            // the pages behind the gap, if the segment comes to it
-            const int to = p.plan.sink_tiles * kKeyTile + c.gap;
-            if (c.gap > 0 && c.tok < to && to < c.end) c.far = entry(c, ((to >> p.page_log2) & ~31) + lane);
-        }
     };
     // this lane's page of the place's tile (pages past the keys: any)
     auto page_of = [&](Place& c) {
-        int rel = (c.tok >> p.page_log2) - c.at;
+        int rel = (c.tok >> unit_log2) - c.at;
         if (rel >= 32) {
             rel -= 32;
             c.at += 32;
@@ -866,12 +863,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto step = [&](Place& c) {
         ++c.count;
         c.tok += kKeyTile;
-        if (kWindow && c.gap > 0 && c.tok == p.plan.sink_tiles * kKeyTile) {
-            c.tok += c.gap;
-            c.at = (c.tok >> p.page_log2) & ~31;
-            c.now = c.far;
-            if (c.tok < c.end) c.next = entry(c, c.at + 32 + lane);
-        }
         if (c.tok < c.end) return false;
         ++c.seg;
         return true;
@@ -887,7 +878,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) return;
         const bool valid = lane_tok < c.keys - c.tok;
         // a page that no row of the item sees is not read, whatever its id
-        const bool unseen = kWindow && c.tok + lane_tok >= p.plan.sinks && c.tok + lane_tok + bp <= c.low;
+        const int first = c.win.key(c.tok + lane_tok);
+        const bool unseen = kWindow && first >= p.plan.sinks && first + bp <= c.win.low;
         if (valid && unseen) {
             id = p.n_pages;
         } else if (valid && (uint32_t)id >= (uint32_t)p.n_pages) {
@@ -895,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             id = p.n_pages;                                   // past the tensor: zeros
         }
         const uint32_t pages = __popc(__ballot_sync(0xffffffffu, valid) & 0xFFu);
-        const int x = c.x + (ppt == 1 ? c.tok & ((1 << p.page_log2) - 1) : 0);        // a 256-token page is two tiles
+        const int x = c.x + (ppt == 1 ? c.win.key(c.tok) & ((1 << p.page_log2) - 1) : 0);        // a 256-token page is two tiles
         if (elect_one()) {
             mbar_expect_tx(full, pages * (uint32_t)(bp * (F8 ? HD : HD * 2)));
         }
@@ -1044,7 +1036,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // p_full covers, as it does the end of the reads of the loaded one
                 if (!F8) {
                     wait(&M->b.v_full[vs], vph);
-                    const int first = win.key_tile(sg.t0 + i) * kKeyTile, valid = sg.keys - first;
+                    const int first = (sg.t0 + i) * kKeyTile, valid = sg.keys - win.gap - first;
                     auto clear = [&](int from, int to) {
                         uint8_t* vt = smem + C::kOffV + (size_t)vs * C::kTileBytes;
 #pragma unroll 1
@@ -1058,7 +1050,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // rows past the last key hold whatever the pages or this buffer held
                     if (ok && valid < kKeyTile) clear(max(valid, 0), kKeyTile);
                     if (kWindow && ok) {                      // and those of keys that no row of the item sees anything
-                        const int gap0 = max(p.plan.sinks - first, 0), gap1 = min(win.low - first, kKeyTile);
+                        const int gap0 = max(p.plan.sinks - first, 0), gap1 = min(win.low - win.gap - first, kKeyTile);
                         if (gap0 < gap1) clear(gap0, gap1);
                     }
                 }
@@ -1335,13 +1327,14 @@ cudaError_t launch_attn_paged(const void* q, int64_t q_stride, const dspark_kv_c
     const int64_t most = (int64_t)b.max_pages * c.page;
     p.plan = WindowPlan{{b.q_off, b.kv_len, b.R, b.T, n_heads / c.n_kv_heads, c.n_kv_heads, most,
                          few ? 0 : (f8 ? 12 : 8), f8 ? tile_lengths(4, 4, 4, 5, 6, 7) : tile_lengths(4, 4, 4, 4, 5, 6)},
-                        0, 0, 0};
+                        0, 0, 0, 0};
     // a window of all that a request may hold is none
     const bool windowed = window > 0 && window < most;
     if (windowed) {
         p.plan.window = window;
         p.plan.sinks = (int)std::min((int64_t)sinks, most);
-        p.plan.sink_tiles = (p.plan.sinks + kKeyTile - 1) / kKeyTile;
+        p.plan.unit = std::min(c.page, kKeyTile);
+        p.plan.head = (p.plan.sinks + p.plan.unit - 1) / p.plan.unit * p.plan.unit;
     }
     p.page_table = b.page_table;
     p.k_scale = c.k_scale;

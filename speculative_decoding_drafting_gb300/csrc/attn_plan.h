@@ -11,10 +11,12 @@
 // that requests of any mix of lengths load the device evenly.  An item that a
 // cut goes through leaves one partial result per piece.
 //
-// With a window (WindowPlan) an item's tiles are the sinks' and, from the first
-// that its first row's window reaches, those up to its end: the tiles between
-// are left out of the count, and tile t of an item is key tile t, or t + skip
-// from the sinks' end on.
+// With a window (WindowPlan) an item's keys are the sinks' pages and, from the
+// page that its first row's window begins in, those up to its end, one after
+// another; its tiles are cut from that line, in which key v stands for key v, or
+// v + gap from the sinks' end on.  (Tiles of the keys themselves left a tile to the
+// sinks and one to the window's beginning, mostly hidden: 10 tiles for a window
+// of 1024 and 4 sinks where this takes 9.)
 #pragma once
 
 #include <stdint.h>
@@ -44,9 +46,10 @@ struct PlanInput {
     uint32_t lengths;              // length of a tile, 5 bits each: up to 8, 16, 24, 32, 48, 64 rows (1 .. 31)
 };
 // Tokens that see the last `window` tokens, their own among them, and the first
-// sink_tiles key tiles' (some of them: that is the kernel's matter).
+// `sinks`.  unit: tokens that are left out together, a page's or a tile's, the
+// smaller; head: the sinks' tokens rounded up to units.
 struct WindowPlan : PlanInput {
-    int window, sinks, sink_tiles;
+    int window, sinks, unit, head;
 };
 DSPARK_HD int plan_length(const PlanInput& p, int rows) {
     return (int)(p.lengths >> 5 * (rows <= 32 ? (rows - 1) / 8 : (rows <= 48 ? 4 : 5))) & 31;
@@ -84,12 +87,19 @@ DSPARK_HD int plan_tile_keys(const PlanInput& p, const Request& q, int j) {
 DSPARK_HD int64_t plan_low(const WindowPlan& p, const Request& q, int j) {
     return (int64_t)q.kv_len - q.q_len + (int64_t)j * kRowTile / p.group - p.window + 1;
 }
-// Key tiles between the sinks' and the window's.
-DSPARK_HD int plan_skip(const PlanInput&, const Request&, int) { return 0; }
-DSPARK_HD int plan_skip(const WindowPlan& p, const Request& q, int j) {
-    const int64_t low = plan_low(p, q, j);
-    const int n = low > 0 ? (int)low / kKeyTile - p.sink_tiles : 0;       // low <= kv_len
-    return n > 0 ? n : 0;
+// The part below a tile of the tokens left out of a request's items: row tile 0
+// leaves out what it can in units, the later ones whole tiles more, so that their
+// number sums in closed form.
+DSPARK_HD int plan_off(const WindowPlan& p, const Request& q) {
+    const int64_t low = plan_low(p, q, 0);
+    return low > p.head ? (int)(low - p.head) / p.unit * p.unit & (kKeyTile - 1) : 0;   // low <= kv_len
+}
+// Tokens between the sinks' pages and the row tile's first.
+DSPARK_HD int plan_gap(const PlanInput&, const Request&, int) { return 0; }
+DSPARK_HD int plan_gap(const WindowPlan& p, const Request& q, int j) {
+    const int off = plan_off(p, q);
+    const int64_t n = plan_low(p, q, j) - p.head - off;
+    return n > 0 ? ((int)n & ~(kKeyTile - 1)) + off : (n == 0 ? off : 0);
 }
 DSPARK_HD int plan_key_tiles(int keys) { return keys > 0 ? (keys - 1) / kKeyTile + 1 : 1; }
 DSPARK_HD int plan_rows(const PlanInput& p, const Request& q, int j) {
@@ -125,24 +135,24 @@ DSPARK_HD_CALL int64_t plan_before(int group, int start, int length, int q_len, 
 DSPARK_HD int64_t plan_tiles_before(const PlanInput& p, const Request& q, int n) {
     return plan_before(p.group, p.start, plan_length(p, kRowTile), q.q_len, q.kv_len, n);
 }
-// Tiles that the first n row tiles skip, each max(0, floor((j + b) / 2 group)) of
-// them: the same sum, with b from the beginning of the first row's window less the
-// sinks' tiles.
-DSPARK_HD_CALL int64_t plan_skipped_before(int group, int64_t ahead, int sink_tiles, int n) {
+// Whole tiles that the first n row tiles leave out, each max(0, floor((j + b) / 2
+// group)) of them: the same sum, b from the tokens left out before row tile 0.
+DSPARK_HD_CALL int64_t plan_left_out_before(int group, int64_t ahead, int n) {
     const uint32_t m = 2u * (uint32_t)group;
-    const int64_t b = (ahead * group >> 6) - (int64_t)m * sink_tiles;
+    const int64_t b = ahead * group >> 6;
     return plan_floor_sum(b + n, m) - plan_floor_sum(b, m);
 }
 DSPARK_HD int64_t plan_tiles_before(const WindowPlan& p, const Request& q, int n) {
-    return plan_before(p.group, p.start, plan_length(p, kRowTile), q.q_len, q.kv_len, n) -
-           plan_skipped_before(p.group, plan_low(p, q, 0), p.sink_tiles, n) * plan_length(p, kRowTile);
+    const int off = plan_off(p, q);
+    return plan_before(p.group, p.start, plan_length(p, kRowTile), q.q_len, q.kv_len - off, n) -
+           plan_left_out_before(p.group, plan_low(p, q, 0) - p.head - off, n) * plan_length(p, kRowTile);
 }
 template <typename P>
 DSPARK_HD_CALL int64_t plan_request_length(P p, int r) {
     const Request q = plan_request(p, r);
     const int n = plan_row_tiles(p, q);
     if (n == 0) return 0;
-    const int64_t last = plan_place(p, plan_length(p, plan_rows(p, q, n - 1)), plan_key_tiles(q.kv_len) - plan_skip(p, q, n - 1));
+    const int64_t last = plan_place(p, plan_length(p, plan_rows(p, q, n - 1)), plan_key_tiles(q.kv_len - plan_gap(p, q, n - 1)));
     return (plan_tiles_before(p, q, n - 1) + last) * p.kv_heads;
 }
 // The row tile that holds place x of request r's items: the last that begins at or before it.
@@ -186,7 +196,7 @@ struct Segment {
     int tok, head;                 // the first row's new token, and its place in the group
     int rest;                      // from the span's end to the beginning of the item's last tile (an unfinished item's: >= 0)
     Request q;
-    int skip;                      // key tiles left out behind the sinks' (0 without a window)
+    int gap;                       // keys left out behind the sinks' (0 without a window)
 };
 
 // Row x of a row tile whose first row is (tok, head): its new token and its
@@ -217,7 +227,7 @@ struct Cursor {
         if (n <= 0) return;
         q = plan_request(p, r);
         j = plan_tile_of(p, q, skip);
-        const int tiles = plan_key_tiles(plan_tile_keys(p, q, j)) - plan_skip(p, q, j), length = plan_length(p, plan_rows(p, q, j));
+        const int tiles = plan_key_tiles(plan_tile_keys(p, q, j) - plan_gap(p, q, j)), length = plan_length(p, plan_rows(p, q, j));
         const int64_t item = plan_place(p, length, tiles);
         skip -= plan_tiles_before(p, q, j) * p.kv_heads;
         h = (int)(skip / item);
@@ -230,8 +240,8 @@ struct Cursor {
         while (end > p.start) {                            // else no further tile begins in the span
             while (q.q_len == 0) q = plan_request(p, ++r); // the span goes on: a request with rows follows
             s.keys = plan_tile_keys(p, q, j);
-            s.skip = plan_skip(p, q, j);
-            s.tiles = plan_key_tiles(s.keys) - s.skip;
+            s.gap = plan_gap(p, q, j);
+            s.tiles = plan_key_tiles(s.keys - s.gap);
             s.rows = plan_rows(p, q, j);
             const int length = plan_length(p, s.rows);
             s.r = r;

@@ -1,6 +1,6 @@
 """The work split of paged attention with a window (csrc/attn_plan.h), compiled
 for the host: over random batches, values out of range among them, the segments
-cover exactly the key tiles that some row of the item sees (and the sinks'),
+cover the keys that some row of the item sees and little else, page by page and
 counted row by row, once each, and every index stays in range."""
 import shutil
 import subprocess
@@ -49,7 +49,8 @@ int main() {
         static_cast<PlanInput&>(p) = PlanInput{off.data(), len.data(), R, T, group, kv_heads, most, start, lengths};
         p.window = (int)pick(1, trial % 8 == 0 ? 1 << 30 : (trial % 2 ? 5000 : 200));
         p.sinks = trial % 3 ? (int)pick(0, trial % 9 ? 20 : 700) : 0;
-        p.sink_tiles = (p.sinks + kKeyTile - 1) / kKeyTile;
+        p.unit = page < kKeyTile ? page : kKeyTile;
+        p.head = (p.sinks + p.unit - 1) / p.unit * p.unit;
         int64_t total = 0;
         std::vector<int64_t> first(R);
         for (int r = 0; r < R; ++r) {
@@ -75,33 +76,35 @@ int main() {
                 CHECK(s.q.a >= 0 && s.q.q_len > 0 && s.q.a + s.q.q_len <= T);
                 CHECK(s.rows >= 1 && s.rows <= kRowTile && (int64_t)s.j * kRowTile + s.rows <= (int64_t)s.q.q_len * group);
                 CHECK(s.keys >= 0 && s.keys <= s.q.kv_len && s.keys <= most);
-                CHECK(0 <= s.t0 && s.t0 < s.t1 && s.t1 <= s.tiles && s.skip >= 0 && (s.skip == 0 || s.tiles > p.sink_tiles));
-                // the item's key tiles are those that hold a key of a row, and the sinks'
-                auto physical = [&](int t) { return t >= p.sink_tiles ? t + s.skip : t; };
-                std::vector<char> need((s.keys + kKeyTile - 1) / kKeyTile + 1, 0);
+                CHECK(0 <= s.t0 && s.t0 < s.t1 && s.t1 <= s.tiles && s.gap >= 0 && s.gap % p.unit == 0);
+                // the item's units are those that hold a key of a row, and the sinks'
+                auto physical = [&](int v) { return v >= p.head ? v + s.gap : v; };
+                std::vector<char> need((s.keys + p.unit - 1) / p.unit + 1, 0);
+                int64_t low = 1ll << 40;
                 for (int x = 0; x < s.rows; ++x) {
                     int i, g;
                     plan_row(group, s.tok, s.head, x, i, g);
-                    const int64_t pos = (int64_t)s.q.kv_len - s.q.q_len + i;
-                    for (int64_t k = pos - p.window + 1 > 0 ? pos - p.window + 1 : 0; k <= pos; k += kKeyTile) need[k / kKeyTile] = 1;
-                    if (pos >= 0) need[pos / kKeyTile] = 1;
-                    for (int64_t k = 0; k < p.sinks && k <= pos; k += kKeyTile) need[k / kKeyTile] = 1;
+                    const int64_t pos = (int64_t)s.q.kv_len - s.q.q_len + i, from = pos - p.window + 1 > 0 ? pos - p.window + 1 : 0;
+                    if (pos >= 0 && from < low) low = from;
+                    for (int64_t k = from / p.unit * p.unit; k <= pos; k += p.unit) need[k / p.unit] = 1;
+                    for (int64_t k = 0; k < p.sinks && k <= pos; k += p.unit) need[k / p.unit] = 1;
                 }
-                int covered = 0;
-                for (int t = 0; t < s.tiles; ++t) {
-                    const int k = physical(t);
-                    CHECK(k == 0 || k * kKeyTile < s.keys);
-                    covered += need[k];
-                    // nothing is taken that is not needed, but for sinks' tiles behind all keys' windows
-                    CHECK(need[k] || s.keys == 0 || k < p.sink_tiles);
+                int covered = 0, extra = 0;
+                for (int v = 0; v < s.tiles * kKeyTile; v += p.unit) {
+                    const int k = physical(v);
+                    if (k >= s.keys) { CHECK(v / kKeyTile == s.tiles - 1); continue; }
+                    covered += need[k / p.unit];
+                    extra += !need[k / p.unit];
                 }
                 int needed = 0;
                 for (char x : need) needed += x;
                 CHECK(covered == needed);
+                // row tile 0 takes nothing else, the later ones less than a tile
+                CHECK(extra * p.unit < (s.j == 0 ? p.unit : kKeyTile));
                 const auto id = std::make_tuple(s.r, s.j, s.h);
                 CHECK(done[id] == s.t0);
-                CHECK(s.t0 == 0 || shape[id] == std::make_pair(s.tiles, s.skip));
-                shape[id] = std::make_pair(s.tiles, s.skip);
+                CHECK(s.t0 == 0 || shape[id] == std::make_pair(s.tiles, s.gap));
+                shape[id] = std::make_pair(s.tiles, s.gap);
                 done[id] = s.t1;
                 ++pieces;
                 CHECK(s.t0 == 0 || pieces == 1);
@@ -136,13 +139,14 @@ int main() {
         static_cast<PlanInput&>(p) = PlanInput{off, len, 1, q_len, group, 1, 1 << 30, 3, 0x02108421u};
         p.window = (int)pick(1, trial % 2 ? 1 << 30 : 5000);
         p.sinks = (int)pick(0, 1000);
-        p.sink_tiles = (p.sinks + kKeyTile - 1) / kKeyTile;
+        p.unit = 16 << pick(0, 3);
+        p.head = (p.sinks + p.unit - 1) / p.unit * p.unit;
         const Request q = plan_request(p, 0);
         int64_t sum = 0;
         const int n = plan_row_tiles(p, q);
         for (int j = 0; j < n; ++j) {
             CHECK(sum == plan_tiles_before(p, q, j));
-            const int tiles = plan_key_tiles(plan_tile_keys(p, q, j)) - plan_skip(p, q, j);
+            const int tiles = plan_key_tiles(plan_tile_keys(p, q, j) - plan_gap(p, q, j));
             CHECK(tiles >= 1);
             sum += plan_place(p, plan_length(p, plan_rows(p, q, j)), tiles);
         }
