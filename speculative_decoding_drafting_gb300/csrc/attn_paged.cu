@@ -169,6 +169,7 @@ __constant__ const BarCounts kBarCounts = bar_counts<F8>();
 
 struct alignas(16) Misc {
     SegInfo seg[kSegs];
+    int2 win[kSegs];                   // with a window: its `low` and `gap`
     float ref[kUnits][kUnitRows];      // reference of a row
     float nref[kUnits][kUnitRows];     // kLift minus it
     float qm[kUnits][kUnitRows];       // 2^e of a row's split
@@ -230,10 +231,11 @@ template <bool kWindow>
 struct Window {
     int low = 0, gap = 0, head = 0;
     __device__ __forceinline__ Window() {}
-    __device__ __forceinline__ Window(const PagedParams& p, const SegInfo& s) {
+    __device__ __forceinline__ Window(const PagedParams& p, const Misc* M, uint32_t seg) {
         if (!kWindow) return;
-        low = (int)max((int64_t)s.q.kv_len - s.q.q_len + s.tok - p.plan.window + 1, (int64_t)0);
-        gap = plan_gap(p.plan, s.q, s.j);
+        const int2 w = M->win[seg % kSegs];
+        low = w.x;
+        gap = w.y;
         head = p.plan.head;
     }
     // the key that place v of the item's keys stands for
@@ -331,9 +333,69 @@ struct SoftState {
     uint32_t seg;                      // segments so far
 };
 
+// With a window, a tile that some row does not see the whole of: the columns that
+// do not see a thread's key, by bit.  Their token stands before the key, their window
+// begins behind it, or it lies past the item's keys; columns past the tile's
+// rows do not see keys that no row sees either, since what lies there must not raise
+// the other columns' references.  (All bits: no row sees it.)
+// first: the position of the tile's first row's token.  Its token k sees the key
+// if first + k >= key, and if it is no sink, first + k < key + window.
+static __device__ __noinline__ uint32_t hidden_columns(int coff, int key, int keys, int first, int window, int sinks, int group,
+                                                       int head) {
+    int seen = kRowTile, hid = kRowTile;
+    if (key < keys) {
+        const int64_t behind = (int64_t)key - first;
+        seen = (int)max(behind, (int64_t)-1) * group - head;
+        if (key >= sinks) hid = (int)min(max(behind + window, (int64_t)0), (int64_t)kRowTile + 1) * group - head;
+    }
+    const int a = min(max(seen - coff, 0), 32), b = min(max(hid - coff, 0), 32);
+    return hid <= 0 ? 0xFFFFFFFFu : (uint32_t)((1ull << a) - 1) | ~(uint32_t)((1ull << b) - 1);
+}
+// The same for e4m3, whose loop is long: gives those columns scores that make their
+// weights zero, in tensor memory itself, so that the loop needs no test per score
+// (24 warps of different code share the instruction caches).  Returns the factor
+// that makes scores of the scores, `mul`, or 1 where that is 0 or that of a key that no
+// row sees and would make NaNs of the infinities; and whether no row sees the key.
+struct Hidden {
+    float mul;
+    bool all;
+};
+static __device__ __noinline__ Hidden hide_scores(uint32_t tS, int cols, uint32_t hidden, float mul) {
+    const bool all = hidden == 0xFFFFFFFFu;
+    if (all) mul = 1.f;
+    const float gone = mul < 0.f ? INFINITY : -INFINITY;
+#pragma unroll 1
+    for (int c0 = 0; c0 < cols; c0 += 8) {
+        float x[8];
+        tmem_ldn<8>(tS + (uint32_t)c0, x);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            if (mul == 0.f) x[c] = 0.f;
+            if ((hidden >> (c0 + c)) & 1u) x[c] = gone;
+        }
+        tmem_st8(tS + (uint32_t)c0, reinterpret_cast<const uint32_t(&)[8]>(x));
+    }
+    tmem_st_wait();
+    return Hidden{mul == 0.f ? 1.f : mul, all};
+}
+
+// e4m3 with a window: rows of a widened V tile that no row of the item sees become
+// zeros, a thread's pieces (`rows` of them, `apart` rows from one to the next).
+static __device__ __noinline__ void clear_rows(uint8_t* to, int ta, int tb, int row, int rows, int apart, int valid, int gap0,
+                                               int gap1) {
+#pragma unroll 1
+    for (int h = 0; h < rows; ++h, row += apart, to += apart * 128) {
+        if (row < valid && !(row >= gap0 && row < gap1)) continue;
+        *reinterpret_cast<uint4*>(to + ta) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(to + tb) = make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
 // One segment's key tiles of unit u.  The unit's threads all
 // walk the same barriers even after a wait ran out (the results are then not
 // stored), so that no named barrier is left waiting.
+// kMost: the rows that the code is made for; 0: any, in blocks of 8 columns that
+// are passed over where there are no rows.
 template <int HD, bool F8, bool kWindow, int kMost>
 __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo& sg, Misc* M, uint8_t* smem,
                                              uint32_t tmem, int u, SoftState& st) {
@@ -343,8 +405,10 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
     const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
     const int tr = wq * 32 + lane;                            // key of the tile; head_dim index of O^T
     // columns of this unit: a half of a wide row tile
-    constexpr bool wide = kMost > kUnitRows;
-    constexpr int N = wide ? kMost / 2 : kMost, streams = wide ? kUnits / 2 : kUnits;
+    constexpr bool any = kMost == 0;
+    const bool wide = any ? sh.wide : kMost > kUnitRows;
+    const int N = any ? (wide ? sh.cols / 2 : (sg.rows + 7) & ~7) : (kMost > kUnitRows ? kMost / 2 : kMost);
+    const int streams = wide ? kUnits / 2 : kUnits;
     const int bar = 1 + u, parity = st.seg & 1;
     const int stream = wide ? u >> 1 : u, coff = wide ? (u & 1) * N : 0;
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
@@ -364,7 +428,7 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
 
     float l = 0.f;                                            // this warp's sum of row `lane`
     const int lim0 = plan_token_keys(sg.q, sg.tok);           // the first row sees the fewest keys
-    const Window<kWindow> win(p, sg);
+    const Window<kWindow> win(p, M, st.seg);
     const int n = sg.n, t0 = sg.t0;
     const uint32_t line = sg.line;
     const float scale2 = p.scale2;
@@ -373,34 +437,24 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
     for (int i = (stream - sh.stream_at(sg, 0)) & (streams - 1); i < n; i += streams) {
         const int v0 = (t0 + i) * kKeyTile, key = win.key(v0 + tr);
         bool edge = win.key(v0 + kKeyTile - 1) >= lim0;       // some row does not see the whole tile
-        // with a window, columns from this one on do not see the key either, since
-        // their windows begin behind it (of all rows: hidden_rows from the tile's first)
-        int hid = kRowTile, hidden_rows = kRowTile;
-        if (kWindow && (v0 < win.head ? p.plan.sinks : v0 + win.gap) < sg.keys - p.plan.window && v0 + kKeyTile > p.plan.sinks) {
-            edge = true;
-            if (key >= p.plan.sinks) {
-                // the first token (from the tile's) that does not
-                const int64_t d = (int64_t)key + p.plan.window - sg.q.kv_len + sg.q.q_len - sg.tok;
-                hidden_rows = (int)min(max(d, (int64_t)0), (int64_t)kRowTile + 1) * p.plan.group - sg.head;
-                hid = hidden_rows - coff;
-            }
-        }
+        if (kWindow)
+            edge = edge || ((v0 < win.head ? p.plan.sinks : v0 + win.gap) < sg.keys - p.plan.window && v0 + kKeyTile > p.plan.sinks);
         // new token k sees the key if kv_len - q_len + k >= key: from this row on.
         // Past the last key no column sees it, the unused ones neither: what
         // lies there must not raise the other columns' references.
-        const int behind = key - sg.q.kv_len + sg.q.q_len - sg.tok;
-        const int seen = !edge ? 0 : (key >= sg.keys ? kRowTile
-                                      : (kWindow ? max(behind, -1) : behind) * p.plan.group - sg.head - coff);
-        // the columns that do not see the key, by bit: one test per score for both ends
-        uint32_t out_of_sight = 0;
+        const int seen = kWindow || !edge ? 0 : (key >= sg.keys ? kRowTile
+                                      : (key - sg.q.kv_len + sg.q.q_len - sg.tok) * p.plan.group - sg.head - coff);
+        uint32_t hidden = 0;
         if (kWindow && edge)
-            out_of_sight = (seen <= 0 ? 0u : 0xFFFFFFFFu >> (32 - min(seen, 32))) | (hid >= 32 ? 0u : 0xFFFFFFFFu << max(hid, 0));
+            hidden = hidden_columns(coff, key, sg.keys, sg.q.kv_len - sg.q.q_len + sg.tok, p.plan.window, p.plan.sinks, p.plan.group,
+                                    sg.head);
         const uint32_t turn = sh.turn_at(sg, i);
         wait_bar(&M->b.s_full[turn][u], (st.phases >> turn) & 1u, ab);
         st.phases ^= 1u << turn;
         tc_fence_after();
         const uint32_t tS = tS0 + (turn ? kColS1 : 0u);
         float mul = scale2, lvs = 0.f, ivs = 1.f;
+        bool unseen = false;                                  // with a window: by every row
         if (F8) {
             const uint32_t at = line + (uint32_t)i;
             const int s = (int)(at % C::kScMod);
@@ -412,7 +466,12 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
             // a wide tile's scales are read by two units
             if (lane == 0) mbar_arrive(&M->b.c_empty[s]);
             if (!wide && lane == 0) mbar_arrive(&M->b.c_empty[s]);
-            if (edge && (key >= sg.keys || (kWindow && hidden_rows <= 0))) vs = 1.f;   // no key here: any scale
+            if (kWindow && edge) {
+                const Hidden h = hide_scores(tS, N, hidden, mul);
+                mul = h.mul;
+                unseen = h.all;
+            }
+            if (kWindow ? unseen : edge && key >= sg.keys) vs = 1.f;     // no key here: any scale
             // Below 2^-100 (a row of zeros has scale 0) 1 / scale would take the sum
             // out of float32's range: there the sum counts the key with 2^-101, and
             // its weight for V is 0 (values below 2^-91 are dropped, not raised).
@@ -427,32 +486,62 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
 #pragma unroll 1
         for (bool raised = false;; raised = true) {
             float top = -INFINITY;
-            auto part = [&](auto first, auto count) {
+            auto exponents = [&](auto first, auto count, float* x) {
                 constexpr int c0 = decltype(first)::value, kB = decltype(count)::value;
-                float x[kB];
-                tmem_ldn<kB>(tS + (uint32_t)c0, x);
 #pragma unroll
-                for (int c = 0; c < kB; c += 2) {
+                for (int c = 0; F8 && c < kB; c += 4) {
+                    const float4 r = *reinterpret_cast<const float4*>(&M->nref[u][c0 + c]);
+                    const float4 qm = *reinterpret_cast<const float4*>(&M->qm[u][c0 + c]);
+#pragma unroll
+                    for (int h = 0; h < 4; h += 2) {
+                        uint64_t y = pack2(x[c + h], x[c + h + 1]);
+                        const uint64_t r2 = h ? pack2(r.z, r.w) : pack2(r.x, r.y);
+                        y = fma2(mul2x(y, h ? pack2(qm.z, qm.w) : pack2(qm.x, qm.y)), mul2, add2(r2, lvs2));
+                        unpack2(y, t[c0 + c + h], t[c0 + c + h + 1]);
+                    }
+                }
+#pragma unroll
+                for (int c = 0; !F8 && c < kB; c += 2) {
                     uint64_t y = pack2(x[c], x[c + 1]);
                     const float2 r = *reinterpret_cast<const float2*>(&M->nref[u][c0 + c]);
-                    if (F8) {
-                        const float2 qm = *reinterpret_cast<const float2*>(&M->qm[u][c0 + c]);
-                        y = fma2(mul2x(y, pack2(qm.x, qm.y)), mul2, add2(pack2(r.x, r.y), lvs2));
-                    } else {
-                        y = fma2(y, mul2, pack2(r.x, r.y));
-                    }
+                    y = fma2(y, mul2, pack2(r.x, r.y));
                     unpack2(y, t[c0 + c], t[c0 + c + 1]);
                 }
-                if (edge) {
+                if (!(kWindow && F8) && edge) {
 #pragma unroll
                     for (int c = 0; c < kB; ++c)
-                        if (kWindow ? (out_of_sight >> (c0 + c)) & 1u : c0 + c < seen) t[c0 + c] = -INFINITY;
+                        if (kWindow ? (hidden >> (c0 + c)) & 1u : c0 + c < seen) t[c0 + c] = -INFINITY;
                 }
 #pragma unroll
-                for (int c = 0; c < kB; ++c) top = fmaxf(top, t[c0 + c]);
+                for (int c = 0; F8 && c < kB; c += 2) top = fmax3(top, t[c0 + c], t[c0 + c + 1]);
+#pragma unroll
+                for (int c = 0; !F8 && c < kB; ++c) top = fmaxf(top, t[c0 + c]);
             };
-            part(std::integral_constant<int, 0>{}, std::integral_constant<int, (N < 16 ? N : 16)>{});
-            if constexpr (N > 16) part(std::integral_constant<int, 16>{}, std::integral_constant<int, N - 16>{});
+            if constexpr (any) {
+                // (the loads in flight together)
+                tmem_ld8_async(tS, t);
+                if (N > 8) tmem_ld8_async(tS + 8u, t + 8);
+                if (N > 16) tmem_ld8_async(tS + 16u, t + 16);
+                if (N > 24) tmem_ld8_async(tS + 24u, t + 24);
+                tmem_ld_wait();
+                auto block = [&](auto first) {
+                    tmem_pin8(t + first);
+                    exponents(first, std::integral_constant<int, 8>{}, t + first);
+                };
+                block(std::integral_constant<int, 0>{});
+                if (N > 8) block(std::integral_constant<int, 8>{});
+                if (N > 16) block(std::integral_constant<int, 16>{});
+                if (N > 24) block(std::integral_constant<int, 24>{});
+            } else {
+                constexpr int kN = kMost > kUnitRows ? kMost / 2 : kMost;
+                auto part = [&](auto first, auto count) {
+                    float x[decltype(count)::value];
+                    tmem_ldn<decltype(count)::value>(tS + (uint32_t)first, x);
+                    exponents(first, count, x);
+                };
+                part(std::integral_constant<int, 0>{}, std::integral_constant<int, (kN < 16 ? kN : 16)>{});
+                if constexpr (kN > 16) part(std::integral_constant<int, 16>{}, std::integral_constant<int, kN - 16>{});
+            }
             // (raised once: scores of 2^28 and more round by more than the threshold)
             if (raised || !named_any(bar, 128, top > C::kLift + C::kLazy)) break;
             // one is too large: raise its reference to its largest score so far
@@ -463,7 +552,7 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     float y = fmaf(F8 ? x[c] * M->qm[u][c0 + c] : x[c], mul, lvs);
-                    if (kWindow ? (out_of_sight >> (c0 + c)) & 1u : c0 + c < seen) y = -INFINITY;
+                    if (kWindow ? !F8 && ((hidden >> (c0 + c)) & 1u) : c0 + c < seen) y = -INFINITY;
                     y = redux_max(y);
                     if (lane == c) mine = y;
                 }
@@ -502,7 +591,8 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
         if (st.tiles > 0) wait_bar(&M->b.pv_done[u], (st.tiles - 1u) & 1u, ab);
         ++st.tiles;
 #pragma unroll
-        for (int c0 = 0; c0 < N; c0 += 8) {
+        for (int c0 = 0; c0 < kUnitRows; c0 += 8) {
+            if (c0 >= N) continue;
             uint32_t pk[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -539,14 +629,13 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
             uint8_t* dst = smem + C::kOffW + (size_t)d * C::kTileBytes;
             constexpr int kPieces = kKeyTile * HD / 16, kPer = HD / 16;
             const int valid = edge ? sg.keys - win.gap - v0 : kKeyTile;          // rows with a key
-            // with a window, rows [gap0, gap1) hold keys that no row of the item sees
-            const int gap0 = kWindow ? p.plan.sinks - v0 : 0, gap1 = kWindow ? win.low - win.gap - v0 : 0;
             // A thread's pieces lie `step` pieces, a multiple of 8 rows, apart: their
             // swizzle is the same.  It reads the two 8-byte halves of a piece in an
             // order that differs between lanes, so that neither the loads nor the
             // stores of a quarter warp meet in a bank.
             auto widen = [&](int x0, auto count, auto step) {
-                constexpr int kN = decltype(count)::value, kStep = decltype(step)::value, kB = 2;
+                const int kN = count, kStep = step;
+                constexpr int kB = 1;
                 const int row0 = x0 / kPer, c0 = (x0 % kPer) * 2, sw = row0 & 7;
                 const int flip = HD == 128 ? ((tr >> 2) ^ (tr >> 3)) & 1 : (tr >> 3) & 1;
                 const uint8_t* from = src + x0 * 16;
@@ -571,19 +660,23 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
                     to += kB * (kStep / kPer) * 128;
                 }
                 // rows without a key become zeros, whatever their places hold
-                if (valid < kKeyTile || (kWindow && max(gap0, 0) < gap1)) {
+                if (kWindow && edge) {
+                    // with a window, rows between the sinks and the window too
+                    clear_rows(to - kN * (kStep / kPer) * 128, ta, tb, row0, kN, kStep / kPer, valid, p.plan.sinks - v0,
+                               win.low - win.gap - v0);
+                } else if (!kWindow && valid < kKeyTile) {
 #pragma unroll 1
                     for (int h = kN; h > 0; --h) {
                         to -= (kStep / kPer) * 128;
-                        const int row = row0 + (h - 1) * (kStep / kPer);
-                        if (kWindow && row < valid && !(row >= gap0 && row < gap1)) continue;
-                        if (!kWindow && row < valid) break;
+                        if (row0 + (h - 1) * (kStep / kPer) < valid) break;
                         *reinterpret_cast<uint4*>(to + ta) = make_uint4(0u, 0u, 0u, 0u);
                         *reinterpret_cast<uint4*>(to + tb) = make_uint4(0u, 0u, 0u, 0u);
                     }
                 }
             };
-            if constexpr (wide)
+            if constexpr (any)
+                widen(wide ? (u & 1) * 128 + tr : tr, wide ? kPieces / 256 : kPieces / 128, wide ? 256 : 128);
+            else if constexpr (kMost > kUnitRows)
                 widen((u & 1) * 128 + tr, std::integral_constant<int, kPieces / 256>{}, std::integral_constant<int, 256>{});
             else
                 widen(tr, std::integral_constant<int, kPieces / 128>{}, std::integral_constant<int, 128>{});
@@ -595,16 +688,29 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
         // the weights' sums (over w / scale for e4m3), while the product runs: a
         // row's sum in one lane, since a sum per row and thread would not fit
         // the registers
+        if constexpr (any) {
+#pragma unroll
+            for (int c0 = 0; c0 < kUnitRows; c0 += 8) {
+                if (c0 >= N) continue;
+                if (F8) {
+#pragma unroll
+                    for (int c = c0; c < c0 + 8; c += 2) unpack2(mul2x(pack2(t[c], t[c + 1]), pack2(ivs, ivs)), t[c], t[c + 1]);
+                }
+                const float sum = lane_sums<8, F8>(t + c0);
+                if (lane >> 3 == c0 >> 3) l += sum;
+            }
+            continue;
+        }
         if (F8) {
 #pragma unroll
-            for (int c = 0; c < N; ++c) t[c] *= ivs;
+            for (int c = 0; c < N; c += 2) unpack2(mul2x(pack2(t[c], t[c + 1]), pack2(ivs, ivs)), t[c], t[c + 1]);
         }
-        if constexpr (N == 24) {
+        if constexpr (kMost == 24 || kMost == 48) {
             float* rest = t + 16;
-            const float a = lane_sums<16>(t), b = lane_sums<8>(rest);
+            const float a = lane_sums<16, F8>(t), b = lane_sums<8, F8>(rest);
             l += lane < 16 ? a : b;
-        } else {
-            l += lane_sums<N>(t);
+        } else if constexpr (!any) {
+            l += lane_sums<(kMost > kUnitRows ? kMost / 2 : kMost), F8>(t);
         }
     }
 
@@ -836,7 +942,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const SegInfo& s = M->seg[at];
         c.more = ok && s.rows > 0;
         if (!c.more) return;
-        c.win = Window<kWindow>(p, s);
+        c.win = Window<kWindow>(p, M, c.seg);
         c.tok = s.t0 * kKeyTile;
         c.end = (s.t0 + s.n) * kKeyTile;
         c.keys = s.keys - c.win.gap;
@@ -1025,7 +1131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Shape sh(sg.rows);
             const uint32_t id = F8 ? idesc_f16_f32(128, sh.cols, true, true) : idesc_bf16_f32(128, sh.cols, true, true);
             const uint32_t set = tmem + kColO * (1u + (nseg & 1u));
-            const Window<kWindow> win(p, sg);
+            const Window<kWindow> win(p, M, nseg);
             if (sg.run != run && elect_one()) umma_commit(&M->b.r_done);
             __syncwarp();
             run = sg.run;
@@ -1117,6 +1223,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) {
                     SegInfo& o = M->seg[made % kSegs];
                     o.rows = 0;
+                    if constexpr (kWindow)
+                        if (more) M->win[made % kSegs] = make_int2((int)max(plan_low(pl, s.q, s.tok), (int64_t)0), s.gap);
                     if (more)
                         o = SegInfo{s.r, s.j, s.h, s.t0, s.t1 - s.t0, s.tiles, s.keys, s.rows, s.tok, s.head, s.rest, line, run,
                                     both ? 2 : place, use, s.q};
@@ -1207,7 +1315,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             // caches 146 and 138; without the one for 8, e4m3 decoding 115.4 and 113.5.
             // (bf16 has no loop for 24: such items are bound by the cache's bytes, and
             // one shape more cost blocks of 1 to 17 tokens 4 %.)
-            if (s.rows <= 8)
+            // (e4m3 with a window: one loop takes any number.  Its code is longer, and with
+            // a loop per number two SMs beside each other, which fetch from one cache, ran
+            // out of it whenever their items had different rows: 128 requests, window
+            // 4096, blocks of 1 and 6 in turn 294 -> 246 us, of 6 alone 251 -> 248.  Over bf16
+            // it is the slower: 256 requests, window 1024, one token 134 -> 150.)
+            if constexpr (kWindow && F8)
+                soft_segment<HD, F8, kWindow, 0>(p, s, M, smem, tmem, u, st);
+            else if (s.rows <= 8)
                 soft_segment<HD, F8, kWindow, 8>(p, s, M, smem, tmem, u, st);
             else if (s.rows <= 16)
                 soft_segment<HD, F8, kWindow, 16>(p, s, M, smem, tmem, u, st);

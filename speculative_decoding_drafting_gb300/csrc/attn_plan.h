@@ -47,7 +47,7 @@ struct PlanInput {
 };
 // Tokens that see the last `window` tokens, their own among them, and the first
 // `sinks`.  unit: tokens that are left out together, a page's or a tile's, the
-// smaller; head: the sinks' tokens rounded up to units.
+// smaller (a power of two); head: the sinks' tokens rounded up to units.
 struct WindowPlan : PlanInput {
     int window, sinks, unit, head;
 };
@@ -83,22 +83,24 @@ DSPARK_HD int plan_tile_keys(const PlanInput& p, const Request& q, int j) {
     // the last row tile's last row sees every key
     return end < rows ? plan_seen(p, q, end - 1) : q.kv_len;
 }
-// The first key that a window ending with row tile j's first row holds (may be negative).
-DSPARK_HD int64_t plan_low(const WindowPlan& p, const Request& q, int j) {
-    return (int64_t)q.kv_len - q.q_len + (int64_t)j * kRowTile / p.group - p.window + 1;
+// The new token that row tile j's first row belongs to.
+DSPARK_HD int plan_first_token(const PlanInput& p, int j) { return j == 0 ? 0 : (int)((int64_t)j * kRowTile / p.group); }
+// The first key that a window ending with new token i holds (may be negative).
+DSPARK_HD int64_t plan_low(const WindowPlan& p, const Request& q, int i) {
+    return (int64_t)q.kv_len - q.q_len + i - p.window + 1;
 }
 // The part below a tile of the tokens left out of a request's items: row tile 0
 // leaves out what it can in units, the later ones whole tiles more, so that their
 // number sums in closed form.
 DSPARK_HD int plan_off(const WindowPlan& p, const Request& q) {
     const int64_t low = plan_low(p, q, 0);
-    return low > p.head ? (int)(low - p.head) / p.unit * p.unit & (kKeyTile - 1) : 0;   // low <= kv_len
+    return low > p.head ? (int)(low - p.head) & (kKeyTile - 1) & ~(p.unit - 1) : 0;     // low <= kv_len
 }
-// Tokens between the sinks' pages and the row tile's first.
+// Tokens between the sinks' pages and those of a row tile that begins with new token i.
 DSPARK_HD int plan_gap(const PlanInput&, const Request&, int) { return 0; }
-DSPARK_HD int plan_gap(const WindowPlan& p, const Request& q, int j) {
+DSPARK_HD int plan_gap(const WindowPlan& p, const Request& q, int i) {
     const int off = plan_off(p, q);
-    const int64_t n = plan_low(p, q, j) - p.head - off;
+    const int64_t n = plan_low(p, q, i) - p.head - off;
     return n > 0 ? ((int)n & ~(kKeyTile - 1)) + off : (n == 0 ? off : 0);
 }
 DSPARK_HD int plan_key_tiles(int keys) { return keys > 0 ? (keys - 1) / kKeyTile + 1 : 1; }
@@ -152,7 +154,7 @@ DSPARK_HD_CALL int64_t plan_request_length(P p, int r) {
     const Request q = plan_request(p, r);
     const int n = plan_row_tiles(p, q);
     if (n == 0) return 0;
-    const int64_t last = plan_place(p, plan_length(p, plan_rows(p, q, n - 1)), plan_key_tiles(q.kv_len - plan_gap(p, q, n - 1)));
+    const int64_t last = plan_place(p, plan_length(p, plan_rows(p, q, n - 1)), plan_key_tiles(q.kv_len - plan_gap(p, q, plan_first_token(p, n - 1))));
     return (plan_tiles_before(p, q, n - 1) + last) * p.kv_heads;
 }
 // The row tile that holds place x of request r's items: the last that begins at or before it.
@@ -227,7 +229,7 @@ struct Cursor {
         if (n <= 0) return;
         q = plan_request(p, r);
         j = plan_tile_of(p, q, skip);
-        const int tiles = plan_key_tiles(plan_tile_keys(p, q, j) - plan_gap(p, q, j)), length = plan_length(p, plan_rows(p, q, j));
+        const int tiles = plan_key_tiles(plan_tile_keys(p, q, j) - plan_gap(p, q, plan_first_token(p, j))), length = plan_length(p, plan_rows(p, q, j));
         const int64_t item = plan_place(p, length, tiles);
         skip -= plan_tiles_before(p, q, j) * p.kv_heads;
         h = (int)(skip / item);
@@ -240,7 +242,8 @@ struct Cursor {
         while (end > p.start) {                            // else no further tile begins in the span
             while (q.q_len == 0) q = plan_request(p, ++r); // the span goes on: a request with rows follows
             s.keys = plan_tile_keys(p, q, j);
-            s.gap = plan_gap(p, q, j);
+            s.tok = (int)((int64_t)j * kRowTile / p.group);
+            s.gap = plan_gap(p, q, s.tok);
             s.tiles = plan_key_tiles(s.keys - s.gap);
             s.rows = plan_rows(p, q, j);
             const int length = plan_length(p, s.rows);
@@ -248,7 +251,6 @@ struct Cursor {
             s.j = j;
             s.h = h;
             s.q = q;
-            s.tok = (int)((int64_t)j * kRowTile / p.group);
             s.head = (int)((int64_t)j * kRowTile - (int64_t)s.tok * p.group);
             s.t0 = t;
             s.t1 = plan_tile_at(p, length, end, s.tiles);

@@ -165,16 +165,24 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
 // Sums over the 32 lanes of the first N = 8, 16 or 32 values per lane; lane i
 // gets the sum of value i % N.  (Each exchange halves the values; what is left
 // of the lanes is summed for one value.)
-template <int N>
+// kPacked: two additions per instruction, which takes aligned pairs of registers.
+template <int N, bool kPacked>
 __device__ __forceinline__ float lane_sums(float* x) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = N / 2; o > 0; o >>= 1) {
         const bool up = lane & o;
+        float keep[N / 2], get[N / 2];
 #pragma unroll
         for (int i = 0; i < o; ++i) {
-            const float keep = up ? x[i + o] : x[i], give = up ? x[i] : x[i + o];
-            x[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+            const float give = up ? x[i] : x[i + o];
+            keep[i] = up ? x[i + o] : x[i];
+            get[i] = __shfl_xor_sync(0xffffffffu, give, o);
+            if (!kPacked || o == 1) x[i] = keep[i] + get[i];
+        }
+        if (kPacked && o > 1) {
+#pragma unroll
+            for (int i = 0; i < o; i += 2) unpack2(add2(pack2(keep[i], keep[i + 1]), pack2(get[i], get[i + 1])), x[i], x[i + 1]);
         }
     }
 #pragma unroll
@@ -282,6 +290,11 @@ __device__ __forceinline__ bool named_any(int id, int threads, bool pred) {
         : "r"(id), "r"(threads), "r"(pred ? 1u : 0u)
         : "memory");
     return r != 0;
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 // Largest value of the warp's lanes (NaN only if every lane's is).
 __device__ __forceinline__ float redux_max(float v) {
@@ -487,6 +500,16 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// 8 columns without waiting: usable after tmem_ld_wait() and tmem_pin8() on them.
+__device__ __forceinline__ void tmem_ld8_async(uint32_t taddr, float* v) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_pin8(float* v) {
+    asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]));
+}
 // N = 4, 8, 16 or 32 consecutive 32-bit columns of this thread's lane, usable on
 // return: the registers are operands of the wait, so that no use of them can
 // be scheduled before it.

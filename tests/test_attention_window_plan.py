@@ -146,7 +146,7 @@ int main() {
         const int n = plan_row_tiles(p, q);
         for (int j = 0; j < n; ++j) {
             CHECK(sum == plan_tiles_before(p, q, j));
-            const int tiles = plan_key_tiles(plan_tile_keys(p, q, j) - plan_gap(p, q, j));
+            const int tiles = plan_key_tiles(plan_tile_keys(p, q, j) - plan_gap(p, q, plan_first_token(p, j)));
             CHECK(tiles >= 1);
             sum += plan_place(p, plan_length(p, plan_rows(p, q, j)), tiles);
         }
