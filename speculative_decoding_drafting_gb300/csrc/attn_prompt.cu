@@ -40,6 +40,7 @@
 // sequences of 100 to 4000 tokens: 590 to 612 us, 1.11 to 1.15 PFLOP/s.  (Taking
 // a quarter of the exponentials from the XU pipe to a polynomial on the FMA pipe
 // cost 18 %: its instructions cost more than the pipe it relieves.)
+#include <algorithm>
 #include <cfloat>
 
 #include <cuda.h>
@@ -93,7 +94,8 @@ struct Misc {
     uint16_t since[2][128];
     // this CTA's entry and the number of entries, where there is no list (a
     // CTA past the last entry has none, and the workspace no room for one)
-    int2 own;
+    alignas(16) int4 own;
+    int4 next[kThreads / 32];           // each warp's next entry of the list
     int entries;
 };
 
@@ -106,17 +108,18 @@ constexpr size_t smem_bytes() {
 
 struct Params {
     const int32_t* seq_off;
-    const int2* list;                   // (sequence, pair of row tiles), longest first
+    const int4* list;                   // pairs of row tiles (a sequence's first row, its tokens, the pair's first), longest first
     const int* count;                   // entries of the list
     int most;                           // entries that the workspace holds
     int single;                         // no CTA gets a second item: each finds its own entry
+    int sectors;                        // out begins on a 32-byte boundary
     uint16_t* out;
     float* lse;
     void* ws;
     int B, T, heads, kv_heads, group, toks;   // toks: tokens of a row tile
-    // with a window: its tokens, the first tokens that stay visible and their key
-    // tiles; v as it lies in memory (for values that are not finite)
-    int window, sinks, sink_tiles;
+    // with a window: its tokens, the first tokens that stay visible, and those in
+    // whole copies; v as it lies in memory (for values that are not finite)
+    int window, sinks, head;
     const uint16_t* v;
     int64_t v_stride;
     float scale2;                       // scale log2(e)
@@ -132,7 +135,7 @@ __device__ __forceinline__ int pairs_of(const Params& p, int b) {
 // their length (the tile's place in its sequence), by a counting sort over
 // 1024 classes of places.  Entries of a class stand in any order: each item's
 // result depends on the item alone.
-__global__ void __launch_bounds__(kPlanThreads) attn_prompt_plan(Params p, int2* list, int* count) {
+__global__ void __launch_bounds__(kPlanThreads) attn_prompt_plan(Params p, int4* list, int* count) {
     pdl_launch_dependents();
     using u64 = unsigned long long;                          // overlapping sequences (bad offsets) can sum to anything
     __shared__ u64 at[kPlanThreads];
@@ -156,10 +159,10 @@ __global__ void __launch_bounds__(kPlanThreads) attn_prompt_plan(Params p, int2*
         for (int b = warp; b < p.B; b += kPlanThreads / 32) {
             const RowRange r = row_range(p.seq_off, b, p.T);
             const int n = (r.b - r.a + pair - 1) / pair;
-            for (int t = lane; t < n; t += 32) f(b, t, kPlanThreads - 1 - (int)((int64_t)t * kPlanThreads / n_class));
+            for (int t = lane; t < n; t += 32) f(r, t, kPlanThreads - 1 - (int)((int64_t)t * kPlanThreads / n_class));
         }
     };
-    each([&](int, int, int c) { atomicAdd(&at[c], u64(1)); });
+    each([&](const RowRange&, int, int c) { atomicAdd(&at[c], u64(1)); });
     __syncthreads();
     // exclusive sums over the classes
     const u64 v = at[tid];
@@ -178,43 +181,41 @@ __global__ void __launch_bounds__(kPlanThreads) attn_prompt_plan(Params p, int2*
     __syncthreads();
     // only offsets that decrease can give more entries than the workspace has
     // room for (sequences that overlap); what does not fit is left out
-    each([&](int b, int t, int c) {
+    each([&](const RowRange& r, int t, int c) {
         const u64 k = atomicAdd(&at[c], u64(1));
-        if (k < (u64)p.most) list[k] = make_int2(b, t);
+        if (k < (u64)p.most) list[k] = make_int4(r.a, r.b - r.a, t * pair, 0);
     });
 }
 
-// With a window an item goes over the sinks' key tiles and those from the first
-// that row tile 0's first window reaches (`from`), in an order in which each row
-// tile's own stand together: those that only row tile 0 sees (`lead`, one at
-// most), the sinks', the rest.  Where nothing lies between the sinks' and the
-// window's, the order is the keys'.
+// With a window an item's keys are the sinks (rounded up to kHeadRows, `head`) and
+// those from the first that row tile 0's first window holds up to its end, one
+// after another; its tiles are cut from that line, in which place v stands for key
+// v, or v + gap from the head's end on.  (Tiles of the keys themselves took one for
+// the sinks alone and half of one before the window: 10 for a window of 1024 and 4
+// sinks where this takes 9.)  Where nothing is left out, head and gap are 0.
+constexpr int kHeadRows = 8;            // rows of a swizzle atom, which a copy can fill by itself
 template <bool kWindow>
 struct Item {
     int a, len;                         // the sequence's first row and its tokens
     int tok0;                           // first token of row tile 0
     int h;                              // key-value head
-    int n0, n1;                         // key tiles of each row tile (0: no rows)
+    int n0, n1;                         // key tiles up to each row tile's last (0: no rows)
     int keys;                           // keys that the item's last token sees
-    int from, lead, sinks;              // with a window; sinks: their tiles in the order (0: the keys' own order)
+    int head, gap, lead;                // with a window; lead: tiles that row tile 1 sees nothing of
     __device__ __forceinline__ int n(int s) const { return s ? n1 : n0; }
     __device__ __forceinline__ int tiles() const { return max(n0, n1); }
     // row tile s goes over tiles begin(s) to n(s)
     __device__ __forceinline__ int begin(int s) const { return kWindow && s && n1 ? lead : 0; }
-    // the key tile that tile j of the item stands for
-    __device__ __forceinline__ int key_tile(int j) const {
-        if (!kWindow) return j;
-        return j < lead ? from + j : (j < lead + sinks ? j - lead : from + j - sinks);
-    }
+    __device__ __forceinline__ int key(int v) const { return kWindow && v >= head ? v + gap : v; }
+    // what tile j's first row would stand for as a key if its last row's key decides
+    __device__ __forceinline__ int key0(int j) const { return key(j * kKeys + kKeys - 1) - (kKeys - 1); }
     // V tiles to clear: with rows past the item's keys, or, the second time, with a
     // key that some row of the item does not see
-    __device__ __forceinline__ bool clears_key_tile(const Params& p, int t, bool second) const {
-        if (!second) return t >= keys / kKeys;
-        if (t >= min((tok0 + 1) / kKeys, (keys - 1) / kKeys)) return true;
-        return kWindow && t * kKeys < keys - p.window && (t + 1) * kKeys > p.sinks;
-    }
     __device__ __forceinline__ bool clears(const Params& p, int j, bool second) const {
-        return clears_key_tile(p, key_tile(j), second);
+        const int k = key0(j);
+        if (!second) return k + kKeys > keys;
+        if (k + kKeys > tok0 + 1 || j + 1 == tiles()) return true;
+        return kWindow && k < keys - p.window && (j + 1) * kKeys > p.sinks;
     }
     // no tile before this one is cleared
     __device__ __forceinline__ int first_cleared(bool second) const {
@@ -249,34 +250,52 @@ __device__ __forceinline__ int2 entry_of(const Params& p, int64_t k, int64_t& co
     return e;
 }
 
+// A CTA's items in turn, asked for by whole warps.  The list's entry for the next one
+// is on its way to the warp's place in shared memory while this one is worked on:
+// items with a window are short, and a load from L2 before each took 5 to 20 % of
+// them.  (Kept in registers it slowed the softmax's loop by 10 %.)
 template <bool kWindow>
-__device__ __forceinline__ bool get_item(const Params& p, const Misc* M, int64_t total, int round, Item<kWindow>& it) {
-    const int64_t n = gridDim.x, c = blockIdx.x;
-    const int64_t k = (int64_t)round * n + ((round & 1) ? n - 1 - c : c);
-    if (k >= total) return false;
+__device__ __forceinline__ bool get_item(const Params& p, Misc* M, int64_t total, int round, Item<kWindow>& it) {
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
+    const uint64_t n = gridDim.x, c = blockIdx.x;
+    auto place = [&](int r) { return (uint64_t)r * n + ((r & 1) ? n - 1 - c : c); };
+    auto entry = [&](uint64_t k) { return (uint64_t)total >> 32 ? k / (uint32_t)p.kv_heads : (uint32_t)k / (uint32_t)p.kv_heads; };
     // the list was written by the kernel before this one
-    const int2 e = p.single ? M->own : __ldcg(p.list + k / p.kv_heads);
-    it.h = (int)(k % p.kv_heads);
-    const RowRange r = row_range(p.seq_off, e.x, p.T);
-    it.a = __shfl_sync(0xffffffffu, r.a, 0);                  // the same in every lane, as the compiler now knows
-    it.len = __shfl_sync(0xffffffffu, r.b, 0) - it.a;
-    it.tok0 = __shfl_sync(0xffffffffu, e.y, 0) * 2 * p.toks;
+    auto ask = [&](uint64_t k) {
+        if (elect_one()) cp_async16_zf(&M->next[warp], p.list + entry(k), 16u);
+    };
+    const uint64_t k = place(round);
+    if (k >= (uint64_t)total) return false;
+    int4 e;
+    if (p.single) {
+        e = M->own;
+    } else {
+        if (round == 0) ask(k);
+        cp_async_wait_all();
+        __syncwarp();
+        e = M->next[warp];
+        __syncwarp();
+        if (place(round + 1) < (uint64_t)total) ask(place(round + 1));
+    }
+    it.h = (int)(k - entry(k) * (uint32_t)p.kv_heads);
+    it.a = __shfl_sync(0xffffffffu, e.x, 0);                  // the same in every lane, as the compiler now knows
+    it.len = __shfl_sync(0xffffffffu, e.y, 0);
+    it.tok0 = __shfl_sync(0xffffffffu, e.z, 0);
+    it.head = it.gap = it.lead = 0;
+    if (kWindow) {
+        const int low = it.tok0 - p.window + 1;
+        if (low > p.head) {
+            it.head = p.head;
+            it.gap = low - p.head;
+            it.lead = p.head ? 0 : p.toks / kKeys;
+        }
+    }
     auto tiles = [&](int first) {
-        return first < it.len ? (min(it.len, first + p.toks) + kKeys - 1) / kKeys : 0;
+        return first < it.len ? (min(it.len, first + p.toks) - it.gap + kKeys - 1) / kKeys : 0;
     };
     it.n0 = tiles(it.tok0);
     it.n1 = tiles(it.tok0 + p.toks);
     it.keys = min(it.len, it.tok0 + 2 * p.toks);
-    if (kWindow) {
-        const int from = max(it.tok0 - p.window + 1, 0) / kKeys;
-        const bool gap = from > p.sink_tiles;
-        it.from = gap ? from : 0;
-        it.sinks = gap ? p.sink_tiles : 0;
-        it.lead = gap && it.n1 ? max(it.tok0 + p.toks - p.window + 1, 0) / kKeys - from : 0;
-        const int less = it.from - it.sinks;
-        it.n0 -= less;
-        if (it.n1) it.n1 -= less;
-    }
     return true;
 }
 
@@ -318,8 +337,21 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
         : "memory");
 }
 
+// 32 bytes; at once where `sectors` says that they begin on a 32-byte boundary.
+__device__ __forceinline__ void store32(uint16_t* dst, const uint32_t (&v)[8], bool sectors) {
+    if (sectors) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                     "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+}
+
 struct Maps {
     CUtensorMap q, k, v;
+    CUtensorMap k_head, v_head;         // with a window: kHeadRows rows
 };
 
 template <int HD>
@@ -352,7 +384,7 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
     using C = Cfg<HD>;
     Bars* B = &M->b[kSecond];
     volatile WaitState* ab = &M->wst;
-    Item<kWindow> it;
+    Item<kWindow> it = {};
 
     if (warp == 0) {
         // ---------------- producer
@@ -360,16 +392,25 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
         uint32_t g = 0, st = 0, ph = 0, nq = 0, used = 0;     // tiles issued; the next ring place and its phase; Q's
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && __all_sync(0xffffffffu, wait_bar_here(bar, parity, ab)); };
-        auto tile = [&](const CUtensorMap* m, int j) {
-            const int t = it.key_tile(j);
+        auto tile = [&](const CUtensorMap* m, const CUtensorMap* head, int j) {
             wait(&B->empty[st], ph ^ 1u);
             if (!ok) return;
-            if (elect_one()) {
+            if (kWindow && j * kKeys < it.head && (j + 1) * kKeys > it.head) {
+                // the end of the sinks and the beginning of the window, 8 rows to a copy
+                if (elect_one()) mbar_expect_tx(&B->full[st], (uint32_t)C::kTileBytes);
+                __syncwarp();
+                if (lane < kKeys / kHeadRows) {
+#pragma unroll
+                    for (int hf = 0; hf < C::kHalves; ++hf)
+                        tma_load_3d(smem + st * C::kTileBytes + hf * C::kHalfBytes + lane * (kHeadRows * 128), head, &B->full[st],
+                                    hf * 64, it.h, it.a + it.key(j * kKeys + lane * kHeadRows), pol_kv);
+                }
+            } else if (elect_one()) {
                 mbar_expect_tx(&B->full[st], (uint32_t)C::kTileBytes);
 #pragma unroll
                 for (int hf = 0; hf < C::kHalves; ++hf)
                     tma_load_3d(smem + st * C::kTileBytes + hf * C::kHalfBytes, m, &B->full[st], hf * 64, it.h,
-                                it.a + t * kKeys, pol_kv);
+                                it.a + it.key(j * kKeys), pol_kv);
             }
             __syncwarp();
             ++g;
@@ -397,12 +438,12 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
         for (int round = 0; ok && get_item(p, M, total, round, it); ++round) {
             const int n = it.tiles();
             query(0);
-            tile(&maps.k, 0);
+            tile(&maps.k, &maps.k_head, 0);
             query(1);
 #pragma unroll 1
             for (int j = 0; ok && j < n; ++j) {
-                if (j) tile(&maps.k, j);
-                tile(&maps.v, j);
+                if (j) tile(&maps.k, &maps.k_head, j);
+                tile(&maps.v, &maps.v_head, j);
             }
         }
         // copies in flight land before the CTA may leave
@@ -578,7 +619,7 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
 #pragma unroll 1
             for (int j = it.first_cleared(kSecond); j < n; ++j) {
                 if (kWindow && !it.clears(p, j, kSecond)) continue;
-                const int key0 = it.key_tile(j) * kKeys;
+                const int key0 = it.key0(j);
                 // the issuers that use the tile have seen it arrive (its parity alone
                 // could be an earlier tile's), and the rows of the items before are stored
                 const uint32_t vi = g + 2 * j + 1, vat = vi % C::kStages;
@@ -667,32 +708,30 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
 #pragma unroll 1
                         for (int d = lane; d < HD; d += 32) {
                             const uint16_t* v = p.v + (int64_t)it.a * p.v_stride + (int64_t)it.h * HD + d;
-                            int plus = -1, minus = -1, plus_sink = 0x7FFFFFFF, minus_sink = 0x7FFFFFFF, k = 0;
+                            int plus = -1, minus = -1, plus_sink = 0x7FFFFFFF, minus_sink = 0x7FFFFFFF, at = 0;
 #pragma unroll 1
                             for (int tok = first; tok < end; ++tok) {
 #pragma unroll 1
-                                while (k <= tok) {
-                                    const int t = k / kKeys;
-                                    if (t >= it.sinks && t < it.from) {
-                                        k = it.from * kKeys;
+                                while (at < n * kKeys) {
+                                    const int k = it.key(at);
+                                    if (k > tok) break;
+                                    if (!it.clears(p, at / kKeys, true)) {
+                                        at = (at / kKeys + 1) * kKeys;
                                         continue;
                                     }
-                                    if (!it.clears_key_tile(p, t, true)) {
-                                        k = (t + 1) * kKeys;
-                                        continue;
-                                    }
+                                    const bool none = at >= p.sinks && at < it.head;      // between the sinks and the head's end
+                                    ++at;
+                                    if (none) continue;
                                     const uint32_t x = v[(int64_t)k * p.v_stride];
-                                    if ((x & 0x7F80u) == 0x7F80u) {
-                                        if ((x & 0x7Fu) || !(x & 0x8000u)) {
-                                            plus = k;
-                                            if (k < p.sinks) plus_sink = min(plus_sink, k);
-                                        }
-                                        if ((x & 0x7Fu) || (x & 0x8000u)) {
-                                            minus = k;
-                                            if (k < p.sinks) minus_sink = min(minus_sink, k);
-                                        }
+                                    if ((x & 0x7F80u) != 0x7F80u) continue;
+                                    if ((x & 0x7Fu) || !(x & 0x8000u)) {
+                                        plus = k;
+                                        if (k < p.sinks) plus_sink = min(plus_sink, k);
                                     }
-                                    ++k;
+                                    if ((x & 0x7Fu) || (x & 0x8000u)) {
+                                        minus = k;
+                                        if (k < p.sinks) minus_sink = min(minus_sink, k);
+                                    }
                                 }
                                 const int low = tok - p.window;
                                 const bool up = (plus >= 0 && plus > low) || plus_sink <= tok;
@@ -731,7 +770,7 @@ template <int HD, bool kWindow, bool kSecond>
 __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint32_t tmem, int64_t total, int warp, int lane) {
     Bars* B = &M->b[kSecond];
     volatile WaitState* ab = &M->wst;
-    Item<kWindow> it;
+    Item<kWindow> it = {};
 
     // ---------------- softmax: thread = row
     const int s = (warp - 4) >> 2, wq = warp & 3;
@@ -758,7 +797,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint32_t 
         uint64_t l2 = 0;                                     // two partial sums
         for (int j = j0; ok && j < n; ++j) {
             if (!wait(&B->s_full[s], ns++ & 1u)) break;
-            const int key0 = it.key_tile(j) * kKeys;
+            const int key0 = it.key0(j);
             float x[128];
 #pragma unroll
             for (int q = 0; q < 4; ++q) tmem_ld32_async(tS + q * 32, x + q * 32);
@@ -776,8 +815,8 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint32_t 
                     if (i > lim) x[i] = hidden;
             }
             // nor the keys before its window and behind the sinks
-            if (kWindow && key0 < first + p.toks - p.window && key0 + kKeys > p.sinks) {
-                const int low = tok - p.window - key0, sink = p.sinks - key0;
+            if (kWindow && key0 < first + p.toks - p.window && (j + 1) * kKeys > p.sinks) {
+                const int low = tok - p.window - key0, sink = p.sinks - j * kKeys;
 #pragma unroll
                 for (int i = 0; i < 128; ++i)
                     if (i <= low && i >= sink) x[i] = hidden;
@@ -841,27 +880,36 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint32_t 
         const float l = a + b, inv = 1.f / l;
         const bool valid = row < p.toks * p.group && tok < it.len;
         const size_t at = (size_t)(it.a + tok) * p.heads + (size_t)it.h * p.group + rg;
+        // the accumulator is read at once and free for the next item before its rows
+        // are stored (but warp 3 mends stored rows)
+        float o[HD];
+#pragma unroll
+        for (int q = 0; q < HD / 32; ++q) tmem_ld32_async(tO + q * 32, o + q * 32);
+        tmem_ready(o);
+#pragma unroll
+        for (int q = 1; q < HD / 32; ++q) tmem_pin(o + q * 32);
+        tc_fence_before();
+        if (!kSecond) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B->o_free[s]);
+        }
         uint32_t most = 0;                                   // bits of the row's largest magnitudes, a NaN's above all
 #pragma unroll
         for (int q = 0; q < HD / 16; ++q) {
-            float o[16];
-            tmem_ldn<16>(tO + q * 16, o);
             uint32_t pk[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * i] * inv, o[2 * i + 1] * inv);
+                const __nv_bfloat162 h = __floats2bfloat162_rn(o[q * 16 + 2 * i] * inv, o[q * 16 + 2 * i + 1] * inv);
                 pk[i] = reinterpret_cast<const uint32_t&>(h);
                 most = __vmaxu2(most, pk[i] & 0x7FFF7FFFu);
             }
-            if (valid) {
-                uint4* dst = reinterpret_cast<uint4*>(p.out + at * HD + q * 16);
-                dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-            }
+            // a whole sector per lane and store, where out allows it
+            if (valid) store32(p.out + at * HD + q * 16, pk, p.sectors);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&B->o_free[s]);
+        if (kSecond) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B->o_free[s]);
+        }
         if (valid && p.lse) p.lse[at] = (ref + log2f(l)) * kLn2;
         if (__any_sync(0xffffffffu, valid && max(most & 0xFFFFu, most >> 16) >= 0x7F80u)) M->again = 1u;
     }
@@ -914,7 +962,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             int64_t count;
             const int2 e = entry_of(p, blockIdx.x / p.kv_heads, count);
             if (lane == 0) {
-                M->own = e;
+                const RowRange r = row_range(p.seq_off, e.x, p.T);
+                M->own = make_int4(r.a, r.b - r.a, e.y * 2 * p.toks, 0);
                 M->entries = (int)min(count, (int64_t)p.most);
             }
         }
@@ -941,6 +990,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         softmax_role<HD, kWindow, false>(p, M, tmem, total, warp, lane);
         if (again()) softmax_role<HD, kWindow, true>(p, M, tmem, total, warp, lane);
     }
+    cp_async_wait_all();                                      // an entry asked for before a wait ran out
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && M->wst.abort) raise_status(p.ws, kStatTimeout);
@@ -957,7 +1007,7 @@ cudaError_t launch(const Maps& maps, const Params& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (!p.single) {
         prof_begin(kPAttnPromptPlan, s);
-        e = launch_kernel(attn_prompt_plan, dim3(1), dim3(kPlanThreads), 0, s, false, p, const_cast<int2*>(p.list),
+        e = launch_kernel(attn_prompt_plan, dim3(1), dim3(kPlanThreads), 0, s, false, p, const_cast<int4*>(p.list),
                           const_cast<int*>(p.count));
         prof_end(s);
         if (e != cudaSuccess) return e;
@@ -976,7 +1026,7 @@ int tile_tokens(int group) { return kRows / group; }
 static size_t list_entries(int B, int T, int group) { return (size_t)T / (2 * tile_tokens(group)) + (size_t)B; }
 
 size_t attn_prompt_workspace_bytes(int B, int T, int n_heads, int n_kv_heads, int) {
-    return sizeof(WsHeader) + 256 + align_up(list_entries(B, T, n_heads / n_kv_heads) * sizeof(int2), 256);
+    return sizeof(WsHeader) + 256 + align_up(list_entries(B, T, n_heads / n_kv_heads) * sizeof(int4), 256);
 }
 
 cudaError_t launch_attn_prompt(const PromptArgs& a, cudaStream_t s) {
@@ -984,8 +1034,9 @@ cudaError_t launch_attn_prompt(const PromptArgs& a, cudaStream_t s) {
     Params p = {};
     p.seq_off = a.seq_off;
     p.count = reinterpret_cast<const int*>(w);
-    p.list = reinterpret_cast<const int2*>(w + 256);
+    p.list = reinterpret_cast<const int4*>(w + 256);
     p.out = static_cast<uint16_t*>(a.out);
+    p.sectors = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
     p.lse = a.lse;
     p.ws = a.ws;
     p.B = a.B;
@@ -1002,7 +1053,7 @@ cudaError_t launch_attn_prompt(const PromptArgs& a, cudaStream_t s) {
     // hidden keys are infinite before the scale: at scale 0 the smallest normal
     // number keeps them so, and every finite score still counts as 0
     p.scale2 = a.scale == 0.f ? FLT_MIN : a.scale * kLog2e;
-    Maps maps;
+    Maps maps = {};
     auto map = [&](CUtensorMap* m, const void* base, int heads, int64_t stride, cuuint32_t b1, cuuint32_t b2) {
         const cuuint64_t dims[3] = {(cuuint64_t)a.head_dim, (cuuint64_t)heads, (cuuint64_t)a.T};
         const cuuint64_t str[2] = {(cuuint64_t)a.head_dim * 2, (cuuint64_t)stride * 2};
@@ -1016,7 +1067,10 @@ cudaError_t launch_attn_prompt(const PromptArgs& a, cudaStream_t s) {
     if (a.window > 0 && a.window < a.T) {
         p.window = a.window;
         p.sinks = a.sinks < a.T ? a.sinks : a.T;
-        p.sink_tiles = (int)(((int64_t)p.sinks + kKeys - 1) / kKeys);
+        p.head = (int)std::min(((int64_t)p.sinks + kHeadRows - 1) / kHeadRows * kHeadRows, (int64_t)0x7FFFFFFF);
+        if (!map(&maps.k_head, a.k, a.n_kv_heads, a.k_stride, 1, kHeadRows) ||
+            !map(&maps.v_head, a.v, a.n_kv_heads, a.v_stride, 1, kHeadRows))
+            return cudaErrorInvalidValue;
         p.v = static_cast<const uint16_t*>(a.v);
         p.v_stride = a.v_stride;
         return a.head_dim == 64 ? launch<64, true>(maps, p, s) : launch<128, true>(maps, p, s);
