@@ -42,6 +42,7 @@
 // cost 18 %: its instructions cost more than the pipe it relieves.)
 #include <algorithm>
 #include <cfloat>
+#include <type_traits>
 
 #include <cuda.h>
 
@@ -209,17 +210,14 @@ struct Item {
     __device__ __forceinline__ int key(int v) const { return kWindow && v >= head ? v + gap : v; }
     // what tile j's first row would stand for as a key if its last row's key decides
     __device__ __forceinline__ int key0(int j) const { return key(j * kKeys + kKeys - 1) - (kKeys - 1); }
-    // V tiles to clear: with rows past the item's keys, or, the second time, with a
-    // key that some row of the item does not see
-    __device__ __forceinline__ bool clears(const Params& p, int j, bool second) const {
-        const int k = key0(j);
-        if (!second) return k + kKeys > keys;
-        if (k + kKeys > tok0 + 1 || j + 1 == tiles()) return true;
-        return kWindow && k < keys - p.window && (j + 1) * kKeys > p.sinks;
+    // V tiles to clear: from this one on, those with rows past the item's keys, or,
+    // the second time, with a key that some row of the item does not see
+    __device__ __forceinline__ int edge(bool second) const {
+        return second ? min((tok0 + 1 - gap) / kKeys, tiles() - 1) : (keys - gap) / kKeys;
     }
-    // no tile before this one is cleared
-    __device__ __forceinline__ int first_cleared(bool second) const {
-        return kWindow ? 0 : (second ? min((tok0 + 1) / kKeys, tiles() - 1) : keys / kKeys);
+    // (with a window, the second time, also some of those before)
+    __device__ __forceinline__ bool clears(const Params& p, int j, bool second) const {
+        return j >= edge(second) || (kWindow && second && key0(j) < keys - p.window && (j + 1) * kKeys > p.sinks);
     }
 };
 
@@ -553,7 +551,7 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
                     }
                 }
                 if (!wait(&B->full[vat], vph)) break;
-                const bool fix = kWindow ? it.clears(p, j, kSecond) : j >= it.first_cleared(kSecond);
+                const bool fix = it.clears(p, j, kSecond);
                 if (j < it.n(s)) {
                     // warp 3 starts while P is still being made
                     if (fix && lane == 0) mbar_arrive(&B->asked[s]);
@@ -617,8 +615,8 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
             const int n = it.tiles();
             uint32_t add = 0;                                 // row tiles that the table matters to, by bit
 #pragma unroll 1
-            for (int j = it.first_cleared(kSecond); j < n; ++j) {
-                if (kWindow && !it.clears(p, j, kSecond)) continue;
+            for (int j = kWindow && kSecond ? 0 : it.edge(kSecond); j < n; ++j) {
+                if (kWindow && kSecond && !it.clears(p, j, kSecond)) continue;
                 const int key0 = it.key0(j);
                 // the issuers that use the tile have seen it arrive (its parity alone
                 // could be an earlier tile's), and the rows of the items before are stored
@@ -795,9 +793,9 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint32_t 
         const int first = it.tok0 + s * p.toks;
         float ref = kFloorRef;
         uint64_t l2 = 0;                                     // two partial sums
-        for (int j = j0; ok && j < n; ++j) {
-            if (!wait(&B->s_full[s], ns++ & 1u)) break;
-            const int key0 = it.key0(j);
+        auto tile = [&](int j, auto masked) {
+            constexpr bool kMasked = decltype(masked)::value;
+            if (!wait(&B->s_full[s], ns++ & 1u)) return false;
             float x[128];
 #pragma unroll
             for (int q = 0; q < 4; ++q) tmem_ld32_async(tS + q * 32, x + q * 32);
@@ -808,18 +806,23 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint32_t 
             __syncwarp();
             if (lane == 0) mbar_arrive(&B->s_read[s]);
             const float hidden = c < 0.f ? INFINITY : -INFINITY;
-            if (key0 + kKeys - 1 > first) {                  // a row of the tile does not see all keys
-                const int lim = tok - key0;
+            if (!kWindow && (j + 1) * kKeys - 1 > first) {   // a row of the tile does not see all keys
+                const int lim = tok - j * kKeys;
 #pragma unroll
                 for (int i = 0; i < 128; ++i)
                     if (i > lim) x[i] = hidden;
             }
-            // nor the keys before its window and behind the sinks
-            if (kWindow && key0 < first + p.toks - p.window && (j + 1) * kKeys > p.sinks) {
-                const int low = tok - p.window - key0, sink = p.sinks - j * kKeys;
+            if constexpr (kMasked) {
+                // neither the keys behind it nor, but for the sinks, those before its window
+                const int key0 = it.key0(j), sees = tok - key0 + 1, low = sees - p.window, sink = p.sinks - j * kKeys;
+                auto first_bits = [](int n) { return n <= 0 ? 0u : 0xFFFFFFFFu >> (32 - min(n, 32)); };
 #pragma unroll
-                for (int i = 0; i < 128; ++i)
-                    if (i <= low && i >= sink) x[i] = hidden;
+                for (int q = 0; q < 128; q += 32) {
+                    const uint32_t seen = first_bits(sees - q) & (~first_bits(low - q) | first_bits(sink - q));
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (!((seen >> i) & 1u)) x[q + i] = hidden;
+                }
             }
             // the row's largest score (a negative scale makes it the smallest product)
             float mx[4] = {x[0], x[1], x[2], x[3]};
@@ -840,7 +843,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint32_t 
                 unpack2(l2, a, b);
                 l2 = pack2(a * f, b * f);
                 if (j > j0) {
-                    if (!wait(&B->pv_done[s], (npv - 1u) & 1u)) break;
+                    if (!wait(&B->pv_done[s], (npv - 1u) & 1u)) return false;
 #pragma unroll
                     for (int q = 0; q < HD / 16; ++q) {
                         float o[16];
@@ -873,6 +876,28 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint32_t 
                 if (lane == 0) mbar_arrive(&B->p_full[s][hf]);
             }
             ++npv;
+            return true;
+        };
+        if constexpr (kWindow) {
+            // Whole sinks' tiles, those that some window begins in or behind, whole ones,
+            // the diagonal's: with the tests in one loop for all (in registers, or as
+            // a pass over the scores in tensor memory) the whole ones took 15 % longer.
+            const int full = max((first + 1 - it.gap) / kKeys, 0);                          // from here on: the diagonal
+            const int clean[2] = {min(min(p.sinks / kKeys, full), n), min(full, n)};
+            const int ends[2] = {min(max((first + p.toks - p.window - it.gap + kKeys - 1) / kKeys, 0), n), n};
+            int j = j0;
+#pragma unroll 1
+            for (int part = 0; ok && part < 2; ++part) {
+#pragma unroll 1
+                for (const int to = part ? clean[1] : clean[0]; ok && j < to; ++j)
+                    if (!tile(j, std::false_type{})) break;
+#pragma unroll 1
+                for (const int to = part ? ends[1] : ends[0]; ok && j < to; ++j)
+                    if (!tile(j, std::true_type{})) break;
+            }
+        } else {
+            for (int j = j0; ok && j < n; ++j)
+                if (!tile(j, std::false_type{})) break;
         }
         if (!ok || !wait(&B->pv_done[s], (npv - 1u) & 1u)) break;
         float a, b;
