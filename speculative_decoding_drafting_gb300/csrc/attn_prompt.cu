@@ -896,7 +896,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint32_t 
                     if (!tile(j, std::true_type{})) break;
             }
         } else {
-            for (int j = j0; ok && j < n; ++j)
+            for (int j = 0; ok && j < n; ++j)
                 if (!tile(j, std::false_type{})) break;
         }
         if (!ok || !wait(&B->pv_done[s], (npv - 1u) & 1u)) break;
