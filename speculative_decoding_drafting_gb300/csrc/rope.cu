@@ -11,11 +11,18 @@
 //
 // Bound by the bytes: each value is read and written once.  Lanes hold 8 values
 // of a head, 4 and the 4 that they are turned with, so that neither a shuffle
-// nor a second load is needed; 16 lanes share a head of 128 (8 one of 64).  A
-// warp takes a token, works out its angles once (each lane 4 / (32 / lanes of a
-// head) of the 4 that it needs) and goes through the token's heads, 8 vectors of
-// 32 lanes at a time, all of their loads in flight before the first is used.
-// With few tokens several warps share one.
+// nor a second load is needed; 16 lanes share a head of 128 (8 one of 64).  A CTA
+// takes up to 4 tokens together: their requests and places are looked up by the
+// lanes of one warp, their angles worked out by all threads, once for all heads,
+// and kept in shared memory.  Then each warp goes through tasks of 4 vectors of 32
+// lanes, in packed float32 arithmetic; the other warps of the SM cover its loads.
+// Measured (GB300, against 6.68 TB/s of a plain copy): 23457 tokens of 28 + 4 heads
+// of 128, three axes, no norm, 63 us, 6.1 TB/s; 41925 tokens of 32 + 8 + 8 heads with
+// norms into an e4m3 cache, the keys also as rows, 189 us, 5.5 TB/s; into a bf16 one
+// 182 to 188 us, 5.9 to 6.1 TB/s.  (A warp per token, with its own look-up and angles,
+// 8 vectors at a time and one value per instruction: 75, 190 and 187, and 91 for 76
+// with norms.  A float32 value per instruction in the present form: 87 with norms, 209
+// into e4m3.)
 #include <algorithm>
 #include <cmath>
 
@@ -29,7 +36,8 @@ namespace dspark {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kVecs = 8;               // vectors of a chunk: 8 of q's or k's heads, or 4 of k's and 4 of v's
+constexpr int kVecs = 4;               // vectors of a task: of q's or k's heads, or 2 of k's and 2 of v's
+constexpr int kToks = 4;               // tokens of a CTA at most (8: 68 us for 64)
 constexpr float kTiny = 0x1p-100f;
 
 enum Mode : int { kRows = 0, kAppendBf16 = 1, kAppendE4m3 = 2 };
@@ -46,7 +54,7 @@ struct RopeParams {
     const int32_t* positions;          // null: the token's place in its request
     int n_axes, rot;
     float amplitude;
-    int T, parts;                      // warps of a token
+    int T, toks;                       // toks: tokens of a CTA
     // the cache
     uint8_t* dst[2];
     float* scale[2];
@@ -92,7 +100,6 @@ struct Place {
     static constexpr int kHeads = 32 / kLanes;                // heads of a vector
     int part, sub, o0, o1;
     bool turns;
-    float c[4], s[4];
 
     __device__ __forceinline__ Place(int lane, int rot) : part(lane % kLanes), sub(lane / kLanes) {
         const int n = rot / 8;                                // lanes that turn
@@ -114,53 +121,76 @@ struct Place {
             w[0] = a.x, w[1] = a.y, w[2] = b.x, w[3] = b.y;
         }
     }
-    // the first and second values of the four pairs
-    __device__ __forceinline__ static void split(const uint32_t (&w)[4], float (&a)[4], float (&b)[4]) {
-        if (kPairs) {
+    // The pairs' first and second values, two and two (one instruction for both).
+    __device__ __forceinline__ static void split(const uint32_t (&w)[4], uint64_t (&a)[2], uint64_t (&b)[2]) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) a[e] = lo16(w[e]), b[e] = hi16(w[e]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                a[2 * e] = lo16(w[e]), a[2 * e + 1] = hi16(w[e]);
-                b[2 * e] = lo16(w[2 + e]), b[2 * e + 1] = hi16(w[2 + e]);
+        for (int e = 0; e < 2; ++e) {
+            if (kPairs) {
+                a[e] = pack2(lo16(w[2 * e]), lo16(w[2 * e + 1]));
+                b[e] = pack2(hi16(w[2 * e]), hi16(w[2 * e + 1]));
+            } else {
+                a[e] = pack2(lo16(w[e]), hi16(w[e]));
+                b[e] = pack2(lo16(w[2 + e]), hi16(w[2 + e]));
             }
         }
     }
-    // a head's values times r and the weights (first and second of the pairs), turned
-    __device__ __forceinline__ void turn(const uint32_t (&w)[4], bool norm, float r, const float (&wa)[4], const float (&wb)[4],
-                                         float (&a)[4], float (&b)[4]) const {
+    __device__ __forceinline__ static float squares(const uint32_t (&w)[4]) {
+        uint64_t a[2], b[2];
         split(w, a, b);
-        if (norm) {
+        float x, y;
+        unpack2(fma2(b[1], b[1], fma2(b[0], b[0], fma2(a[1], a[1], mul2x(a[0], a[0])))), x, y);
+        return x + y;
+    }
+    // a head's values times r and the weights
+    __device__ __forceinline__ static void norm(uint64_t (&a)[2], uint64_t (&b)[2], float r, const uint64_t (&wa)[2],
+                                                const uint64_t (&wb)[2]) {
+        const uint64_t r2 = pack2(r, r);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) a[e] *= r * wa[e], b[e] *= r * wb[e];
+        for (int e = 0; e < 2; ++e) a[e] = mul2x(a[e], mul2x(r2, wa[e])), b[e] = mul2x(b[e], mul2x(r2, wb[e]));
+    }
+    // turned by the cosines, sines and negative sines of the lane's four angles
+    __device__ __forceinline__ void turn(uint64_t (&a)[2], uint64_t (&b)[2], const uint64_t (&c)[2], const uint64_t (&s)[2],
+                                         const uint64_t (&minus_s)[2]) const {
+        if (!turns) return;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint64_t x = a[e], y = b[e];
+            a[e] = fma2(x, c[e], mul2x(y, minus_s[e]));
+            b[e] = fma2(y, c[e], mul2x(x, s[e]));
         }
-        if (turns) {
+    }
+    // as float32 in the order of the row: o0 .. o0 + 3, then o1 .. o1 + 3
+    __device__ __forceinline__ static void in_order(const uint64_t (&a)[2], const uint64_t (&b)[2], float (&x)[8]) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float x = a[e], y = b[e];
-                a[e] = fmaf(x, c[e], -(y * s[e]));
-                b[e] = fmaf(y, c[e], x * s[e]);
+        for (int e = 0; e < 2; ++e) {
+            if (kPairs) {
+                unpack2(a[e], x[4 * e], x[4 * e + 2]);
+                unpack2(b[e], x[4 * e + 1], x[4 * e + 3]);
+            } else {
+                unpack2(a[e], x[2 * e], x[2 * e + 1]);
+                unpack2(b[e], x[4 + 2 * e], x[5 + 2 * e]);
             }
         }
     }
-    __device__ __forceinline__ void store(uint16_t* row, const float (&a)[4], const float (&b)[4]) const {
-        if (kPairs)
-            *reinterpret_cast<uint4*>(row + o0) =
-                make_uint4(two_bf16(a[0], b[0]), two_bf16(a[1], b[1]), two_bf16(a[2], b[2]), two_bf16(a[3], b[3]));
-        else {
-            *reinterpret_cast<uint2*>(row + o0) = make_uint2(two_bf16(a[0], a[1]), two_bf16(a[2], a[3]));
-            *reinterpret_cast<uint2*>(row + o1) = make_uint2(two_bf16(b[0], b[1]), two_bf16(b[2], b[3]));
+    __device__ __forceinline__ void store(uint16_t* row, const uint64_t (&a)[2], const uint64_t (&b)[2]) const {
+        float x[8];
+        in_order(a, b, x);
+        const uint2 u = make_uint2(two_bf16(x[0], x[1]), two_bf16(x[2], x[3])), v = make_uint2(two_bf16(x[4], x[5]), two_bf16(x[6], x[7]));
+        if (kPairs) {
+            *reinterpret_cast<uint4*>(row + o0) = make_uint4(u.x, u.y, v.x, v.y);
+        } else {
+            *reinterpret_cast<uint2*>(row + o0) = u;
+            *reinterpret_cast<uint2*>(row + o1) = v;
         }
     }
-    __device__ __forceinline__ void weights(const void* w, int dtype, float (&a)[4], float (&b)[4]) const {
+    __device__ __forceinline__ void weights(const void* w, int dtype, uint64_t (&a)[2], uint64_t (&b)[2]) const {
         if (dtype == DSPARK_F32) {
             const float4 u = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + o0));
             const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + o1));
-            if (kPairs)
-                a[0] = u.x, b[0] = u.y, a[1] = u.z, b[1] = u.w, a[2] = v.x, b[2] = v.y, a[3] = v.z, b[3] = v.w;
-            else
-                a[0] = u.x, a[1] = u.y, a[2] = u.z, a[3] = u.w, b[0] = v.x, b[1] = v.y, b[2] = v.z, b[3] = v.w;
+            a[0] = kPairs ? pack2(u.x, u.z) : pack2(u.x, u.y);
+            a[1] = kPairs ? pack2(v.x, v.z) : pack2(u.z, u.w);
+            b[0] = kPairs ? pack2(u.y, u.w) : pack2(v.x, v.y);
+            b[1] = kPairs ? pack2(v.y, v.w) : pack2(v.z, v.w);
         } else {
             const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(w) + o0));
             const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(w) + o1));
@@ -170,232 +200,256 @@ struct Place {
     }
 };
 
+// What a CTA knows of one of its tokens.
+struct Token {
+    int64_t row;                       // of head 0 in the cache, in units of a head's rows (negative: no place)
+    int pos;                           // place in its request
+    int in;                            // whether it belongs to one
+};
+
+// The tokens [t0, t0 + n) (n <= kToks) by one warp, a lane for each.
+__device__ __forceinline__ void look_up(const RopeParams& p, int t0, int n, Token* out) {
+    const int lane = threadIdx.x & 31, t = t0 + min(lane, n - 1);
+    const int64_t most = (int64_t)p.max_pages << p.page_log2;
+    // the first token's request, and how many begin up to each of the others
+    const int r0 = find_request(p.q_off, p.R, t0);
+    const int begins = r0 + 1 + lane < p.R ? __ldg(p.q_off + r0 + 1 + lane) : 0x7FFFFFFF;
+    int r = r0;
+#pragma unroll 1
+    for (int i = 1; i < n; ++i) {
+        const uint32_t m = __ballot_sync(0xffffffffu, begins <= t0 + i);
+        // all 32 have begun: many of them empty
+        const int ri = m == 0xFFFFFFFFu ? find_request(p.q_off, p.R, t0 + i) : r0 + __popc(m);
+        if (lane == i) r = ri;
+    }
+    if (lane >= n) return;
+    const RowRange rows = row_range(p.q_off, r, p.T);
+    Token k;
+    k.in = t >= rows.a && t < rows.b;
+    k.pos = clamped_len(p.kv_len, r, most) - (rows.b - t);
+    k.row = -1;
+    if (k.in && k.pos >= 0 && p.heads[1] > 0) {
+        const int page = __ldg(p.page_table + (size_t)r * p.max_pages + (k.pos >> p.page_log2));
+        if (page >= 0 && page < p.n_pages)
+            k.row = (((int64_t)page * p.heads[1]) << p.page_log2) + (k.pos & ((1 << p.page_log2) - 1));
+        else
+            raise_status(p.ws, kStatBadPage);
+    }
+    out[lane] = k;
+}
+
 template <int HD, bool kPairs, int MODE>
 __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const __grid_constant__ RopeParams p) {
     using P = Place<HD, kPairs>;
-    constexpr int kLanes = P::kLanes, kHeads = P::kHeads;
-    constexpr int kOwn = 4 / kHeads;                          // angles that a lane works out
-    const int lane = threadIdx.x & 31;
-    P at(lane, p.rot);
-    const int64_t most = (int64_t)p.max_pages << p.page_log2;
-    if (MODE != kRows && blockIdx.x == gridDim.x - 1) check_requests(p.q_off, p.kv_len, p.R, p.T, most, p.ws);
+    constexpr int kLanes = P::kLanes, kHeads = P::kHeads, kHalf = HD / 2;
+    constexpr int kStep = kVecs * kHeads;                     // heads of a task
+    // whether the next task's loads are issued before this one's work: it takes
+    // registers, and pays where there is much of it (41925 tokens into an e4m3 cache 195
+    // -> 189 us; rows with a norm 70 -> 74, without one 63 -> 64)
+    constexpr bool kAhead = MODE == kAppendE4m3;
+    __shared__ __align__(16) float cosines[kToks][kHalf], sines[kToks][kHalf];
+    __shared__ Token tokens[kToks];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const P at(lane, p.rot);
+    if (MODE != kRows && blockIdx.x == gridDim.x - 1)
+        check_requests(p.q_off, p.kv_len, p.R, p.T, (int64_t)p.max_pages << p.page_log2, p.ws);
 
-    uint64_t turn[kOwn];
-    int axis[kOwn];
+    const int t0 = blockIdx.x * p.toks, n = min(p.toks, p.T - t0);
+    // a token's tasks: heads of q, then heads of k, or 2 vectors of k's heads and 2 of v's
+    constexpr int kKvStep = MODE == kRows ? kStep : kStep / 2;
+    const int first_kv = (p.heads[0] + kStep - 1) / kStep, per = first_kv + (p.heads[1] + kKvStep - 1) / kKvStep;
+    // task c's vectors of token i (heads that are not there are not loaded: their lanes
+    // work on what the registers hold and store nothing)
+    auto load = [&](int i, int c, uint32_t (&w)[kVecs][4]) {
+        const int64_t t = t0 + i;
+        const bool kv = c >= first_kv;
+        const int h0 = kv ? (c - first_kv) * kKvStep : c * kStep, heads = kv ? p.heads[1] : p.heads[0];
+        const uint16_t* row = (kv ? p.src[1] + t * p.src_stride[1] : p.src[0] + t * p.src_stride[0]) + (h0 + at.sub) * HD;
+        const uint16_t* vrow = MODE == kRows ? nullptr : p.src[2] + t * p.src_stride[2] + (h0 + at.sub) * HD + at.part * 8;
 #pragma unroll
-    for (int e = 0; e < kOwn; ++e) {
-        const int f = at.part * 4 + at.sub * kOwn + e;
-        turn[e] = p.turn[f];
-        axis[e] = p.axis[f];
+        for (int v = 0; v < kVecs; ++v) {
+            if (MODE != kRows && kv && v >= kVecs / 2) {
+                if (h0 + (v - kVecs / 2) * kHeads + at.sub >= heads) continue;
+                const uint4 x = __ldcs(reinterpret_cast<const uint4*>(vrow + (v - kVecs / 2) * (kHeads * HD)));
+                w[v][0] = x.x, w[v][1] = x.y, w[v][2] = x.z, w[v][3] = x.w;
+            } else if (h0 + v * kHeads + at.sub < heads) {
+                at.load(row + v * (kHeads * HD), w[v]);
+            }
+        }
+    };
+    // where a warp is: token i of the CTA, task c of it
+    int i = 0, c = warp;
+    auto settle = [&]() {
+        while (c >= per) c -= per, ++i;
+    };
+    settle();
+    uint32_t w[kVecs][4];
+    if (i < n) load(i, c, w);
+
+    // the tokens' places and angles, while the first loads are in flight
+    if (MODE != kRows) {
+        if (warp == 0) look_up(p, t0, n, tokens);
+        __syncthreads();
     }
-    const int q_chunks = (p.heads[0] + kVecs * kHeads - 1) / (kVecs * kHeads);
-    const int kv_step = (MODE == kRows ? kVecs : kVecs / 2) * kHeads;
-    const int chunks = q_chunks + (p.heads[1] + kv_step - 1) / kv_step;
-
-    const int64_t warps = (int64_t)gridDim.x * kWarps;
-    for (int64_t task = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); task < (int64_t)p.T * p.parts; task += warps) {
-        const int t = p.parts == 1 ? (int)task : (int)((uint32_t)task / (uint32_t)p.parts);
-        bool known = false, in = true;
-        int64_t slot_row = -1;                                // row of head 0 in the cache (in units of heads' rows)
-        // the token's request, place and angles, while the first chunk's loads are in flight
-        auto look = [&]() {
-            known = true;
-            int pos = 0;
-            if (MODE != kRows) {
-                const int r = find_request(p.q_off, p.R, t);
-                const RowRange rows = row_range(p.q_off, r, p.T);
-                in = t >= rows.a && t < rows.b;
-                if (!in) return;
-                pos = clamped_len(p.kv_len, r, most) - (rows.b - t);
-                if (pos >= 0 && p.heads[1] > 0) {
-                    const int page = __ldg(p.page_table + (size_t)r * p.max_pages + (pos >> p.page_log2));
-                    if (page >= 0 && page < p.n_pages)
-                        slot_row = (((int64_t)page * p.heads[1]) << p.page_log2) + (pos & ((1 << p.page_log2) - 1));
-                    else if (lane == 0)
-                        raise_status(p.ws, kStatBadPage);
-                }
+    if (p.rot > 0) {
+        const int f = threadIdx.x % kHalf;
+        const uint64_t turn = p.turn[f];
+        const int axis = p.axis[f];
+        if (f < p.rot / 2) {
+            for (int k = threadIdx.x / kHalf; k < n; k += kWarps * 32 / kHalf) {
+                const int x = p.positions ? __ldg(p.positions + (int64_t)(t0 + k) * p.n_axes + axis)
+                                          : (MODE == kRows ? 0 : tokens[k].pos);
+                const int part = (int)((turn * (uint64_t)(int64_t)x) >> 32);               // of a turn, in 2^-32
+                float cs, sn;
+                sincospif((float)part * 0x1p-31f, &sn, &cs);
+                cosines[k][f] = cs * p.amplitude;
+                sines[k][f] = sn * p.amplitude;
             }
-            if (p.rot == 0) return;
-            float cs[kOwn], sn[kOwn];
-#pragma unroll
-            for (int e = 0; e < kOwn; ++e) {
-                const int x = p.positions ? __ldg(p.positions + (size_t)t * p.n_axes + axis[e]) : pos;
-                const int f = (int)((turn[e] * (uint64_t)(int64_t)x) >> 32);             // in 2^-32 turns
-                sincospif((float)f * 0x1p-31f, &sn[e], &cs[e]);
-                sn[e] *= p.amplitude;
-                cs[e] *= p.amplitude;
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                at.c[e] = __shfl_sync(0xffffffffu, cs[e % kOwn], e / kOwn * kLanes + at.part);
-                at.s[e] = __shfl_sync(0xffffffffu, sn[e % kOwn], e / kOwn * kLanes + at.part);
-            }
-        };
-        auto sum = [](float a, float b) { return a + b; };
+        }
+        __syncthreads();
+    }
+    auto sum = [](float a, float b) { return a + b; };
 #pragma unroll 1
-        for (int c = p.parts == 1 ? 0 : (int)((uint32_t)task % (uint32_t)p.parts); c < chunks; c += p.parts) {
-            float wa[4], wb[4];
-            if (MODE == kRows || c < q_chunks) {
-                // ---------------- 8 vectors of q's heads (or of k's, without a cache)
-                const int which = MODE == kRows && c >= q_chunks ? 1 : 0;
-                const int h0 = (which ? c - q_chunks : c) * kVecs * kHeads + at.sub, heads = p.heads[which];
-                const uint16_t* src = p.src[which] + (int64_t)t * p.src_stride[which];
-                const bool norm = p.w[which] != nullptr;
-                uint32_t w[kVecs][4];
+    while (i < n) {
+        const int ti = i, tc = c;
+        const int64_t t = t0 + ti;
+        c += kWarps;
+        settle();
+        uint32_t next[kVecs][4];
+        if (kAhead && i < n) load(i, c, next);
+        uint64_t cs[2], sn[2], minus_sn[2];
+        if (at.turns) {
+            const float4 x = *reinterpret_cast<const float4*>(&cosines[ti][at.part * 4]), y = *reinterpret_cast<const float4*>(&sines[ti][at.part * 4]);
+            cs[0] = pack2(x.x, x.y), cs[1] = pack2(x.z, x.w);
+            sn[0] = pack2(y.x, y.y), sn[1] = pack2(y.z, y.w);
+            minus_sn[0] = pack2(-y.x, -y.y), minus_sn[1] = pack2(-y.z, -y.w);
+        }
+        const bool in = MODE == kRows || tokens[ti].in;
+        const bool kv = tc >= first_kv;
+        const void* weights = kv ? p.w[1] : p.w[0];
+        uint64_t wa[2], wb[2];
+        if (weights) at.weights(weights, p.w_dtype, wa, wb);
+        if (in && (MODE == kRows || !kv)) {
+            // ---------------- heads of q (or of k, without a cache)
+            const int h0 = (kv ? tc - first_kv : tc) * kStep, heads = kv ? p.heads[1] : p.heads[0];
+            float r = 1.f;
+            if (weights) {
+                float sq[kVecs];
 #pragma unroll
-                for (int i = 0; i < kVecs; ++i) {
-                    w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0u;
-                    if (h0 + i * kHeads < heads) at.load(src + (int64_t)(h0 + i * kHeads) * HD, w[i]);
-                }
-                if (norm) at.weights(p.w[which], p.w_dtype, wa, wb);
-                if (!known) look();
-                if (!in) break;
-                float r = 1.f;
-                if (norm) {
-                    float sq[kVecs];
+                for (int v = 0; v < kVecs; ++v) sq[v] = P::squares(w[v]);
+                r = __frsqrt_rn(fmaf(join_rows<kVecs, kLanes>(sq, at.part, sum), 1.f / HD, p.eps));
+            }
+            uint16_t* row = (kv ? p.out[1] + t * p.out_stride[1] : p.out[0] + t * p.out_stride[0]) + (h0 + at.sub) * HD;
 #pragma unroll
-                    for (int i = 0; i < kVecs; ++i) {
-                        float a[4], b[4];
-                        P::split(w[i], a, b);
-                        sq[i] = 0.f;
+            for (int v = 0; v < kVecs; ++v) {
+                if (h0 + v * kHeads >= heads) break;
+                uint64_t a[2], b[2];
+                P::split(w[v], a, b);
+                if (weights) P::norm(a, b, __shfl_sync(0xffffffffu, r, at.sub * kLanes + v * (kLanes / kVecs)), wa, wb);
+                at.turn(a, b, cs, sn, minus_sn);
+                if (h0 + v * kHeads + at.sub < heads) at.store(row + v * (kHeads * HD), a, b);
+            }
+        } else if (in) {
+            // ---------------- heads of k and v, into the cache
+            constexpr int N = kVecs / 2;
+            const int h0 = (tc - first_kv) * kKvStep + at.sub, heads = p.heads[1];
+            const int64_t slot = tokens[ti].row;
+            uint64_t a[N][2], b[N][2];
+            float r = 1.f;
+            if (weights) {
+                float sq[N];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) sq[i] = fmaf(b[e], b[e], fmaf(a[e], a[e], sq[i]));
-                    }
-                    r = __frsqrt_rn(fmaf(join_rows<kVecs, kLanes>(sq, at.part, sum), 1.f / HD, p.eps));
-                }
-                uint16_t* out = p.out[which] + (int64_t)t * p.out_stride[which];
+                for (int v = 0; v < N; ++v) sq[v] = P::squares(w[v]);
+                r = __frsqrt_rn(fmaf(join_rows<N, kLanes>(sq, at.part, sum), 1.f / HD, p.eps));
+            }
 #pragma unroll
-                for (int i = 0; i < kVecs; ++i) {
-                    float a[4], b[4];
-                    const float ri = norm ? __shfl_sync(0xffffffffu, r, at.sub * kLanes + i * (kLanes / kVecs)) : 1.f;
-                    at.turn(w[i], norm, ri, wa, wb, a, b);
-                    if (h0 + i * kHeads < heads) at.store(out + (int64_t)(h0 + i * kHeads) * HD, a, b);
-                }
-            } else {
-                // ---------------- 4 vectors of k's heads and of v's, into the cache
-                constexpr int N = kVecs / 2;
-                const int h0 = (c - q_chunks) * N * kHeads + at.sub, heads = p.heads[1];
-                const uint16_t* ks = p.src[1] + (int64_t)t * p.src_stride[1];
-                const uint16_t* vs = p.src[2] + (int64_t)t * p.src_stride[2];
-                const bool norm = p.w[1] != nullptr;
-                uint32_t w[N][4];
-                uint4 v[N];
+            for (int v = 0; v < N; ++v) {
+                P::split(w[v], a[v], b[v]);
+                if (weights) P::norm(a[v], b[v], __shfl_sync(0xffffffffu, r, at.sub * kLanes + v * (kLanes / N)), wa, wb);
+                at.turn(a[v], b[v], cs, sn, minus_sn);
+                if (p.out[1] && h0 + v * kHeads < heads)
+                    at.store(p.out[1] + t * p.out_stride[1] + (h0 + v * kHeads) * HD, a[v], b[v]);
+            }
+            if (slot >= 0 && MODE == kAppendBf16) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const int h = h0 + i * kHeads;
-                    w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0u;
-                    v[i] = make_uint4(0u, 0u, 0u, 0u);
+                for (int v = 0; v < N; ++v) {
+                    const int h = h0 + v * kHeads;
                     if (h >= heads) continue;
-                    at.load(ks + (int64_t)h * HD, w[i]);
-                    v[i] = __ldcs(reinterpret_cast<const uint4*>(vs + (int64_t)h * HD + at.part * 8));
+                    const int64_t row = (slot + ((int64_t)h << p.page_log2)) * HD;
+                    at.store(reinterpret_cast<uint16_t*>(p.dst[0]) + row, a[v], b[v]);
+                    *reinterpret_cast<uint4*>(p.dst[1] + (row + at.part * 8) * 2) = make_uint4(w[N + v][0], w[N + v][1], w[N + v][2], w[N + v][3]);
                 }
-                if (norm) at.weights(p.w[1], p.w_dtype, wa, wb);
-                if (!known) look();
-                if (!in) break;
-                float r = 1.f;
-                if (norm) {
-                    float sq[N];
+            }
+            if (slot >= 0 && MODE == kAppendE4m3) {
+                // the rows' largest magnitudes (as bits, which order a NaN above
+                // infinity), one scale and one reciprocal per row
+                float m[kVecs], x[N][8];
 #pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        float a[4], b[4];
-                        P::split(w[i], a, b);
-                        sq[i] = 0.f;
+                for (int v = 0; v < N; ++v) {
+                    P::in_order(a[v], b[v], x[v]);
+                    uint32_t most = 0u, y = 0u;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) sq[i] = fmaf(b[e], b[e], fmaf(a[e], a[e], sq[i]));
-                    }
-                    r = __frsqrt_rn(fmaf(join_rows<N, kLanes>(sq, at.part, sum), 1.f / HD, p.eps));
+                    for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(x[v][e]) & 0x7FFFFFFFu);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y = __vmaxu2(y, w[N + v][e] & 0x7FFF7FFFu);
+                    m[v] = __uint_as_float(most);
+                    m[N + v] = __uint_as_float(max(y & 0xFFFFu, y >> 16) << 16);
                 }
-                float a[N][4], b[N][4];
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const float ri = norm ? __shfl_sync(0xffffffffu, r, at.sub * kLanes + i * (kLanes / N)) : 1.f;
-                    at.turn(w[i], norm, ri, wa, wb, a[i], b[i]);
-                    if (p.out[1] && h0 + i * kHeads < heads)
-                        at.store(p.out[1] + (int64_t)t * p.out_stride[1] + (int64_t)(h0 + i * kHeads) * HD, a[i], b[i]);
+                const float big = join_rows<kVecs, kLanes>(m, at.part, [](float x, float y) {
+                    return __uint_as_float(max(__float_as_uint(x), __float_as_uint(y)));
+                });
+                float inv = 0.f;
+                {
+                    constexpr int kOwn = kLanes / kVecs;      // lanes that hold a row's largest
+                    const int v = at.part / kOwn, kv = v / N, h = h0 + v % N * kHeads;
+                    if (at.part % kOwn == 0 && h < heads) p.scale[kv][slot + ((int64_t)h << p.page_log2)] = __fdiv_rn(big, 448.f);
+                    // below 2^-100 the reciprocal would overflow float32: such rows (a
+                    // negative sign marks them) are scaled up by 2^64 first; rows that are
+                    // zero or not finite get codes of zero
+                    if (big > 0.f && big < INFINITY)
+                        inv = big < kTiny ? -__fdiv_rn(448.f, big * 0x1p64f) : __fdiv_rn(448.f, big);
                 }
-                if (slot_row < 0) continue;
-                if (MODE == kAppendBf16) {
+                const bool as_given = !weights && p.rot == 0;    // k as it came: its midpoints count, as v's do
 #pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        const int h = h0 + i * kHeads;
-                        if (h >= heads) continue;
-                        const int64_t row = slot_row + ((int64_t)h << p.page_log2);
-                        at.store(reinterpret_cast<uint16_t*>(p.dst[0]) + row * HD, a[i], b[i]);
-                        *reinterpret_cast<uint4*>(p.dst[1] + (row * HD + at.part * 8) * 2) = v[i];
-                    }
-                } else {
-                    // the rows' largest magnitudes (as bits, which order a NaN above
-                    // infinity), one scale and one reciprocal per row
-                    float m[kVecs];
+                for (int v = 0; v < kVecs; ++v) {
+                    const int h = h0 + v % N * kHeads;
+                    const float f = __shfl_sync(0xffffffffu, inv, at.sub * kLanes + v * (kLanes / kVecs));
+                    const float up = f < 0.f ? 0x1p64f : 1.f;
+                    const uint64_t up2 = pack2(up, up), f2 = pack2(fabsf(f), fabsf(f));
+                    if (h >= heads) continue;
+                    const int64_t row = (slot + ((int64_t)h << p.page_log2)) * HD;
+                    if (v >= N) {
+                        uint32_t q[4];
 #pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        uint32_t x = 0u, y = 0u;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            x = max(x, max(__float_as_uint(a[i][e]) & 0x7FFFFFFFu, __float_as_uint(b[i][e]) & 0x7FFFFFFFu));
-                            const uint32_t u = e == 0 ? v[i].x : (e == 1 ? v[i].y : (e == 2 ? v[i].z : v[i].w));
-                            y = __vmaxu2(y, u & 0x7FFF7FFFu);
-                        }
-                        m[i] = __uint_as_float(x);
-                        m[N + i] = __uint_as_float(max(y & 0xFFFFu, y >> 16) << 16);
-                    }
-                    const float big = join_rows<kVecs, kLanes>(m, at.part, [](float x, float y) {
-                        return __uint_as_float(max(__float_as_uint(x), __float_as_uint(y)));
-                    });
-                    float inv = 0.f;
-                    {
-                        const int i = at.part / (kLanes / kVecs), kv = i / N, h = h0 + (i % N) * kHeads;
-                        if (at.part % (kLanes / kVecs) == 0 && h < heads)
-                            p.scale[kv][slot_row + ((int64_t)h << p.page_log2)] = __fdiv_rn(big, 448.f);
-                        // below 2^-100 the reciprocal would overflow float32: such rows (a
-                        // negative sign marks them) are scaled up by 2^64 first; rows that are
-                        // zero or not finite get codes of zero
-                        if (big > 0.f && big < INFINITY)
-                            inv = big < kTiny ? -__fdiv_rn(448.f, big * 0x1p64f) : __fdiv_rn(448.f, big);
-                    }
-                    const bool as_given = !norm && p.rot == 0;   // k as it came: its midpoints count, as v's do
-#pragma unroll
-                    for (int i = 0; i < kVecs; ++i) {
-                        const int h = h0 + (i % N) * kHeads;
-                        const float f = __shfl_sync(0xffffffffu, inv, at.sub * kLanes + i * (kLanes / kVecs));
-                        const float up = f < 0.f ? 0x1p64f : 1.f;
-                        const uint64_t up2 = pack2(up, up), f2 = pack2(fabsf(f), fabsf(f));
-                        if (h >= heads) continue;
-                        const int64_t row = (slot_row + ((int64_t)h << p.page_log2)) * HD;
-                        if (i >= N) {
-                            const uint32_t in4[4] = {v[i % N].x, v[i % N].y, v[i % N].z, v[i % N].w};
-                            uint32_t q[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) q[e] = quantise2(mul2x(pack2(lo16(in4[e]), hi16(in4[e])), up2), f2);
-                            uint2 code = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
-                            if (f == 0.f) code = make_uint2(0u, 0u);
-                            *reinterpret_cast<uint2*>(p.dst[1] + row + at.part * 8) = code;
-                        } else {
-                            // float32 values: their quotient is rounded to e4m3 as it stands
-                            float (&x)[4] = a[i];
-                            float (&y)[4] = b[i];
-                            auto two = [&](float g, float h2) {
-                                const uint64_t u = mul2x(pack2(g, h2), up2);
-                                if (as_given) return quantise2(u, f2);
-                                float2 z;
-                                unpack2(mul2x(u, f2), z.x, z.y);
-                                return (uint32_t)__nv_cvt_float2_to_fp8x2(z, __NV_SATFINITE, __NV_E4M3);
-                            };
-                            uint32_t c0, c1;
-                            if (kPairs) {
-                                c0 = two(x[0], y[0]) | two(x[1], y[1]) << 16;
-                                c1 = two(x[2], y[2]) | two(x[3], y[3]) << 16;
-                            } else {
-                                c0 = two(x[0], x[1]) | two(x[2], x[3]) << 16;
-                                c1 = two(y[0], y[1]) | two(y[2], y[3]) << 16;
-                            }
-                            if (f == 0.f) c0 = c1 = 0u;
-                            *reinterpret_cast<uint32_t*>(p.dst[0] + row + at.o0) = c0;
-                            *reinterpret_cast<uint32_t*>(p.dst[0] + row + at.o1) = c1;
-                        }
+                        for (int e = 0; e < 4; ++e) q[e] = quantise2(mul2x(pack2(lo16(w[v][e]), hi16(w[v][e])), up2), f2);
+                        uint2 code = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+                        if (f == 0.f) code = make_uint2(0u, 0u);
+                        *reinterpret_cast<uint2*>(p.dst[1] + row + at.part * 8) = code;
+                    } else {
+                        // float32 values: their quotient is rounded to e4m3 as it stands
+                        auto two = [&](float g, float h2) {
+                            const uint64_t u = mul2x(pack2(g, h2), up2);
+                            if (as_given) return quantise2(u, f2);
+                            float2 z;
+                            unpack2(mul2x(u, f2), z.x, z.y);
+                            return (uint32_t)__nv_cvt_float2_to_fp8x2(z, __NV_SATFINITE, __NV_E4M3);
+                        };
+                        const float (&y)[8] = x[v % N];
+                        uint32_t c0 = two(y[0], y[1]) | two(y[2], y[3]) << 16, c1 = two(y[4], y[5]) | two(y[6], y[7]) << 16;
+                        if (f == 0.f) c0 = c1 = 0u;
+                        *reinterpret_cast<uint32_t*>(p.dst[0] + row + at.o0) = c0;
+                        *reinterpret_cast<uint32_t*>(p.dst[0] + row + at.o1) = c1;
                     }
                 }
             }
+        }
+        if (kAhead) {
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[v][e] = next[v][e];
+        } else if (i < n) {
+            load(i, c, w);
         }
     }
 }
@@ -405,7 +459,7 @@ __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const __grid_constant
 uint64_t turns_of(double inv_freq) {
     double x = std::fabs(inv_freq) / 6.283185307179586476925;
     x -= std::floor(x);                                       // exact
-    const uint64_t n = (uint64_t)std::ldexp(x, 64);
+    const uint64_t n = (uint64_t)(x * 0x1p64);
     return inv_freq < 0 ? 0 - n : n;
 }
 
@@ -467,15 +521,10 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
         p.n_pages = c.n_pages;
         p.page_log2 = ceil_log2_i(c.page);
     }
-    // A warp per token where that fills the device; with fewer tokens their chunks
-    // are spread over more warps, which work the angles out again.
-    const int heads = 256 / a.head_dim;                       // heads of a vector
-    const int kv_step = (mode == kRows ? kVecs : kVecs / 2) * heads;
-    const int chunks = (a.n_heads + kVecs * heads - 1) / (kVecs * heads) + (a.n_kv_heads + kv_step - 1) / kv_step;
-    const int64_t full = (int64_t)num_sms() * 16;
-    p.parts = (int)std::min((int64_t)chunks, std::max((int64_t)1, full / a.T));
-    const int64_t ctas = ((int64_t)a.T * p.parts + kWarps - 1) / kWarps;
-    const int grid = (int)std::min(ctas, (int64_t)num_sms() * 16);
+    // Tokens share a CTA where there are enough of them to fill the device (about 6
+    // CTAs an SM) all the same.
+    p.toks = (int)std::min((int64_t)kToks, std::max((int64_t)1, (int64_t)a.T / (num_sms() * 6)));
+    const int grid = (a.T - 1) / p.toks + 1;
     const int name = mode == kRows ? kPQkRope : kPRopeWrite;
     prof_begin(name, s);
     cudaError_t e;
