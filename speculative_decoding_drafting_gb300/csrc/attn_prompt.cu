@@ -42,6 +42,7 @@
 // cost 18 %: its instructions cost more than the pipe it relieves.)
 #include <algorithm>
 #include <cfloat>
+#include <cmath>
 #include <type_traits>
 
 #include <cuda.h>
@@ -82,6 +83,11 @@ struct Bars {
     // of its reader.  Either ended in a wait that ran out, with many sequences of
     // a few tiles.)
     uint64_t asked[2], fixed[8];
+    // A row tile's result lies in its ring place: by place as well, since the softmax
+    // may be through the next item's before warp 3 has looked at this one's.
+    uint64_t staged[8];
+    // A row tile's exponentials of a tile that both go over are made: the other's turn.
+    uint64_t turn[2];
     uint64_t done;
 };
 
@@ -123,7 +129,8 @@ struct Params {
     int window, sinks, head;
     const uint16_t* v;
     int64_t v_stride;
-    float scale2;                       // scale log2(e)
+    float scale2;                       // |scale| log2(e)
+    int negate;                         // a negative scale: the products are negated
 };
 
 // Pairs of row tiles of a sequence.
@@ -205,6 +212,10 @@ struct Item {
     int head, gap, lead;                // with a window; lead: tiles that row tile 1 sees nothing of
     __device__ __forceinline__ int n(int s) const { return s ? n1 : n0; }
     __device__ __forceinline__ int tiles() const { return max(n0, n1); }
+    // Places of the ring that the item takes: K and V of its tiles, and the first time
+    // one for each row tile's result (the tiles are equally large).
+    __device__ __forceinline__ int results(bool second) const { return second ? 0 : (n1 ? 2 : 1); }
+    __device__ __forceinline__ uint32_t places(bool second) const { return (uint32_t)(2 * tiles() + results(second)); }
     // row tile s goes over tiles begin(s) to n(s)
     __device__ __forceinline__ int begin(int s) const { return kWindow && s && n1 ? lead : 0; }
     __device__ __forceinline__ int key(int v) const { return kWindow && v >= head ? v + gap : v; }
@@ -350,6 +361,7 @@ __device__ __forceinline__ void store32(uint16_t* dst, const uint32_t (&v)[8], b
 struct Maps {
     CUtensorMap q, k, v;
     CUtensorMap k_head, v_head;         // with a window: kHeadRows rows
+    CUtensorMap out;
 };
 
 template <int HD>
@@ -359,6 +371,7 @@ __device__ __forceinline__ void init_bars(Bars* B) {
         mbar_init(&B->full[i], 1);
         mbar_init(&B->empty[i], 2);
         mbar_init(&B->fixed[i], 1);
+        mbar_init(&B->staged[i], 4);
     }
     for (int s = 0; s < 2; ++s) {
         mbar_init(&B->q_full[s], 1);
@@ -368,6 +381,7 @@ __device__ __forceinline__ void init_bars(Bars* B) {
         mbar_init(&B->p_full[s][0], 4);
         mbar_init(&B->p_full[s][1], 4);
         mbar_init(&B->asked[s], 1);
+        mbar_init(&B->turn[s], 4);
         mbar_init(&B->pv_done[s], 1);
         mbar_init(&B->o_free[s], 4);
     }
@@ -443,6 +457,19 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
                 if (j) tile(&maps.k, &maps.k_head, j);
                 tile(&maps.v, &maps.v_head, j);
             }
+            // places for the results
+#pragma unroll 1
+            for (int s = 0; ok && s < it.results(kSecond); ++s) {
+                wait(&B->empty[st], ph ^ 1u);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive(&B->full[st]);
+                __syncwarp();
+                ++g;
+                if (++st == C::kStages) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            }
         }
         // copies in flight land before the CTA may leave
         if (ab->abort && lane == 0) {
@@ -455,7 +482,8 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
     } else if (warp < 3) {
         // ---------------- MMA issuer of row tile s
         const int s = warp - 1;
-        constexpr uint32_t id_qk = idesc_bf16_f32(128, 64, false, false);
+        // (a negative scale: bit 13 negates Q)
+        const uint32_t id_qk = idesc_bf16_f32(128, 64, false, false) | (uint32_t)p.negate << 13;
         constexpr uint32_t id_pv = idesc_bf16_f32(128, HD, false, true);
         // descriptors of Q and of the first ring tile; others lie a constant number
         // of 16-byte units on (addresses stay inside the 14-bit field)
@@ -591,6 +619,8 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
                     if (lane == 0) mbar_arrive(&B->empty[kat]);
                 }
             }
+#pragma unroll 1
+            for (int i = 0; i < it.results(kSecond); ++i) next();
         }
         // the tensor core is idle before its memory is given back
         if (elect_one()) {
@@ -602,6 +632,7 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
         // ---------------- clear the last V tiles
         uint32_t g = 0;                                       // ring tiles before this item
         uint32_t asked = 0, stored = 0;                       // parity of each row tile's next request and store, by bit
+        uint32_t laid = 0;                                    // of each ring place's next result
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             ok = ok && __all_sync(0xffffffffu, wait_bar_here(bar, parity, ab));
@@ -692,7 +723,27 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&B->fixed[vat]);
             }
-            g += 2 * n;
+            // the results go from their ring places to out, but for those of a sequence's end
+#pragma unroll 1
+            for (int s = 0; s < it.results(kSecond); ++s) {
+                const uint32_t at = (g + 2 * n + s) % C::kStages;
+                if (!wait(&B->staged[at], (laid >> at) & 1u)) break;
+                laid ^= 1u << at;
+                if (lane == 0) {
+                    const int first = it.tok0 + s * p.toks;
+                    if (first + p.toks <= it.len) {
+#pragma unroll
+                        for (int hf = 0; hf < C::kHalves; ++hf)
+                            tma_store_3d(&maps.out, smem + at * C::kTileBytes + hf * C::kHalfBytes, hf * 64, it.h * p.group, it.a + first);
+                        tma_store_commit();
+                        tma_store_wait_read();
+                    }
+                    mbar_arrive(&B->empty[at]);
+                    mbar_arrive(&B->empty[at]);
+                }
+                __syncwarp();
+            }
+            g += it.places(kSecond);
             // what was taken out of V goes to the rows that see it, once they are
             // stored (the next item's cannot be before this warp has cleared its tiles)
 #pragma unroll 1
@@ -760,12 +811,18 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
                 if (it.n(s)) stored ^= 1u << s;
             }
         }
+        // what the second time stores comes after
+        if (!kSecond) {
+            if (lane == 0) tma_store_wait();
+            __syncwarp();
+        }
     }
 }
 
 // One time over the CTA's items: the softmax warps.
 template <int HD, bool kWindow, bool kSecond>
-__device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint32_t tmem, int64_t total, int warp, int lane) {
+__device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint8_t* smem, uint32_t tmem, int64_t total, int warp, int lane) {
+    using C = Cfg<HD>;
     Bars* B = &M->b[kSecond];
     volatile WaitState* ab = &M->wst;
     Item<kWindow> it = {};
@@ -779,7 +836,18 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint32_t 
     const int rt = row / p.group, rg = row - rt * p.group;   // token and head of the row inside its tile
     const float c = p.scale2;
     const uint64_t c2 = pack2(c, c);
-    uint32_t ns = 0, npv = 0;
+    uint32_t ns = 0, npv = 0, g = 0;                         // g: ring places before this item
+    // The two row tiles take turns at the exponentials of the tiles that both go over,
+    // row tile 0 first, so that one's run beside the other's products.  Left alone they
+    // settled in step or out of step as small changes of the code would have it: both
+    // at the exponentials at once, 12001 tokens took 893 us, out of step 780, and in
+    // turns they take 730 (head_dim 64: 693, 661, 610; 30001 tokens, window 4096: 1441,
+    // 1360, 1257).
+    uint32_t nt = 0;                                         // such tiles so far
+    auto in_turns = [&](int j) { return j >= it.begin(1) && j < min(it.n0, it.n1); };
+    auto hand_over = [&](int j) {
+        if (in_turns(j) && lane == 0) mbar_arrive(&B->turn[1 - s]);
+    };
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         ok = __all_sync(0xffffffffu, wait_bar_here(bar, parity, ab));
@@ -788,6 +856,8 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint32_t 
     };
     for (int round = 0; ok && get_item(p, M, total, round, it); ++round) {
         const int n = it.n(s), j0 = it.begin(s);
+        const uint32_t mine = g + (uint32_t)(2 * it.tiles() + s);   // the ring place for the result
+        g += it.places(kSecond);
         if (!n) continue;
         const int tok = it.tok0 + s * p.toks + rt;           // sees keys 0 .. tok
         const int first = it.tok0 + s * p.toks;
@@ -805,12 +875,11 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint32_t 
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&B->s_read[s]);
-            const float hidden = c < 0.f ? INFINITY : -INFINITY;
             if (!kWindow && (j + 1) * kKeys - 1 > first) {   // a row of the tile does not see all keys
                 const int lim = tok - j * kKeys;
 #pragma unroll
                 for (int i = 0; i < 128; ++i)
-                    if (i > lim) x[i] = hidden;
+                    if (i > lim) x[i] = -INFINITY;
             }
             if constexpr (kMasked) {
                 // neither the keys behind it nor, but for the sinks, those before its window
@@ -821,20 +890,14 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint32_t 
                     const uint32_t seen = first_bits(sees - q) & (~first_bits(low - q) | first_bits(sink - q));
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if (!((seen >> i) & 1u)) x[q + i] = hidden;
+                        if (!((seen >> i) & 1u)) x[q + i] = -INFINITY;
                 }
             }
-            // the row's largest score (a negative scale makes it the smallest product)
+            // the row's largest score
             float mx[4] = {x[0], x[1], x[2], x[3]};
-            if (c >= 0.f) {
 #pragma unroll
-                for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
-            } else {
-#pragma unroll
-                for (int i = 4; i < 128; ++i) mx[i & 3] = fminf(mx[i & 3], x[i]);
-            }
-            const float top = c >= 0.f ? fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c
-                                       : fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3])) * c;
+            for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
             if (__any_sync(0xffffffffu, top > ref + kLazy)) {
                 // each row by its own scores alone: the others' do not reach its bits
                 const float m = top > ref + kLazy ? top : ref, f = ex2_approx(ref - m);
@@ -855,6 +918,10 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint32_t 
                 }
             }
             const uint64_t r2 = pack2(-ref, -ref);
+            if (in_turns(j)) {
+                if ((s || nt) && !wait(&B->turn[s], (s ? nt : nt - 1u) & 1u)) return false;
+                ++nt;
+            }
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 uint32_t pk[32];
@@ -869,11 +936,18 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint32_t 
                     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
                     pk[i] = reinterpret_cast<const uint32_t&>(h);
                 }
+                // (with a window before the weights are stored: window 1024 445 -> 435 us,
+                // but 12001 tokens without one 730 -> 742)
+                if (kWindow && hf) {
+                    __syncwarp();
+                    hand_over(j);
+                }
                 tmem_st32(tS + hf * 32, pk);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&B->p_full[s][hf]);
+                if (!kWindow && hf) hand_over(j);
             }
             ++npv;
             return true;
@@ -918,6 +992,13 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint32_t 
             __syncwarp();
             if (lane == 0) mbar_arrive(&B->o_free[s]);
         }
+        // A whole row tile goes to out by way of a ring place: rows lie 32 to an
+        // instruction, one per lane, and stored as they are took 5000 cycles of the 16000
+        // to 40000 of an item.  The last one of a sequence must not touch the rows
+        // behind it; and what is mended is stored as it is.
+        const bool direct = kSecond || first + p.toks > it.len;
+        uint8_t* stage = smem + mine % C::kStages * C::kTileBytes;
+        if (!kSecond && !wait(&B->full[mine % C::kStages], mine / C::kStages & 1u)) break;
         uint32_t most = 0;                                   // bits of the row's largest magnitudes, a NaN's above all
 #pragma unroll
         for (int q = 0; q < HD / 16; ++q) {
@@ -928,8 +1009,20 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint32_t 
                 pk[i] = reinterpret_cast<const uint32_t&>(h);
                 most = __vmaxu2(most, pk[i] & 0x7FFF7FFFu);
             }
-            // a whole sector per lane and store, where out allows it
-            if (valid) store32(p.out + at * HD + q * 16, pk, p.sectors);
+            if (!direct) {
+                uint8_t* to = stage + (q / 4) * C::kHalfBytes + row * 128;
+                const int c0 = q % 4 * 2;
+                *reinterpret_cast<uint4*>(to + ((c0 ^ row) & 7) * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                *reinterpret_cast<uint4*>(to + (((c0 + 1) ^ row) & 7) * 16) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+            } else if (valid) {
+                // a whole sector per lane and store, where out allows it
+                store32(p.out + at * HD + q * 16, pk, p.sectors);
+            }
+        }
+        if (!kSecond) {
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B->staged[mine % C::kStages]);
         }
         if (kSecond) {
             __syncwarp();
@@ -961,6 +1054,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tmap(&maps.q);
         prefetch_tmap(&maps.k);
         prefetch_tmap(&maps.v);
+        prefetch_tmap(&maps.out);
     }
     if (warp == 1) tmem_alloc(&M->tmem, 512);
     // rows of Q that no token of an item fills are zeros (these for the whole
@@ -1012,8 +1106,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (again()) few_roles<HD, kWindow, true>(maps, p, M, smem, tmem, total, warp, lane);
     } else {
         regs_raise<200>();
-        softmax_role<HD, kWindow, false>(p, M, tmem, total, warp, lane);
-        if (again()) softmax_role<HD, kWindow, true>(p, M, tmem, total, warp, lane);
+        softmax_role<HD, kWindow, false>(p, M, smem, tmem, total, warp, lane);
+        if (again()) softmax_role<HD, kWindow, true>(p, M, smem, tmem, total, warp, lane);
     }
     cp_async_wait_all();                                      // an entry asked for before a wait ran out
     tc_fence_before();
@@ -1077,7 +1171,8 @@ cudaError_t launch_attn_prompt(const PromptArgs& a, cudaStream_t s) {
     p.single = (int64_t)p.most * p.kv_heads <= num_sms();
     // hidden keys are infinite before the scale: at scale 0 the smallest normal
     // number keeps them so, and every finite score still counts as 0
-    p.scale2 = a.scale == 0.f ? FLT_MIN : a.scale * kLog2e;
+    p.scale2 = a.scale == 0.f ? FLT_MIN : std::fabs(a.scale) * kLog2e;
+    p.negate = a.scale < 0.f;
     Maps maps = {};
     auto map = [&](CUtensorMap* m, const void* base, int heads, int64_t stride, cuuint32_t b1, cuuint32_t b2) {
         const cuuint64_t dims[3] = {(cuuint64_t)a.head_dim, (cuuint64_t)heads, (cuuint64_t)a.T};
@@ -1085,6 +1180,7 @@ cudaError_t launch_attn_prompt(const PromptArgs& a, cudaStream_t s) {
         const cuuint32_t box[3] = {64, b1, b2};
         return make_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
     };
+    if (!map(&maps.out, a.out, a.n_heads, (int64_t)a.n_heads * a.head_dim, (cuuint32_t)p.group, (cuuint32_t)p.toks)) return cudaErrorInvalidValue;
     if (!map(&maps.q, a.q, a.n_heads, a.q_stride, (cuuint32_t)p.group, (cuuint32_t)p.toks) ||
         !map(&maps.k, a.k, a.n_kv_heads, a.k_stride, 1, kKeys) || !map(&maps.v, a.v, a.n_kv_heads, a.v_stride, 1, kKeys))
         return cudaErrorInvalidValue;
