@@ -213,6 +213,7 @@ struct PagedParams {
     JoinDesc* desc;                    // [grid]
     float* part;                       // [grid][2] pieces: m [kRowTile], l [kRowTile], O [kRowTile][HD]
     int max_pages, n_pages, page_log2, heads;
+    int blocks;                        // not one new token to each request
     float scale2;                      // scale log2(e)
 };
 
@@ -1315,12 +1316,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             // caches 146 and 138; without the one for 8, e4m3 decoding 115.4 and 113.5.
             // (bf16 has no loop for 24: such items are bound by the cache's bytes, and
             // one shape more cost blocks of 1 to 17 tokens 4 %.)
-            // (e4m3 with a window: one loop takes any number.  Its code is longer, and with
-            // a loop per number two SMs beside each other, which fetch from one cache, ran
-            // out of it whenever their items had different rows: 128 requests, window
-            // 4096, blocks of 1 and 6 in turn 294 -> 246 us, of 6 alone 251 -> 248.  Over bf16
-            // it is the slower: 256 requests, window 1024, one token 134 -> 150.)
-            if constexpr (kWindow && F8)
+            // (With a window and blocks of tokens, which may differ, one loop takes any
+            // number: the code is longer, and with a loop per number two SMs beside each
+            // other, which fetch from one cache, ran out of it whenever their items had
+            // different rows.  128 requests, e4m3, window 4096, blocks of 1 and 6 in turn 294
+            // -> 246 us; of 1 to 9 over bf16, 64 heads of 64, window 1000, 120 -> 107.  For
+            // single tokens, of equal rows, it is the slower: 256 requests, window 1024, 200
+            // -> 238 us over e4m3, 129 -> 166 over bf16 of 64.)
+            if (kWindow && p.blocks)
                 soft_segment<HD, F8, kWindow, 0>(p, s, M, smem, tmem, u, st);
             else if (s.rows <= 8)
                 soft_segment<HD, F8, kWindow, 8>(p, s, M, smem, tmem, u, st);
@@ -1463,6 +1466,7 @@ cudaError_t launch_attn_paged(const void* q, int64_t q_stride, const dspark_kv_c
     p.n_pages = c.n_pages;
     p.page_log2 = ceil_log2_i(c.page);
     p.heads = n_heads;
+    p.blocks = b.T != b.R;
     p.scale2 = scale * kLog2e;
     // a page's planes of all heads are one run of n_kv_heads * page rows; the
     // page is a dimension of its own, so coordinates stay small and an id past
