@@ -449,6 +449,7 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
         if (kWindow && edge)
             hidden = hidden_columns(coff, key, sg.keys, sg.q.kv_len - sg.q.q_len + sg.tok, p.plan.window, p.plan.sinks, p.plan.group,
                                     sg.head);
+        const bool some_hidden = kWindow && !F8 && __any_sync(0xffffffffu, hidden != 0u);      // among the warp's keys
         const uint32_t turn = sh.turn_at(sg, i);
         wait_bar(&M->b.s_full[turn][u], (st.phases >> turn) & 1u, ab);
         st.phases ^= 1u << turn;
@@ -508,7 +509,7 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
                     y = fma2(y, mul2, pack2(r.x, r.y));
                     unpack2(y, t[c0 + c], t[c0 + c + 1]);
                 }
-                if (!(kWindow && F8) && edge) {
+                if (!(kWindow && F8) && (kWindow ? some_hidden : edge)) {
 #pragma unroll
                     for (int c = 0; c < kB; ++c)
                         if (kWindow ? (hidden >> (c0 + c)) & 1u : c0 + c < seen) t[c0 + c] = -INFINITY;
