@@ -681,7 +681,8 @@ typedef struct {
  *             They may be q and k themselves, with the same strides; otherwise
  *             nothing of inputs and outputs may overlap.
  * All of float32 up to one rounding per value.  q, k, q_out and k_out are
- * 16-byte aligned device memory of the current device.  head_dim 64 or 128,
+ * 16-byte aligned device memory of the current device, as are positions and the
+ * norm's weights.  head_dim 64 or 128,
  * n_heads in [1, 2^19], n_kv_heads in [0, 4096], T >= 0 (SHAPE; T = 0 returns OK
  * at once).  No workspace.
  */

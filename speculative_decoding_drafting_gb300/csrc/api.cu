@@ -505,6 +505,12 @@ static int check_norm(const dspark_head_norm_t* n) {
     return DSPARK_OK;
 }
 
+// What both calls read besides their rows.
+static bool turns_on_device(const dspark_rope_t* rope, const dspark_head_norm_t* norm, const int32_t* positions) {
+    if (rope && positions && !on_current_device(positions)) return false;
+    return !norm || ((!norm->q_w || on_current_device(norm->q_w)) && (!norm->k_w || on_current_device(norm->k_w)));
+}
+
 static bool rows_ok(const void* p, int64_t stride, int heads, int dim) {
     return p && aligned16(p) && stride_ok(stride, heads, dim);
 }
@@ -524,7 +530,7 @@ int dspark_qk_rope(const void* q, const void* k, int64_t q_stride, int64_t k_str
     if (n_kv_heads > 0 && (!rows_ok(k, k_stride, n_kv_heads, head_dim) || !rows_ok(k_out, k_out_stride, n_kv_heads, head_dim)))
         return DSPARK_ERR_INVALID_ARG;
     if (!on_current_device(q) || !on_current_device(q_out) ||
-        (n_kv_heads > 0 && (!on_current_device(k) || !on_current_device(k_out))))
+        (n_kv_heads > 0 && (!on_current_device(k) || !on_current_device(k_out))) || !turns_on_device(rope, norm, positions))
         return DSPARK_ERR_INVALID_ARG;
     RopeArgs a = {};
     a.q = q; a.k = k; a.q_stride = q_stride; a.k_stride = k_stride;
@@ -556,7 +562,8 @@ int dspark_rope_write(const dspark_kv_cache_t* cache, const dspark_kv_batch_t* b
     if (k_out && !rows_ok(k_out, k_out_stride, hk, dim)) return DSPARK_ERR_INVALID_ARG;
     if (!ws || !aligned256(ws) || ws_bytes < sizeof(WsHeader)) return DSPARK_ERR_WORKSPACE;
     if (!cache_on_device(cache) || !on_current_device(K) || !on_current_device(V) ||
-        (n_heads > 0 && (!on_current_device(q) || !on_current_device(q_out))) || (k_out && !on_current_device(k_out)))
+        (n_heads > 0 && (!on_current_device(q) || !on_current_device(q_out))) || (k_out && !on_current_device(k_out)) ||
+        !turns_on_device(rope, norm, positions))
         return DSPARK_ERR_INVALID_ARG;
     RopeArgs a = {};
     a.q = q; a.k = K; a.v = V; a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;

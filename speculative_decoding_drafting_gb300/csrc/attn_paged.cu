@@ -986,7 +986,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) return;
         const bool valid = lane_tok < c.keys - c.tok;
         // a page that no row of the item sees is not read, whatever its id
-        const int first = c.win.key(c.tok + lane_tok);
+        const int first = c.win.key(valid ? c.tok + lane_tok : 0);
         const bool unseen = kWindow && first >= p.plan.sinks && first + bp <= c.win.low;
         if (valid && unseen) {
             id = p.n_pages;

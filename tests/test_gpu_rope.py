@@ -428,15 +428,21 @@ def test_rows_that_are_not_device_memory_are_refused():
     def at(name, moved):
         return (host if name == moved else dev)[name].data_ptr()
 
+    places = [pos, torch.zeros(3, dtype=torch.int32).pin_memory()]
+    weights = [torch.ones(dim, device=DEV), torch.ones(dim).pin_memory()]
+
+    def norm(m):
+        return ctypes.byref(binding._HeadNorm(weights[m == "wq"].data_ptr(), weights[m == "wk"].data_ptr(), 0, EPS))
+
     def write(m):
-        return L.dspark_rope_write(c, b, at("q", m), at("K", m), at("V", m), 256, 128, 128, heads, None, rope._ref, None,
-                                   at("qo", m), at("ko", m), 256, 128, ws.data_ptr(), 256, None)
+        return L.dspark_rope_write(c, b, at("q", m), at("K", m), at("V", m), 256, 128, 128, heads, places[m == "pos"].data_ptr(),
+                                   rope._ref, norm(m), at("qo", m), at("ko", m), 256, 128, ws.data_ptr(), 256, None)
 
     def turn(m):
-        return L.dspark_qk_rope(at("q", m), at("K", m), 256, 128, pos.data_ptr(), T, heads, hk, dim, rope._ref, None,
-                                at("qo", m), at("ko", m), 256, 128, None)
+        return L.dspark_qk_rope(at("q", m), at("K", m), 256, 128, places[m == "pos"].data_ptr(), T, heads, hk, dim, rope._ref,
+                                norm(m), at("qo", m), at("ko", m), 256, 128, None)
 
-    for call, names in ((write, "q K V qo ko"), (turn, "q K qo ko")):
+    for call, names in ((write, "q K V qo ko pos wq wk"), (turn, "q K qo ko pos wq wk")):
         assert call(None) == 0
         for name in names.split():
             assert call(name) == -1, name
