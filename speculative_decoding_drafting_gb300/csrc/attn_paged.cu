@@ -62,6 +62,14 @@
 // Keys a row must not see get weight 0 by selection, not by multiplication;
 // V rows past the item's last key are zeroed in shared memory, since 0 times
 // a stale NaN would be NaN.
+//
+// With a window (kWindow) an item's tiles are cut from its visible pages (the
+// sinks' and the window's, attn_plan.h), hidden pages inside a tile are not read,
+// and V rows that no row of the item sees are zeroed like those past its end.
+// Measured: 256 requests of 200 to 12000 keys, one token, 64 heads over 8 of 64,
+// window 1024, 4 sinks, bf16 116 to 121 us, 4.4 to 4.6 TB/s of the visible rows (of 128,
+// 32 over 8: 172, 6.2); 128 requests, blocks of 1 to 6, 32 over 8 of 128, window
+// 4096, 16 sinks, e4m3 254 us, 4.1 TB/s, bf16 306, 6.6.
 #include <algorithm>
 #include <type_traits>
 

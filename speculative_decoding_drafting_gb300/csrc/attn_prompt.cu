@@ -16,30 +16,38 @@
 //               S_s's columns (bf16).  (One warp for both left the tensor core
 //               idle for a third of the time, between its waits.)
 //   warp 3      zeroes the rows of the last V tile that no row of the item may
-//               see (0 times another sequence's NaN would be NaN)
+//               see (0 times another sequence's NaN would be NaN), and sends
+//               finished row tiles from their ring places to out
 //   warps 4-11  softmax, one warpgroup per row tile, one row per thread: no
 //               exchange between threads; the reference m is raised only when
 //               a score exceeds it by more than 2^8, so the accumulator is
-//               rescaled once or twice per item rather than at every tile
+//               rescaled once or twice per item rather than at every tile.  The
+//               two take turns at their exponentials
 // Items (a pair of row tiles and a key-value head) are handed out from the
 // longest to the shortest, forwards and backwards over the CTAs in turn.
 //
+// With a window (kWindow) an item's keys are the sinks and what its windows reach,
+// one after another (Item), so it takes window / 128 + 1 tiles wherever it stands.
+//
 // 0 times a NaN or an infinity is NaN, so such a value in V would reach the rows
-// before its token too.  A CTA that has stored a row that is not finite goes over
-// its items once more: warp 3 then takes what is not finite out of the V tiles
+// that do not see its token too.  A CTA that has stored a row that is not finite goes
+// over its items once more: warp 3 then takes what is not finite out of the V tiles
 // that some row of the item does not see the whole of, and adds it to the rows
 // that do see it when they are stored.  (Looking through those tiles in the
 // first place made 12001 tokens 12 % and packed prompts 20 % slower: warp 3's
 // loads wait behind the tensor core's reads of shared memory.)
 //
 // Bound by the tensor core and the softmax beside it: the two products of a
-// tile of 128 x 128 scores take it about 1024 cycles at head_dim 128.
-// Measured (GB300): one sequence of 12001 tokens, 32 heads over 8 of 128: 789
-// to 847 us, 1.39 to 1.50 PFLOP/s of the causal half (a plain bf16 product of
-// 8192^3 runs at 1.90 in a burst and 1.73 under the power cap), of 64: 676 us; 16
-// sequences of 100 to 4000 tokens: 590 to 612 us, 1.11 to 1.15 PFLOP/s.  (Taking
+// tile of 128 x 128 scores take it about 1024 cycles at head_dim 128, and a turn
+// of 128 exponentials a row as long.
+// Measured (GB300): one sequence of 12001 tokens, 32 heads over 8 of 128: 740
+// to 798 us, 1.48 to 1.60 PFLOP/s of the causal half (a plain bf16 product of
+// 8192^3 runs at 1.91 in a burst and 1.70 under the power cap), of 64: 606 us; 16
+// sequences of 100 to 4000 tokens: 504 to 553 us, 1.23 to 1.34 PFLOP/s.  30001 tokens,
+// window 4096, 128 sinks: 1250 to 1358 us, 1.42 to 1.54 PFLOP/s; window 1024, 4 sinks:
+// 422 us, 1.18; 16 sequences of 100 to 6000, window 1024: 668 us, 1.08.  (Taking
 // a quarter of the exponentials from the XU pipe to a polynomial on the FMA pipe
-// cost 18 %: its instructions cost more than the pipe it relieves.)
+// cost 13 to 18 %: its instructions cost more than the pipe it relieves.)
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
