@@ -342,8 +342,8 @@ struct SoftState {
     uint32_t seg;                      // segments so far
 };
 
-// With a window, a tile that some row does not see the whole of: the columns that
-// do not see a thread's key, by bit.  Their token stands before the key, their window
+// With a window, a tile of more than one token's rows that some row does not see
+// the whole of: the columns that do not see a thread's key, by bit.  Their token stands before the key, their window
 // begins behind it, or it lies past the item's keys; columns past the tile's
 // rows do not see keys that no row sees either, since what lies there must not raise
 // the other columns' references.  (All bits: no row sees it.)
@@ -451,13 +451,16 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
         // new token k sees the key if kv_len - q_len + k >= key: from this row on.
         // Past the last key no column sees it, the unused ones neither: what
         // lies there must not raise the other columns' references.
-        const int seen = kWindow || !edge ? 0 : (key >= sg.keys ? kRowTile
-                                      : (key - sg.q.kv_len + sg.q.q_len - sg.tok) * p.plan.group - sg.head - coff);
+        int seen = 0;
+        if (kWindow && !any)
+            seen = edge && (key >= sg.keys || (key >= p.plan.sinks && key < win.low)) ? kRowTile : 0;      // one token's rows
+        else if (!kWindow && edge)
+            seen = key >= sg.keys ? kRowTile : (key - sg.q.kv_len + sg.q.q_len - sg.tok) * p.plan.group - sg.head - coff;
         uint32_t hidden = 0;
-        if (kWindow && edge)
+        if (kWindow && any && edge)
             hidden = hidden_columns(coff, key, sg.keys, sg.q.kv_len - sg.q.q_len + sg.tok, p.plan.window, p.plan.sinks, p.plan.group,
                                     sg.head);
-        const bool some_hidden = kWindow && !F8 && __any_sync(0xffffffffu, hidden != 0u);      // among the warp's keys
+        const bool some_hidden = kWindow && any && !F8 && __any_sync(0xffffffffu, hidden != 0u);      // among the warp's keys
         const uint32_t turn = sh.turn_at(sg, i);
         wait_bar(&M->b.s_full[turn][u], (st.phases >> turn) & 1u, ab);
         st.phases ^= 1u << turn;
@@ -476,12 +479,12 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
             // a wide tile's scales are read by two units
             if (lane == 0) mbar_arrive(&M->b.c_empty[s]);
             if (!wide && lane == 0) mbar_arrive(&M->b.c_empty[s]);
-            if (kWindow && edge) {
+            if (kWindow && any && edge) {
                 const Hidden h = hide_scores(tS, N, hidden, mul);
                 mul = h.mul;
                 unseen = h.all;
             }
-            if (kWindow ? unseen : edge && key >= sg.keys) vs = 1.f;     // no key here: any scale
+            if (kWindow ? unseen || seen > 0 : edge && key >= sg.keys) vs = 1.f;     // no key here: any scale
             // Below 2^-100 (a row of zeros has scale 0) 1 / scale would take the sum
             // out of float32's range: there the sum counts the key with 2^-101, and
             // its weight for V is 0 (values below 2^-91 are dropped, not raised).
@@ -517,10 +520,10 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
                     y = fma2(y, mul2, pack2(r.x, r.y));
                     unpack2(y, t[c0 + c], t[c0 + c + 1]);
                 }
-                if (!(kWindow && F8) && (kWindow ? some_hidden : edge)) {
+                if (!(kWindow && any && F8) && (kWindow && any ? some_hidden : edge)) {
 #pragma unroll
                     for (int c = 0; c < kB; ++c)
-                        if (kWindow ? (hidden >> (c0 + c)) & 1u : c0 + c < seen) t[c0 + c] = -INFINITY;
+                        if (kWindow && any ? (hidden >> (c0 + c)) & 1u : c0 + c < seen) t[c0 + c] = -INFINITY;
                 }
 #pragma unroll
                 for (int c = 0; F8 && c < kB; c += 2) top = fmax3(top, t[c0 + c], t[c0 + c + 1]);
@@ -562,7 +565,7 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     float y = fmaf(F8 ? x[c] * M->qm[u][c0 + c] : x[c], mul, lvs);
-                    if (kWindow ? !F8 && ((hidden >> (c0 + c)) & 1u) : c0 + c < seen) y = -INFINITY;
+                    if (kWindow && any ? !F8 && ((hidden >> (c0 + c)) & 1u) : c0 + c < seen) y = -INFINITY;
                     y = redux_max(y);
                     if (lane == c) mine = y;
                 }
@@ -983,13 +986,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++c.seg;
         return true;
     };
-    auto load = [&](auto which, Place& c, int id) {
-        constexpr bool kIsV = decltype(which)::value;
-        constexpr uint32_t kRing = kIsV ? C::kV : C::kK;
-        uint64_t* full = (kIsV ? M->b.v_full : M->b.k_full) + c.slot;
-        ok = ok && __all_sync(0xffffffffu, wait_bar((kIsV ? M->b.v_empty : M->b.k_empty) + c.slot, c.phase ^ 1u, ab));
+    auto load = [&](auto is_v, Place& c, int id) {
+        const uint32_t ring = is_v ? C::kV : C::kK;
+        uint64_t *const full0 = is_v ? M->b.v_full : M->b.k_full, *const empty0 = is_v ? M->b.v_empty : M->b.k_empty;
+        uint8_t* const ring0 = smem + (is_v ? C::kOffV : 0);
+        const CUtensorMap* const map = is_v ? &maps.v : &maps.k;
+        uint64_t* full = full0 + c.slot;
+        ok = ok && __all_sync(0xffffffffu, wait_bar(empty0 + c.slot, c.phase ^ 1u, ab));
         const uint32_t cs = c.count % C::kScMod;
-        if (F8 && !kIsV)
+        if (F8 && !is_v)
             ok = ok && __all_sync(0xffffffffu, wait_bar(&M->b.c_empty[cs], ((c.count / C::kScMod) & 1u) ^ 1u, ab));
         if (!ok) return;
         const bool valid = lane_tok < c.keys - c.tok;
@@ -1008,8 +1013,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_expect_tx(full, pages * (uint32_t)(bp * (F8 ? HD : HD * 2)));
         }
         __syncwarp();
-        uint8_t* dst = smem + (kIsV ? C::kOffV : 0) + c.slot * C::kLoadBytes;
-        if (F8 && !kIsV) {
+        uint8_t* dst = ring0 + c.slot * C::kLoadBytes;
+        if (F8 && !is_v) {
             // the tile's 2 x 128 scales, 4 tokens to a lane: a tensor copy per page,
             // 64 bytes each at 16 tokens, took 248 us where this took 216 (64
             // requests of 8192 tokens, 8 heads of 128; 208 by now)
@@ -1022,47 +1027,98 @@ __global__ void __launch_bounds__(kThreads, 1)
             cp_async16_zf(sc + C::kScBytes / 2, p.v_scale + at, in ? 16u : 0u);
             cp_async_arrive(&M->b.c_full[cs]);
         }
-#pragma unroll 1
-        for (uint32_t k = 0; k < pages; ++k) {
-            const int pid = __shfl_sync(0xffffffffu, id, k);
-            if (elect_one()) {
+        // each page by the lane that holds its id (one lane for all of them, with the ids
+        // handed to it: 148 us for 137, 256 requests, window 1024, one token over e4m3 of 64)
+        if (lane < (int)pages) {
+            dst += lane * bp * (F8 ? HD : 128);
 #pragma unroll
-                for (int hf = 0; hf < (F8 ? 1 : C::kHalves); ++hf)
-                    tma_load_3d(dst + hf * C::kHalfBytes, kIsV ? &maps.v : &maps.k, full, hf * 64, x, pid, c.pol);
-            }
-            dst += bp * (F8 ? HD : 128);
+            for (int hf = 0; hf < (F8 ? 1 : C::kHalves); ++hf)
+                tma_load_3d(dst + hf * C::kHalfBytes, map, full, hf * 64, x, id, c.pol);
         }
         __syncwarp();
-        if (++c.slot == kRing) {
+        if (++c.slot == ring) {
             c.slot = 0;
             c.phase ^= 1u;
         }
     };
     // copies in flight of a ring, after an abort
-    auto drain = [&](uint64_t* full, uint32_t ring, uint32_t count) {
+    auto drain = [&](uint64_t* full, uint32_t places, uint32_t count) {
         if (ab->abort && lane == 0)
 #pragma unroll 1
-            for (uint32_t k = count > ring ? count - ring : 0; k < count; ++k)
-                mbar_wait_for(&full[k % ring], (k / ring) & 1u, ab->limit);
+            for (uint32_t k = count > places ? count - places : 0; k < count; ++k)
+                mbar_wait_for(&full[k % places], (k / places) & 1u, ab->limit);
         __syncwarp();
     };
 
-    if (warp == 0) {
-        // ---------------- K tiles
+    // Segments; K and V tiles.  (One code for both warps, since the warps' code is
+    // what the instruction caches run out of: 256 requests, window 1024, one token over
+    // bf16 of 64 133 -> 117 us.  e4m3 without a window, whose code is shorter by the
+    // window's and where K's loads have the scales to bring, has one for each: decoding
+    // 131 -> 127, blocks of 1 to 6 316 -> 300.)
+    auto loads = [&](auto is_v) {
+        Cursor cur;
+        if (is_v) cur.start(pl, M->start_r, M->start_skip, end - begin);
+        uint32_t made = 0, line = 0, run = 0;                 // segments listed, their key tiles
+        bool wide = false, more = is_v;                       // (the warp of V lists them)
+        int place = 0;                                        // the next Q place
+        uint32_t use = 0;
         Place c = {};
-        enter(c);
+        for (;;) {
+            // before each segment's tiles, list it and those after it that there is
+            // room for (the others never need more to get through this one)
 #pragma unroll 1
-        while (ok && c.more) {
-            load(std::false_type{}, c, page_of(c));
-            if (!ok) break;
-            const uint32_t seg = c.seg;
-            if (step(c)) {
-                if (lane == 0) mbar_arrive(&M->b.seg_empty[seg % kSegs]);
-                enter(c);
+            while (more) {
+                uint64_t* bar = &M->b.seg_empty[made % kSegs];
+                const uint32_t par = ((made / kSegs) & 1u) ^ 1u;
+                if (made == c.seg)
+                    ok = __all_sync(0xffffffffu, wait_bar(bar, par, ab));
+                else if (!__all_sync(0xffffffffu, mbar_test(bar, par)))
+                    break;
+                if (!ok) break;
+                Segment s;
+                more = cur.next(pl, s);
+                if (more && Shape(s.rows).wide != wide) {
+                    wide = !wide;
+                    run = line;
+                }
+                const bool both = more && Shape(s.rows).cols > C::kQRows;
+                if (lane == 0) {
+                    SegInfo& o = M->seg[made % kSegs];
+                    o.rows = 0;
+                    if constexpr (kWindow)
+                        if (more) M->win[made % kSegs] = make_int2((int)max(plan_low(pl, s.q, s.tok), (int64_t)0), s.gap);
+                    if (more)
+                        o = SegInfo{s.r, s.j, s.h, s.t0, s.t1 - s.t0, s.tiles, s.keys, s.rows, s.tok, s.head, s.rest, line, run,
+                                    both ? 2 : place, use, s.q};
+                    mbar_arrive(&M->b.seg_full[made % kSegs]);
+                }
+                __syncwarp();
+                if (more) line += (uint32_t)(s.t1 - s.t0);
+                use += (both || place == 0 ? 1u : 0u) + (both || place == 1 ? 0x10000u : 0u);
+                use &= 0x7FFF7FFFu;                           // parities are what counts
+                if (!both) place ^= 1;
+                ++made;
             }
+            if (!ok) break;
+            enter(c);
+            if (!c.more) break;
+            bool last = false;
+#pragma unroll 1
+            while (ok && !last) {
+                load(is_v, c, page_of(c));
+                last = step(c);
+            }
+            if (!ok) break;
+            if (lane == 0) mbar_arrive(&M->b.seg_empty[(c.seg - 1) % kSegs]);
         }
-        drain(M->b.k_full, C::kK, c.count);
-        if (F8) drain(M->b.c_full, C::kScMod, c.count);
+        drain(is_v ? M->b.v_full : M->b.k_full, is_v ? C::kV : C::kK, c.count);
+        if (F8 && !is_v) drain(M->b.c_full, C::kScMod, c.count);
+    };
+    if (F8 && !kWindow ? warp == 0 : warp == 0 || warp == 2) {
+        if constexpr (F8 && !kWindow) loads(std::false_type{});
+        else loads(warp == 2);
+    } else if (F8 && !kWindow && warp == 2) {
+        if constexpr (F8 && !kWindow) loads(std::true_type{});
     } else if (warp == 1) {
         // ---------------- scores S^T = K Q^T
         // A stream's columns are free once the weights of its tile before are
@@ -1202,64 +1258,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait_for(&M->b.done, 0, ab->limit);
         }
         __syncwarp();
-    } else if (warp == 2) {
-        // ---------------- segments and V tiles
-        Cursor cur;
-        cur.start(pl, M->start_r, M->start_skip, end - begin);
-        uint32_t made = 0, line = 0, run = 0;                 // segments listed, their key tiles
-        bool wide = false, more = true;
-        int place = 0;                                        // the next Q place
-        uint32_t use = 0;
-        Place c = {};
-        for (;;) {
-            // before each segment's tiles, list it and those after it that there is
-            // room for (the others never need more to get through this one)
-#pragma unroll 1
-            while (more) {
-                uint64_t* bar = &M->b.seg_empty[made % kSegs];
-                const uint32_t par = ((made / kSegs) & 1u) ^ 1u;
-                if (made == c.seg)
-                    ok = __all_sync(0xffffffffu, wait_bar(bar, par, ab));
-                else if (!__all_sync(0xffffffffu, mbar_test(bar, par)))
-                    break;
-                if (!ok) break;
-                Segment s;
-                more = cur.next(pl, s);
-                if (more && Shape(s.rows).wide != wide) {
-                    wide = !wide;
-                    run = line;
-                }
-                const bool both = more && Shape(s.rows).cols > C::kQRows;
-                if (lane == 0) {
-                    SegInfo& o = M->seg[made % kSegs];
-                    o.rows = 0;
-                    if constexpr (kWindow)
-                        if (more) M->win[made % kSegs] = make_int2((int)max(plan_low(pl, s.q, s.tok), (int64_t)0), s.gap);
-                    if (more)
-                        o = SegInfo{s.r, s.j, s.h, s.t0, s.t1 - s.t0, s.tiles, s.keys, s.rows, s.tok, s.head, s.rest, line, run,
-                                    both ? 2 : place, use, s.q};
-                    mbar_arrive(&M->b.seg_full[made % kSegs]);
-                }
-                __syncwarp();
-                if (more) line += (uint32_t)(s.t1 - s.t0);
-                use += (both || place == 0 ? 1u : 0u) + (both || place == 1 ? 0x10000u : 0u);
-                use &= 0x7FFF7FFFu;                           // parities are what counts
-                if (!both) place ^= 1;
-                ++made;
-            }
-            if (!ok) break;
-            enter(c);
-            if (!c.more) break;
-            bool last = false;
-#pragma unroll 1
-            while (ok && !last) {
-                load(std::true_type{}, c, page_of(c));
-                last = step(c);
-            }
-            if (!ok) break;
-            if (lane == 0) mbar_arrive(&M->b.seg_empty[(c.seg - 1) % kSegs]);
-        }
-        drain(M->b.v_full, C::kV, c.count);
     } else if (warp >= 4 + 4 * kUnits) {
         // ---------------- Q rows of the segment to come, and the finished one
         constexpr int kLanes = HD / 8, kStep = 128 / kLanes;  // 8 values per lane; rows per step
@@ -1326,13 +1324,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (bf16 has no loop for 24: such items are bound by the cache's bytes, and
             // one shape more cost blocks of 1 to 17 tokens 4 %.)
             // (With a window and blocks of tokens, which may differ, one loop takes any
-            // number: the code is longer, and with a loop per number two SMs beside each
-            // other, which fetch from one cache, ran out of it whenever their items had
+            // number, and any mask: the code is longer, and with a loop per number two SMs beside
+            // each other, which fetch from one cache, ran out of it whenever their items had
             // different rows.  128 requests, e4m3, window 4096, blocks of 1 and 6 in turn 294
-            // -> 246 us; of 1 to 9 over bf16, 64 heads of 64, window 1000, 120 -> 107.  For
-            // single tokens, of equal rows, it is the slower: 256 requests, window 1024, 200
-            // -> 238 us over e4m3, 129 -> 166 over bf16 of 64.)
-            if (kWindow && p.blocks)
+            // -> 246 us; of 1 to 9 over bf16, 64 heads of 64, window 1000, 120 -> 107.  Single
+            // tokens keep a loop of their number: their rows see the same keys, so
+            // that a key is hidden from all or none.  256 requests, window 1024, bf16 of 64 129
+            // us against 166 in the one loop, e4m3 200 and 238; e4m3 of 64 with the test of a
+            // key instead of masks by row 175 -> 148.)
+            if (kWindow && (p.blocks || s.head + s.rows > p.plan.group))
                 soft_segment<HD, F8, kWindow, 0>(p, s, M, smem, tmem, u, st);
             else if (s.rows <= 8)
                 soft_segment<HD, F8, kWindow, 8>(p, s, M, smem, tmem, u, st);

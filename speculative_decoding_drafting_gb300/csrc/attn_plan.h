@@ -114,8 +114,8 @@ DSPARK_HD int64_t plan_place(const PlanInput& p, int length, int t) { return p.s
 // The first key tile that begins at or after place x of an item.
 DSPARK_HD int plan_tile_at(const PlanInput& p, int length, int64_t x, int tiles) {
     if (x <= p.start) return 0;
-    const int64_t t = (x - p.start + length - 1) / length;
-    return (int)(t < tiles ? t : tiles);
+    if (x > plan_place(p, length, tiles - 1)) return tiles;
+    return (int)(((uint32_t)(x - p.start) + (uint32_t)length - 1u) / (uint32_t)length);   // inside the item: below 2^30
 }
 // Length of a request's first n row tiles, all of them full and none its last:
 // row tile j reads kv_len - q_len + floor((64 j + 63) / group) + 1 keys, so it
@@ -242,7 +242,7 @@ struct Cursor {
         while (end > p.start) {                            // else no further tile begins in the span
             while (q.q_len == 0) q = plan_request(p, ++r); // the span goes on: a request with rows follows
             s.keys = plan_tile_keys(p, q, j);
-            s.tok = (int)((int64_t)j * kRowTile / p.group);
+            s.tok = plan_first_token(p, j);
             s.gap = plan_gap(p, q, s.tok);
             s.tiles = plan_key_tiles(s.keys - s.gap);
             s.rows = plan_rows(p, q, j);
