@@ -79,6 +79,28 @@ def test_paged_lengths(dtype, heads, kv_heads, dim, page, window, sinks):
 
 
 @pytest.mark.parametrize("dtype", [BF, F8])
+@pytest.mark.parametrize("heads,kv_heads,dim,page", [
+    (8, 2, 128, 16), (4, 4, 64, 32), (24, 2, 128, 64), (20, 1, 64, 128), (40, 1, 128, 16), (64, 1, 64, 256), (100, 1, 64, 16)])
+def test_paged_single_tokens(dtype, heads, kv_heads, dim, page):
+    """One new token each, for every way that rows of a token are laid out; and as
+    many tokens as requests that are not one each."""
+    for window, sinks in ((1, 0), (16, 3), (128, 0), (130, 17), (300, 200), (1000, 4)):
+        _check(Scene(KV, heads, kv_heads, dim, page, dtype, seed=heads + window), [min(n, 1) for n in KV], window, sinks)
+        _check(Scene(KV, heads, kv_heads, dim, page, dtype, seed=heads), [1] + [1 - (n == 0) for n in KV[1:-1]] + [3],
+               window, sinks)
+    one = [n for n in KV if n]
+    _check(Scene(one, heads, kv_heads, dim, page, dtype, seed=1), [1] * len(one), 140, 5)
+    _check(Scene(one, heads, kv_heads, dim, page, dtype, seed=2), [1] * (len(one) - 3) + [0, 0, 3], 140, 5)
+
+
+@pytest.mark.parametrize("dtype", [BF, F8])
+def test_paged_single_tokens_sharp_and_flat_scores(dtype):
+    for scale in (1.0, 0.0, -0.3):
+        for heads, kv_heads in ((8, 1), (48, 1)):
+            _check(Scene([700, 130], heads, kv_heads, 128, 16, dtype, seed=6, size=8.0), [1, 1], 200, 3, scale=scale)
+
+
+@pytest.mark.parametrize("dtype", [BF, F8])
 def test_paged_one_request_split_over_the_device(dtype):
     for window, sinks in ((1024, 4), (9000, 1000), (20000, 1), (130, 5000), (1 << 40, 7)):
         _check(Scene([20011], 8, 2, 128, 16, dtype, seed=1), [3], window, sinks)
