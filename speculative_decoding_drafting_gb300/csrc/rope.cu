@@ -299,9 +299,13 @@ __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const __grid_constant
             for (int k = threadIdx.x / kHalf; k < n; k += kWarps * 32 / kHalf) {
                 const int x = p.positions ? __ldg(p.positions + (int64_t)(t0 + k) * p.n_axes + axis)
                                           : (MODE == kRows ? 0 : tokens[k].pos);
-                const int part = (int)((turn * (uint64_t)(int64_t)x) >> 32);               // of a turn, in 2^-32
-                float cs, sn;
-                sincospif((float)part * 0x1p-31f, &sn, &cs);
+                // of a turn, in 2^-32: the nearest quarter, and what is left of it, whose float32
+                // is off by 2^-28 turns at most (that of the whole by 2^-26)
+                const uint32_t part = (uint32_t)((turn * (uint64_t)(int64_t)x) >> 32), quarter = (part + (1u << 29)) >> 30;
+                float u, v;
+                sincospif((float)(int)(part - (quarter << 30)) * 0x1p-31f, &v, &u);
+                float cs = quarter & 1u ? -v : u, sn = quarter & 1u ? u : v;
+                if (quarter & 2u) cs = -cs, sn = -sn;
                 cosines[k][f] = cs * p.amplitude;
                 sines[k][f] = sn * p.amplitude;
             }

@@ -5,8 +5,8 @@ Bounds (half a bf16 step is 2^-8 of the value, half a float32 step 2^-24):
 * a normed value x r w: the sum of head_dim squares passes 8 + 4 additions of
   positive terms (12 half steps), its root halves that; the mean and eps, the
   root and two products add 5: under 2^-20 of the value in all;
-* cosine and sine: the turn's fraction as float32 is off by 2^-25 of a half
-  turn, 2^-23.3 rad, the functions by one step and the amplitude's product by half
+* cosine and sine: the turn's fraction beyond the nearest quarter as float32 is off
+  by 2^-27 of a half turn, 2^-25.3 rad, the functions by one step and the amplitude's product by half
   a step: under 2^-22 of the amplitude together (exact frequencies and
   positions); the two products and the sum add 3 half steps of |a| + |b|;
 * a turned value: (|a| + |b|) amplitude (2^-20 + 2^-22 + 3 2^-24) < 2^-19 of that
