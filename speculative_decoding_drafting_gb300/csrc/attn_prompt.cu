@@ -15,19 +15,21 @@
 //   warps 1, 2  MMA issuers, one per row tile s: S_s and O_s in TMEM, P_s over
 //               S_s's columns (bf16).  (One warp for both left the tensor core
 //               idle for a third of the time, between its waits.)
-//   warp 3      zeroes the rows of the last V tile that no row of the item may
-//               see (0 times another sequence's NaN would be NaN), and sends
+//   warp 3      zeroes the rows of a sequence's last V tile that are not its own
+//               (0 times another sequence's NaN would be NaN), and sends
 //               finished row tiles from their ring places to out
 //   warps 4-11  softmax, one warpgroup per row tile, one row per thread: no
 //               exchange between threads; the reference m is raised only when
 //               a score exceeds it by more than 2^8, so the accumulator is
-//               rescaled once or twice per item rather than at every tile.  The
-//               two take turns at their exponentials
+//               rescaled once or twice per item rather than at every tile.
+//               Without a window the two take turns at their exponentials; with
+//               one they work on half tiles (kSplit)
 // Items (a pair of row tiles and a key-value head) are handed out from the
 // longest to the shortest, forwards and backwards over the CTAs in turn.
 //
 // With a window (kWindow) an item's keys are the sinks and what its windows reach,
-// one after another (Item), so it takes window / 128 + 1 tiles wherever it stands.
+// one after another (Item), so it takes window / 128 + 1 tiles wherever it stands,
+// and about 8000 cycles beside its tiles' 2570 each.
 //
 // 0 times a NaN or an infinity is NaN, so such a value in V would reach the rows
 // that do not see its token too.  A CTA that has stored a row that is not finite goes
@@ -44,10 +46,10 @@
 // to 798 us, 1.48 to 1.60 PFLOP/s of the causal half (a plain bf16 product of
 // 8192^3 runs at 1.91 in a burst and 1.70 under the power cap), of 64: 606 us; 16
 // sequences of 100 to 4000 tokens: 504 to 553 us, 1.23 to 1.34 PFLOP/s.  30001 tokens,
-// window 4096, 128 sinks: 1250 to 1358 us, 1.42 to 1.54 PFLOP/s; window 1024, 4 sinks:
-// 422 us, 1.18; 16 sequences of 100 to 6000, window 1024: 668 us, 1.08.  (Taking
-// a quarter of the exponentials from the XU pipe to a polynomial on the FMA pipe
-// cost 13 to 18 %: its instructions cost more than the pipe it relieves.)
+// window 4096, 128 sinks: 1150 to 1252 us, 1.54 to 1.68; window 1024, 4 sinks:
+// 412 to 425 us, 1.17 to 1.21; 16 sequences of 100 to 6000, window 1024: 600 to 640, 1.12 to 1.20.
+// (Taking a quarter of the exponentials from the XU pipe to a polynomial on the FMA
+// pipe cost 13 to 18 %: its instructions cost more than the pipe it relieves.)
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -81,6 +83,16 @@ struct Cfg {
     static constexpr int kOffMisc = kOffQ + 2 * kTileBytes;
 };
 
+// With a window a tile's 64 keys are a step of their own: their scores, weights and
+// product follow one another while the other 64's do, in columns of their own, so that
+// neither the tensor core nor the softmax waits for a whole tile of the other (30001
+// tokens, window 4096, 1256 -> 1178 us; 16 of 100 to 6000, head_dim 64, window 1024, 520
+// -> 464).  A row's reference then follows the halves.  Without one the reference
+// follows whole tiles, which results' last bits depend on, and the row tiles take turns;
+// turns of halves gained nothing.
+template <bool kWindow>
+constexpr bool kSplit = kWindow;
+
 struct Bars {
     uint64_t full[8], empty[8];
     uint64_t q_full[2], q_empty[2], s_full[2], s_read[2], p_full[2][2], pv_done[2], o_free[2];
@@ -97,6 +109,9 @@ struct Bars {
     // A row tile's exponentials of a tile that both go over are made: the other's turn.
     uint64_t turn[2];
     uint64_t done;
+    // kSplit: the scores of a tile's other 64 keys (s_full's are the first), and the
+    // product with its first 64
+    uint64_t s_more[2], pv_half[2];
 };
 
 struct Misc {
@@ -229,10 +244,13 @@ struct Item {
     __device__ __forceinline__ int key(int v) const { return kWindow && v >= head ? v + gap : v; }
     // what tile j's first row would stand for as a key if its last row's key decides
     __device__ __forceinline__ int key0(int j) const { return key(j * kKeys + kKeys - 1) - (kKeys - 1); }
-    // V tiles to clear: from this one on, those with rows past the item's keys, or,
-    // the second time, with a key that some row of the item does not see
+    // V tiles to clear: from this one on, those with rows past the sequence's end, or,
+    // the second time, with a key that some row of the item does not see.  (The
+    // first time with rows past the item's keys, later tokens of the sequence: their
+    // weights are 0, and if one is not finite the second time comes anyway; to clear
+    // them took window 1024 packed 630 us for 609.)
     __device__ __forceinline__ int edge(bool second) const {
-        return second ? min((tok0 + 1 - gap) / kKeys, tiles() - 1) : (keys - gap) / kKeys;
+        return second ? min((tok0 + 1 - gap) / kKeys, tiles() - 1) : (keys < len ? tiles() : (keys - gap) / kKeys);
     }
     // (with a window, the second time, also some of those before)
     __device__ __forceinline__ bool clears(const Params& p, int j, bool second) const {
@@ -385,11 +403,13 @@ __device__ __forceinline__ void init_bars(Bars* B) {
         mbar_init(&B->q_full[s], 1);
         mbar_init(&B->q_empty[s], 1);
         mbar_init(&B->s_full[s], 1);
+        mbar_init(&B->s_more[s], 1);
         mbar_init(&B->s_read[s], 4);
         mbar_init(&B->p_full[s][0], 4);
         mbar_init(&B->p_full[s][1], 4);
         mbar_init(&B->asked[s], 1);
         mbar_init(&B->turn[s], 4);
+        mbar_init(&B->pv_half[s], 1);
         mbar_init(&B->pv_done[s], 1);
         mbar_init(&B->o_free[s], 4);
     }
@@ -526,8 +546,8 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
                     const uint32_t off = (kk / 4) * (C::kHalfBytes / 16) + (kk % 4) * 2;
                     umma_bf16(tS + half * 64, dq + off, b + off, id_qk, kk ? 1u : 0u);
                 }
-                if (!half) {
-                    umma_commit(&B->s_full[s]);
+                if (kSplit<kWindow> || !half) umma_commit(kSplit<kWindow> && half ? &B->s_more[s] : &B->s_full[s]);
+                if (kSplit<kWindow> ? half : !half) {
                     umma_commit(&B->empty[at]);
                     if (j + 1 == it.n(s)) umma_commit(&B->q_empty[s]);
                 }
@@ -565,8 +585,8 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
             if (!wait(&B->full[st], ph)) break;
             if (it.n(s)) {
                 // (the item before it has been read and multiplied)
-                scores(st, 1, j0);
-                scores(st, 0, j0);
+                scores(st, kSplit<kWindow> ? 0 : 1, j0);
+                scores(st, kSplit<kWindow> ? 1 : 0, j0);
             } else if (lane == 0) {
                 mbar_arrive(&B->empty[st]);
             }
@@ -578,7 +598,7 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
                 next();
                 const uint32_t kat = st, kph = ph;
                 if (j + 1 < n) next();
-                if (j < it.n(s)) {
+                if (!kSplit<kWindow> && j < it.n(s)) {
                     if (!wait(&B->s_read[s], nr & 1u)) break;
                     nr ^= 1u;
                     if (j + 1 < it.n(s)) {
@@ -607,17 +627,23 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
                             const uint64_t b = dv + vat * (C::kTileBytes / 16) + half * 512;
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                umma_bf16_ts(tO, tS + half * 32 + kk * 8, b + kk * 128, id_pv, ((j - j0) | half | kk) ? 1u : 0u);
+                                umma_bf16_ts(tO, tS + half * (kSplit<kWindow> ? 64 : 32) + kk * 8, b + kk * 128, id_pv,
+                                             ((j - j0) | half | kk) ? 1u : 0u);
+                            if (kSplit<kWindow> && !half) umma_commit(&B->pv_half[s]);
                             if (half) {
                                 umma_commit(&B->pv_done[s]);
                                 umma_commit(&B->empty[vat]);
                             }
                         }
                         __syncwarp();
+                        if (kSplit<kWindow> && j + 1 < it.n(s)) {
+                            if (!half && !wait(&B->full[kat], kph)) break;
+                            scores(kat, half, j + 1);
+                        }
                     }
                     if (!ok) break;
                     np ^= 1u;
-                    if (j + 1 < it.n(s)) scores(kat, 0, j + 1);
+                    if (!kSplit<kWindow> && j + 1 < it.n(s)) scores(kat, 0, j + 1);
                 } else if (lane == 0) {
                     mbar_arrive(&B->empty[vat]);
                 }
@@ -845,12 +871,11 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint8_t* 
     const float c = p.scale2;
     const uint64_t c2 = pack2(c, c);
     uint32_t ns = 0, npv = 0, g = 0;                         // g: ring places before this item
-    // The two row tiles take turns at the exponentials of the tiles that both go over,
+    // Without a window the two row tiles take turns at the exponentials of the tiles that both go over,
     // row tile 0 first, so that one's run beside the other's products.  Left alone they
     // settled in step or out of step as small changes of the code would have it: both
     // at the exponentials at once, 12001 tokens took 893 us, out of step 780, and in
-    // turns they take 730 (head_dim 64: 693, 661, 610; 30001 tokens, window 4096: 1441,
-    // 1360, 1257).
+    // turns they take 730 (head_dim 64: 693, 661, 610).
     uint32_t nt = 0;                                         // such tiles so far
     auto in_turns = [&](int j) { return j >= it.begin(1) && j < min(it.n0, it.n1); };
     auto hand_over = [&](int j) {
@@ -862,17 +887,96 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint8_t* 
         tc_fence_after();
         return ok;
     };
-    for (int round = 0; ok && get_item(p, M, total, round, it); ++round) {
+    // (with a window, whose items are short, the next one is worked out while the last
+    // product of this one runs: window 128 187 -> 160 us, window 1024 packed 612 -> 597)
+    Item<kWindow> coming = {};
+    bool more = kWindow && get_item(p, M, total, 0, coming);
+    for (int round = 0; ok && (kWindow ? more : get_item(p, M, total, round, it)); ++round) {
+        if (kWindow) it = coming;
         const int n = it.n(s), j0 = it.begin(s);
         const uint32_t mine = g + (uint32_t)(2 * it.tiles() + s);   // the ring place for the result
         g += it.places(kSecond);
-        if (!n) continue;
+        if (!n) {
+            if (kWindow) more = get_item(p, M, total, round + 1, coming);
+            continue;
+        }
         const int tok = it.tok0 + s * p.toks + rt;           // sees keys 0 .. tok
         const int first = it.tok0 + s * p.toks;
         float ref = kFloorRef;
         uint64_t l2 = 0;                                     // two partial sums
-        auto tile = [&](int j, auto masked) {
-            constexpr bool kMasked = decltype(masked)::value;
+        // 64 keys of tile j
+        auto half_tile = [&](int j, int hf, auto masked) {
+            if (!wait(hf ? &B->s_more[s] : &B->s_full[s], ns & 1u)) return false;
+            float x[64];
+            tmem_ld32_async(tS + hf * 64, x);
+            tmem_ld32_async(tS + hf * 64 + 32, x + 32);
+            tmem_ready(x);
+            tmem_pin(x + 32);
+            if constexpr (decltype(masked)::value) {
+                // neither the keys behind it nor, but for the sinks, those before its window
+                const int key0 = it.key0(j) + hf * 64, sees = tok - key0 + 1, low = sees - p.window, sink = p.sinks - j * kKeys - hf * 64;
+                auto first_bits = [](int n) { return n <= 0 ? 0u : 0xFFFFFFFFu >> (32 - min(n, 32)); };
+#pragma unroll
+                for (int q = 0; q < 64; q += 32) {
+                    const uint32_t seen = first_bits(sees - q) & (~first_bits(low - q) | first_bits(sink - q));
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (!((seen >> i) & 1u)) x[q + i] = -INFINITY;
+                }
+            }
+            // the row's largest score
+            float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+            for (int i = 4; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+            if (__any_sync(0xffffffffu, top > ref + kLazy)) {
+                // each row by its own scores alone: the others' do not reach its bits
+                const float m = top > ref + kLazy ? top : ref, f = ex2_approx(ref - m);
+                ref = m;
+                float a, b;
+                unpack2(l2, a, b);
+                l2 = pack2(a * f, b * f);
+                if (j > j0 || hf) {                          // what the accumulator holds so far
+                    if (!wait(hf ? &B->pv_half[s] : &B->pv_done[s], (hf ? npv : npv - 1u) & 1u)) return false;
+#pragma unroll
+                    for (int q = 0; q < HD / 16; ++q) {
+                        float o[16];
+                        tmem_ldn<16>(tO + q * 16, o);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] *= f;
+                        tmem_st16(tO + q * 16, o);
+                    }
+                }
+            }
+            const uint64_t r2 = pack2(-ref, -ref);
+            uint32_t pk[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                float a, b;
+                unpack2(fma2(pack2(x[2 * i], x[2 * i + 1]), c2, r2), a, b);
+                a = ex2_approx(a);
+                b = ex2_approx(b);
+                l2 = add2(l2, pack2(a, b));
+                // bf16 for the product with V; the sum keeps float32
+                const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+                pk[i] = reinterpret_cast<const uint32_t&>(h);
+            }
+            tmem_st32(tS + hf * 64, pk);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B->p_full[s][hf]);
+            return true;
+        };
+        auto tile = [&](int j, [[maybe_unused]] auto masked) {
+            if constexpr (kSplit<kWindow>) {
+#pragma unroll 1
+                for (int hf = 0; hf < 2; ++hf)
+                    if (!half_tile(j, hf, masked)) return false;
+                ++ns;
+                ++npv;
+                return true;
+            }
             if (!wait(&B->s_full[s], ns++ & 1u)) return false;
             float x[128];
 #pragma unroll
@@ -883,23 +987,11 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint8_t* 
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&B->s_read[s]);
-            if (!kWindow && (j + 1) * kKeys - 1 > first) {   // a row of the tile does not see all keys
+            if ((j + 1) * kKeys - 1 > first) {               // a row of the tile does not see all keys
                 const int lim = tok - j * kKeys;
 #pragma unroll
                 for (int i = 0; i < 128; ++i)
                     if (i > lim) x[i] = -INFINITY;
-            }
-            if constexpr (kMasked) {
-                // neither the keys behind it nor, but for the sinks, those before its window
-                const int key0 = it.key0(j), sees = tok - key0 + 1, low = sees - p.window, sink = p.sinks - j * kKeys;
-                auto first_bits = [](int n) { return n <= 0 ? 0u : 0xFFFFFFFFu >> (32 - min(n, 32)); };
-#pragma unroll
-                for (int q = 0; q < 128; q += 32) {
-                    const uint32_t seen = first_bits(sees - q) & (~first_bits(low - q) | first_bits(sink - q));
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (!((seen >> i) & 1u)) x[q + i] = -INFINITY;
-                }
             }
             // the row's largest score
             float mx[4] = {x[0], x[1], x[2], x[3]};
@@ -944,18 +1036,12 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint8_t* 
                     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
                     pk[i] = reinterpret_cast<const uint32_t&>(h);
                 }
-                // (with a window before the weights are stored: window 1024 445 -> 435 us,
-                // but 12001 tokens without one 730 -> 742)
-                if (kWindow && hf) {
-                    __syncwarp();
-                    hand_over(j);
-                }
                 tmem_st32(tS + hf * 32, pk);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&B->p_full[s][hf]);
-                if (!kWindow && hf) hand_over(j);
+                if (hf) hand_over(j);
             }
             ++npv;
             return true;
@@ -981,12 +1067,15 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint8_t* 
             for (int j = 0; ok && j < n; ++j)
                 if (!tile(j, std::false_type{})) break;
         }
-        if (!ok || !wait(&B->pv_done[s], (npv - 1u) & 1u)) break;
+        if (!ok) break;
+        const bool valid = row < p.toks * p.group && tok < it.len;
+        const size_t at = (size_t)(it.a + tok) * p.heads + (size_t)it.h * p.group + rg;
+        const bool direct = kSecond || first + p.toks > it.len;
+        if (kWindow) more = get_item(p, M, total, round + 1, coming);
+        if (!wait(&B->pv_done[s], (npv - 1u) & 1u)) break;
         float a, b;
         unpack2(l2, a, b);
         const float l = a + b, inv = 1.f / l;
-        const bool valid = row < p.toks * p.group && tok < it.len;
-        const size_t at = (size_t)(it.a + tok) * p.heads + (size_t)it.h * p.group + rg;
         // the accumulator is read at once and free for the next item before its rows
         // are stored (but warp 3 mends stored rows)
         float o[HD];
@@ -1004,7 +1093,6 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint8_t* 
         // instruction, one per lane, and stored as they are took 5000 cycles of the 16000
         // to 40000 of an item.  The last one of a sequence must not touch the rows
         // behind it; and what is mended is stored as it is.
-        const bool direct = kSecond || first + p.toks > it.len;
         uint8_t* stage = smem + mine % C::kStages * C::kTileBytes;
         if (!kSecond && !wait(&B->full[mine % C::kStages], mine / C::kStages & 1u)) break;
         uint32_t most = 0;                                   // bits of the row's largest magnitudes, a NaN's above all
