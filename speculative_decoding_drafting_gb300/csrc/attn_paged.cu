@@ -12,10 +12,10 @@
 // bound by the cache's bytes: 64 KB of bf16 per key tile take the SM about
 // 2800 cycles at the measured copy rate, its two products under 600.
 // Measured (GB300, against 6.68 TB/s of a plain copy): 256 requests of 200 to
-// 4000 keys, blocks of 1 to 6 tokens, 32 heads over 8 of 128, bf16: 330 to 335
+// 4000 keys, blocks of 1 to 6 tokens, 32 heads over 8 of 128, bf16: 327 to 335
 // us, 6.7 TB/s; 64 requests of 500 to 8000 e4m3 keys, one token, 64 heads over 8:
-// 113 us, 5.1 TB/s (5.6 TB/s at 8192 keys each); two requests of 150001 and
-// 260001 e4m3 keys at most, blocks of 6, 32 heads over 4: 138 us, 3.8 TB/s.
+// 112 us, 5.2 TB/s (5.6 TB/s at 8192 keys each); two requests of 150001 and
+// 260001 e4m3 keys at most, blocks of 6, 32 heads over 4: 135 us, 3.9 TB/s.
 //
 // One persistent CTA per SM walks an equal span of the line of all items' key
 // tiles (attn_plan.h); pieces of split items go to the workspace and a second
@@ -67,9 +67,9 @@
 // sinks' and the window's, attn_plan.h), hidden pages inside a tile are not read,
 // and V rows that no row of the item sees are zeroed like those past its end.
 // Measured: 256 requests of 200 to 12000 keys, one token, 64 heads over 8 of 64,
-// window 1024, 4 sinks, bf16 116 to 121 us, 4.4 to 4.6 TB/s of the visible rows (of 128,
-// 32 over 8: 172, 6.2); 128 requests, blocks of 1 to 6, 32 over 8 of 128, window
-// 4096, 16 sinks, e4m3 254 us, 4.1 TB/s, bf16 306, 6.6.
+// window 1024, 4 sinks, bf16 104 us, 5.15 TB/s of the visible rows (117 with a cold L2; of
+// 128, 32 over 8: 170, 6.3, e4m3 138, 4.0); 128 requests, blocks of 1 to 6, 32 over 8 of
+// 128, window 4096, 16 sinks, e4m3 256 us, 4.1 TB/s, bf16 302, 6.7.
 #include <algorithm>
 #include <type_traits>
 
