@@ -402,7 +402,11 @@ __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const __grid_constant
                 const float big = join_rows<kVecs, kLanes>(m, at.part, [](float x, float y) {
                     return __uint_as_float(max(__float_as_uint(x), __float_as_uint(y)));
                 });
-                float inv = 0.f;
+                // 448 / big as inv + rest, to about 48 bits: a quotient is then rounded once, so
+                // that where a turn by 0 leaves a row's bf16 values as they came their
+                // midpoints are ties, as v's are (one product with inv took the wrong
+                // side of 5 times as many as a division)
+                float inv = 0.f, rest = 0.f;
                 {
                     constexpr int kOwn = kLanes / kVecs;      // lanes that hold a row's largest
                     const int v = at.part / kOwn, kv = v / N, h = h0 + v % N * kHeads;
@@ -410,16 +414,20 @@ __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const __grid_constant
                     // below 2^-100 the reciprocal would overflow float32: such rows (a
                     // negative sign marks them) are scaled up by 2^64 first; rows that are
                     // zero or not finite get codes of zero
-                    if (big > 0.f && big < INFINITY)
-                        inv = big < kTiny ? -__fdiv_rn(448.f, big * 0x1p64f) : __fdiv_rn(448.f, big);
+                    if (big > 0.f && big < INFINITY) {
+                        const float a = big < kTiny ? big * 0x1p64f : big;
+                        inv = __fdiv_rn(448.f, a);
+                        rest = fmaf(-inv, a, 448.f) * inv * (1.f / 448.f);
+                        if (big < kTiny) inv = -inv;
+                    }
                 }
-                const bool as_given = !weights && p.rot == 0;    // k as it came: its midpoints count, as v's do
 #pragma unroll
                 for (int v = 0; v < kVecs; ++v) {
                     const int h = h0 + v % N * kHeads;
                     const float f = __shfl_sync(0xffffffffu, inv, at.sub * kLanes + v * (kLanes / kVecs));
+                    const float lo = v < N ? __shfl_sync(0xffffffffu, rest, at.sub * kLanes + v * (kLanes / kVecs)) : 0.f;
                     const float up = f < 0.f ? 0x1p64f : 1.f;
-                    const uint64_t up2 = pack2(up, up), f2 = pack2(fabsf(f), fabsf(f));
+                    const uint64_t up2 = pack2(up, up), f2 = pack2(fabsf(f), fabsf(f)), lo2 = pack2(lo, lo);
                     if (h >= heads) continue;
                     const int64_t row = (slot + ((int64_t)h << p.page_log2)) * HD;
                     if (v >= N) {
@@ -430,12 +438,10 @@ __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const __grid_constant
                         if (f == 0.f) code = make_uint2(0u, 0u);
                         *reinterpret_cast<uint2*>(p.dst[1] + row + at.part * 8) = code;
                     } else {
-                        // float32 values: their quotient is rounded to e4m3 as it stands
                         auto two = [&](float g, float h2) {
                             const uint64_t u = mul2x(pack2(g, h2), up2);
-                            if (as_given) return quantise2(u, f2);
                             float2 z;
-                            unpack2(mul2x(u, f2), z.x, z.y);
+                            unpack2(fma2(u, f2, mul2x(u, lo2)), z.x, z.y);
                             return (uint32_t)__nv_cvt_float2_to_fp8x2(z, __NV_SATFINITE, __NV_E4M3);
                         };
                         const float (&y)[8] = x[v % N];

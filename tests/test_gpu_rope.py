@@ -275,6 +275,39 @@ def test_keys_as_they_come_are_quantised_as_the_write_does():
         assert torch.equal(u, v)
 
 
+@pytest.mark.parametrize("dim,rot,pairs,heads", [(128, 128, False, 3), (64, 64, True, 2), (128, 32, True, 1)])
+def test_keys_turned_by_nothing_are_quantised_as_the_write_does(dim, rot, pairs, heads):
+    """Positions of 0 turn by nothing: codes and scales are the write's, bit for bit,
+    midpoints of two codes among them; at other positions that holds for what lies
+    behind the turned values, where the row's largest value lies there too."""
+    g = torch.Generator().manual_seed(dim + rot)
+    n = 200
+    # rows of +-m c / 2^s with the largest 7 m: quotients 64 c / 2^s, midpoints for odd c
+    # of 5 bits, and 64 / m is inexact
+    m = torch.tensor([3, 5, 7, 9, 11, 13])[torch.arange(n) % 6][:, None, None]
+    c = torch.randint(8, 16, (n, heads, dim), generator=g) * 2 + 1
+    c = torch.where(c * m > 255, torch.full((), 17), c) * torch.randint(0, 2, c.shape, generator=g).mul(2).sub(1)
+    x = (m * c).float() * torch.exp2(-torch.randint(3, 9, c.shape, generator=g).float())
+    x[:, :, -1:] = 7.0 * m
+    x[n // 2:] *= 2.0 ** -105                                 # below 2^-100 the rows are scaled up first
+    K = x.to(BF).to(DEV)
+    V = torch.zeros_like(K)
+    s = Paged([n], heads, dim, 16, F8, seed=1)
+    args = (_off([n]), _i32([n]), s.table)
+    a, b, c = s.empty(), s.empty(), s.empty()
+    rope = binding.Rope(_freq(rot), interleaved=pairs)
+    binding.kv_write(b, K, V, *args)
+    binding.rope_write(a, None, K, V, *args, rope=rope, positions=torch.zeros(n, dtype=torch.int32, device=DEV))
+    for x, y in zip(_bits(a), _bits(b)):
+        assert torch.equal(x, y)
+    if rot < dim:
+        # (a pair of values up to 31 m / 8 turns to 5.5 m at most)
+        binding.rope_write(c, None, K, V, *args, rope=rope)
+        codes, _, scale, _ = _bits(c)
+        want, _, ours, _ = _bits(b)
+        assert torch.equal(scale, ours) and torch.equal(codes[..., rot:], want[..., rot:])
+
+
 def test_tiny_keys_keep_their_precision():
     """Turned rows far below 1 (their reciprocals would overflow float32)."""
     g = torch.Generator().manual_seed(7)
