@@ -250,7 +250,7 @@ struct Item {
     // weights are 0, and if one is not finite the second time comes anyway; to clear
     // them took window 1024 packed 630 us for 609.)
     __device__ __forceinline__ int edge(bool second) const {
-        return second ? min((tok0 + 1 - gap) / kKeys, tiles() - 1) : (keys < len ? tiles() : (keys - gap) / kKeys);
+        return second ? min((tok0 + 1 - gap) / kKeys, tiles() - 1) : (tiles() * kKeys + gap <= len ? tiles() : (keys - gap) / kKeys);
     }
     // (with a window, the second time, also some of those before)
     __device__ __forceinline__ bool clears(const Params& p, int j, bool second) const {
