@@ -46,8 +46,8 @@
 // to 798 us, 1.48 to 1.60 PFLOP/s of the causal half (a plain bf16 product of
 // 8192^3 runs at 1.91 in a burst and 1.70 under the power cap), of 64: 606 us; 16
 // sequences of 100 to 4000 tokens: 504 to 553 us, 1.23 to 1.34 PFLOP/s.  30001 tokens,
-// window 4096, 128 sinks: 1150 to 1252 us, 1.54 to 1.68; window 1024, 4 sinks:
-// 412 to 425 us, 1.17 to 1.21; 16 sequences of 100 to 6000, window 1024: 600 to 640, 1.12 to 1.20.
+// window 4096, 128 sinks: 1150 to 1270 us, 1.52 to 1.68; window 1024, 4 sinks:
+// 412 to 425 us, 1.17 to 1.21; 16 sequences of 100 to 6000, window 1024: 600 to 645, 1.11 to 1.20.
 // (Taking a quarter of the exponentials from the XU pipe to a polynomial on the FMA
 // pipe cost 13 to 18 %: its instructions cost more than the pipe it relieves.)
 #include <algorithm>
