@@ -587,8 +587,10 @@ size_t dspark_attn_prompt_workspace_size(int B, int T, int n_heads, int n_kv_hea
  *        device memory of the current device
  *   seq_off [B + 1] int32, not decreasing, in [0, T] (a value outside is taken as
  *        the nearest in range; the status word records DSPARK_ERR_BAD_PAGE)
- *   out  [T, n_heads, head_dim] bfloat16, lse [T, n_heads] float or NULL; rows
- *        that belong to no sequence stay untouched
+ *   out  [T, n_heads, head_dim] bfloat16, 16-byte aligned, lse [T, n_heads] float or
+ *        NULL; rows that belong to no sequence stay untouched.  out and lse may be
+ *        any memory that the device writes in place (dspark_host_pointer among it);
+ *        an out of the current device's own is stored in whole tiles
  * Values that are not finite reach the rows that see them and no others: not
  * another sequence's, and not those of earlier tokens (a NaN or an infinity in v
  * is added to the rows it belongs to; such a call takes about twice the time).

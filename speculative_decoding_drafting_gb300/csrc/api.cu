@@ -467,7 +467,8 @@ static int attn_prompt(const void* q, const void* k, const void* v, int64_t q_st
     PromptArgs a;
     a.q = q; a.k = k; a.v = v; a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
     a.seq_off = seq_off; a.B = B; a.T = T; a.n_heads = n_heads; a.n_kv_heads = n_kv_heads; a.head_dim = head_dim;
-    a.scale = scale; a.window = window; a.sinks = sinks; a.out = out; a.lse = lse; a.ws = ws;
+    a.scale = scale; a.window = window; a.sinks = sinks; a.out = out; a.out_on_device = on_current_device(out);
+    a.lse = lse; a.ws = ws;
     return cuda_status(launch_attn_prompt(a, static_cast<cudaStream_t>(stream)));
 }
 

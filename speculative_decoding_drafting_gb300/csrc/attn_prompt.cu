@@ -143,6 +143,7 @@ struct Params {
     int most;                           // entries that the workspace holds
     int single;                         // no CTA gets a second item: each finds its own entry
     int sectors;                        // out begins on a 32-byte boundary
+    int bulk;                           // out is this device's memory: whole row tiles go there by bulk copies
     uint16_t* out;
     float* lse;
     void* ws;
@@ -765,7 +766,7 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
                 laid ^= 1u << at;
                 if (lane == 0) {
                     const int first = it.tok0 + s * p.toks;
-                    if (first + p.toks <= it.len) {
+                    if (p.bulk && first + p.toks <= it.len) {
 #pragma unroll
                         for (int hf = 0; hf < C::kHalves; ++hf)
                             tma_store_3d(&maps.out, smem + at * C::kTileBytes + hf * C::kHalfBytes, hf * 64, it.h * p.group, it.a + first);
@@ -1070,7 +1071,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint8_t* 
         if (!ok) break;
         const bool valid = row < p.toks * p.group && tok < it.len;
         const size_t at = (size_t)(it.a + tok) * p.heads + (size_t)it.h * p.group + rg;
-        const bool direct = kSecond || first + p.toks > it.len;
+        const bool direct = kSecond || !p.bulk || first + p.toks > it.len;
         if (kWindow) more = get_item(p, M, total, round + 1, coming);
         if (!wait(&B->pv_done[s], (npv - 1u) & 1u)) break;
         float a, b;
@@ -1092,7 +1093,8 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint8_t* 
         // A whole row tile goes to out by way of a ring place: rows lie 32 to an
         // instruction, one per lane, and stored as they are took 5000 cycles of the 16000
         // to 40000 of an item.  The last one of a sequence must not touch the rows
-        // behind it; and what is mended is stored as it is.
+        // behind it; what is mended is stored as it is, and so is an out that is not this
+        // device's memory (mapped host memory, a peer's): plain stores reach any of them.
         uint8_t* stage = smem + mine % C::kStages * C::kTileBytes;
         if (!kSecond && !wait(&B->full[mine % C::kStages], mine / C::kStages & 1u)) break;
         uint32_t most = 0;                                   // bits of the row's largest magnitudes, a NaN's above all
@@ -1150,7 +1152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tmap(&maps.q);
         prefetch_tmap(&maps.k);
         prefetch_tmap(&maps.v);
-        prefetch_tmap(&maps.out);
+        if (p.bulk) prefetch_tmap(&maps.out);
     }
     if (warp == 1) tmem_alloc(&M->tmem, 512);
     // rows of Q that no token of an item fills are zeros (these for the whole
@@ -1252,6 +1254,7 @@ cudaError_t launch_attn_prompt(const PromptArgs& a, cudaStream_t s) {
     p.list = reinterpret_cast<const int4*>(w + 256);
     p.out = static_cast<uint16_t*>(a.out);
     p.sectors = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
+    p.bulk = a.out_on_device;
     p.lse = a.lse;
     p.ws = a.ws;
     p.B = a.B;
@@ -1276,7 +1279,7 @@ cudaError_t launch_attn_prompt(const PromptArgs& a, cudaStream_t s) {
         const cuuint32_t box[3] = {64, b1, b2};
         return make_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
     };
-    if (!map(&maps.out, a.out, a.n_heads, (int64_t)a.n_heads * a.head_dim, (cuuint32_t)p.group, (cuuint32_t)p.toks)) return cudaErrorInvalidValue;
+    if (p.bulk && !map(&maps.out, a.out, a.n_heads, (int64_t)a.n_heads * a.head_dim, (cuuint32_t)p.group, (cuuint32_t)p.toks)) return cudaErrorInvalidValue;
     if (!map(&maps.q, a.q, a.n_heads, a.q_stride, (cuuint32_t)p.group, (cuuint32_t)p.toks) ||
         !map(&maps.k, a.k, a.n_kv_heads, a.k_stride, 1, kKeys) || !map(&maps.v, a.v, a.n_kv_heads, a.v_stride, 1, kKeys))
         return cudaErrorInvalidValue;

@@ -142,6 +142,7 @@ struct PromptArgs {
     float scale;
     int window, sinks;                      // window 0: none
     void* out;
+    bool out_on_device;                     // out is memory of the current device
     float* lse;
     void* ws;
 };
