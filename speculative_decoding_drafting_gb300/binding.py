@@ -683,32 +683,35 @@ class Rope:
 
 class HeadNorm:
     """RMS norm of each query and key head with weights ``q`` and ``k``
-    [head_dim], float32 or bfloat16 CUDA tensors (None: that side is not normed)."""
+    [head_dim], float32 or bfloat16 CUDA tensors (None: that side is not normed).
+    Each call takes the weights and ``eps`` as they are then: a module that was
+    moved, cast or given other weights needs no new one."""
 
     def __init__(self, q=None, k=None, eps: float = 1e-6):
-        given = [w for w in (q, k) if w is not None]
+        self.q, self.k, self.eps = q, k, eps
+        self._struct()
+
+    def _struct(self, dim: Optional[int] = None) -> _HeadNorm:
+        given = [w for w in (self.q, self.k) if w is not None]
         if not given:
             raise ValueError("HeadNorm takes weights for queries, keys or both")
         if any(w.dtype != given[0].dtype or w.dim() != 1 for w in given):
             raise ValueError("the weights must be vectors of one dtype")
-        self.q, self.k, self.eps = q, k, eps
-        self._c = _HeadNorm(_p(q), _p(k), _dt(given[0]), eps)
-        self._ref = ctypes.byref(self._c)
-
-    def _check(self, dim):
-        _shape("the norm's q", self.q, (dim,))
-        _shape("the norm's k", self.k, (dim,))
+        if dim is not None:
+            _shape("the norm's q", self.q, (dim,))
+            _shape("the norm's k", self.k, (dim,))
+        return _HeadNorm(_p(self.q), _p(self.k), _dt(given[0]), self.eps)
 
 
 def _turn_args(rope, norm, positions, T, dim):
     """Checks of what both calls share; the positions' and the structs' addresses."""
     if norm is not None:
-        norm._check(dim)
+        norm = ctypes.byref(norm._struct(dim))
     if positions is not None:
         if rope is None:
             raise ValueError("positions go with a rope")
         _shape("positions", positions, (T,) if rope.n_axes == 1 and positions.dim() == 1 else (T, rope.n_axes), torch.int32)
-    return _p(positions), rope and rope._ref, norm and norm._ref
+    return _p(positions), rope and rope._ref, norm
 
 
 def _rows_out(out, name, T, heads, dim, dev):
