@@ -670,10 +670,14 @@ class Rope:
             raise ValueError(f"1 to 64 frequencies, got {len(inv_freq)}")
         if len(axis) != len(inv_freq) or min(axis) < 0 or max(axis) > 3:
             raise ValueError("axis must hold a number from 0 to 3 for each frequency")
-        self.n_axes = max(axis) + 1 if n_axes is None else int(n_axes)
-        self._c = _Rope(2 * len(inv_freq), int(interleaved), self.n_axes, amplitude, (ctypes.c_uint8 * 64)(*axis),
-                        (ctypes.c_double * 64)(*inv_freq))
+        self._c = _Rope(2 * len(inv_freq), int(interleaved), max(axis) + 1 if n_axes is None else int(n_axes), amplitude,
+                        (ctypes.c_uint8 * 64)(*axis), (ctypes.c_double * 64)(*inv_freq))
         self._ref = ctypes.byref(self._c)
+
+    @property
+    def n_axes(self) -> int:
+        """Axes of the positions that it takes (fixed, like the rest of it)."""
+        return self._c.n_axes
 
     @classmethod
     def from_theta(cls, rot: int, theta: float = 10000.0, **kw) -> "Rope":

@@ -94,3 +94,18 @@ def test_a_norm_is_checked_at_the_call(lib):
         with pytest.raises(TypeError):
             call()
         norm.q = norm.k = good
+
+
+def test_positions_are_checked_against_what_the_kernel_reads(lib):
+    """A rope's number of axes is the one that its struct holds: setting it apart from
+    that would pass positions that the kernel reads past."""
+    rope = binding.Rope([1.0, 0.5, 0.25, 0.1], [0, 1, 2, 0])
+    with pytest.raises(AttributeError):
+        rope.n_axes = 1
+    assert rope.n_axes == rope._c.n_axes == 3
+    for call in _calls(rope, None, _Cuda(torch.zeros((3, 3), dtype=torch.int32))):
+        call()
+        assert lib.rope.n_axes == 3
+    for call in _calls(rope, None, _Cuda(torch.zeros((3,), dtype=torch.int32))):
+        with pytest.raises(ValueError, match="positions must"):
+            call()
