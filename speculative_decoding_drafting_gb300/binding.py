@@ -1,8 +1,9 @@
 """Thin Python binding of libdspark.so (ctypes; argument marshalling only).
 
 Every function takes CUDA torch tensors, passes their device pointers and the
-current CUDA stream to the C ABI of ``include/dspark.h`` and returns the
-output tensors it allocated.  All arithmetic of the cycle runs in the
+current CUDA stream, or the one given as ``stream``, to the C ABI of
+``include/dspark.h`` and returns the output tensors it allocated (on the stream
+that writes them).  All arithmetic of the cycle runs in the
 library's kernels; this module only checks types, allocates outputs and the
 workspace, and translates status codes into exceptions.  There is no CPU
 fallback: if the library cannot be loaded, importing a function raises.
@@ -209,7 +210,7 @@ class _Conf(ctypes.Structure):
                 ("t", ctypes.c_void_p)]
 
 
-def _conf(conf_w, conf_H, out, R, gamma, dev, conf_t=None):
+def _conf(conf_w, conf_H, out, R, gamma, dev, conf_t=None, stream=None):
     """Fill out["c"] and return a dspark_conf_t pointer (None: head off)."""
     if conf_w is None:
         return None, None
@@ -218,14 +219,36 @@ def _conf(conf_w, conf_H, out, R, gamma, dev, conf_t=None):
     if conf_H is not None and conf_H.dtype != torch.bfloat16:
         raise TypeError("confidence-head H must be bfloat16")
     if "c" not in out:
-        out["c"] = torch.empty((R, gamma), dtype=torch.float32, device=dev)
+        out["c"] = _empty((R, gamma), torch.float32, dev, stream)
     if conf_t is not None and conf_t.dtype != torch.float64:
         raise TypeError("per-position temperatures must be float64")
     st = _Conf(_p(conf_H), _p(conf_w), 0 if conf_H is None else conf_H.shape[2], _p(out["c"]), _p(conf_t))
     return st, ctypes.byref(st)
 
 
-def _workspace(nbytes: int, device) -> torch.Tensor:
+def _on(stream, make):
+    """What ``make()`` allocates and enqueues, on the stream of a call that was given
+    one: on the current stream its zeros could come after the call's kernels, and
+    its memory be that of earlier work which the call does not wait for.  The
+    current stream, where the caller may use the result, is recorded."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        t = make()
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
+def _empty(shape, dtype, device, stream=None) -> torch.Tensor:
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _on(stream, lambda: torch.empty(shape, dtype=dtype, device=device))
+
+
+def _workspace(nbytes: int, device, stream=None) -> torch.Tensor:
+    if stream is not None:
+        return _on(stream, lambda: _workspace(nbytes, device))
     # torch's caching allocator returns 512-byte aligned blocks; the first
     # word (the device status word) must start at zero.
     ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
@@ -285,15 +308,15 @@ def draft_markov(U, anchor, W1, W2, temperature: float, seed: int, req_ids=None,
     dev = U.device
     _draft_shapes(R, gamma, V, r, anchor, W1, W2, req_ids)
     if out is None:
-        out = dict(tokens=torch.empty((R, gamma), dtype=torch.int32, device=dev),
-                   q_tok=torch.empty((R, gamma), dtype=torch.float32, device=dev),
-                   lse=torch.empty((R, gamma), dtype=torch.float64, device=dev),
-                   code=torch.empty((R, gamma, r), dtype=torch.float32, device=dev))
+        out = dict(tokens=_empty((R, gamma), torch.int32, dev, stream),
+                   q_tok=_empty((R, gamma), torch.float32, dev, stream),
+                   lse=_empty((R, gamma), torch.float64, dev, stream),
+                   code=_empty((R, gamma, r), torch.float32, dev, stream))
     _draft_out_shapes(out, R, gamma, r)
     nbytes = L.dspark_draft_workspace_size(R, gamma, V, r, 0)
     if ws is None:
-        ws = _workspace(nbytes, dev)
-    keep, cp = _conf(conf_w, conf_H, out, R, gamma, dev, conf_t)
+        ws = _workspace(nbytes, dev, stream)
+    keep, cp = _conf(conf_w, conf_H, out, R, gamma, dev, conf_t, stream)
     code = L.dspark_draft_markov_conf(_p(U), _dt(U), _p(anchor), _p(W1), _p(W2), _dt(W1), R, gamma, V, r,
                                       int(seed) & 0xFFFFFFFFFFFFFFFF, _p(req_ids), float(temperature),
                                       _p(out["tokens"]), _p(out["q_tok"]), _p(out["lse"]), _p(out["code"]),
@@ -318,17 +341,17 @@ def draft_rnn(U, anchor, W1, W2, Wgco, H, temperature: float, seed: int, req_ids
     _shape("Wgco", Wgco, (2 * r + d, 3 * r))
     _shape("H", H, (R, gamma, d))
     if out is None:
-        out = dict(tokens=torch.empty((R, gamma), dtype=torch.int32, device=dev),
-                   q_tok=torch.empty((R, gamma), dtype=torch.float32, device=dev),
-                   lse=torch.empty((R, gamma), dtype=torch.float64, device=dev),
-                   code=torch.empty((R, gamma, r), dtype=torch.float32, device=dev),
-                   state=torch.empty((R, r), dtype=torch.float32, device=dev))
+        out = dict(tokens=_empty((R, gamma), torch.int32, dev, stream),
+                   q_tok=_empty((R, gamma), torch.float32, dev, stream),
+                   lse=_empty((R, gamma), torch.float64, dev, stream),
+                   code=_empty((R, gamma, r), torch.float32, dev, stream),
+                   state=_empty((R, r), torch.float32, dev, stream))
     _draft_out_shapes(out, R, gamma, r)
     _shape("state", out.get("state"), (R, r), torch.float32)
     nbytes = L.dspark_draft_workspace_size(R, gamma, V, r, d)
     if ws is None:
-        ws = _workspace(nbytes, dev)
-    keep, cp = _conf(conf_w, conf_H, out, R, gamma, dev, conf_t)
+        ws = _workspace(nbytes, dev, stream)
+    keep, cp = _conf(conf_w, conf_H, out, R, gamma, dev, conf_t, stream)
     code = L.dspark_draft_rnn_conf(_p(U), _dt(U), _p(anchor), _p(W1), _p(W2), _p(Wgco), _dt(W1), _p(H), d,
                                    R, gamma, V, r, int(seed) & 0xFFFFFFFFFFFFFFFF, _p(req_ids), float(temperature),
                                    _p(out["tokens"]), _p(out["q_tok"]), _p(out["lse"]), _p(out["code"]),
@@ -360,11 +383,11 @@ def verify(P, U, W2, draft, temperature: float, seed: int, verify_len=None, req_
     if p_stage is not None:
         _shape("p_stage", p_stage, (R, G1, V), P.dtype)
     if out is None:
-        out = dict(out_tokens=torch.empty((R, G1), dtype=torch.int32, device=dev),
-                   accept_len=torch.empty((R,), dtype=torch.int32, device=dev),
-                   n_out=torch.empty((R,), dtype=torch.int32, device=dev),
-                   p_tok=torch.empty((R, gamma), dtype=torch.float32, device=dev),
-                   lse_p=torch.empty((R, G1), dtype=torch.float64, device=dev))
+        out = dict(out_tokens=_empty((R, G1), torch.int32, dev, stream),
+                   accept_len=_empty((R,), torch.int32, dev, stream),
+                   n_out=_empty((R,), torch.int32, dev, stream),
+                   p_tok=_empty((R, gamma), torch.float32, dev, stream),
+                   lse_p=_empty((R, G1), torch.float64, dev, stream))
     _shape("out_tokens", out["out_tokens"], (R, G1), torch.int32)
     _shape("accept_len", out["accept_len"], (R,), torch.int32)
     _shape("n_out", out["n_out"], (R,), torch.int32)
@@ -372,7 +395,7 @@ def verify(P, U, W2, draft, temperature: float, seed: int, verify_len=None, req_
     _shape("lse_p", out.get("lse_p"), (R, G1), torch.float64)
     nbytes = L.dspark_verify_workspace_size(R, gamma, V, r)
     if ws is None:
-        ws = _workspace(nbytes, dev)
+        ws = _workspace(nbytes, dev, stream)
     code = L.dspark_verify_staged(_p(P), _dt(P), _p(U), _dt(U), _p(W2), _dt(W2), _p(draft["tokens"]),
                                   _p(draft["q_tok"]), _p(draft["lse"]), _p(draft["code"]), _p(verify_len),
                                   R, gamma, V, r, int(seed) & 0xFFFFFFFFFFFFFFFF, _p(req_ids), float(temperature),
@@ -392,11 +415,11 @@ def schedule(c, sps, ws=None, out=None, stream=None, budget=None):
     R, gamma = c.shape
     dev = c.device
     if out is None:
-        out = dict(verify_len=torch.empty((R,), dtype=torch.int32, device=dev),
-                   theta=torch.empty((1,), dtype=torch.float64, device=dev),
-                   n_star=torch.empty((1,), dtype=torch.int32, device=dev))
+        out = dict(verify_len=_empty((R,), torch.int32, dev, stream),
+                   theta=_empty((1,), torch.float64, dev, stream),
+                   n_star=_empty((1,), torch.int32, dev, stream))
     if ws is None:
-        ws = _workspace(L.dspark_schedule_workspace_size(R, gamma), dev)
+        ws = _workspace(L.dspark_schedule_workspace_size(R, gamma), dev, stream)
     if budget is None:
         code = L.dspark_schedule(_p(c), _p(sps), sps.numel(), R, gamma, _p(out["verify_len"]), _p(out["theta"]),
                                  _p(out["n_star"]), _p(ws), ws.numel(), _stream(stream))
@@ -418,7 +441,7 @@ def schedule_threshold(c, theta: float, mode: int = 0, out=None, stream=None):
     L = load()
     R, gamma = c.shape
     if out is None:
-        out = torch.empty((R,), dtype=torch.int32, device=c.device)
+        out = _empty((R,), torch.int32, c.device, stream)
     code = L.dspark_schedule_threshold(_p(c), R, gamma, float(theta), int(mode), _p(out), _stream(stream))
     _check("dspark_schedule_threshold", code)
     return out
@@ -434,12 +457,12 @@ def sts_fit(c, accept_len, grid, M: int = 15, ws=None, out=None, stream=None):
     if grid.dtype != torch.float64 or accept_len.dtype != torch.int32:
         raise TypeError("grid must be float64 and accept_len int32")
     if out is None:
-        out = dict(t=torch.empty((gamma,), dtype=torch.float64, device=dev),
-                   g=torch.empty((gamma,), dtype=torch.int32, device=dev),
-                   ece=torch.empty((gamma,), dtype=torch.float64, device=dev),
-                   gap=torch.empty((gamma,), dtype=torch.float64, device=dev))
+        out = dict(t=_empty((gamma,), torch.float64, dev, stream),
+                   g=_empty((gamma,), torch.int32, dev, stream),
+                   ece=_empty((gamma,), torch.float64, dev, stream),
+                   gap=_empty((gamma,), torch.float64, dev, stream))
     if ws is None:
-        ws = _workspace(L.dspark_sts_workspace_size(N, gamma, G, M), dev)
+        ws = _workspace(L.dspark_sts_workspace_size(N, gamma, G, M), dev, stream)
     code = L.dspark_sts_fit(_p(c), _p(accept_len), N, gamma, _p(grid), G, M, _p(out["t"]), _p(out["g"]),
                             _p(out["ece"]), _p(out["gap"]), _p(ws), ws.numel(), _stream(stream))
     _check("dspark_sts_fit", code)
@@ -452,7 +475,7 @@ def sts_apply(c, t, out=None, stream=None):
     L = load()
     N, gamma = c.shape
     if out is None:
-        out = torch.empty_like(c)
+        out = _empty(c.shape, c.dtype, c.device, stream)
     code = L.dspark_sts_apply(_p(c), N, gamma, _p(t), _p(out), _stream(stream))
     _check("dspark_sts_apply", code)
     return out
@@ -543,7 +566,7 @@ def kv_write(cache: KvCache, K, V, q_off, kv_len, page_table, ws=None, stream=No
     vp, vs = _token_rows("V", V, T, cache.n_kv_heads, cache.head_dim)
     c = cache._struct()
     if ws is None:
-        ws = _workspace(L.dspark_kv_workspace_size(), cache.k.device)
+        ws = _workspace(L.dspark_kv_workspace_size(), cache.k.device, stream)
     code = L.dspark_kv_write(ctypes.byref(c), ctypes.byref(b), kp, vp, ks, vs, _p(ws), ws.numel(), _stream(stream))
     _check("dspark_kv_write", code)
     return ws
@@ -557,12 +580,12 @@ def kv_read(cache: KvCache, kv_off, page_table, n_tokens: int, ws=None, out=None
     shape = (n_tokens, cache.n_kv_heads, cache.head_dim)
     b = _batch(kv_off, None, page_table, n_tokens)
     if out is None:
-        out = {name: torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device) for name in ("K", "V")}
+        out = {name: _empty(shape, torch.bfloat16, cache.k.device, stream) for name in ("K", "V")}
     for name in ("K", "V"):
         _shape(name, out[name], shape, torch.bfloat16)
     c = cache._struct()
     if ws is None:
-        ws = _workspace(L.dspark_kv_workspace_size(), cache.k.device)
+        ws = _workspace(L.dspark_kv_workspace_size(), cache.k.device, stream)
     code = L.dspark_kv_read(ctypes.byref(c), ctypes.byref(b), _p(out["K"]), _p(out["V"]), _p(ws), ws.numel(),
                             _stream(stream))
     _check("dspark_kv_read", code)
@@ -570,11 +593,11 @@ def kv_read(cache: KvCache, kv_off, page_table, n_tokens: int, ws=None, out=None
     return out
 
 
-def _attn_out(out, lse, T, heads, dim, dev):
+def _attn_out(out, lse, T, heads, dim, dev, stream=None):
     if out is None:
-        out = dict(out=torch.empty((T, heads, dim), dtype=torch.bfloat16, device=dev))
+        out = dict(out=_empty((T, heads, dim), torch.bfloat16, dev, stream))
         if lse:
-            out["lse"] = torch.empty((T, heads), dtype=torch.float32, device=dev)
+            out["lse"] = _empty((T, heads), torch.float32, dev, stream)
         return out
     _shape("out", out["out"], (T, heads, dim), torch.bfloat16)
     _shape("lse", out.get("lse"), (T, heads), torch.float32)
@@ -602,10 +625,10 @@ def attn_paged(q, cache: KvCache, q_off, kv_len, page_table, scale: Optional[flo
     T, heads, dim = q.shape
     b = _batch(q_off, kv_len, page_table, T)
     qp, qs = _token_rows("q", q, T, heads, cache.head_dim)
-    out = _attn_out(out, lse, T, heads, dim, q.device)
+    out = _attn_out(out, lse, T, heads, dim, q.device, stream)
     c = cache._struct()
     if ws is None:
-        ws = _workspace(L.dspark_attn_paged_workspace_size(b.R, T, heads, cache.n_kv_heads, dim), q.device)
+        ws = _workspace(L.dspark_attn_paged_workspace_size(b.R, T, heads, cache.n_kv_heads, dim), q.device, stream)
     local = _window(window, sinks)
     name = "dspark_attn_paged_window" if local else "dspark_attn_paged"
     code = getattr(L, name)(qp, qs, ctypes.byref(c), ctypes.byref(b), heads, float(dim ** -0.5 if scale is None else scale),
@@ -631,9 +654,9 @@ def attn_prompt(q, k, v, seq_off, scale: Optional[float] = None, lse: bool = Fal
     qp, qs = _token_rows("q", q, T, heads, dim)
     kp, ks = _token_rows("k", k, T, kv_heads, dim)
     vp, vs = _token_rows("v", v, T, kv_heads, dim)
-    out = _attn_out(out, lse, T, heads, dim, q.device)
+    out = _attn_out(out, lse, T, heads, dim, q.device, stream)
     if ws is None:
-        ws = _workspace(L.dspark_attn_prompt_workspace_size(B, T, heads, kv_heads, dim), q.device)
+        ws = _workspace(L.dspark_attn_prompt_workspace_size(B, T, heads, kv_heads, dim), q.device, stream)
     local = _window(window, sinks)
     name = "dspark_attn_prompt_window" if local else "dspark_attn_prompt"
     code = getattr(L, name)(qp, kp, vp, qs, ks, vs, _p(seq_off), B, T, heads, kv_heads, dim,
@@ -718,10 +741,10 @@ def _turn_args(rope, norm, positions, T, dim):
     return _p(positions), rope and rope._ref, norm
 
 
-def _rows_out(out, name, T, heads, dim, dev):
+def _rows_out(out, name, T, heads, dim, dev, stream=None):
     """The output rows of that name, made if need be, with their address and stride."""
     if out.get(name) is None:
-        t = out[name] = torch.empty((T, heads, dim), dtype=torch.bfloat16, device=dev)
+        t = out[name] = _empty((T, heads, dim), torch.bfloat16, dev, stream)
         return t.data_ptr(), heads * dim
     return _token_rows(name, out[name], T, heads, dim)
 
@@ -738,14 +761,14 @@ def qk_rope(q, k, positions, rope: Optional[Rope] = None, norm: Optional[HeadNor
         raise ValueError("a rope takes positions")
     out = {} if out is None else out
     qp, qs = _token_rows("q", q, T, heads, dim)
-    qo, qos = _rows_out(out, "q", T, heads, dim, q.device)
+    qo, qos = _rows_out(out, "q", T, heads, dim, q.device, stream)
     kv_heads = kp = ks = ko = kos = 0
     if k is not None:
         if k.dim() != 3:
             raise ValueError("k must have shape (T, n_kv_heads, head_dim)")
         kv_heads = k.shape[1]
         kp, ks = _token_rows("k", k, T, kv_heads, dim)
-        ko, kos = _rows_out(out, "k", T, kv_heads, dim, q.device)
+        ko, kos = _rows_out(out, "k", T, kv_heads, dim, q.device, stream)
     code = L.dspark_qk_rope(qp, kp or None, qs, ks, pos, T, heads, kv_heads, dim, rp, np_, qo, ko or None, qos, kos,
                             _stream(stream))
     _check("dspark_qk_rope", code)
@@ -774,12 +797,12 @@ def rope_write(cache: KvCache, q, K, V, q_off, kv_len, page_table, rope: Optiona
             raise ValueError("q must have shape (T, n_heads, head_dim)")
         heads = q.shape[1]
         qp, qs = _token_rows("q", q, T, heads, dim)
-        qo, qos = _rows_out(out, "q", T, heads, dim, dev)
+        qo, qos = _rows_out(out, "q", T, heads, dim, dev, stream)
     if keep or out.get("k") is not None:
-        ko, kos = _rows_out(out, "k", T, cache.n_kv_heads, dim, dev)
+        ko, kos = _rows_out(out, "k", T, cache.n_kv_heads, dim, dev, stream)
     c = cache._struct()
     if ws is None:
-        ws = _workspace(L.dspark_kv_workspace_size(), dev)
+        ws = _workspace(L.dspark_kv_workspace_size(), dev, stream)
     code = L.dspark_rope_write(ctypes.byref(c), ctypes.byref(b), qp, kp, vp, qs, ks, vs, heads, pos, rp, np_, qo, ko, qos, kos,
                                _p(ws), ws.numel(), _stream(stream))
     _check("dspark_rope_write", code)
@@ -796,7 +819,7 @@ def philox4x32_10(ctr, key, out=None, stream=None):
     _shape("ctr", ctr, (n, 4), torch.int32)
     _shape("key", key, (n, 2), torch.int32)
     if out is None:
-        out = torch.empty((n, 4), dtype=torch.int32, device=ctr.device)
+        out = _empty((n, 4), torch.int32, ctr.device, stream)
     _shape("out", out, (n, 4), torch.int32)
     code = L.dspark_philox4x32_10(_p(ctr), _p(key), _p(out), n, _stream(stream))
     _check("dspark_philox4x32_10", code)
