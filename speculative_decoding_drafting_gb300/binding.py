@@ -716,28 +716,35 @@ class HeadNorm:
 
     def __init__(self, q=None, k=None, eps: float = 1e-6):
         self.q, self.k, self.eps = q, k, eps
-        self._struct()
+        self._c = _HeadNorm()
+        self._ref = ctypes.byref(self._c)
+        self._arg()
 
-    def _struct(self, dim: Optional[int] = None) -> _HeadNorm:
-        given = [w for w in (self.q, self.k) if w is not None]
-        if not given:
+    def _arg(self, dim: Optional[int] = None):
+        """The struct, filled anew (a new one for each call takes a microsecond longer)."""
+        q, k = self.q, self.k
+        one = k if q is None else q
+        if one is None:
             raise ValueError("HeadNorm takes weights for queries, keys or both")
-        if any(w.dtype != given[0].dtype or w.dim() != 1 for w in given):
+        if (k is not None and k.dtype != one.dtype) or (dim is None and any(w is not None and w.dim() != 1 for w in (q, k))):
             raise ValueError("the weights must be vectors of one dtype")
         if dim is not None:
-            _shape("the norm's q", self.q, (dim,))
-            _shape("the norm's k", self.k, (dim,))
-        return _HeadNorm(_p(self.q), _p(self.k), _dt(given[0]), self.eps)
+            _shape("the norm's q", q, (dim,))
+            _shape("the norm's k", k, (dim,))
+        c = self._c
+        c.q_w, c.k_w, c.w_dtype, c.eps = _p(q), _p(k), _dt(one), self.eps
+        return self._ref
 
 
 def _turn_args(rope, norm, positions, T, dim):
     """Checks of what both calls share; the positions' and the structs' addresses."""
     if norm is not None:
-        norm = ctypes.byref(norm._struct(dim))
+        norm = norm._arg(dim)
     if positions is not None:
         if rope is None:
             raise ValueError("positions go with a rope")
-        _shape("positions", positions, (T,) if rope.n_axes == 1 and positions.dim() == 1 else (T, rope.n_axes), torch.int32)
+        axes = rope.n_axes
+        _shape("positions", positions, (T,) if axes == 1 and positions.dim() == 1 else (T, axes), torch.int32)
     return _p(positions), rope and rope._ref, norm
 
 
