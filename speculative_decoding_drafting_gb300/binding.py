@@ -610,8 +610,9 @@ def _window(window, sinks):
         if sinks:
             raise ValueError("sinks go with a window")
         return ()
-    # longer than any request is as good as the longest the ABI can say
-    return min(int(window), 0x7FFFFFFF), min(int(sinks), 0x7FFFFFFF)
+    # longer than any request is as good as the longest the ABI can say, and what is below
+    # its range is refused like the lowest in it
+    return tuple(max(-1 << 31, min(int(n), 0x7FFFFFFF)) for n in (window, sinks))
 
 
 def attn_paged(q, cache: KvCache, q_off, kv_len, page_table, scale: Optional[float] = None, lse: bool = False,
