@@ -682,11 +682,11 @@ typedef struct {
  *   q_out, k_out  bfloat16 in the shapes of q and k, with strides of their own.
  *             They may be q and k themselves, with the same strides; otherwise
  *             nothing of inputs and outputs may overlap.
- * All of float32 up to one rounding per value.  q, k, q_out and k_out are
- * 16-byte aligned device memory of the current device, as are positions and the
- * norm's weights.  head_dim 64 or 128,
- * n_heads in [1, 2^19], n_kv_heads in [0, 4096], T >= 0 (SHAPE; T = 0 returns OK
- * at once).  No workspace.
+ * All of float32 up to one rounding per value.  q, k, q_out and k_out and the
+ * norm's weights are 16-byte aligned device memory of the current device;
+ * positions are device memory too, aligned as int32 are (a slice from any token on
+ * will do).  head_dim 64 or 128, n_heads in [1, 2^19], n_kv_heads in [0, 4096],
+ * T >= 0 (SHAPE; T = 0 returns OK at once).  No workspace.
  */
 int dspark_qk_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride, const int32_t* positions,
                    int T, int n_heads, int n_kv_heads, int head_dim,
