@@ -270,8 +270,6 @@ __device__ __forceinline__ void tma_load_2d_mc(void* dst, const CUtensorMap* m, 
         : "memory");
 }
 
-// Order this thread's generic shared-memory accesses before later accesses
-// of the asynchronous proxy (TMA, tcgen05 operands).
 // Tile of shared memory -> tensor, in the issuing thread's group of stores.  The
 // thread that issued and committed them waits: until their shared memory has been
 // read, or until they are done.
@@ -285,6 +283,8 @@ __device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk
 __device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+// Order this thread's generic shared-memory accesses before later accesses
+// of the asynchronous proxy (TMA, tcgen05 operands).
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Barrier of `threads` threads (whole warps) of the CTA, numbered 1..15.
