@@ -648,7 +648,6 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
             // stores of a quarter warp meet in a bank.
             auto widen = [&](int x0, auto count, auto step) {
                 const int kN = count, kStep = step;
-                constexpr int kB = 1;
                 const int row0 = x0 / kPer, c0 = (x0 % kPer) * 2, sw = row0 & 7;
                 const int flip = HD == 128 ? ((tr >> 2) ^ (tr >> 3)) & 1 : (tr >> 3) & 1;
                 const uint8_t* from = src + x0 * 16;
@@ -656,21 +655,12 @@ __device__ __forceinline__ void soft_segment(const PagedParams& p, const SegInfo
                 const int a = flip * 8, b = 8 - a;
                 const int ta = (((c0 & 7) + flip) ^ sw) * 16, tb = (((c0 & 7) + 1 - flip) ^ sw) * 16;
 #pragma unroll 1
-                for (int h = 0; h < kN; h += kB) {
-                    uint2 v[2 * kB];
-#pragma unroll
-                    for (int k = 0; k < kB; ++k) {
-                        v[2 * k] = *reinterpret_cast<const uint2*>(from + k * kStep * 16 + a);
-                        v[2 * k + 1] = *reinterpret_cast<const uint2*>(from + k * kStep * 16 + b);
-                    }
-#pragma unroll
-                    for (int k = 0; k < kB; ++k) {
-                        *reinterpret_cast<uint4*>(to + k * (kStep / kPer) * 128 + ta) = e4m3x8_to_half8(v[2 * k].x, v[2 * k].y);
-                        *reinterpret_cast<uint4*>(to + k * (kStep / kPer) * 128 + tb) =
-                            e4m3x8_to_half8(v[2 * k + 1].x, v[2 * k + 1].y);
-                    }
-                    from += kB * kStep * 16;
-                    to += kB * (kStep / kPer) * 128;
+                for (int h = 0; h < kN; ++h) {
+                    const uint2 v = *reinterpret_cast<const uint2*>(from + a), w = *reinterpret_cast<const uint2*>(from + b);
+                    *reinterpret_cast<uint4*>(to + ta) = e4m3x8_to_half8(v.x, v.y);
+                    *reinterpret_cast<uint4*>(to + tb) = e4m3x8_to_half8(w.x, w.y);
+                    from += kStep * 16;
+                    to += (kStep / kPer) * 128;
                 }
                 // rows without a key become zeros, whatever their places hold
                 if (kWindow && edge) {

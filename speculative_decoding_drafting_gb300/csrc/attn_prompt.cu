@@ -878,7 +878,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint8_t* 
     // at the exponentials at once, 12001 tokens took 893 us, out of step 780, and in
     // turns they take 730 (head_dim 64: 693, 661, 610).
     uint32_t nt = 0;                                         // such tiles so far
-    auto in_turns = [&](int j) { return j >= it.begin(1) && j < min(it.n0, it.n1); };
+    auto in_turns = [&](int j) { return j < min(it.n0, it.n1); };
     auto hand_over = [&](int j) {
         if (in_turns(j) && lane == 0) mbar_arrive(&B->turn[1 - s]);
     };
