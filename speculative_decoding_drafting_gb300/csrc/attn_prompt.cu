@@ -666,7 +666,8 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
     } else if (warp == 3) {
         // ---------------- clear the last V tiles
         uint32_t g = 0;                                       // ring tiles before this item
-        uint32_t asked = 0, stored = 0;                       // parity of each row tile's next request and store, by bit
+        uint32_t asked = 0;                                   // parity of each row tile's next request, by bit
+        [[maybe_unused]] uint32_t stored = 0;                 // the second time: and of its next item's stores
         uint32_t laid = 0;                                    // of each ring place's next result
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -685,7 +686,7 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
                 if (kWindow && kSecond && !it.clears(p, j, kSecond)) continue;
                 const int key0 = it.key0(j);
                 // the issuers that use the tile have seen it arrive (its parity alone
-                // could be an earlier tile's), and the rows of the items before are stored
+                // could be an earlier tile's)
                 const uint32_t vi = g + 2 * j + 1, vat = vi % C::kStages;
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
@@ -779,11 +780,19 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
                 __syncwarp();
             }
             g += it.places(kSecond);
-            // what was taken out of V goes to the rows that see it, once they are
-            // stored (the next item's cannot be before this warp has cleared its tiles)
+            // What was taken out of V goes to the rows that see it, once they are
+            // stored.  The stores of items with nothing to add are waited for too, so that
+            // this warp's count of them is never behind: with a window the issuers ask
+            // for an item's tiles before the one before it is stored, and a wait for this
+            // item's parity alone would then pass at once, and the softmax store over
+            // what was added.  (Nor can stores run ahead: a row tile has a tile to be
+            // cleared in each of its items.)
 #pragma unroll 1
-            for (int s = 0; s < 2; ++s) {
-                if ((add >> s & 1u) && wait(&B->o_free[s], (stored >> s) & 1u)) {
+            for (int s = 0; kSecond && s < 2; ++s) {
+                if (!it.n(s)) continue;
+                if (!wait(&B->o_free[s], (stored >> s) & 1u)) break;
+                stored ^= 1u << s;
+                if (add >> s & 1u) {
                     const int first = it.tok0 + s * p.toks, end = min(first + p.toks, it.len);
                     if constexpr (kWindow) {
                         // the cleared tiles' keys in their order, each when the first token
@@ -843,7 +852,6 @@ __device__ __forceinline__ void few_roles(const Maps& maps, const Params& p, Mis
                         }
                     }
                 }
-                if (it.n(s)) stored ^= 1u << s;
             }
         }
         // what the second time stores comes after
