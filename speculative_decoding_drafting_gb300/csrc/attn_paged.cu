@@ -59,9 +59,12 @@
 // the weights, whatever the scales, lie below 2^15.5 with fp16's 11 bits down to
 // 2^-24 of the row's largest; the sum takes w / scale.
 //
-// Keys a row must not see get weight 0 by selection, not by multiplication;
-// V rows past the item's last key are zeroed in shared memory, since 0 times
-// a stale NaN would be NaN.
+// Keys a row must not see get weight 0 by selection, not by multiplication (but for
+// blocks over e4m3 with a window: there a hidden score becomes an infinity, which the
+// scales multiply, so a NaN among the scales of a key that some row of the block sees
+// reaches its other rows; the call asks for finite keys and values); V rows past
+// the item's last key are zeroed in shared memory, since 0 times a stale NaN would
+// be NaN.
 //
 // With a window (kWindow) an item's tiles are cut from its visible pages (the
 // sinks' and the window's, attn_plan.h), hidden pages inside a tile are not read,
@@ -221,7 +224,10 @@ struct PagedParams {
     JoinDesc* desc;                    // [grid]
     float* part;                       // [grid][2] pieces: m [kRowTile], l [kRowTile], O [kRowTile][HD]
     int max_pages, n_pages, page_log2, heads;
-    int blocks;                        // not one new token to each request
+    // As many new tokens as requests, or not.  (Not: blocks, as a rule; a batch of single
+    // tokens with idle requests in it counts as such too, and its tokens take the time
+    // that blocks' loop takes, 166 and 238 us where 129 and 200 are measured below.)
+    int blocks;
     float scale2;                      // scale log2(e)
 };
 
@@ -822,6 +828,9 @@ __device__ __forceinline__ void finish_segment(const PagedParams& p, const SegIn
     named_sync(5, 128);                                       // row_at and join are no longer read
 }
 
+// (80 registers at most.  The kernels without a window need no more; with one the loops
+// by row count and the one for any rows together spill: 144 bytes stored and 200 loaded
+// over bf16, 224 to 232 and 392 to 400 over e4m3.)
 template <int HD, bool F8, bool kWindow>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_paged_kernel(const __grid_constant__ Maps maps, const PagedParams p) {

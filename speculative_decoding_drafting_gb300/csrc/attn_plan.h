@@ -14,9 +14,11 @@
 // With a window (WindowPlan) an item's keys are the sinks' pages and, from the
 // page that its first row's window begins in, those up to its end, one after
 // another; its tiles are cut from that line, in which key v stands for key v, or
-// v + gap from the sinks' end on.  (Tiles of the keys themselves left a tile to the
-// sinks and one to the window's beginning, mostly hidden: 10 tiles for a window
-// of 1024 and 4 sinks where this takes 9.)
+// v + gap from the sinks' end on.  One token's line is at most
+// head + window + unit - 1 long (WindowPlan).  (Tiles of the keys themselves left a
+// tile to the sinks and one to the window's beginning, mostly hidden: 10 tiles for
+// a window of 1024 and 4 sinks where this takes 9 with pages of up to 64 tokens.  With
+// larger ones it takes up to 10 too.)
 #pragma once
 
 #include <stdint.h>

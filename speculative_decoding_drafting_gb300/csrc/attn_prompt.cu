@@ -28,8 +28,9 @@
 // longest to the shortest, forwards and backwards over the CTAs in turn.
 //
 // With a window (kWindow) an item's keys are the sinks and what its windows reach,
-// one after another (Item), so it takes window / 128 + 1 tiles wherever it stands,
-// and about 8000 cycles beside its tiles' 2570 each.
+// one after another (Item): at most (head + window + tokens of the pair - 1) / 128 tiles,
+// rounded up, wherever it stands.  With window 1024 a tile that every row sees takes 2550
+// cycles, the two end tiles about 1000 more each, and the way to the next item 2700.
 //
 // 0 times a NaN or an infinity is NaN, so such a value in V would reach the rows
 // that do not see its token too.  A CTA that has stored a row that is not finite goes
@@ -46,8 +47,9 @@
 // to 798 us, 1.48 to 1.60 PFLOP/s of the causal half (a plain bf16 product of
 // 8192^3 runs at 1.91 in a burst and 1.70 under the power cap), of 64: 606 us; 16
 // sequences of 100 to 4000 tokens: 504 to 553 us, 1.23 to 1.34 PFLOP/s.  30001 tokens,
-// window 4096, 128 sinks: 1150 to 1270 us, 1.52 to 1.68; window 1024, 4 sinks:
-// 412 to 425 us, 1.17 to 1.21; 16 sequences of 100 to 6000, window 1024: 600 to 645, 1.11 to 1.20.
+// window 4096, 128 sinks: 1150 us by itself, 1243 to 1300 among other passes, 1.48 to 1.68;
+// window 1024, 4 sinks: 412 to 425 us, 1.17 to 1.21; 16 sequences of 100 to 6000, window 1024:
+// 600 to 650, 1.10 to 1.20.
 // (Taking a quarter of the exponentials from the XU pipe to a polynomial on the FMA
 // pipe cost 13 to 18 %: its instructions cost more than the pipe it relieves.)
 #include <algorithm>
@@ -224,7 +226,8 @@ __global__ void __launch_bounds__(kPlanThreads) attn_prompt_plan(Params p, int4*
 // after another; its tiles are cut from that line, in which place v stands for key
 // v, or v + gap from the head's end on.  (Tiles of the keys themselves took one for
 // the sinks alone and half of one before the window: 10 for a window of 1024 and 4
-// sinks where this takes 9.)  Where nothing is left out, head and gap are 0.
+// sinks where this takes 9, with four query heads to a key-value head.)  Where nothing is
+// left out, head and gap are 0.
 constexpr int kHeadRows = 8;            // rows of a swizzle atom, which a copy can fill by itself
 template <bool kWindow>
 struct Item {
@@ -966,7 +969,8 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint8_t* 
                 a = ex2_approx(a);
                 b = ex2_approx(b);
                 l2 = add2(l2, pack2(a, b));
-                // bf16 for the product with V; the sum keeps float32
+                // bf16 for the product with V (half a step: 2^-9 of the binade), whose factors
+                // the tensor core takes at that rate; the sum keeps float32
                 const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
                 pk[i] = reinterpret_cast<const uint32_t&>(h);
             }
@@ -1041,7 +1045,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Misc* M, uint8_t* 
                     a = ex2_approx(a);
                     b = ex2_approx(b);
                     l2 = add2(l2, pack2(a, b));
-                    // bf16 for the product with V; the sum keeps float32
+                    // bf16 for the product with V, as above; the sum keeps float32
                     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
                     pk[i] = reinterpret_cast<const uint32_t&>(h);
                 }

@@ -4,10 +4,11 @@
 // A head x of head_dim values becomes y = x w / sqrt(mean x^2 + eps) (where there
 // is a norm), and its first `rot` values are turned in pairs (a, b):
 //   a' = a cos t - b sin t,  b' = b cos t + a sin t,  t = position x inv_freq
-// The turns of a position are the fraction of position x (inv_freq / 2 pi), which
-// a 64-bit integer product of the position and the frequency in units of 2^-64
-// turns gives exactly, however far the position; cosine and sine of it are
-// float32, and everything up to the one rounding of a stored value is float32.
+// The turns of a position are the fraction of position x (inv_freq / 2 pi).  The
+// frequency in units of 2^-64 turns is rounded once, to 53 bits; its product with the
+// position in 64-bit integers loses whole turns and nothing else, however far the
+// position.  Cosine and sine of the fraction are float32, and everything up to the
+// one rounding of a stored value is float32.
 //
 // Bound by the bytes: each value is read and written once.  Lanes hold 8 values
 // of a head, 4 and the 4 that they are turned with, so that neither a shuffle
