@@ -82,3 +82,27 @@ def test_a_status_is_not_cleared_by_the_busy_stream(name, wrapped):
     r = call(types.SimpleNamespace(cuda_stream=side.cuda_stream) if wrapped else side, table)
     torch.cuda.synchronize()
     assert binding.workspace_status(r["ws"]) == -9
+
+
+@pytest.mark.parametrize("name", ["qk_rope", "rope_write", "attn_paged", "attn_local", "attn_prompt", "prompt_local", "kv_read"])
+def test_captured_on_a_stream_beside_the_capturing_one(name):
+    """A call on a forked stream makes its buffers in the graph's pool; replays agree."""
+    call = _calls()[name]
+    table = _i32([[2, 0, 3]])
+    want = call(None, table)
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = call(side, table)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        for n, t in got.items():
+            if n != "ws":
+                t.fill_(0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for n, t in want.items():
+            if n != "ws":
+                assert torch.equal(got[n].view(torch.uint8), t.view(torch.uint8)), n
